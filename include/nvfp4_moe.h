@@ -25,7 +25,10 @@
  * nvfp4_moe_forward_routed), the W4A4 comparison variant
  * (nvfp4_moe_set_act_quant), a dense W4A16 NVFP4 linear (nvfp4_linear_*), an
  * allocation-free decode forward (nvfp4_moe_forward_decode_static) and a
- * decode forward on pinned host buffers (nvfp4_moe_forward_host).
+ * decode forward on pinned host buffers (nvfp4_moe_forward_host).  The 4-bit
+ * products a layer is made of are there on their own too: NVFP4 experts over
+ * ragged row groups, with the gradient of their input (nvfp4_grouped_*), and
+ * a dense linear with INT4 weights and group scales (nvfp4_int4_*).
  *
  * Conventions for every call:
  *   - returns a status, never throws, never prints unless NVFP4_MOE_LOG=1;
@@ -435,6 +438,120 @@ nvfp4_moe_status nvfp4_linear_pack(nvfp4_moe_t h, const uint8_t* w_q, const uint
  * the x pointer it was captured with.  Concurrent forwards on one handle
  * race on its workspace: serialise them on one stream. */
 nvfp4_moe_status nvfp4_linear_forward(nvfp4_moe_t h, int T, const void* x, void* out, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Grouped W4A16 NVFP4 products: E matrices W_e [N][K] in the experts' format,
+ * each multiplied with its own run of rows.  For layers whose steps do not
+ * fit nvfp4_moe_forward -- another activation, biases or adapters between the
+ * products, rows that arrive already sorted from another rank -- and for
+ * tuning what surrounds the frozen experts:
+ *   forward : out[r] = gs_e W_e   x[r]    [R][K] -> [R][N]
+ *   backward: dx[r]  = gs_e W_e^T dy[r]   [R][N] -> [R][K]
+ * for offsets[e] <= r < offsets[e+1].  The 4-bit weights are constants, so dx
+ * is the product's only gradient.  E = 1 is a dense linear's gradient.
+ *
+ * A grouped handle is an nvfp4_moe_t: nvfp4_moe_destroy, nvfp4_moe_last_error,
+ * nvfp4_moe_set_path, nvfp4_moe_get_status, nvfp4_moe_set_profiling /
+ * get_stage_times (the product counts as the down GEMM),
+ * nvfp4_moe_debug_packed_blob and nvfp4_moe_debug_set_fault apply to it; the
+ * MoE layer's and the other products' calls return NVFP4_MOE_ERR_INVALID_ARG
+ * (nvfp4_moe_debug_dequant NVFP4_MOE_ERR_NOT_IMPLEMENTED).
+ * ------------------------------------------------------------------------- */
+typedef struct nvfp4_grouped_config {
+  int num_experts;  /* E: 1..256 */
+  int out_features; /* N: 16..16384, a multiple of 16 */
+  int in_features;  /* K: 128..16384, a multiple of 128 */
+  int max_rows;     /* largest R of any call, 1..2^24 */
+  int out_dtype;    /* nvfp4_moe_out_dtype of out and of dx */
+  int device;       /* CUDA device ordinal */
+} nvfp4_grouped_config;
+
+/* Allocate a grouped handle: the packed matrices (E*Np*K*9/16 bytes, Np = N
+ * rounded up to a multiple of 128) on config->device; no workspace.
+ * Synchronous.  *out is NULL on failure. */
+nvfp4_moe_status nvfp4_grouped_create(const nvfp4_grouped_config* config, nvfp4_moe_t* out);
+
+/* Copy the matrices into the handle's device layout (per expert that of
+ * nvfp4_linear_pack; forward and backward read the same bytes).  DEVICE
+ * inputs:
+ *   w_q [E][N][K/2]  uint8  E2M1 codes, as in nvfp4_linear_pack (16-byte aligned)
+ *   w_s [E][N][K/16] uint8  E4M3 scales
+ *   gscale [E]       float  tensor scales: finite and > 0, else
+ *                           NVFP4_MOE_ERR_BAD_SCALE and the handle stays unpacked
+ * Synchronous.  Inputs may be freed once the call returns. */
+nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uint8_t* w_s, const float* gscale,
+                                    cudaStream_t stream);
+
+/* The products above, enqueued on `stream`; no host synchronisation, no
+ * allocation and no workspace: calls on one handle may overlap and be captured
+ * (the tensor descriptor over x is encoded on the host each call, so a captured
+ * graph replays with the pointers it was captured with, and with the offsets
+ * their memory then holds).
+ *   R        rows of x and out, 0..max_rows; 0 does nothing
+ *   offsets  [E+1] int32 DEVICE, 0 <= offsets[0] <= .. <= offsets[E] <= R: read
+ *            on the device.  An expert may have no row; rows outside
+ *            offsets[0]..offsets[E]-1 are read by no product and left as they
+ *            are in out.  Offsets that break the rule compute nothing and set
+ *            NVFP4_MOE_ERR_DEVICE_CHECK (nvfp4_moe_get_status).
+ *   x, dy    BF16 DEVICE, 16-byte aligned, rows ld elements apart
+ *   out, dx  BF16 or FP32 (config.out_dtype) DEVICE, 16-byte aligned; must not
+ *            overlap the input
+ *   ld*      at least the row length, a multiple of 8, at most 2^24
+ * Products are exact in FP32 and accumulated in FP32; one rounding to BF16 at
+ * the end.  The forward takes the streaming kernel for few rows (by default up
+ * to 4 per expert on average, nvfp4_moe_set_path forces either; the streaming
+ * kernel takes at most 4096 rows), the tcgen05 GEMM above; the backward always
+ * the GEMM. */
+nvfp4_moe_status nvfp4_grouped_forward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* x, int64_t ldx,
+                                       void* out, int64_t ldo, cudaStream_t stream);
+nvfp4_moe_status nvfp4_grouped_backward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* dy, int64_t ld_dy,
+                                        void* dx, int64_t ld_dx, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense linear with INT4 weights and group scales, for up to 16 tokens: the
+ * other weight-only 4-bit format dense layers come in.
+ *   out[t][n] = sum_k s[n][k/g] * (q[n][k] - z[n][k/g]) * x[t][k]
+ * q 0..15, one scale and one zero point per g consecutive elements of a row.
+ * An INT4 handle is an nvfp4_moe_t with the same calls as a grouped one;
+ * nvfp4_moe_set_path and nvfp4_moe_debug_set_fault have no effect on it.
+ * ------------------------------------------------------------------------- */
+typedef enum nvfp4_moe_act_dtype {
+  NVFP4_MOE_ACT_BF16 = 0,
+  NVFP4_MOE_ACT_F16 = 1
+} nvfp4_moe_act_dtype;
+
+typedef struct nvfp4_int4_config {
+  int out_features; /* N: 16..2^20, a multiple of 16 */
+  int in_features;  /* K: 128..65536, a multiple of 128 */
+  int group_size;   /* g: 32, 64 or 128 */
+  int max_tokens;   /* largest T of any forward, 1..16 */
+  int act_dtype;    /* nvfp4_moe_act_dtype of x and of the scales */
+  int out_f32;      /* 1: out is FP32, 0: x's type */
+  int device;       /* CUDA device ordinal */
+} nvfp4_int4_config;
+
+/* Allocate an INT4 handle: the packed matrix (N*K/2 bytes of codes, 3 bytes a
+ * group) on config->device.  Synchronous.  *out is NULL on failure. */
+nvfp4_moe_status nvfp4_int4_create(const nvfp4_int4_config* config, nvfp4_moe_t* out);
+
+/* Copy the matrix into the handle's device layout.  DEVICE inputs:
+ *   w_q   [N][K/2] uint8   codes, element 2j in the low nibble of byte j (16-byte aligned)
+ *   scale [N][K/g] BF16 or FP16 (config.act_dtype), finite
+ *   zero  [N][K/g] uint8   zero points 0..15, or NULL: 8 everywhere
+ * NVFP4_MOE_ERR_BAD_SCALE, and the handle is left unpacked, for a scale that is
+ * not finite or a zero point above 15.  Synchronous.  Inputs may be freed once
+ * the call returns. */
+nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* scale, const uint8_t* zero,
+                                 cudaStream_t stream);
+
+/* out [T][N] as above, 1 <= T <= max_tokens; x [T][K] and out DEVICE, 16-byte
+ * aligned, rows ldx / ldo elements apart (at least the row length, a multiple
+ * of 8, at most 2^24), not overlapping.  The products (q - z) * x are exact and
+ * summed in FP32, each group's sum times its scale in FP32, one rounding at
+ * the end.  Enqueued on `stream`; no host synchronisation, no allocation and
+ * no workspace: calls on one handle may overlap and be captured. */
+nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t ldx, void* out, int64_t ldo,
+                                    cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -44,6 +44,17 @@ class LinearConfig(ctypes.Structure):
                 ("decode_max_tokens", ctypes.c_int), ("out_dtype", ctypes.c_int), ("device", ctypes.c_int)]
 
 
+class GroupedConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int), ("out_features", ctypes.c_int), ("in_features", ctypes.c_int),
+                ("max_rows", ctypes.c_int), ("out_dtype", ctypes.c_int), ("device", ctypes.c_int)]
+
+
+class Int4Config(ctypes.Structure):
+    _fields_ = [("out_features", ctypes.c_int), ("in_features", ctypes.c_int), ("group_size", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("act_dtype", ctypes.c_int), ("out_f32", ctypes.c_int),
+                ("device", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -51,7 +62,7 @@ def header_functions():
     """Names of the functions include/nvfp4_moe.h declares."""
     with open(HEADER) as f:
         text = f.read()
-    return sorted(set(re.findall(r"\b(nvfp4_(?:moe|linear)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(nvfp4_(?:moe|linear|grouped|int4)_[a-z_0-9]+)\s*\(", text)))
 
 
 def load_library(path: str | None = None):
@@ -63,7 +74,7 @@ def load_library(path: str | None = None):
     if not os.path.exists(p):
         raise FileNotFoundError(f"{p} is missing: run __graft_entry__.build() (nvcc, sm_103a) first")
     lib = ctypes.CDLL(p)
-    vp, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    vp, i, f, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_int64
     sigs = {
         "nvfp4_moe_create": (i, [ctypes.POINTER(Config), ctypes.POINTER(vp)]),
         "nvfp4_moe_pack": (i, [vp, vp, vp, vp, vp, vp, vp]),
@@ -96,6 +107,13 @@ def load_library(path: str | None = None):
         "nvfp4_linear_create": (i, [ctypes.POINTER(LinearConfig), ctypes.POINTER(vp)]),
         "nvfp4_linear_pack": (i, [vp, vp, vp, vp, vp]),
         "nvfp4_linear_forward": (i, [vp, i, vp, vp, vp]),
+        "nvfp4_grouped_create": (i, [ctypes.POINTER(GroupedConfig), ctypes.POINTER(vp)]),
+        "nvfp4_grouped_pack": (i, [vp, vp, vp, vp, vp]),
+        "nvfp4_grouped_forward": (i, [vp, i, vp, vp, ll, vp, ll, vp]),
+        "nvfp4_grouped_backward": (i, [vp, i, vp, vp, ll, vp, ll, vp]),
+        "nvfp4_int4_create": (i, [ctypes.POINTER(Int4Config), ctypes.POINTER(vp)]),
+        "nvfp4_int4_pack": (i, [vp, vp, vp, vp, vp]),
+        "nvfp4_int4_forward": (i, [vp, i, vp, ll, vp, ll, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -116,6 +134,18 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _rows(t, cols, dtype, what):
+    """(address, row stride) of a CUDA matrix [rows][cols] whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype:
+        raise ValueError(f"{what}: expected [rows][{cols}] {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{what}: expected contiguous rows")
+    # a single row has no stride to speak of
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else -(-cols // 8) * 8
+
+
 def _host_ptr(t):
     """A page-locked CPU tensor's address (the library checks that CUDA maps it)."""
     if t.is_cuda or not t.is_pinned():
@@ -125,9 +155,10 @@ def _host_ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream=None):
+def _stream(stream=None, device=None):
+    """`stream`, or the current one of `device` (default: the current device)."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
+    s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
 
 
@@ -326,6 +357,112 @@ class Linear(MoELayer):
         n = (self.N + 127) // 128 * 128 * self.K * 9 // 16  # rows padded to whole 128-row blocks
         out = torch.empty((n,), dtype=torch.uint8, device=f"cuda:{self.device}")
         st = self.lib.nvfp4_moe_debug_packed_blob(self.h, _ptr(out), n, _stream(stream))
+        self._check(st, "nvfp4_moe_debug_packed_blob")
+        return out
+
+
+class Grouped(MoELayer):
+    """NVFP4 experts over ragged row groups (nvfp4_grouped_create ... nvfp4_moe_destroy)."""
+
+    def __init__(self, num_experts, out_features, in_features, max_rows, device=0, out_f32=False):
+        self.lib = load_library()
+        self.cfg = GroupedConfig(num_experts, out_features, in_features, max_rows, 1 if out_f32 else 0, device)
+        self.out_f32 = out_f32
+        self.E, self.N, self.K = num_experts, out_features, in_features
+        self.device = device
+        h = ctypes.c_void_p()
+        st = self.lib.nvfp4_grouped_create(ctypes.byref(self.cfg), ctypes.byref(h))
+        if st != 0:
+            raise Nvfp4MoeError(st, "nvfp4_grouped_create: " + self.lib.nvfp4_moe_status_string(st).decode())
+        self.h = h
+
+    def nvfp4_grouped_pack(self, w_q, w_s, gscale, stream=None):
+        """w_q [E][N][K/2] and w_s [E][N][K/16] uint8, gscale [E] float32."""
+        import torch
+        for t, shape, dt in ((w_q, (self.E, self.N, self.K // 2), torch.uint8),
+                             (w_s, (self.E, self.N, self.K // 16), torch.uint8), (gscale, (self.E,), torch.float32)):
+            if tuple(t.shape) != shape or t.dtype != dt:
+                raise ValueError(f"nvfp4_grouped_pack: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
+        st = self.lib.nvfp4_grouped_pack(self.h, _ptr(w_q), _ptr(w_s), _ptr(gscale), _stream(stream, self.device))
+        self._check(st, "nvfp4_grouped_pack")
+
+    def _product(self, fn, what, x, offsets, out, wi, wo, stream):
+        import torch
+        if offsets.dtype != torch.int32 or offsets.shape != (self.E + 1,):
+            raise ValueError(f"{what}: expected int32 offsets [{self.E + 1}]")
+        if x.shape[0] != out.shape[0]:
+            raise ValueError(f"{what}: the input has {x.shape[0]} rows, the output {out.shape[0]}")
+        xp, ldx = _rows(x, wi, torch.bfloat16, what)
+        op, ldo = _rows(out, wo, torch.float32 if self.out_f32 else torch.bfloat16, what)
+        self._check(fn(self.h, x.shape[0], _ptr(offsets), xp, ldx, op, ldo, _stream(stream, self.device)), what)
+        return out
+
+    def nvfp4_grouped_forward(self, x, offsets, out, stream=None):
+        """out[r] = gs_e W_e x[r] for the rows of every expert e; other rows of out stay as they are."""
+        return self._product(self.lib.nvfp4_grouped_forward, "nvfp4_grouped_forward", x, offsets, out, self.K, self.N,
+                             stream)
+
+    def nvfp4_grouped_backward(self, dy, offsets, dx, stream=None):
+        """dx[r] = gs_e W_e^T dy[r]: the gradient of nvfp4_grouped_forward's input."""
+        return self._product(self.lib.nvfp4_grouped_backward, "nvfp4_grouped_backward", dy, offsets, dx, self.N, self.K,
+                             stream)
+
+    def nvfp4_moe_debug_packed_blob(self, stream=None):
+        import torch
+        n = self.E * ((self.N + 127) // 128 * 128) * self.K * 9 // 16
+        out = torch.empty((n,), dtype=torch.uint8, device=f"cuda:{self.device}")
+        st = self.lib.nvfp4_moe_debug_packed_blob(self.h, _ptr(out), n, _stream(stream, self.device))
+        self._check(st, "nvfp4_moe_debug_packed_blob")
+        return out
+
+
+class Int4Linear(MoELayer):
+    """A dense linear with INT4 weights and group scales (nvfp4_int4_create ... nvfp4_moe_destroy)."""
+
+    def __init__(self, out_features, in_features, group_size, max_tokens=16, act_f16=False, device=0, out_f32=False):
+        self.lib = load_library()
+        self.cfg = Int4Config(out_features, in_features, group_size, max_tokens, 1 if act_f16 else 0,
+                              1 if out_f32 else 0, device)
+        self.out_f32, self.act_f16 = out_f32, act_f16
+        self.N, self.K, self.group = out_features, in_features, group_size
+        self.device = device
+        h = ctypes.c_void_p()
+        st = self.lib.nvfp4_int4_create(ctypes.byref(self.cfg), ctypes.byref(h))
+        if st != 0:
+            raise Nvfp4MoeError(st, "nvfp4_int4_create: " + self.lib.nvfp4_moe_status_string(st).decode())
+        self.h = h
+
+    def _act(self):
+        import torch
+        return torch.float16 if self.act_f16 else torch.bfloat16
+
+    def nvfp4_int4_pack(self, w_q, scale, zero=None, stream=None):
+        """w_q [N][K/2] uint8, scale [N][K/group] in x's type, zero [N][K/group] uint8 or None (8 everywhere)."""
+        import torch
+        groups = (self.N, self.K // self.group)
+        for t, shape, dt in ((w_q, (self.N, self.K // 2), torch.uint8), (scale, groups, self._act()),
+                             (zero, groups, torch.uint8)):
+            if t is not None and (tuple(t.shape) != shape or t.dtype != dt):
+                raise ValueError(f"nvfp4_int4_pack: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
+        st = self.lib.nvfp4_int4_pack(self.h, _ptr(w_q), _ptr(scale), _ptr(zero), _stream(stream, self.device))
+        self._check(st, "nvfp4_int4_pack")
+
+    def nvfp4_int4_forward(self, x, out, stream=None):
+        """out [T][N] = x [T][K] times the matrix, T <= max_tokens."""
+        import torch
+        if x.shape[0] != out.shape[0]:
+            raise ValueError(f"nvfp4_int4_forward: x has {x.shape[0]} rows, out {out.shape[0]}")
+        xp, ldx = _rows(x, self.K, self._act(), "nvfp4_int4_forward")
+        op, ldo = _rows(out, self.N, torch.float32 if self.out_f32 else self._act(), "nvfp4_int4_forward")
+        st = self.lib.nvfp4_int4_forward(self.h, x.shape[0], xp, ldx, op, ldo, _stream(stream, self.device))
+        self._check(st, "nvfp4_int4_forward")
+        return out
+
+    def nvfp4_moe_debug_packed_blob(self, stream=None):
+        import torch
+        n = self.N * self.K // 2 + 3 * self.N * (self.K // self.group)
+        out = torch.empty((n,), dtype=torch.uint8, device=f"cuda:{self.device}")
+        st = self.lib.nvfp4_moe_debug_packed_blob(self.h, _ptr(out), n, _stream(stream, self.device))
         self._check(st, "nvfp4_moe_debug_packed_blob")
         return out
 

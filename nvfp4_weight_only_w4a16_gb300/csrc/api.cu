@@ -18,6 +18,14 @@ struct nvfp4_moe {
   nvfp4_moe_config cfg;
   bool linear = false;  // a dense linear (nvfp4_linear_create): cfg holds E = 1, hidden = N padded to 128, inter = K
   int lin_n = 0;        // a dense linear's N (output features)
+  // a product handle (nvfp4_grouped_create, nvfp4_int4_create): `linear` is set too, so that no MoE call takes it,
+  // and ws holds the status word alone
+  enum Kind { kLayerOrLinear, kGrouped, kInt4 } kind = kLayerOrLinear;
+  nvfp4_int4_config i4{};
+  size_t product_bytes = 0;  // a product handle's packed matrix (matrices)
+  void* i4_scales = nullptr; // INT4: scales, zero points (inside blob) and whether the last pack had any
+  uint8_t* i4_zeros = nullptr;
+  bool i4_has_zeros = false;
   RouteParams rp{};     // scoring rule (nvfp4_moe_set_scoring); rp.bias points at `bias` when set
   float* bias = nullptr;  // [num_experts] device copy of the choice bias
   void* w_router = nullptr;  // [num_experts][hidden] BF16 router weight (nvfp4_moe_set_router)
@@ -94,12 +102,13 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// 2D BF16 [rows][cols] row-major, box = 64 columns x box_rows rows, 128B swizzle.
-bool encode_rows_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 16) {
+// 2D BF16 [rows][cols], rows ld elements apart (0: cols), box = 64 columns x box_rows rows, 128B swizzle.
+bool encode_rows_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 16,
+                     uint64_t ld = 0) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
+  cuuint64_t strides[1] = {(ld ? ld : cols) * 2};
   cuuint32_t box[2] = {64, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -141,7 +150,7 @@ int choose_path(const nvfp4_moe* h, int T, int k) {
 
 nvfp4_moe_status check_forward_args(nvfp4_moe* h, const void* logits, int T, int top_k, int path) {
   if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
-  if (h->linear) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "a dense-linear handle: call nvfp4_linear_forward");
+  if (h->linear) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "not an MoE handle: call its own forward");
   if (!h->packed) return fail(h, NVFP4_MOE_ERR_NOT_PACKED, "forward before a successful pack");
   if (!logits) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "router_logits is NULL");
   if (!aligned(logits, h->cfg.logits_dtype == NVFP4_MOE_LOGITS_BF16 ? 2 : 4))
@@ -515,7 +524,7 @@ nvfp4_moe_status nvfp4_moe_debug_set_fault(nvfp4_moe_t h, int fault) {
 nvfp4_moe_status nvfp4_moe_pack(nvfp4_moe_t h, const uint8_t* w13_q, const uint8_t* w13_s, const uint8_t* w2_q,
                                 const uint8_t* w2_s, const float* gscale, cudaStream_t st) {
   if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
-  if (h->linear) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "a dense-linear handle: call nvfp4_linear_pack");
+  if (h->linear) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "not an MoE handle: call its own pack");
   if (!w13_q || !w13_s || !w2_q || !w2_s || !gscale) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "pack: NULL input");
   if (!aligned(w13_q, 16) || !aligned(w2_q, 16) || !aligned(w13_s, 4) || !aligned(w2_s, 4) || !aligned(gscale, 4))
     return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "pack: misaligned input");
@@ -764,7 +773,7 @@ nvfp4_moe_status nvfp4_moe_debug_trace(nvfp4_moe_t h, uint64_t* host_dst, size_t
 nvfp4_moe_status nvfp4_moe_debug_packed_blob(nvfp4_moe_t h, void* dst, size_t dst_bytes, cudaStream_t st) {
   if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
   if (!h->packed) return fail(h, NVFP4_MOE_ERR_NOT_PACKED, "debug_packed_blob before pack");
-  const size_t n = blob_bytes_of(h->cfg, h->linear);
+  const size_t n = h->product_bytes ? h->product_bytes : blob_bytes_of(h->cfg, h->linear);
   if (!dst || dst_bytes < n) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "debug_packed_blob: destination too small");
   DeviceGuard g(h->cfg.device);
   cudaError_t e = cudaMemcpyAsync(dst, h->blob, n, cudaMemcpyDeviceToDevice, st);
@@ -829,7 +838,8 @@ nvfp4_moe_status nvfp4_linear_create(const nvfp4_linear_config* c, nvfp4_moe_t* 
 nvfp4_moe_status nvfp4_linear_pack(nvfp4_moe_t h, const uint8_t* w_q, const uint8_t* w_s, const float* gscale,
                                    cudaStream_t st) {
   if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
-  if (!h->linear) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "not a dense-linear handle: call nvfp4_moe_pack");
+  if (!h->linear || h->kind != nvfp4_moe::kLayerOrLinear)
+    return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "not a dense-linear handle: call its own pack");
   if (!w_q || !w_s || !gscale) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "linear_pack: NULL input");
   if (!aligned(w_q, 16) || !aligned(w_s, 4) || !aligned(gscale, 4))
     return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "linear_pack: misaligned input");
@@ -854,7 +864,8 @@ nvfp4_moe_status nvfp4_linear_pack(nvfp4_moe_t h, const uint8_t* w_q, const uint
 
 nvfp4_moe_status nvfp4_linear_forward(nvfp4_moe_t h, int T, const void* x, void* out, cudaStream_t st) {
   if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
-  if (!h->linear) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "not a dense-linear handle: call nvfp4_moe_forward");
+  if (!h->linear || h->kind != nvfp4_moe::kLayerOrLinear)
+    return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "not a dense-linear handle: call its own forward");
   if (!h->packed) return fail(h, NVFP4_MOE_ERR_NOT_PACKED, "linear_forward before a successful pack");
   if (T < 1 || T > h->cfg.max_tokens) return fail(h, NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "T outside 1..max_tokens");
   if (!x || !out) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "x or out is NULL");
@@ -896,6 +907,256 @@ nvfp4_moe_status nvfp4_linear_forward(nvfp4_moe_t h, int T, const void* x, void*
   h->last_T = T;
   h->last_k = 1;
   h->last_routed = false;
+  return NVFP4_MOE_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Products outside the layer: grouped NVFP4 experts, the INT4 linear.
+// ---------------------------------------------------------------------------
+namespace {
+// A handle with a blob of `bytes`, n_scales tensor scales and a status word, on `device`.
+nvfp4_moe_status create_product(nvfp4_moe::Kind kind, int device, size_t bytes, int n_scales, nvfp4_moe** out) {
+  nvfp4_moe* h = new (std::nothrow) nvfp4_moe();
+  if (!h) return NVFP4_MOE_ERR_WORKSPACE;
+  h->kind = kind;
+  h->linear = true;
+  h->cfg.device = device;
+  h->product_bytes = bytes;
+  const char* lg = getenv("NVFP4_MOE_LOG");
+  h->log = lg && lg[0] == '1';
+  const char* fp = getenv("NVFP4_MOE_FORCE_PATH");
+  if (fp && !strcmp(fp, "decode")) h->path = NVFP4_MOE_PATH_DECODE;
+  if (fp && !strcmp(fp, "prefill")) h->path = NVFP4_MOE_PATH_PREFILL;
+  DeviceGuard g(device);
+  cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device);
+  h->ws_bytes = sizeof(DeviceStatus);
+  if (cudaMalloc(&h->blob, bytes) != cudaSuccess || cudaMalloc(&h->gscale, sizeof(float) * n_scales) != cudaSuccess ||
+      cudaMalloc(&h->ws_mem, h->ws_bytes) != cudaSuccess) {
+    cudaGetLastError();
+    nvfp4_moe_destroy(h);
+    return NVFP4_MOE_ERR_WORKSPACE;
+  }
+  h->ws.status = static_cast<DeviceStatus*>(h->ws_mem);
+  if (cudaMemset(h->ws_mem, 0, h->ws_bytes) != cudaSuccess) {
+    nvfp4_moe_destroy(h);
+    return NVFP4_MOE_ERR_CUDA;
+  }
+  *out = h;
+  return NVFP4_MOE_OK;
+}
+
+bool device_ok(int device) {
+  int ndev = 0;
+  return cudaGetDeviceCount(&ndev) == cudaSuccess && device >= 0 && device < ndev;
+}
+
+// Event record around a product: its time counts as the down GEMM stage.
+void record(cudaEvent_t (&ev)[5], int i0, int i1, cudaStream_t st) {
+  for (int i = i0; i <= i1; ++i)
+    if (ev[i]) cudaEventRecord(ev[i], st);
+}
+
+nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t* offsets, const void* in,
+                              int64_t ldi, void* out, int64_t ldo, cudaStream_t st) {
+  const char* what = backward ? "grouped_backward" : "grouped_forward";
+  const auto bad = [&](nvfp4_moe_status s, const char* msg) { return fail(h, s, std::string(what) + ": " + msg); };
+  if (h->kind != nvfp4_moe::kGrouped) return bad(NVFP4_MOE_ERR_INVALID_ARG, "not a grouped handle");
+  if (!h->packed) return bad(NVFP4_MOE_ERR_NOT_PACKED, "before a successful pack");
+  if (R < 0 || R > h->cfg.max_tokens) return bad(NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "R outside 0..max_rows");
+  if (R == 0) return NVFP4_MOE_OK;
+  const int N = h->lin_n, K = h->cfg.inter, E = h->cfg.num_experts;
+  const int wi = backward ? N : K, wo = backward ? K : N;
+  if (!offsets || !in || !out) return bad(NVFP4_MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(offsets, 4) || !aligned(in, 16) || !aligned(out, 16))
+    return bad(NVFP4_MOE_ERR_INVALID_ARG, "offsets not 4-byte or rows not 16-byte aligned");
+  if (ldi < wi || ldo < wo || ldi % 8 || ldo % 8 || ldi > (1 << 24) || ldo > (1 << 24))
+    return bad(NVFP4_MOE_ERR_INVALID_ARG, "a row stride is below the row length, above 2^24 or no multiple of 8");
+  if (!backward && h->path == NVFP4_MOE_PATH_DECODE && R > kGemvMaxRows)
+    return bad(NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "the decode path takes at most 4096 rows");
+  const bool stream = !backward && (h->path == NVFP4_MOE_PATH_DECODE ||
+                                    (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= 4 * E));
+  DeviceGuard g(h->cfg.device);
+  CUtensorMap map{};
+  if (!stream && !encode_rows_map(&map, const_cast<void*>(in), (uint64_t)R, (uint64_t)wi, 16, (uint64_t)ldi))
+    return fail(h, NVFP4_MOE_ERR_CUDA, std::string(what) + ": cuTensorMapEncodeTiled failed");
+  GroupedProduct p{};
+  p.blob = h->blob;
+  p.gscale = h->gscale;
+  p.E = E;
+  p.N = N;
+  p.K = K;
+  p.offsets = offsets;
+  p.R = R;
+  p.in = in;
+  p.ldi = ldi;
+  p.out = out;
+  p.ldo = ldo;
+  p.out_f32 = h->cfg.out_dtype == NVFP4_MOE_OUT_F32;
+  p.num_sms = h->num_sms;
+  p.status = h->ws.status;
+  p.fault = h->fault;
+  cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
+  const nvfp4_moe_status s = take_events(h, ev);
+  if (s != NVFP4_MOE_OK) return s;
+  record(ev, 0, 2, st);
+  const cudaError_t e = stream ? launch_grouped_gemv(p, st) : launch_grouped_gemm(p, backward, map, st);
+  if (e != cudaSuccess) return cuda_fail(h, e, what);
+  record(ev, 3, 4, st);
+  return NVFP4_MOE_OK;
+}
+}  // namespace
+
+extern "C" {
+
+nvfp4_moe_status nvfp4_grouped_create(const nvfp4_grouped_config* c, nvfp4_moe_t* out) {
+  if (!out) return NVFP4_MOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!c) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (c->num_experts < 1 || c->num_experts > 256) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->out_features < 16 || c->out_features > 16384 || c->out_features % 16) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->in_features < 128 || c->in_features > 16384 || c->in_features % 128) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->max_rows < 1 || c->max_rows > (1 << 24)) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->out_dtype != NVFP4_MOE_OUT_BF16 && c->out_dtype != NVFP4_MOE_OUT_F32) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (!device_ok(c->device)) return NVFP4_MOE_ERR_INVALID_ARG;
+  const int Np = (c->out_features + 127) / 128 * 128;
+  nvfp4_moe* h = nullptr;
+  const nvfp4_moe_status s =
+      create_product(nvfp4_moe::kGrouped, c->device, (size_t)c->num_experts * linear_layout(Np, c->in_features).stride,
+                     c->num_experts, &h);
+  if (s != NVFP4_MOE_OK) return s;
+  h->cfg.num_experts = c->num_experts;
+  h->cfg.hidden = Np;
+  h->cfg.inter = c->in_features;
+  h->cfg.max_tokens = c->max_rows;
+  h->cfg.max_top_k = 1;
+  h->cfg.out_dtype = c->out_dtype;
+  h->lin_n = c->out_features;
+  *out = h;
+  return NVFP4_MOE_OK;
+}
+
+nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uint8_t* w_s, const float* gscale,
+                                    cudaStream_t st) {
+  if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (h->kind != nvfp4_moe::kGrouped) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "grouped_pack: not a grouped handle");
+  if (!w_q || !w_s || !gscale) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "grouped_pack: NULL input");
+  if (!aligned(w_q, 16) || !aligned(w_s, 4) || !aligned(gscale, 4))
+    return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "grouped_pack: misaligned input");
+  DeviceGuard g(h->cfg.device);
+  const int E = h->cfg.num_experts;
+  std::vector<float> gs((size_t)E);
+  cudaError_t e = cudaMemcpyAsync(gs.data(), gscale, sizeof(float) * E, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_fail(h, e, "grouped_pack: reading gscale");
+  for (int i = 0; i < E; ++i)
+    if (!(gs[i] > 0.0f) || gs[i] > 3.4e38f) {
+      h->packed = false;
+      return fail(h, NVFP4_MOE_ERR_BAD_SCALE,
+                  "grouped_pack: the tensor scale of expert " + std::to_string(i) + " is not finite > 0");
+    }
+  e = cudaMemcpyAsync(h->gscale, gscale, sizeof(float) * E, cudaMemcpyDeviceToDevice, st);
+  if (e == cudaSuccess) e = launch_pack_grouped(w_q, w_s, h->blob, E, h->lin_n, h->cfg.hidden, h->cfg.inter, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_fail(h, e, "grouped_pack launch");
+  h->packed = true;
+  return NVFP4_MOE_OK;
+}
+
+nvfp4_moe_status nvfp4_grouped_forward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* x, int64_t ldx,
+                                       void* out, int64_t ldo, cudaStream_t st) {
+  if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
+  return grouped_impl(h, false, R, offsets, x, ldx, out, ldo, st);
+}
+
+nvfp4_moe_status nvfp4_grouped_backward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* dy, int64_t ld_dy,
+                                        void* dx, int64_t ld_dx, cudaStream_t st) {
+  if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
+  return grouped_impl(h, true, R, offsets, dy, ld_dy, dx, ld_dx, st);
+}
+
+nvfp4_moe_status nvfp4_int4_create(const nvfp4_int4_config* c, nvfp4_moe_t* out) {
+  if (!out) return NVFP4_MOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!c) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (c->out_features < 16 || c->out_features > (1 << 20) || c->out_features % 16) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->in_features < 128 || c->in_features > (1 << 16) || c->in_features % 128) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->group_size != 32 && c->group_size != 64 && c->group_size != 128) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->max_tokens < 1 || c->max_tokens > kDecodeMaxTokens) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->act_dtype != NVFP4_MOE_ACT_BF16 && c->act_dtype != NVFP4_MOE_ACT_F16) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (c->out_f32 != 0 && c->out_f32 != 1) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (!device_ok(c->device)) return NVFP4_MOE_ERR_INVALID_ARG;
+  // codes, 16-bit scales, zero-point bytes
+  const size_t n = (size_t)c->out_features * c->in_features, groups = n / c->group_size;
+  nvfp4_moe* h = nullptr;
+  const nvfp4_moe_status s = create_product(nvfp4_moe::kInt4, c->device, n / 2 + 3 * groups, 1, &h);
+  if (s != NVFP4_MOE_OK) return s;
+  h->i4 = *c;
+  h->i4_scales = h->blob + n / 2;
+  h->i4_zeros = h->blob + n / 2 + 2 * groups;
+  *out = h;
+  return NVFP4_MOE_OK;
+}
+
+nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* scale, const uint8_t* zero,
+                                 cudaStream_t st) {
+  if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (h->kind != nvfp4_moe::kInt4) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "int4_pack: not an INT4 handle");
+  if (!w_q || !scale) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "int4_pack: NULL input");
+  if (!aligned(w_q, 16) || !aligned(scale, 2)) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "int4_pack: misaligned input");
+  DeviceGuard g(h->cfg.device);
+  h->packed = false;
+  int bad = 0;
+  int* bad_dev = reinterpret_cast<int*>(h->gscale);  // an INT4 handle has no tensor scale
+  cudaError_t e = launch_pack_int4(w_q, scale, zero, h->i4.act_dtype == NVFP4_MOE_ACT_F16, h->i4.out_features,
+                                   h->i4.in_features, h->i4.group_size, h->blob, h->i4_scales, h->i4_zeros, bad_dev, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&bad, bad_dev, sizeof(int), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_fail(h, e, "int4_pack");
+  if (bad)
+    return fail(h, NVFP4_MOE_ERR_BAD_SCALE,
+                "int4_pack: " + std::to_string(bad) + " groups have a scale that is not finite or a zero point above 15");
+  h->i4_has_zeros = zero != nullptr;
+  h->packed = true;
+  return NVFP4_MOE_OK;
+}
+
+nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t ldx, void* out, int64_t ldo,
+                                    cudaStream_t st) {
+  if (!h) return NVFP4_MOE_ERR_INVALID_ARG;
+  if (h->kind != nvfp4_moe::kInt4) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "int4_forward: not an INT4 handle");
+  if (!h->packed) return fail(h, NVFP4_MOE_ERR_NOT_PACKED, "int4_forward before a successful pack");
+  if (T < 1 || T > h->i4.max_tokens) return fail(h, NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "int4_forward: T outside 1..max_tokens");
+  if (!x || !out) return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "int4_forward: x or out is NULL");
+  if (!aligned(x, 16) || !aligned(out, 16))
+    return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "int4_forward: x or out not 16-byte aligned");
+  if (ldx < h->i4.in_features || ldo < h->i4.out_features || ldx % 8 || ldo % 8 || ldx > (1 << 24) || ldo > (1 << 24))
+    return fail(h, NVFP4_MOE_ERR_INVALID_ARG,
+                "int4_forward: a row stride is below the row length, above 2^24 or no multiple of 8");
+  DeviceGuard g(h->cfg.device);
+  Int4Product p{};
+  p.codes = h->blob;
+  p.scales = h->i4_scales;
+  p.zeros = h->i4_has_zeros ? h->i4_zeros : nullptr;
+  p.N = h->i4.out_features;
+  p.K = h->i4.in_features;
+  p.group = h->i4.group_size;
+  p.T = T;
+  p.act_f16 = h->i4.act_dtype == NVFP4_MOE_ACT_F16;
+  p.x = x;
+  p.ldx = ldx;
+  p.out = out;
+  p.ldo = ldo;
+  p.out_f32 = h->i4.out_f32;
+  p.num_sms = h->num_sms;
+  cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
+  const nvfp4_moe_status s = take_events(h, ev);
+  if (s != NVFP4_MOE_OK) return s;
+  record(ev, 0, 2, st);
+  const cudaError_t e = launch_int4_gemv(p, st);
+  if (e != cudaSuccess) return cuda_fail(h, e, "int4_forward");
+  record(ev, 3, 4, st);
   return NVFP4_MOE_OK;
 }
 

@@ -160,6 +160,54 @@ cudaError_t launch_prefill_ffn(const LayerDims& d, const uint8_t* blob, const fl
                                cudaEvent_t mid, void* out, cudaStream_t st);
 size_t prefill_smem_bytes();
 
+// One product over ragged row groups: rows offsets[e] .. offsets[e+1] - 1 of in
+// times expert e's matrix (blob: E matrices of linear_layout(N rounded up to
+// 128, K)), or its transpose in the backward direction.
+struct GroupedProduct {
+  const uint8_t* blob;
+  const float* gscale;     // [E]
+  int E, N, K;
+  const int32_t* offsets;  // [E + 1] device
+  int R;                   // rows of in and out
+  const void* in;          // BF16 [R][K] (backward [R][N]), ld elements apart
+  long long ldi;
+  void* out;               // BF16 or FP32 [R][N] (backward [R][K])
+  long long ldo;
+  int out_f32;
+  int num_sms;
+  DeviceStatus* status;
+  int fault;
+};
+// rows_map: in as [R][K or N] BF16, box {64, 16}, 128B swizzle.
+cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const CUtensorMap& rows_map, cudaStream_t st);
+// The forward for few rows, streamed through registers (gemv.cu).
+cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st);
+constexpr int kGemvMaxRows = 4096;  // grid limit of launch_grouped_gemv
+
+// y [T][N] = x [T][K] times an INT4 matrix with group scales and zero points.
+struct Int4Product {
+  const uint8_t* codes;    // packed, see gemv.cu
+  const void* scales;
+  const uint8_t* zeros;    // NULL: every zero point is 8
+  int N, K, group;
+  int T;                   // 1..16
+  int act_f16;             // x and the scales are FP16, else BF16
+  const void* x;           // [T][K], ldx elements apart
+  long long ldx;
+  void* out;               // [T][N], ldo elements apart: FP32, or x's type
+  long long ldo;
+  int out_f32;
+  int num_sms;
+};
+cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st);
+// Canonical INT4 (w_q [N][K/2], scale [N][K/group] 16-bit, zero [N][K/group] or NULL) into the layout of
+// gemv.cu; bad [1] receives the number of scales that are not finite and zero points above 15.
+cudaError_t launch_pack_int4(const uint8_t* w_q, const void* scale, const uint8_t* zero, int act_f16, int N, int K,
+                             int group, uint8_t* codes, void* scales, uint8_t* zeros, int* bad, cudaStream_t st);
+// E matrices [N][K] into E linear_layout(Np, K) blobs one after another.
+cudaError_t launch_pack_grouped(const uint8_t* w_q, const uint8_t* w_s, uint8_t* blob, int E, int N, int Np, int K,
+                                cudaStream_t st);
+
 cudaError_t launch_combine(const LayerDims& d, int T, int k, const Workspace& ws, void* out,
                            cudaStream_t st);
 

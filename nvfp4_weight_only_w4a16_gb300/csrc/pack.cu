@@ -180,6 +180,16 @@ cudaError_t launch_pack_linear(const uint8_t* w_q, const uint8_t* w_s, uint8_t* 
   return cudaGetLastError();
 }
 
+cudaError_t launch_pack_grouped(const uint8_t* w_q, const uint8_t* w_s, uint8_t* blob, int E, int N, int Np, int K,
+                                cudaStream_t st) {
+  const ExpertLayout L = linear_layout(Np, K);
+  const int thr = 256;
+  const size_t nseg = (size_t)Np * K / 32;
+  pack_matrix_kernel<<<dim3((unsigned)((nseg + thr - 1) / thr), E), thr, 0, st>>>(
+      w_q, w_s, blob, L.stride, L.w2, Np, K, 0, (size_t)N * K / 2, (size_t)N * K / 16, N);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_debug_dequant(const uint8_t* blob, const float* gscale, int H, int I, int expert,
                                  int which, int via_bf16, float* out, cudaStream_t st) {
   const ExpertLayout L = expert_layout(H, I);
