@@ -978,8 +978,10 @@ nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t*
   const bool stream = !backward && (h->path == NVFP4_MOE_PATH_DECODE ||
                                     (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= 4 * E));
   DeviceGuard g(h->cfg.device);
+  const GroupedTiling tiling = grouped_tiling(E, R, backward ? K / 128 : (N + 127) / 128);
   CUtensorMap map{};
-  if (!stream && !encode_rows_map(&map, const_cast<void*>(in), (uint64_t)R, (uint64_t)wi, 16, (uint64_t)ldi))
+  if (!stream &&
+      !encode_rows_map(&map, const_cast<void*>(in), (uint64_t)R, (uint64_t)wi, (uint32_t)tiling.box, (uint64_t)ldi))
     return fail(h, NVFP4_MOE_ERR_CUDA, std::string(what) + ": cuTensorMapEncodeTiled failed");
   GroupedProduct p{};
   p.blob = h->blob;
@@ -1001,7 +1003,7 @@ nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t*
   const nvfp4_moe_status s = take_events(h, ev);
   if (s != NVFP4_MOE_OK) return s;
   record(ev, 0, 2, st);
-  const cudaError_t e = stream ? launch_grouped_gemv(p, st) : launch_grouped_gemm(p, backward, map, st);
+  const cudaError_t e = stream ? launch_grouped_gemv(p, st) : launch_grouped_gemm(p, backward, tiling, map, st);
   if (e != cudaSuccess) return cuda_fail(h, e, what);
   record(ev, 3, 4, st);
   return NVFP4_MOE_OK;

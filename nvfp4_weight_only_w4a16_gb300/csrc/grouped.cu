@@ -4,24 +4,29 @@
 //   backward: dx[r][k] = gs_e sum_n W_e[n][k] dy[r][n]
 // for the rows off[e] <= r < off[e+1] of every expert e.
 //
-// Both directions read the same packed bytes.  The weights are the 128-row M
-// operand and the rows the N operand (a multiple of 16, up to 256), so that an
-// expert with few rows pays for few columns.  A work unit is one 128-feature
-// output block of one token tile; its reduction runs over 128 x 128 weight
-// squares: two neighbouring packed tiles (128 weight rows x 64 K each).  A
-// square is dequantised to BF16 -- exact: an E2M1 x E4M3 product has at most 6
-// significant bits -- into shared memory as rows of 64 K elements (128 B,
-// 128B swizzle).  That one image serves both products: read K-major it is the
-// forward operand (M = weight row, reduction = K), read M-major it is its
-// transpose (M = K element, reduction = weight row).  Only the descriptors, and
-// which half of a square makes up a 64-long reduction step, differ.
+// Both directions read the same packed bytes.  The weights are the M operand and
+// the rows the N operand, so that an expert with few rows pays for few columns.
+// The reduction runs over 128 x 128 weight squares: two neighbouring packed tiles
+// (128 weight rows x 64 K each).  A square is dequantised to BF16 -- exact: an
+// E2M1 x E4M3 product has at most 6 significant bits -- into shared memory as rows
+// of 64 K elements (128 B, 128B swizzle).  That one image serves both products:
+// read K-major it is the forward operand (M = weight row, reduction = K), read
+// M-major it is its transpose (M = K element, reduction = weight row).  Only the
+// descriptors, and which part of a square a 64-long half step takes, differ.
 //
-// One CTA per SM, 16 warps: 0 packed-weight producer (bulk copies into a ring),
-// 1 MMA issuer, 2 row producer (TMA, zero fill past the matrix), 4-7 epilogue
-// (TMEM -> gs -> BF16/FP32 -> global), 8-15 dequantisers.  Two accumulator
-// buffers of 256 columns: the epilogue of a unit overlaps the next one's MMAs.
-// The row offsets are read on the device; every CTA derives the same unit list
-// from them, so nothing is written but the output.
+// kCtas = 2: a pair of CTAs on neighbouring multiprocessors works on 256 output
+// features (128 each) of one tile of up to 256 rows, M = 256 MMAs: each CTA
+// dequantises its own 128 x 128 squares and loads half of the rows, which both
+// halves of the MMA read.  kCtas = 1, 128 features, where there is no second block
+// to pair with.
+//
+// One CTA per multiprocessor, 24 warps: 0 packed-weight producer (bulk copies into
+// a ring), 1 MMA issuer (the pair's first CTA), 2 row producer (TMA, zero fill past
+// the matrix), 4-7 epilogue (TMEM -> gs -> shared -> 16-byte stores), 8-23
+// dequantisers in two teams that take turns.  Two accumulator buffers of 256
+// columns: the epilogue of a unit overlaps the next one's MMAs.  The row offsets
+// are read on the device; every CTA derives the same unit list from them, so
+// nothing is written but the output.
 #include <mutex>
 
 #include "common.cuh"
@@ -31,13 +36,15 @@
 namespace nvfp4moe {
 
 namespace gg {
-constexpr int kThreads = 512;
-constexpr int kDequantWarps = 8, kEpiWarps = 4;
+constexpr int kThreads = 768;
+constexpr int kTeamWarps = 8, kDequantWarps = 2 * kTeamWarps, kEpiWarps = 4;
 constexpr int kPairBytes = 2 * kTileBytes;  // one 128 x 128 weight square, packed
-constexpr int kABytes = 16384;              // half a square in BF16: one 64-long reduction step
-constexpr int kMaxStages = 8, kMaxRaw = 16;
+constexpr int kHalfBytes = 16384;           // half a square in BF16: 64 long in the reduction
+constexpr int kMaxStages = 6, kMaxRaw = 16;
 constexpr int kSmemMax = 232448;
 constexpr int kCtlBytes = 4096;             // tables and barriers in front of the rings
+constexpr int kEpiBytes = 2048;             // per epilogue warp
+constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
 }  // namespace gg
 
 struct GroupedArgs {
@@ -47,6 +54,7 @@ struct GroupedArgs {
   const int32_t* offsets;  // [E + 1]
   int E, R;
   int NB;                  // 128-feature output blocks
+  int NU;                  // work units across the features: NB or, in pairs, half of it
   int steps;               // 128-long reduction steps
   size_t block_stride;     // bytes from one output block's first square to the next one's
   size_t step_stride;      // bytes from one reduction step's square to the next
@@ -54,7 +62,8 @@ struct GroupedArgs {
   void* out;
   long long ldo;
   int out_f32;
-  int tile_rows;           // rows per token tile, a multiple of 16 up to 256
+  int tile_rows;           // rows per token tile, a multiple of 64 up to 256
+  int box;                 // rows per TMA box, divides tile_rows / kCtas
   int stages, raw_stages;
   DeviceStatus* st;
   int fault;
@@ -75,8 +84,9 @@ struct GroupedUnit {
   int e, row0, rows, nb;
 };
 
+template <int kCtas>
 __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedCtl& c, const GroupedArgs& a, int u) {
-  const int t = u / a.NB;
+  const int t = u / a.NU;
   int lo = 0, hi = a.E;  // the expert e with tile[e] <= t < tile[e + 1]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -85,69 +95,94 @@ __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedCtl& c, const G
   }
   const int m = c.off[lo + 1] - c.off[lo], nt = c.tile[lo + 1] - c.tile[lo], j = t - c.tile[lo];
   // an expert's tiles are of one size, so that none is a small remainder
-  const int per = ((m + nt - 1) / nt + 15) & ~15;
+  constexpr int kRound = 16 * kCtas - 1;
+  const int per = ((m + nt - 1) / nt + kRound) & ~kRound;
   GroupedUnit r;
   r.e = lo;
   r.row0 = c.off[lo] + j * per;
   r.rows = min(per, m - j * per);
-  r.nb = u - t * a.NB;
+  r.nb = (u - t * a.NU) * kCtas;
   return r;
 }
 
-// K-major A and B operands use sw128_desc.  M-major A operand, 128B swizzle: 64 M
-// elements by 8 reduction rows per 1024-byte atom, the next 8 rows 1024 B on, the
-// next 64 M elements one panel (64 rows x 128 B) on.
+// M-major A operand, 128B swizzle: 64 M elements by 8 reduction rows per 1024-byte
+// atom, the next 8 rows 1024 B on, the next 64 M elements one panel (64 rows x
+// 128 B) on.
 __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// 16 weights (8 bytes of codes, one scale) -> 8 BF16 pairs, exact.
-__device__ __forceinline__ void dequant16_bf16(uint32_t c0, uint32_t c1, uint32_t s2, uint32_t (&o)[8]) {
+// Two E2M1 x E4M3 products as a BF16 pair: FP16 x FP16 -> FP32 multiplies (exact),
+// one packing conversion (exact).
+__device__ __forceinline__ uint32_t scaled_pair_bf16(uint32_t codes_f16x2, uint32_t scale_f16) {
+  float lo, hi;
+  asm("{\n .reg .b16 l, h, s, u;\n mov.b32 {l, h}, %2;\n mov.b32 {s, u}, %3;\n"
+      " fma.rn.f32.f16 %0, l, s, 0f00000000;\n fma.rn.f32.f16 %1, h, s, 0f00000000;\n}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(codes_f16x2), "r"(scale_f16));
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 16 weights (8 bytes of codes; scale in the low half of s) -> 8 BF16 pairs.
+__device__ __forceinline__ void dequant16_bf16(uint32_t c0, uint32_t c1, uint32_t s, uint32_t (&o)[8]) {
   uint32_t v[4];
   e2m1x8_to_f16x2x4(c0, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = f16x2_to_bf16x2(hmul2_u32(v[i], s2));
+  for (int i = 0; i < 4; ++i) o[i] = scaled_pair_bf16(v[i], s);
   e2m1x8_to_f16x2x4(c1, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[4 + i] = f16x2_to_bf16x2(hmul2_u32(v[i], s2));
+  for (int i = 0; i < 4; ++i) o[4 + i] = scaled_pair_bf16(v[i], s);
 }
 
-template <bool kBackward>
+template <bool kBackward, int kCtas>
 __global__ void __launch_bounds__(gg::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap, GroupedArgs a) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   GroupedCtl& ctl = *reinterpret_cast<GroupedCtl*>(smem);
-  uint8_t* ring = smem + gg::kCtlBytes;
-  const int stage_bytes = gg::kABytes + a.tile_rows * 128;
+  uint8_t* ring = smem + gg::kRingOff;
+  // a stage: the operand's two halves, then the rows' two halves (this CTA's share of the tile)
+  const int b_half = a.tile_rows / kCtas * 128;
+  const int stage_bytes = 2 * gg::kHalfBytes + 2 * b_half;
   uint8_t* raw = ring + a.stages * stage_bytes;
+  const uint32_t ring_addr = smem_u32(ring);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
+  const int first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
   volatile int* abort_flag = &ctl.abort_flag;
 
   for (int i = threadIdx.x; i <= a.E; i += gg::kThreads) ctl.off[i] = a.offsets[i];
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.raw_stages; ++s) {
       mbar_init(ctl.raw_full + s, 1);
-      mbar_init(ctl.raw_empty + s, gg::kDequantWarps);
+      mbar_init(ctl.raw_empty + s, gg::kTeamWarps);
     }
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(ctl.a_full + s, gg::kDequantWarps);
-      mbar_init(ctl.b_full + s, 1);
+      mbar_init(ctl.a_full + s, kCtas * gg::kTeamWarps);  // waited for by the pair's first CTA
+      mbar_init(ctl.b_full + s, 1);                          // the same
       mbar_init(ctl.empty + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(ctl.acc_full + b, 1);
-      mbar_init(ctl.acc_empty + b, gg::kEpiWarps);
+      mbar_init(ctl.acc_empty + b, kCtas * gg::kEpiWarps);
     }
     ctl.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (kCtas == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   __syncthreads();
   if (warp == 0) {  // token tiles per expert, 8 experts a lane; offsets that do not ascend within 0..R give no tile
@@ -180,102 +215,127 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (kCtas == 2) cluster_sync_all();  // the other CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  const int total = ctl.tile[a.E] * a.NB;
+  const int total = ctl.tile[a.E] * a.NU;
 
   if (warp == 0) {
     if (lane == 0) {
-      // ---------------- packed weights ----------------
+      // ---------------- packed weights of this CTA's 128 features ----------------
       uint32_t it = 0;
+      RingPos p;
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok && a.fault != 1; u += gridDim.x) {
-        const GroupedUnit w = grouped_unit(ctl, a, u);
-        const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)w.nb * a.block_stride;
-        for (int s = 0; s < a.steps; ++s, ++it) {
-          const int sr = it % a.raw_stages;
-          if (!mbar_wait(ctl.raw_empty + sr, ((it / a.raw_stages) & 1u) ^ 1u, abort_flag, a.st, 911)) {
+      for (int u = first; u < total && ok && a.fault != 1; u += stride) {
+        const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
+        // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
+        const int nb = min(w.nb + rank, a.NB - 1);
+        const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)nb * a.block_stride;
+        for (int s = 0; s < a.steps; ++s, ++it, p.step(a.raw_stages)) {
+          if (!mbar_wait(ctl.raw_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 911)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(ctl.raw_full + sr, gg::kPairBytes);
-          bulk_g2s(raw + sr * gg::kPairBytes, src + (size_t)s * a.step_stride, gg::kPairBytes, ctl.raw_full + sr);
+          mbar_arrive_expect_tx(ctl.raw_full + p.slot, gg::kPairBytes);
+          bulk_g2s(raw + p.slot * gg::kPairBytes, src + (size_t)s * a.step_stride, gg::kPairBytes, ctl.raw_full + p.slot);
         }
       }
       if (!ok) drain_copies(ctl.raw_full, it, a.raw_stages);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      uint32_t ia = 0, j = 0;
-      for (int u = blockIdx.x; u < total; u += gridDim.x, ++j) {
-        const GroupedUnit w = grouped_unit(ctl, a, u);
-        const uint32_t idesc = idesc_bf16(128, (w.rows + 15) & ~15) | (kBackward ? 1u << 15 : 0u);
+    // ---------------- MMA issuer: the whole warp walks the loop, one lane issues ----------------
+    uint32_t j = 0;
+    RingPos p;
+    if (rank == 0) {
+      for (int u = first; u < total; u += stride, ++j) {
+        const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
+        const uint32_t idesc =
+            idesc_bf16(128 * kCtas, (w.rows + 16 * kCtas - 1) & ~(16 * kCtas - 1)) | (kBackward ? 1u << 15 : 0u);
         const uint32_t buf = j & 1u;
-        if (!mbar_wait(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
+        if (!mbar_wait_cluster(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * 256u;
         bool ok = true;
-        for (int s = 0; s < 2 * a.steps; ++s, ++ia) {
-          const int sa = ia % a.stages;
-          const uint32_t ph = (ia / a.stages) & 1u;
-          if (!mbar_wait(ctl.b_full + sa, ph, abort_flag, a.st, 913) ||
-              !mbar_wait(ctl.a_full + sa, ph, abort_flag, a.st, 914)) {
+        for (int s = 0; s < a.steps; ++s, p.step(a.stages)) {
+          if (!mbar_wait_cluster(ctl.b_full + p.slot, p.phase, abort_flag, a.st, 913) ||
+              !mbar_wait_cluster(ctl.a_full + p.slot, p.phase, abort_flag, a.st, 914)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = smem_u32(ring + sa * stage_bytes);
+          const uint32_t st = ring_addr + (uint32_t)(p.slot * stage_bytes);
           const uint64_t ad = kBackward ? sw128_desc_mn(st) : sw128_desc(st);
-          const uint64_t bd = sw128_desc(st + gg::kABytes);
+          const uint64_t bd = sw128_desc(st + 2 * gg::kHalfBytes);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
-            umma_bf16(d, ad + (kBackward ? 128u : 2u) * kk, bd + 2u * kk, idesc, (s | kk) != 0 ? 1u : 0u);
-          umma_commit(ctl.empty + sa);
+            for (int kk = 0; kk < 8; ++kk) {  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
+              const uint64_t ak = ad + (uint32_t)(kk >> 2) * (gg::kHalfBytes >> 4) + (kBackward ? 128u : 2u) * (kk & 3);
+              const uint64_t bk = bd + (uint32_t)(kk >> 2) * (uint32_t)(b_half >> 4) + 2u * (kk & 3);
+              if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, (s | kk) != 0 ? 1u : 0u);
+              else umma_bf16(d, ak, bk, idesc, (s | kk) != 0 ? 1u : 0u);
+            }
+            if (kCtas == 2) umma_commit_pair(ctl.empty + p.slot);
+            else umma_commit(ctl.empty + p.slot);
+          }
+          __syncwarp();
         }
         if (!ok) break;
-        umma_commit(ctl.acc_full + buf);
-      }
-    }
-  } else if (warp == 2) {
-    // ---------------- rows of x (dy): boxes of 16 rows x 64 reduction elements ----------------
-    uint32_t it = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < total && ok && a.fault != 1; u += gridDim.x) {
-      const GroupedUnit w = grouped_unit(ctl, a, u);
-      const int nbox = (w.rows + 15) >> 4;
-      for (int s = 0; s < 2 * a.steps; ++s, ++it) {
-        const int sa = it % a.stages;
-        int got = 1;
-        if (lane == 0) {
-          got = mbar_wait(ctl.empty + sa, ((it / a.stages) & 1u) ^ 1u, abort_flag, a.st, 915);
-          if (got) mbar_arrive_expect_tx(ctl.b_full + sa, (uint32_t)nbox * 2048u);
+        if (elect_one()) {
+          if (kCtas == 2) umma_commit_pair(ctl.acc_full + buf);
+          else umma_commit(ctl.acc_full + buf);
         }
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) {
-          ok = false;
-          break;
-        }
-        if (lane < nbox)
-          tma_2d(ring + sa * stage_bytes + gg::kABytes + lane * 2048, &tmap, s * 64, w.row0 + 16 * lane, ctl.b_full + sa);
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) drain_copies(ctl.b_full, it, a.stages);
+  } else if (warp == 2) {
+    // ---------------- rows of x (dy): this CTA's half of the tile, boxes of 64 reduction elements ----------------
+    uint32_t it = 0;
+    RingPos p;
+    bool ok = true;
+    for (int u = first; u < total && ok && a.fault != 1; u += stride) {
+      const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
+      const int share = ((w.rows + 16 * kCtas - 1) & ~(16 * kCtas - 1)) / kCtas;
+      const int nbox = (share + a.box - 1) / a.box;
+      const int row0 = w.row0 + rank * share;
+      for (int s = 0; s < a.steps; ++s, ++it, p.step(a.stages)) {
+        if (!mbar_wait(ctl.empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 915)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* dst = ring + p.slot * stage_bytes + 2 * gg::kHalfBytes;
+          if (rank == 0) mbar_arrive_expect_tx(ctl.b_full + p.slot, (uint32_t)(kCtas * 2 * nbox * a.box) * 128u);
+          const uint32_t bar = kCtas == 2 ? map_rank(ctl.b_full + p.slot, 0) : 0u;
+          for (int h = 0; h < 2; ++h)
+            for (int b = 0; b < nbox; ++b) {
+              if (kCtas == 2) tma_2d_pair(dst + h * b_half + b * a.box * 128, &tmap, s * 128 + h * 64, row0 + b * a.box, bar);
+              else tma_2d(dst + h * b_half + b * a.box * 128, &tmap, s * 128 + h * 64, row0 + b * a.box, ctl.b_full + p.slot);
+            }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {
+      if (rank == 0) drain_copies(ctl.b_full, it, a.stages);
+      else
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // its copies complete on the first CTA's barriers
+    }
   } else if (warp >= 8) {
-    // ---------------- dequantisers: warp w takes one 16-row sub-block of each 64-long step ----------------
-    const int w = warp - 8, q = lane & 3;
+    // ---------------- dequantisers: two teams take turns at the squares; warp w of a team takes one 16-row
+    // sub-block of each half, so that its waits and its fence are paid once for 64 weights a lane ----------------
+    const int team = (warp - 8) >> 3, w = (warp - 8) & 7, q = lane & 3;
     const int slot = seg_pos(lane);
-    // forward: step h is tile h (K elements 64 h ..), all 128 rows; backward: rows 64 h .. of both tiles
+    // forward: half h is tile h (K elements 64 h ..), all 128 rows; backward: rows 64 h .. of both tiles
     const int r = (kBackward ? (w & 3) * 16 : w * 16) + (lane >> 2);
     const uint32_t dst0 = (kBackward ? (uint32_t)(w >> 2) * 8192u : 0u) + (uint32_t)r * 128u;
     const uint32_t x0 = (uint32_t)((2 * q) ^ (r & 7)) * 16u, x1 = (uint32_t)((2 * q + 1) ^ (r & 7)) * 16u;
-    uint32_t ir = 0, ia = 0;
+    RingPos pr, pa;
+    int mine = 0;  // team of the current square
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      for (int s = 0; s < a.steps && ok; ++s, ++ir) {
-        const int sr = ir % a.raw_stages;
-        if (!mbar_wait(ctl.raw_full + sr, (ir / a.raw_stages) & 1u, abort_flag, a.st, 916)) {
+    for (int u = first; u < total && ok; u += stride) {
+      for (int s = 0; s < a.steps; ++s, mine ^= 1, pr.step(a.raw_stages), pa.step(a.stages)) {
+        if (mine != team) continue;
+        if (!mbar_wait(ctl.raw_full + pr.slot, pr.phase, abort_flag, a.st, 916)) {
           ok = false;
           break;
         }
@@ -283,77 +343,113 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         uint32_t sc[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* tile = raw + sr * gg::kPairBytes + (kBackward ? w >> 2 : h) * kTileBytes;
+          const uint8_t* tile = raw + pr.slot * gg::kPairBytes + (kBackward ? w >> 2 : h) * kTileBytes;
           const int sb = kBackward ? 4 * h + (w & 3) : w;
           c[h] = *reinterpret_cast<const uint4*>(tile + sb * 512 + slot * 16);
           sc[h] = *reinterpret_cast<const uint16_t*>(tile + kTileCodes + sb * 64 + slot * 2);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(ctl.raw_empty + sr);
+        if (lane == 0) mbar_arrive(ctl.raw_empty + pr.slot);
+        if (!mbar_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) {
+          ok = false;
+          break;
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h, ++ia) {
-          const int sa = ia % a.stages;
-          if (!mbar_wait(ctl.empty + sa, ((ia / a.stages) & 1u) ^ 1u, abort_flag, a.st, 917)) {
-            ok = false;
-            break;
-          }
+        for (int h = 0; h < 2; ++h) {
           const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
-          const uint32_t p = smem_u32(ring + sa * stage_bytes) + dst0;
+          const uint32_t p = ring_addr + (uint32_t)(pa.slot * stage_bytes + h * gg::kHalfBytes) + dst0;
           uint32_t o[8];
-          dequant16_bf16(c[h].x, c[h].y, dup_lo(s2), o);
+          dequant16_bf16(c[h].x, c[h].y, s2, o);
           sts128(p + x0, o[0], o[1], o[2], o[3]);
           sts128(p + x1, o[4], o[5], o[6], o[7]);
-          dequant16_bf16(c[h].z, c[h].w, dup_hi(s2), o);
+          dequant16_bf16(c[h].z, c[h].w, s2 >> 16, o);
           sts128(p + 1024u + x0, o[0], o[1], o[2], o[3]);
           sts128(p + 1024u + x1, o[4], o[5], o[6], o[7]);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ctl.a_full + sa);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 2 && rank) mbar_arrive_cluster(map_rank(ctl.a_full + pa.slot, 0));
+          else mbar_arrive(ctl.a_full + pa.slot);
         }
       }
     }
   } else if (warp >= 4) {
-    // ---------------- epilogue: warp w reads TMEM lanes 32 (w % 4) .., one output feature a lane ----------------
-    const int i = 32 * (warp & 3) + lane;
+    // ---------------- epilogue: warp w reads TMEM lanes 32 (w % 4) .., one output feature a lane, and turns
+    // 32 (FP32: 16) rows x 32 features through shared memory into 16-byte stores ----------------
+    const int quarter = warp & 3;
+    uint8_t* buf_s = smem + gg::kCtlBytes + quarter * gg::kEpiBytes;
     uint32_t j = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++j) {
-      const GroupedUnit w = grouped_unit(ctl, a, u);
+    for (int u = first; u < total; u += stride, ++j) {
+      const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
       const float gs = __ldg(a.gscale + w.e);
       const uint32_t buf = j & 1u;
       if (!mbar_wait(ctl.acc_full + buf, (j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
-      const uint32_t t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + buf * 256u;
-      const int f = 128 * w.nb + i;
-      for (int col = 0; col < w.rows; col += 32) {
-        uint32_t v[2][16];
-        const bool two = col + 16 < w.rows;
-        tmem_ld16_nw(t + (uint32_t)col, v[0]);
-        if (two) tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        if (f < a.n_out) {
-          const long long base = (long long)(w.row0 + col) * a.ldo + f;
+      const uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * 256u;
+      const int f0 = 128 * (w.nb + rank) + 32 * quarter;  // beyond n_out for a block computed twice
+      if (f0 < a.n_out) {
+        for (int col = 0; col < w.rows; col += 32) {
+          uint32_t v[2][16];
+          tmem_ld16_nw(t + (uint32_t)col, v[0]);
+          tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);  // past the tile's last column: unwritten columns, not stored
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          if (a.out_f32) {
 #pragma unroll
-          for (int jj = 0; jj < 32; ++jj) {
-            if (col + jj < w.rows) {
-              const float y = gs * __uint_as_float(v[jj >> 4][jj & 15]);
-              if (a.out_f32) reinterpret_cast<float*>(a.out)[base + jj * a.ldo] = y;
-              else reinterpret_cast<__nv_bfloat16*>(a.out)[base + jj * a.ldo] = __float2bfloat16_rn(y);
+            for (int hh = 0; hh < 2; ++hh) {
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                *reinterpret_cast<float*>(buf_s + i * 128 + lane * 4) = gs * __uint_as_float(v[hh][i]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 4 * i + (lane >> 3), f = f0 + 4 * (lane & 7), rr = col + 16 * hh + row;
+                if (rr < w.rows && f < a.n_out)
+                  *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (long long)(w.row0 + rr) * a.ldo + f) =
+                      *reinterpret_cast<const uint4*>(buf_s + row * 128 + (lane & 7) * 16);
+              }
+            }
+          } else {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              *reinterpret_cast<__nv_bfloat16*>(buf_s + i * 64 + lane * 2) =
+                  __float2bfloat16_rn(gs * __uint_as_float(v[i >> 4][i & 15]));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * i + (lane >> 2), f = f0 + 8 * (lane & 3), rr = col + row;
+              if (rr < w.rows && f < a.n_out)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)(w.row0 + rr) * a.ldo + f) =
+                    *reinterpret_cast<const uint4*>(buf_s + row * 64 + (lane & 3) * 16);
             }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ctl.acc_empty + buf);
+      if (lane == 0) {
+        if (kCtas == 2) mbar_arrive_cluster(map_rank(ctl.acc_empty + buf, 0));
+        else mbar_arrive(ctl.acc_empty + buf);
+      }
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (kCtas == 2) cluster_sync_all();  // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (kCtas == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+typedef void (*GroupedKernel)(const CUtensorMap, GroupedArgs);
+static GroupedKernel grouped_kernel(bool backward, bool pair) {
+  return backward ? (pair ? grouped_gemm_kernel<true, 2> : grouped_gemm_kernel<true, 1>)
+                  : (pair ? grouped_gemm_kernel<false, 2> : grouped_gemm_kernel<false, 1>);
 }
 
 // The opt-in shared-memory size, once per device.
@@ -366,15 +462,28 @@ static cudaError_t set_grouped_attrs() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && dev < kCached && done[dev]) return cudaSuccess;
-  for (const void* f : {(const void*)grouped_gemm_kernel<false>, (const void*)grouped_gemm_kernel<true>}) {
-    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, gg::kSmemMax);
+  for (int i = 0; i < 4; ++i) {
+    e = cudaFuncSetAttribute((const void*)grouped_kernel(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             gg::kSmemMax);
     if (e != cudaSuccess) return e;
   }
   if (dev >= 0 && dev < kCached) done[dev] = true;
   return cudaSuccess;
 }
 
-cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const CUtensorMap& rows_map, cudaStream_t st) {
+GroupedTiling grouped_tiling(int E, int R, int out_blocks) {
+  GroupedTiling t;
+  t.ctas = out_blocks > 1 ? 2 : 1;
+  // rows per token tile: wide tiles dequantise a weight square once for many rows, narrow ones leave
+  // shared memory for a deeper packed ring, which the few-rows end needs to stream weights
+  const int avg = R / E;
+  t.tile_rows = avg > 64 ? 256 : avg > 32 ? 128 : 64;
+  t.box = t.tile_rows / t.ctas < 64 ? t.tile_rows / t.ctas : 64;
+  return t;
+}
+
+cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const GroupedTiling& t,
+                                const CUtensorMap& rows_map, cudaStream_t st) {
   cudaError_t e = set_grouped_attrs();
   if (e != cudaSuccess) return e;
   const int Np = (p.N + 127) / 128 * 128, nch = p.K / kChunk;
@@ -387,6 +496,7 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const CU
   a.E = p.E;
   a.R = p.R;
   a.NB = backward ? p.K / 128 : Np / 128;
+  a.NU = (a.NB + t.ctas - 1) / t.ctas;
   a.steps = backward ? Np / 128 : p.K / 128;
   a.block_stride = backward ? (size_t)gg::kPairBytes : row_block;
   a.step_stride = backward ? row_block : (size_t)gg::kPairBytes;
@@ -396,16 +506,25 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const CU
   a.out_f32 = p.out_f32;
   a.st = p.status;
   a.fault = p.fault;
-  // rows per token tile: wide tiles dequantise a weight square once for many rows, narrow ones leave
-  // shared memory for a deeper packed ring, which the few-rows end needs to stream weights
-  const int avg = p.R / p.E;
-  a.tile_rows = avg > 64 ? 256 : avg > 32 ? 128 : 64;
-  a.stages = 4;
-  const int left = gg::kSmemMax - 1024 - gg::kCtlBytes - a.stages * (gg::kABytes + a.tile_rows * 128);
-  a.raw_stages = left / gg::kPairBytes < gg::kMaxRaw ? left / gg::kPairBytes : gg::kMaxRaw;
-  const auto fn = backward ? grouped_gemm_kernel<true> : grouped_gemm_kernel<false>;
-  fn<<<p.num_sms, gg::kThreads, gg::kSmemMax, st>>>(rows_map, a);
-  return cudaGetLastError();
+  a.tile_rows = t.tile_rows;
+  a.box = t.box;
+  const int stage = 2 * gg::kHalfBytes + 2 * (t.tile_rows / t.ctas) * 128;
+  const int room = gg::kSmemMax - 1024 - gg::kRingOff;
+  a.stages = stage > 49152 ? (room - 2 * gg::kPairBytes) / stage : 4;
+  const int left = (room - a.stages * stage) / gg::kPairBytes;
+  a.raw_stages = left < gg::kMaxRaw ? left : gg::kMaxRaw;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.num_sms / t.ctas * t.ctas));
+  cfg.blockDim = dim3(gg::kThreads);
+  cfg.dynamicSmemBytes = gg::kSmemMax;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)t.ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, grouped_kernel(backward, t.ctas == 2), rows_map, a);
 }
 
 }  // namespace nvfp4moe

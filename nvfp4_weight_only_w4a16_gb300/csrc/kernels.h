@@ -178,8 +178,16 @@ struct GroupedProduct {
   DeviceStatus* status;
   int fault;
 };
-// rows_map: in as [R][K or N] BF16, box {64, 16}, 128B swizzle.
-cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const CUtensorMap& rows_map, cudaStream_t st);
+// How launch_grouped_gemm cuts a product whose output has out_blocks blocks of 128 features.
+struct GroupedTiling {
+  int ctas;       // 2: pairs of CTAs on 256 features, 1: single ones
+  int tile_rows;  // rows per tile
+  int box;        // rows per TMA box
+};
+GroupedTiling grouped_tiling(int E, int R, int out_blocks);
+// rows_map: in as [R][K or N] BF16, box {64, tiling.box}, 128B swizzle.
+cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const GroupedTiling& tiling,
+                                const CUtensorMap& rows_map, cudaStream_t st);
 // The forward for few rows, streamed through registers (gemv.cu).
 cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st);
 constexpr int kGemvMaxRows = 4096;  // grid limit of launch_grouped_gemv
