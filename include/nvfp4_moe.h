@@ -522,7 +522,7 @@ typedef enum nvfp4_moe_act_dtype {
 
 typedef struct nvfp4_int4_config {
   int out_features; /* N: 16..2^20, a multiple of 16 */
-  int in_features;  /* K: 128..65536, a multiple of 128 */
+  int in_features;  /* K: 128..16384, a multiple of 128 */
   int group_size;   /* g: 32, 64 or 128 */
   int max_tokens;   /* largest T of any forward, 1..16 */
   int act_dtype;    /* nvfp4_moe_act_dtype of x and of the scales */
@@ -530,8 +530,8 @@ typedef struct nvfp4_int4_config {
   int device;       /* CUDA device ordinal */
 } nvfp4_int4_config;
 
-/* Allocate an INT4 handle: the packed matrix (N*K/2 bytes of codes, 3 bytes a
- * group) on config->device.  Synchronous.  *out is NULL on failure. */
+/* Allocate an INT4 handle: the packed matrix (N*K/2 bytes of codes and 3 bytes a
+ * group, N rounded up to a multiple of 32) on config->device.  Synchronous.  *out is NULL on failure. */
 nvfp4_moe_status nvfp4_int4_create(const nvfp4_int4_config* config, nvfp4_moe_t* out);
 
 /* Copy the matrix into the handle's device layout.  DEVICE inputs:

@@ -460,7 +460,7 @@ class Int4Linear(MoELayer):
 
     def nvfp4_moe_debug_packed_blob(self, stream=None):
         import torch
-        n = self.N * self.K // 2 + 3 * self.N * (self.K // self.group)
+        n = (self.N + 31) // 32 * 32 * (self.K // 2 + 3 * (self.K // self.group))
         out = torch.empty((n,), dtype=torch.uint8, device=f"cuda:{self.device}")
         st = self.lib.nvfp4_moe_debug_packed_blob(self.h, _ptr(out), n, _stream(stream, self.device))
         self._check(st, "nvfp4_moe_debug_packed_blob")

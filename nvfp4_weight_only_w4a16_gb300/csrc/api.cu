@@ -23,9 +23,7 @@ struct nvfp4_moe {
   enum Kind { kLayerOrLinear, kGrouped, kInt4 } kind = kLayerOrLinear;
   nvfp4_int4_config i4{};
   size_t product_bytes = 0;  // a product handle's packed matrix (matrices)
-  void* i4_scales = nullptr; // INT4: scales, zero points (inside blob) and whether the last pack had any
-  uint8_t* i4_zeros = nullptr;
-  bool i4_has_zeros = false;
+  bool i4_zeros = false;     // INT4: the last pack had zero points
   RouteParams rp{};     // scoring rule (nvfp4_moe_set_scoring); rp.bias points at `bias` when set
   float* bias = nullptr;  // [num_experts] device copy of the choice bias
   void* w_router = nullptr;  // [num_experts][hidden] BF16 router weight (nvfp4_moe_set_router)
@@ -1083,20 +1081,17 @@ nvfp4_moe_status nvfp4_int4_create(const nvfp4_int4_config* c, nvfp4_moe_t* out)
   *out = nullptr;
   if (!c) return NVFP4_MOE_ERR_INVALID_ARG;
   if (c->out_features < 16 || c->out_features > (1 << 20) || c->out_features % 16) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
-  if (c->in_features < 128 || c->in_features > (1 << 16) || c->in_features % 128) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->in_features < 128 || c->in_features > 16384 || c->in_features % 128) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
   if (c->group_size != 32 && c->group_size != 64 && c->group_size != 128) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
   if (c->max_tokens < 1 || c->max_tokens > kDecodeMaxTokens) return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;
   if (c->act_dtype != NVFP4_MOE_ACT_BF16 && c->act_dtype != NVFP4_MOE_ACT_F16) return NVFP4_MOE_ERR_INVALID_ARG;
   if (c->out_f32 != 0 && c->out_f32 != 1) return NVFP4_MOE_ERR_INVALID_ARG;
   if (!device_ok(c->device)) return NVFP4_MOE_ERR_INVALID_ARG;
-  // codes, 16-bit scales, zero-point bytes
-  const size_t n = (size_t)c->out_features * c->in_features, groups = n / c->group_size;
   nvfp4_moe* h = nullptr;
-  const nvfp4_moe_status s = create_product(nvfp4_moe::kInt4, c->device, n / 2 + 3 * groups, 1, &h);
+  const nvfp4_moe_status s = create_product(
+      nvfp4_moe::kInt4, c->device, int4_packed_bytes(c->out_features, c->in_features, c->group_size, true), 1, &h);
   if (s != NVFP4_MOE_OK) return s;
   h->i4 = *c;
-  h->i4_scales = h->blob + n / 2;
-  h->i4_zeros = h->blob + n / 2 + 2 * groups;
   *out = h;
   return NVFP4_MOE_OK;
 }
@@ -1112,14 +1107,14 @@ nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* 
   int bad = 0;
   int* bad_dev = reinterpret_cast<int*>(h->gscale);  // an INT4 handle has no tensor scale
   cudaError_t e = launch_pack_int4(w_q, scale, zero, h->i4.act_dtype == NVFP4_MOE_ACT_F16, h->i4.out_features,
-                                   h->i4.in_features, h->i4.group_size, h->blob, h->i4_scales, h->i4_zeros, bad_dev, st);
+                                   h->i4.in_features, h->i4.group_size, h->blob, bad_dev, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(&bad, bad_dev, sizeof(int), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(h, e, "int4_pack");
   if (bad)
     return fail(h, NVFP4_MOE_ERR_BAD_SCALE,
                 "int4_pack: " + std::to_string(bad) + " groups have a scale that is not finite or a zero point above 15");
-  h->i4_has_zeros = zero != nullptr;
+  h->i4_zeros = zero != nullptr;
   h->packed = true;
   return NVFP4_MOE_OK;
 }
@@ -1138,9 +1133,8 @@ nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t
                 "int4_forward: a row stride is below the row length, above 2^24 or no multiple of 8");
   DeviceGuard g(h->cfg.device);
   Int4Product p{};
-  p.codes = h->blob;
-  p.scales = h->i4_scales;
-  p.zeros = h->i4_has_zeros ? h->i4_zeros : nullptr;
+  p.packed = h->blob;
+  p.zeros = h->i4_zeros;
   p.N = h->i4.out_features;
   p.K = h->i4.in_features;
   p.group = h->i4.group_size;

@@ -2,35 +2,48 @@
 // the grouped NVFP4 forward, and the INT4 linear with group scales.
 //
 //   NVFP4: y[r][n] = gs_e sum_k e2m1(W_e[n][k]) s_e[n][k/16] x[r][k]
-//   INT4 : y[t][n] = sum_g s[n][g] sum_{k in g} (q[n][k] - z[n][g]) x[t][k]
+//   INT4 : y[t][n] = sum_g s[n][g] (sum_{k in g} q[n][k] x[t][k] - z[n][g] sum_{k in g} x[t][k])
 //
-// Bound by the weight bytes, so the weights go from global memory straight into
-// registers (16 bytes a lane, a warp reading 512 contiguous bytes), are
-// dequantised there into the A fragments of m16n8k16 and multiplied with up to
-// 8 * kTiles rows of x held in shared memory; FP32 accumulation.  A warp owns
-// one 16-row group of weights and every KS-th 128-element step of K; the KS
-// warps of a group are summed through shared memory in a fixed order.  kDepth
-// steps are in flight per warp, and the first ones are issued before x is
-// staged.  K is taken in slabs whose x fits shared memory.
+// Bound by the weight bytes: what counts is how many of them are in flight (a read
+// takes about 1.7 us under load, so 96 KB and more a multiprocessor) and how few
+// instructions a byte costs.  Each of a CTA's warps streams its weights through a
+// ring of its own in shared memory (cp.async, no barrier: a lane reads back what it
+// copied itself, but for the scales), turns them into the A fragments of m16n8k16 in
+// registers and multiplies them with up to 8 rows of x, also in shared memory; FP32
+// accumulation.  The unit of distribution is a granule of kRg 16-row groups over all
+// of K: one persistent CTA a multiprocessor takes an equal contiguous run of them,
+// kWarps / KS at a time, of which each is shared by KS warps that take every KS-th
+// 128-element step of K and are summed through shared memory in a fixed order, one
+// barrier each time.  The rings run ahead across that, and across new rows of x.
 //
-// NVFP4 values are multiplied by their scale in FP16 (exact: at most 6
-// significant bits), so x enters as FP16 too, each row of a slab times a power
-// of two that brings its largest finite magnitude into [2^13, 2^14); what that
-// drops lies 2^-37 below the row's maximum.  INT4 codes q - z are exact in
-// BF16 and FP16, x enters as it is, and the scales multiply each group's FP32
-// sum: no product is rounded before the sum.
+// Both formats run on FP16 operands.  x enters as FP16 times a power of two per row
+// that brings its largest finite magnitude into [2^13, 2^14); what that drops lies
+// 2^-37 below the row's maximum.  NVFP4 codes times their scale are exact in FP16
+// (at most 6 significant bits).  An INT4 code needs no conversion: its four bits,
+// masked in place, are the FP16 subnormal q 2^-24, or q 2^-20 one nibble higher,
+// which x's matching elements, staged times 2^-4, make good.  The zero point comes
+// off a group's FP32 sum with the sum of x over the group, which is staged too.
+#include <mutex>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace nvfp4moe {
 
 namespace gv {
-constexpr int kThreads = 256, kWarps = 8;
-constexpr int kDepth = 4;  // 128-element K steps in flight per warp
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kStep = 128;
+constexpr int kRg = 2;            // 16-row groups a warp multiplies with the same x: two chains of MMAs
+constexpr int kRows = 8;          // rows of x at a time: the MMA's N
+constexpr int kDepth = 3;         // steps in flight per warp, kRg KB of codes each
+constexpr int kSmem = 190 * 1024; // of rings and x
+constexpr int kStageBatch = 8;    // 16-byte pieces of x a thread holds while its row's maximum is found
 }  // namespace gv
 
 enum class W4 { kNvfp4, kInt4G32, kInt4G64, kInt4G128 };
+__host__ __device__ constexpr int int4_groups(W4 f) {  // of 128 elements of a row
+  return f == W4::kInt4G32 ? 4 : f == W4::kInt4G64 ? 2 : 1;
+}
 
 struct GemvArgs {
   // NVFP4
@@ -40,14 +53,13 @@ struct GemvArgs {
   const int32_t* offsets;
   int E, R;
   // INT4
-  const uint8_t* codes;
-  const void* scales;
-  const uint8_t* zeros;
+  const uint8_t* packed;
   int T;
   // both
   int N, K;
-  int KS;          // warps along K per 16-row group: 1, 2, 4, 8
-  int slab_steps;  // 128-element steps of x in shared memory, a multiple of kDepth * KS
+  int KS;          // warps along K per granule: 1, 2, 4, 8, 16
+  int tile_rows;   // rows of x per tile, up to 8
+  int tiles;       // INT4: ceil(T / tile_rows)
   int pitch;       // bytes of one x row in shared memory
   const void* x;
   long long ldx;
@@ -57,414 +69,516 @@ struct GemvArgs {
   DeviceStatus* st;
 };
 
-// ---- the MMA's operand type -------------------------------------------------
-template <bool kBf16>
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (kBf16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+// D += A B (m16n8k16, FP16 in, FP32 out); not volatile, so that the two row groups' chains interleave.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() {  // all but the latest kDepth - 1 groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(gv::kDepth - 1) : "memory");
 }
 
-// One 128-element step of a 16-row group, as loaded: the lane's codes of both
-// 64-element chunks and its scales (and zero points).
-template <W4 kFmt>
-struct StepRaw {
-  static constexpr int kGroups = kFmt == W4::kInt4G32 ? 4 : kFmt == W4::kInt4G64 ? 2 : 1;  // per step (INT4)
-  uint4 c[2];
-  uint32_t s[kFmt == W4::kNvfp4 ? 2 : kGroups];  // INT4: {row r, row r + 8} 16-bit scales per group
-  uint32_t z[kFmt == W4::kNvfp4 ? 1 : (kGroups + 1) / 2];  // INT4: {r, r + 8} bytes per group
+// One 128-element step of a granule (two 16-row groups).
+//   NVFP4: in the packed tiles, the two groups' codes are 1024 contiguous bytes of each of the step's two tiles and
+//   their scales 128; a slot holds [chunk][group][512 B] codes (lane t's at seg_pos(t)), then [chunk][group][64 B] scales.
+//   INT4: packed as [N/32][K/128] blocks, one block a slot's contents: [group][chunk][32 lanes][16 B] codes -- lane
+//   4 r + t holds the words of row r's elements 8 t .. 8 t + 7 and 32 + 8 t .. of the chunk, then row r + 8's; nibble i
+//   of a word is element 2 i, nibble 4 + i element 2 i + 1 -- then [group][8 r][128/g][2: row r, row r + 8] 16-bit
+//   scales and, if the matrix has any, zero points alike in bytes.
+template <W4 kFmt, bool kZeros>
+struct Step {
+  static constexpr bool kNv = kFmt == W4::kNvfp4;
+  static constexpr int kGroups = int4_groups(kFmt);
+  static constexpr int kCodes = gv::kRg * 1024;
+  static constexpr int kZeroOff = kCodes + 64 * kGroups;
+  static constexpr int kBytes = kNv ? kCodes + 256 : kZeroOff + (kZeros ? 32 * kGroups : 0);  // of a slot
+  static constexpr int kStride = kNv ? 2 * kTileBytes : kBytes;  // in memory, from a step to the next
+  uint4 c[gv::kRg][2];                     // the lane's codes
+  uint32_t s[gv::kRg][kNv ? 2 : kGroups];  // INT4: {row r, row r + 8} 16-bit scales per group
+  uint32_t z[gv::kRg][(kGroups + 1) / 2];  // INT4: {r, r + 8} bytes per group
+
+  // Start the copy of a step into a slot.  c: the lane's place in the codes; s (NVFP4): lanes 0..15's in the scales.
+  static __device__ __forceinline__ void copy(const uint8_t* c, const uint8_t* s, uint32_t slot, int lane) {
+    const uint32_t d = slot + lane * 16;
+    if (kNv) {
+      copy16(d, c);
+      copy16(d + 512, c + 512);
+      copy16(d + 1024, c + kTileBytes);
+      copy16(d + 1536, c + kTileBytes + 512);
+      if (lane < 16) copy16(d + kCodes, s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) copy16(d + 512 * i, c + 512 * i);
+      if (lane < (kBytes - kCodes) / 16) copy16(d + kCodes, c + kCodes);
+    }
+  }
+  // The lane's part of a landed step.
+  __device__ __forceinline__ void read(const uint8_t* slot, int lane) {
+    constexpr int G = kGroups;
+#pragma unroll
+    for (int q = 0; q < gv::kRg; ++q)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        c[q][h] = *reinterpret_cast<const uint4*>(slot + (kNv ? 1024 * h + 512 * q + seg_pos(lane) * 16 : 1024 * q + 512 * h + lane * 16));
+#pragma unroll
+    for (int q = 0; q < gv::kRg; ++q) {
+      const uint8_t* sp = slot + kCodes + (kNv ? q * 64 + seg_pos(lane) * 2 : q * 32 * G + (lane >> 2) * 4 * G);
+      const uint8_t* zp = slot + kZeroOff + q * 16 * G + (lane >> 2) * 2 * G;
+      if (kNv) {
+        s[q][0] = *reinterpret_cast<const uint16_t*>(sp);
+        s[q][G > 0 ? 1 : 0] = *reinterpret_cast<const uint16_t*>(sp + 128);
+      } else if (G == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sp);
+        s[q][0] = v.x;
+        s[q][G > 1 ? 1 : 0] = v.y;
+        s[q][G > 2 ? 2 : 0] = v.z;
+        s[q][G > 3 ? 3 : 0] = v.w;
+        if (kZeros) {
+          const uint2 v2 = *reinterpret_cast<const uint2*>(zp);
+          z[q][0] = v2.x;
+          z[q][G > 2 ? 1 : 0] = v2.y;
+        }
+      } else if (G == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(sp);
+        s[q][0] = v.x;
+        s[q][G > 1 ? 1 : 0] = v.y;
+        if (kZeros) z[q][0] = *reinterpret_cast<const uint32_t*>(zp);
+      } else {
+        s[q][0] = *reinterpret_cast<const uint32_t*>(sp);
+        if (kZeros) z[q][0] = *reinterpret_cast<const uint16_t*>(zp);
+      }
+    }
+  }
 };
 
-// INT4 layout: codes [N/16][K/64][32 lanes][16 B] -- lane 4 r + t holds the words of row r's elements
-// 8 t .. 8 t + 7 and 32 + 8 t .. of the chunk, then row r + 8's; nibble i of a word is element 2 i, nibble
-// 4 + i element 2 i + 1.  Scales [N/16][K/128][8 r][128/group][2: row r, row r + 8] 16-bit, zeros alike in bytes.
-template <W4 kFmt>
-__device__ __forceinline__ void load_step(const GemvArgs& a, const uint8_t* codes, const uint8_t* sc,
-                                          const uint8_t* zr, int step, int lane, StepRaw<kFmt>& w) {
-  if (kFmt == W4::kNvfp4) {  // codes: the sub-block's bytes in the row block's first tile
-    const uint8_t* p = codes + (size_t)(2 * step) * kTileBytes;
-    const int slot = seg_pos(lane);
+template <bool kBf16>
+__device__ __forceinline__ float scale_of(uint32_t v, int hi) {
+  if (kBf16) return __uint_as_float(hi ? v & 0xFFFF0000u : v << 16);
+  return __half2float(__ushort_as_half((unsigned short)(hi ? v >> 16 : v & 0xFFFFu)));
+}
+__device__ __forceinline__ float byte_of(uint32_t v, int i) {  // 0..255, exactly
+  return __uint_as_float(0x4B000000u | ((v >> (8 * i)) & 0xFFu)) - 8388608.0f;
+}
+
+// acc += the step's (16 kRg) x 8 products.  xl: the lane's x row at the step's first element and the lane's
+// position in it; sl: the lane's group sums of x at the step's first group (INT4).
+template <W4 kFmt, bool kBf16, bool kZeros>
+__device__ __forceinline__ void use_step(const Step<kFmt, kZeros>& w, const uint8_t* xl, const float* sl,
+                                         float (&acc)[gv::kRg][4]) {
+  uint32_t x[2][8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w.c[h] = ldg_stream(p + h * kTileBytes + slot * 16);
-      w.s[h] = __ldg(reinterpret_cast<const uint16_t*>(sc + (size_t)(2 * step + h) * kTileBytes + slot * 2));
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      // NVFP4: 16 elements a lane and chunk; INT4: 8 elements of either half of the chunk
+      const uint4 v = *reinterpret_cast<const uint4*>(xl + h * 128 + p * (kFmt == W4::kNvfp4 ? 16 : 64));
+      x[h][4 * p] = v.x, x[h][4 * p + 1] = v.y, x[h][4 * p + 2] = v.z, x[h][4 * p + 3] = v.w;
     }
+  if (kFmt == W4::kNvfp4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < gv::kRg; ++q) {
+        const uint32_t s2 = e4m3x2_to_f16x2(w.s[q][h]);
+        const uint32_t slo = dup_lo(s2), shi = dup_hi(s2);
+        uint32_t lo[2][4], hi[2][4];
+        e2m1x8_to_f16x2x4(w.c[q][h].x, lo[0]);
+        e2m1x8_to_f16x2x4(w.c[q][h].y, lo[1]);
+        e2m1x8_to_f16x2x4(w.c[q][h].z, hi[0]);
+        e2m1x8_to_f16x2x4(w.c[q][h].w, hi[1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_16816(acc[q], hmul2_u32(lo[j >> 1][2 * (j & 1)], slo), hmul2_u32(hi[j >> 1][2 * (j & 1)], shi),
+                    hmul2_u32(lo[j >> 1][2 * (j & 1) + 1], slo), hmul2_u32(hi[j >> 1][2 * (j & 1) + 1], shi), x[h][2 * j],
+                    x[h][2 * j + 1]);
+      }
   } else {
-    constexpr int G = StepRaw<kFmt>::kGroups;
-    const uint8_t* p = codes + (size_t)step * 1024 + lane * 16;
-    w.c[0] = ldg_stream(p);
-    w.c[1] = ldg_stream(p + 512);
-    const uint8_t* s = sc + ((size_t)step * 8 + (lane >> 2)) * (G * 4);
-    if (G == 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
-      w.s[0] = v.x;
-      w.s[G > 1 ? 1 : 0] = v.y;
-      w.s[G > 2 ? 2 : 0] = v.z;
-      w.s[G > 3 ? 3 : 0] = v.w;
-      if (zr) {
-        const uint2 z = __ldg(reinterpret_cast<const uint2*>(zr + ((size_t)step * 8 + (lane >> 2)) * 8));
-        w.z[0] = z.x;
-        w.z[G > 2 ? 1 : 0] = z.y;
-      }
-    } else if (G == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-      w.s[0] = v.x;
-      w.s[G > 1 ? 1 : 0] = v.y;
-      if (zr) w.z[0] = __ldg(reinterpret_cast<const uint32_t*>(zr + ((size_t)step * 8 + (lane >> 2)) * 4));
-    } else {
-      w.s[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-      if (zr) w.z[0] = __ldg(reinterpret_cast<const uint16_t*>(zr + ((size_t)step * 8 + (lane >> 2)) * 2));
-    }
-  }
-}
-
-template <bool kBf16>
-__device__ __forceinline__ float half_of(uint32_t v, int hi) {
-  const unsigned short u = (unsigned short)(hi ? v >> 16 : v & 0xFFFFu);
-  return kBf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-}
-
-// Pair i of a code word minus the zero point, exact in the operand type:
-// magic | q is 128 + q (BF16) or 1024 + q (FP16), and zm holds magic + z twice.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t int4_pair(uint32_t w, int i, uint32_t zm) {
-  uint32_t v;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(kBf16 ? 0x43004300u : 0x64006400u));
-  uint32_t r;
-  if (kBf16) asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zm));
-  else asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zm));
-  return r;
-}
-template <bool kBf16>
-__device__ __forceinline__ uint32_t int4_zero_magic(uint32_t z) {  // z: 0..15
-  return kBf16 ? 0x43004300u | (z * 0x00010001u) : 0x64006400u | (z * 0x00010001u);
-}
-
-// The B fragments' words of one chunk for token g: 8 words (16 elements) in the order the MMAs use them.
-template <W4 kFmt>
-__device__ __forceinline__ void load_x(const uint8_t* row, int chunk, int t, uint32_t (&x)[8]) {
-  const uint8_t* p = row + chunk * 128 + (kFmt == W4::kNvfp4 ? 32 * t : 16 * t);
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint4 b = *reinterpret_cast<const uint4*>(p + (kFmt == W4::kNvfp4 ? 16 : 64));
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
-// acc += the step's 16 x (8 kTiles) products.  xs: shared x rows, chunk0 the step's first chunk in the slab.
-template <W4 kFmt, bool kBf16, int kTiles>
-__device__ __forceinline__ void use_step(const StepRaw<kFmt>& w, const uint8_t* xs, int pitch, int chunk0, int rows,
-                                         bool zeros, int lane, float (&acc)[kTiles][4]) {
-  const int g = lane >> 2, t = lane & 3;
-  float part[kTiles][4];
+    constexpr int G = int4_groups(kFmt);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t x[kTiles][8];
+    for (int g = 0; g < G; ++g) {
+      const float2 sx = *reinterpret_cast<const float2*>(sl + g * gv::kRows);
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      if (8 * n + g < rows) {
-        load_x<kFmt>(xs + (8 * n + g) * pitch, chunk0 + h, t, x[n]);
-      } else {
+      for (int q = 0; q < gv::kRg; ++q) {
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[n][i] = 0u;
-      }
-    }
-    const uint4 c = w.c[h];
-    if (kFmt == W4::kNvfp4) {
-      const uint32_t s2 = e4m3x2_to_f16x2(w.s[h]);
-      const uint32_t slo = dup_lo(s2), shi = dup_hi(s2);
-      uint32_t lo[2][4], hi[2][4];
-      e2m1x8_to_f16x2x4(c.x, lo[0]);
-      e2m1x8_to_f16x2x4(c.y, lo[1]);
-      e2m1x8_to_f16x2x4(c.z, hi[0]);
-      e2m1x8_to_f16x2x4(c.w, hi[1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t A[4] = {hmul2_u32(lo[j >> 1][2 * (j & 1)], slo), hmul2_u32(hi[j >> 1][2 * (j & 1)], shi),
-                               hmul2_u32(lo[j >> 1][2 * (j & 1) + 1], slo), hmul2_u32(hi[j >> 1][2 * (j & 1) + 1], shi)};
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) mma_16816<false>(acc[n], A, x[n][2 * j], x[n][2 * j + 1]);
-      }
-    } else {
-      constexpr int G = StepRaw<kFmt>::kGroups;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int run = 2 * h + hf;           // 32-element run of the step
-        const int grp = run * G / 4;          // its group
-        if (run * G % 4 == 0) {
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
+        for (int run = g * (4 / G); run < (g + 1) * (4 / G); ++run) {  // 32 elements
+          const uint4 c = w.c[q][run >> 1];
+          const uint32_t l = run & 1 ? c.y : c.x, h = run & 1 ? c.w : c.z;
+          const uint32_t* xr = x[run >> 1] + 4 * (run & 1);
+          const uint32_t l8 = l >> 8, h8 = h >> 8;
+          mma_16816(part, l & 0x000F000Fu, h & 0x000F000Fu, l & 0x00F000F0u, h & 0x00F000F0u, xr[0], xr[1]);
+          mma_16816(part, l8 & 0x000F000Fu, h8 & 0x000F000Fu, l8 & 0x00F000F0u, h8 & 0x00F000F0u, xr[2], xr[3]);
         }
-        const uint32_t zz = zeros ? w.z[grp >> 1] >> (16 * (grp & 1)) : 0x0808u;
-        const uint32_t zlo = int4_zero_magic<kBf16>(zz & 0xFFu), zhi = int4_zero_magic<kBf16>((zz >> 8) & 0xFFu);
-        const uint32_t wl = hf ? c.y : c.x, wh = hf ? c.w : c.z;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t A[4] = {int4_pair<kBf16>(wl, 2 * u, zlo), int4_pair<kBf16>(wh, 2 * u, zhi),
-                                 int4_pair<kBf16>(wl, 2 * u + 1, zlo), int4_pair<kBf16>(wh, 2 * u + 1, zhi)};
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n) mma_16816<kBf16>(part[n], A, x[n][4 * hf + 2 * u], x[n][4 * hf + 2 * u + 1]);
+        float z0 = 8.0f, z1 = 8.0f;
+        if (kZeros) {
+          const uint32_t zz = w.z[q][g >> 1] >> (16 * (g & 1));
+          z0 = byte_of(zz, 0), z1 = byte_of(zz, 1);
         }
-        if ((run + 1) * G % 4 == 0) {
-          const float s0 = half_of<kBf16>(w.s[grp], 0), s1 = half_of<kBf16>(w.s[grp], 1);
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n) {
-            acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
-            acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
-            acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
-            acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
-          }
-        }
+        const float s0 = scale_of<kBf16>(w.s[q][g], 0), s1 = scale_of<kBf16>(w.s[q][g], 1);
+        acc[q][0] = fmaf(s0, fmaf(-z0, sx.x, part[0]), acc[q][0]);
+        acc[q][1] = fmaf(s0, fmaf(-z0, sx.y, part[1]), acc[q][1]);
+        acc[q][2] = fmaf(s1, fmaf(-z1, sx.x, part[2]), acc[q][2]);
+        acc[q][3] = fmaf(s1, fmaf(-z1, sx.y, part[3]), acc[q][3]);
       }
     }
   }
 }
 
-// x rows row0 .. row0 + rows - 1, K elements k0 .. k0 + len - 1, into shared memory as they are.
-__device__ __forceinline__ void stage_raw(const void* x, long long ldx, long long row0, int rows, int k0, int len,
-                                          uint8_t* xs, int pitch) {
-  const int per = len / 8;  // 16-byte pieces of a row
-  for (int i = threadIdx.x; i < rows * per; i += gv::kThreads) {
+// 2^e as a product of two floats, for |e| <= 252.
+__device__ __forceinline__ float2 pow2_pair(int e) {
+  const int a = e >> 1, b = e - a;
+  return make_float2(__int_as_float((127 + a) << 23), __int_as_float((127 + b) << 23));
+}
+
+// x rows row0 .. row0 + rows - 1 into shared memory as FP16 times 2^-p per row, xexp[r] = p; INT4: elements 2, 3,
+// 6 and 7 of every 8 times another 2^-4, and 2^-24 times the sums over each group of 128 / G elements into
+// sums[group][8].  down[r] is 2^-p and xexp[r] = p.  amax: one word per row, zero on entry and on exit.  Every
+// thread of the CTA calls it; its last writes are not yet visible to the others.
+template <W4 kFmt, bool kBf16>
+__device__ __forceinline__ void stage_x(const GemvArgs& a, int row0, int rows, uint8_t* xs, float* sums, unsigned* amax,
+                                        int* xexp, float2* down) {
+  constexpr int kLanes = kFmt == W4::kNvfp4 ? 1 : 16 / int4_groups(kFmt);  // threads (of 8 elements) per group
+  const int per = a.K / 8;  // 16-byte pieces of a row
+  const int total = rows * per;
+  const auto piece = [&](int i) {
+    const int r = i / per;
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (long long)(row0 + r) * a.ldx) +
+                 (i - r * per));
+  };
+  const auto value = [](uint32_t w, int hi) {
+    return kBf16 ? __uint_as_float(hi ? w & 0xFFFF0000u : w << 16)
+                 : __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xFFFFu)));
+  };
+  const auto store = [&](int i, bool ok, const uint4& v) {  // whole warps: lanes with nothing to store take part in the sums
     const int r = i / per, p = i - r * per;
-    *reinterpret_cast<uint4*>(xs + r * pitch + p * 16) =
-        __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + (row0 + r) * ldx + k0) + p);
-  }
-}
-
-// The same as FP16 times 2^-p per row, xexp[r] = p.  amax: one word per row, zero on entry and on exit.
-__device__ __forceinline__ void stage_f16(const void* x, long long ldx, long long row0, int rows, int k0, int len,
-                                          uint8_t* xs, int pitch, unsigned* amax, int* xexp) {
-  const int per = len / 8;
-  for (int i0 = 0; i0 < rows * per; i0 += gv::kThreads) {
-    const int i = i0 + (int)threadIdx.x;
-    unsigned m = 0;
-    int r = -1;
-    if (i < rows * per) {
-      r = i / per;
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + (row0 + r) * ldx + k0) +
-                            (i - r * per));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // magnitude bits order like the values; infinities and NaN do not count
-        const unsigned lo = (w[j] & 0x7FFFu) << 16, hi = w[j] & 0x7FFF0000u;
-        if (lo < 0x7F800000u) m = max(m, lo);
-        if (hi < 0x7F800000u) m = max(m, hi);
-      }
-    }
-    // one atomic per warp when its lanes share a row
-    const int r0 = __shfl_sync(0xffffffffu, r, 0);
-    if (__all_sync(0xffffffffu, r == r0)) {
-      m = __reduce_max_sync(0xffffffffu, m);
-      if ((threadIdx.x & 31) == 0 && r >= 0) atomicMax(amax + r, m);
-    } else if (r >= 0) {
-      atomicMax(amax + r, m);
-    }
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < rows) xexp[threadIdx.x] = prescale_exp(__uint_as_float(amax[threadIdx.x]));
-  __syncthreads();
-  if ((int)threadIdx.x < rows) amax[threadIdx.x] = 0u;
-  for (int i = threadIdx.x; i < rows * per; i += gv::kThreads) {
-    const int r = i / per, p = i - r * per;
-    const uint4 v =
-        __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + (row0 + r) * ldx + k0) + p);
+    const float2 f2 = down[r];
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    const int ex = xexp[r];
     uint32_t o[4];
+    float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __half2 h = __floats2half2_rn(ldexpf(__uint_as_float(w[j] << 16), -ex),
-                                          ldexpf(__uint_as_float(w[j] & 0xFFFF0000u), -ex));
+      __half2 h = __floats2half2_rn(value(w[j], 0) * f2.x * f2.y, value(w[j], 1) * f2.x * f2.y);
+      if (kFmt != W4::kNvfp4) {
+        if (j & 1) h = __hmul2(h, __float2half2_rn(0.0625f));  // what the MMA multiplies with q 2^-20
+        const float2 f = __half22float2(h);
+        sum += (j & 1 ? 16.0f : 1.0f) * (f.x + f.y);
+      }
       o[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(xs + r * pitch + p * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (ok) *reinterpret_cast<uint4*>(xs + r * a.pitch + p * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (kFmt != W4::kNvfp4) {  // a group's threads are neighbours (K is a multiple of 128)
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, kLanes);
+      if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = sum * 0x1p-24f;
+    }
+  };
+  // rows in batches whose pieces all threads hold at once (whole rows, so that their maxima are known)
+  const int batch_rows = max(1, gv::kStageBatch * gv::kThreads / per);
+  for (int rb = 0; rb < rows; rb += batch_rows) {
+    const int i0 = rb * per, i1 = min(total, (rb + batch_rows) * per);
+    const bool held = i1 - i0 <= gv::kStageBatch * gv::kThreads;
+    uint4 v[gv::kStageBatch];
+    for (int b0 = i0; b0 < i1; b0 += gv::kStageBatch * gv::kThreads) {
+#pragma unroll
+      for (int b = 0; b < gv::kStageBatch; ++b) {
+        const int i = b0 + b * gv::kThreads + (int)threadIdx.x;
+        v[b] = i < i1 ? piece(i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int b = 0; b < gv::kStageBatch; ++b) {
+        const int i = b0 + b * gv::kThreads + (int)threadIdx.x;
+        if (b0 + b * gv::kThreads >= i1) break;
+        unsigned m = 0;  // largest finite magnitude, as FP32 bits, which order like the values
+        if (i < i1) {
+          const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const unsigned lo = __float_as_uint(fabsf(value(w[j], 0))), hi = __float_as_uint(fabsf(value(w[j], 1)));
+            if (lo < 0x7F800000u) m = max(m, lo);
+            if (hi < 0x7F800000u) m = max(m, hi);
+          }
+        }
+        const int r = i < i1 ? i / per : -1;
+        const int r0 = __shfl_sync(0xffffffffu, r, 0);
+        if (__all_sync(0xffffffffu, r == r0 || r < 0)) {  // one atomic per warp where its lanes share a row
+          m = __reduce_max_sync(0xffffffffu, m);
+          if ((threadIdx.x & 31) == 0 && r >= 0) atomicMax(amax + r, m);
+        } else if (r >= 0) {
+          atomicMax(amax + r, m);
+        }
+      }
+    }
+    __syncthreads();
+    const int r = rb + (int)threadIdx.x;
+    if (r < min(rows, rb + batch_rows)) {
+      xexp[r] = prescale_exp(__uint_as_float(amax[r]));
+      down[r] = pow2_pair(-xexp[r]);
+    }
+    __syncthreads();
+    if (r < min(rows, rb + batch_rows)) amax[r] = 0u;
+    for (int b0 = i0; b0 < i1; b0 += gv::kStageBatch * gv::kThreads) {
+#pragma unroll
+      for (int b = 0; b < gv::kStageBatch; ++b) {
+        const int i = b0 + b * gv::kThreads + (int)threadIdx.x;
+        if (b0 + b * gv::kThreads >= i1) break;
+        const bool ok = i < i1;  // i1 - i0 is a multiple of 16: a group's threads are all in or all out
+        store(ok ? i : i0, ok, held ? v[b] : piece(ok ? i : i0));
+      }
+    }
   }
 }
 
-template <W4 kFmt, bool kBf16, int kTiles>
-__global__ void __launch_bounds__(gv::kThreads, 2) gemv_kernel(GemvArgs a) {
-  extern __shared__ __align__(16) uint8_t xs[];
-  __shared__ unsigned amax[8 * kTiles];
-  __shared__ int xexp[8 * kTiles];
-  __shared__ int unit[3];  // expert, first row, rows
-  __shared__ int wsum[gv::kWarps];
+template <W4 kFmt, bool kBf16, bool kZeros>
+__global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
+  using S = Step<kFmt, kZeros>;
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the group sums
+  __shared__ unsigned amax[gv::kRows];
+  __shared__ int xexp[gv::kRows];
+  __shared__ float2 down[gv::kRows];
+  __shared__ int tile_of[257];  // NVFP4: x tiles before expert e
+  __shared__ int wsum[8];
+  __shared__ float red[2][gv::kWarps][4 * gv::kRg][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kRows = 8 * kTiles;
-  int e = 0, row0 = 0, rows = a.T;
-  if (kFmt == W4::kNvfp4) {
-    // blockIdx.y -> (expert, tile of at most kRows rows); thread i looks at expert i
-    if (threadIdx.x < kRows) amax[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) unit[2] = 0;
+
+  int tiles = a.tiles;
+  if (threadIdx.x < gv::kRows) amax[threadIdx.x] = 0u;
+  if (S::kNv) {  // tiles of at most tile_rows rows of one expert; thread i looks at expert i
     const int i = threadIdx.x;
     const int o0 = i < a.E ? __ldg(a.offsets + i) : 0, o1 = i < a.E ? __ldg(a.offsets + i + 1) : 0;
     const bool bad = o0 < 0 || o1 < o0 || o1 > a.R;
-    const int nt = (o1 - o0 + kRows - 1) / kRows;
+    const int nt = (o1 - o0 + a.tile_rows - 1) / a.tile_rows;
     int before = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, before, o);
       if (lane >= o) before += v;
     }
-    if (lane == 31) wsum[warp] = before;
+    if (lane == 31 && warp < 8) wsum[warp] = before;
     if (__syncthreads_or(bad)) {  // offsets that do not ascend within 0..R: nothing is computed
-      if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) report(a.st, kFlagBounds, 920);
+      if (threadIdx.x == 0 && blockIdx.x == 0) report(a.st, kFlagBounds, 920);
       return;
     }
-    before -= nt;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    const int j = (int)blockIdx.y - before;
-    if (j >= 0 && j < nt) {
-      unit[0] = i;
-      unit[1] = o0 + j * kRows;
-      unit[2] = min(kRows, o1 - o0 - j * kRows);
+    if (i < 256) {
+      for (int w = 0; w < warp; ++w) before += wsum[w];
+      tile_of[i + 1] = before;
     }
+    if (i == 0) tile_of[0] = 0;
     __syncthreads();
-    e = unit[0], row0 = unit[1], rows = unit[2];
-    if (rows == 0) return;
+    tiles = tile_of[256];
   }
-  const int RG = gv::kWarps / a.KS;
-  const int rgroups = a.N / 16;
-  const int ks = warp / RG;
-  const int rg = blockIdx.x * RG + warp % RG;
-  const bool active = rg < rgroups;
-  const int steps = a.K / gv::kStep;
-
-  const uint8_t *codes, *sc, *zr = nullptr;
-  if (kFmt == W4::kNvfp4) {
-    const uint8_t* tile = a.blob + (size_t)e * a.expert_stride + (size_t)(rg >> 3) * (a.K / kChunk) * kTileBytes;
-    codes = tile + (rg & 7) * 512;
-    sc = tile + kTileCodes + (rg & 7) * 64;
-  } else {
-    constexpr int G = StepRaw<kFmt>::kGroups;
-    codes = a.codes + (size_t)rg * steps * 1024;
-    sc = static_cast<const uint8_t*>(a.scales) + (size_t)rg * steps * (32 * G);
-    if (a.zeros) zr = a.zeros + (size_t)rg * steps * (16 * G);
+  const int steps = a.K / gv::kStep, rgroups = a.N / 16;
+  const int granules = (rgroups + gv::kRg - 1) / gv::kRg;  // of a matrix
+  const int RG = gv::kWarps / a.KS;                        // granules at a time
+  const int ks = warp % a.KS, wg = warp / a.KS;
+  // this CTA's run of granules.  NVFP4: tile * granules + granule, over all CTAs.  INT4: CTAs c, c + 1, ..
+  // c + tiles - 1 take the same granules for one tile of x each, so that they share the weights in L2
+  int u0, u1, tile = S::kNv ? -1 : (int)blockIdx.x % tiles;
+  {
+    const int n = S::kNv ? (int)gridDim.x : (int)gridDim.x / tiles;
+    const int c = S::kNv ? (int)blockIdx.x : (int)blockIdx.x / tiles;
+    const long long all = S::kNv ? (long long)tiles * granules : granules;
+    u0 = (int)(all * c / n);
+    u1 = c < n ? (int)(all * (c + 1) / n) : u0;
   }
+  if (u0 >= u1) return;
+  const auto expert_of = [&](int t) {  // the expert with tile_of[e] <= t < tile_of[e + 1]
+    int e = 0, hi = 256;
+    while (hi - e > 1) {
+      const int mid = (e + hi) >> 1;
+      if (tile_of[mid] <= t) e = mid;
+      else hi = mid;
+    }
+    return e;
+  };
 
-  StepRaw<kFmt> buf[gv::kDepth];
-#pragma unroll
-  for (int d = 0; d < gv::kDepth; ++d)
-    if (active && ks + d * a.KS < steps) load_step<kFmt>(a, codes, sc, zr, ks + d * a.KS, lane, buf[d]);
-
-  float acc[kTiles][4], part[kTiles][4];
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = part[n][i] = 0.f;
-
-  for (int s0 = 0; s0 < steps; s0 += a.slab_steps) {
-    const int s1 = min(s0 + a.slab_steps, steps);
-    if (s0) __syncthreads();  // the previous slab has been used
-    if (kFmt == W4::kNvfp4)
-      stage_f16(a.x, a.ldx, row0, rows, s0 * gv::kStep, (s1 - s0) * gv::kStep, xs, a.pitch, amax, xexp);
-    else
-      stage_raw(a.x, a.ldx, 0, rows, s0 * gv::kStep, (s1 - s0) * gv::kStep, xs, a.pitch);
-    __syncthreads();
-    if (active) {
-      for (int s = s0 + ks; s < s1; s += gv::kDepth * a.KS) {
-#pragma unroll
-        for (int d = 0; d < gv::kDepth; ++d) {
-          const int sd = s + d * a.KS;
-          if (sd < s1) {
-            use_step<kFmt, kBf16, kTiles>(buf[d], xs, a.pitch, 2 * (sd - s0), rows, zr != nullptr, lane,
-                                          kFmt == W4::kNvfp4 ? part : acc);
-            const int nx = sd + gv::kDepth * a.KS;
-            if (nx < steps) load_step<kFmt>(a, codes, sc, zr, nx, lane, buf[d]);
-          }
+  // ---- the copy side: the warp's next step to copy is number lk of its my_steps in the granule it is at; lnext is
+  // where the next batch of granules starts, lleft how many granules the tile has from there on ----
+  const int my_steps = (steps - ks + a.KS - 1) / a.KS;
+  uint8_t* ring = smem + warp * (gv::kDepth * S::kBytes);
+  const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
+  int lnext = u0, lk = 0, lslot = 0, lleft = 0;
+  const uint8_t *lbase = nullptr, *pc = nullptr, *ps = nullptr;
+  const int row_block = a.K / kChunk * kTileBytes;
+  const int dstep = a.KS * S::kStride;
+  const auto next_granule = [&] {  // point the copies at the warp's next granule; false: it has no more
+    while (my_steps > 0 && lnext < u1) {
+      if (S::kNv && lleft == 0) {  // a new tile: its expert
+        const int t = lnext / granules;
+        lleft = granules - (lnext - t * granules);
+        lbase = a.blob + (size_t)expert_of(t) * a.expert_stride + (size_t)ks * S::kStride;
+      }
+      const int n = S::kNv ? min(RG, min(lleft, u1 - lnext)) : min(RG, u1 - lnext);
+      const int g = (S::kNv ? granules - lleft : lnext) + wg;
+      const bool mine = wg < n;  // the last batch of a tile or of the run may leave warps idle
+      lnext += n;
+      lleft -= n;
+      if (mine) {
+        if (S::kNv) {
+          const uint8_t* p = lbase + (size_t)(g >> 2) * row_block;
+          pc = p + (g & 3) * 1024 + lane * 16;
+          ps = p + kTileCodes + (g & 3) * 128 + (lane >> 3) * kTileBytes + (lane & 7) * 16;
+        } else {
+          pc = a.packed + ((size_t)g * steps + ks) * S::kStride + lane * 16;
         }
-      }
-      if (kFmt == W4::kNvfp4) {  // undo the slab's row scales
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * n + 2 * (lane & 3) + (i & 1);
-            if (r < rows) acc[n][i] += ldexpf(part[n][i], xexp[r]);
-            part[n][i] = 0.f;
-          }
+        return true;
       }
     }
-  }
+    return false;
+  };
+  bool more = next_granule();
+  const auto copy_next = [&] {  // one group, empty past the end
+    if (more) {
+      S::copy(pc, ps, ring_addr + lslot * S::kBytes, lane);
+      lslot = lslot == gv::kDepth - 1 ? 0 : lslot + 1;
+      pc += dstep;
+      ps += dstep;
+      if (++lk == my_steps) {
+        lk = 0;
+        more = next_granule();
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < gv::kDepth; ++d) copy_next();
 
-  if (a.KS > 1) {  // sum the group's warps in order
+  // ---- the product side ----
+  uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kBytes;
+  float* sums = reinterpret_cast<float*>(xs + (size_t)a.tile_rows * a.pitch);
+  int row0 = 0, rows = 0;
+  float gs = 1.0f;
+  const uint8_t* xl0 = nullptr;
+  // a lane whose token does not exist reads the last one's row: its column of the products is not stored
+  const auto aim_x = [&] {
+    xl0 = xs + min(lane >> 2, rows - 1) * a.pitch + (lane & 3) * (S::kNv ? 32 : 16) + ks * 256;
+  };
+  if (!S::kNv) {
+    row0 = tile * a.tile_rows;
+    rows = min(a.tile_rows, a.T - row0);
+    stage_x<kFmt, kBf16>(a, row0, rows, xs, sums, amax, xexp, down);
     __syncthreads();
-    float* red = reinterpret_cast<float*>(xs);
-    if (ks > 0) {
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[((warp * kTiles + n) * 4 + i) * 32 + lane] = acc[n][i];
-    }
-    __syncthreads();
-    if (ks == 0) {
-      for (int w = warp + RG; w < gv::kWarps; w += RG)
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] += red[((w * kTiles + n) * 4 + i) * 32 + lane];
-    }
+    aim_x();
   }
-  if (ks == 0 && active) {
-    const float gs = kFmt == W4::kNvfp4 ? __ldg(a.gscale + e) : 1.0f;
+  const float* sl0 = sums + ks * (S::kGroups * gv::kRows) + 2 * (lane & 3);
+  int phase = 0, left = 0, slot = 0;
+  for (int u = u0; u < u1;) {
+    if (S::kNv && left == 0) {  // the next tile: its expert, its rows of x
+      if (tile >= 0) __syncthreads();  // every warp is done with the last one's
+      tile = u / granules;
+      left = granules - (u - tile * granules);
+      const int e = expert_of(tile);
+      const int r0 = __ldg(a.offsets + e), r1 = __ldg(a.offsets + e + 1);
+      row0 = r0 + (tile - tile_of[e]) * a.tile_rows;
+      rows = min(a.tile_rows, r1 - row0);
+      gs = __ldg(a.gscale + e);
+      stage_x<kFmt, true>(a, row0, rows, xs, sums, amax, xexp, down);
+      __syncthreads();
+      aim_x();
+    }
+    const int n = S::kNv ? min(RG, min(left, u1 - u)) : min(RG, u1 - u);
+    const int g0 = S::kNv ? granules - left : u;
+    float acc[gv::kRg][4];
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n)
+    for (int q = 0; q < gv::kRg; ++q)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * n + 2 * (lane & 3) + (i & 1);
-        const int f = 16 * rg + (lane >> 2) + 8 * (i >> 1);
-        if (r < rows) {
-          const long long o = (long long)(row0 + r) * a.ldo + f;
-          const float y = kFmt == W4::kNvfp4 ? gs * acc[n][i] : acc[n][i];
-          if (a.out_f32) static_cast<float*>(a.out)[o] = y;
-          else if (kFmt == W4::kNvfp4 || kBf16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
-          else static_cast<__half*>(a.out)[o] = __float2half_rn(y);
-        }
+      for (int i = 0; i < 4; ++i) acc[q][i] = 0.f;
+    if (wg < n) {
+      const uint8_t* xl = xl0;
+      const float* sl = sl0;
+      for (int k = 0; k < my_steps; ++k) {
+        copies_wait();
+        __syncwarp();  // the other lanes' copies (the scales) too
+        S w;
+        w.read(ring + slot * S::kBytes, lane);
+        slot = slot == gv::kDepth - 1 ? 0 : slot + 1;
+        __syncwarp();  // read by all before it is filled again
+        copy_next();
+        use_step<kFmt, kBf16, kZeros>(w, xl, sl, acc);
+        xl += a.KS * 256;
+        sl += a.KS * (S::kGroups * gv::kRows);
       }
+    }
+    // the batch's sums into out: slot s of a lane is row group s / 4, element s % 4 of the accumulator
+    const auto store = [&](int granule, int s, float y) {
+      const int rg = (g0 + granule) * gv::kRg + (s >> 2), r = 2 * (lane & 3) + (s & 1);
+      if (r < rows && rg < rgroups) {
+        const long long o = (long long)(row0 + r) * a.ldo + 16 * rg + (lane >> 2) + 8 * ((s >> 1) & 1);
+        const float2 up = pow2_pair(S::kNv ? xexp[r] : xexp[r] + 24);
+        y = y * up.x * up.y;
+        if (S::kNv) y *= gs;
+        if (a.out_f32) static_cast<float*>(a.out)[o] = y;
+        else if (S::kNv || kBf16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
+        else static_cast<__half*>(a.out)[o] = __float2half_rn(y);
+      }
+    };
+    float(*part)[4 * gv::kRg][32] = red[phase];
+    phase ^= 1;  // the next batch's sums go to the other buffer: one barrier a batch
+#pragma unroll
+    for (int s = 0; s < 4 * gv::kRg; ++s) part[warp][s][lane] = acc[s >> 2][s & 3];
+    __syncthreads();
+    for (int j = warp; j < 4 * gv::kRg * n; j += gv::kWarps) {
+      const int g = j / (4 * gv::kRg), s = j % (4 * gv::kRg);
+      float y = 0.f;
+      for (int w = 0; w < a.KS; ++w) y += part[g * a.KS + w][s][lane];
+      store(g, s, y);
+    }
+    u += n;
+    left -= n;
   }
 }
 
-// Warps along K (KS): as few as give at least two CTAs a multiprocessor -- a
-// wider CTA stages x for more weight rows -- and 8 where the matrix is small.
-static int pick_ks(int row_tiles, int N, int num_sms, int ks_max) {
-  int ks = 1;
-  while (ks < ks_max && (long long)row_tiles * ((N / 16 + gv::kWarps / ks - 1) / (gv::kWarps / ks)) < 2 * num_sms) ks *= 2;
-  return ks;
-}
-
-// x's shared-memory layout for up to max_rows rows: at most 64 KB, three CTAs' worth a multiprocessor.
-static size_t set_slab(GemvArgs& a, int max_rows, int pad) {
+// Warps along K: few, for few barriers, but as many as keep every warp busy with the CTA's share of granules.
+static void set_steps(GemvArgs& a, long long granules_per_cta) {
   const int steps = a.K / gv::kStep;
-  const int most = max_rows <= 8 ? 32 : 16;  // 128-element steps: a multiple of kDepth * KS (KS <= 8, or 4 above 8 rows)
-  a.slab_steps = most;
-  a.pitch = (steps < most ? steps : most) * gv::kStep * 2 + pad;
-  const size_t red = (size_t)gv::kWarps * 32 * 4 * 4 * (max_rows <= 8 ? 1 : 2);  // the K sum reuses it
-  const size_t x = (size_t)max_rows * a.pitch;
-  return x > red ? x : red;
+  if (granules_per_cta < 1) granules_per_cta = 1;
+  float best = 0.f;
+  for (int ks = gv::kWarps; ks >= 1; ks /= 2) {
+    const int spw = (steps + ks - 1) / ks;
+    float used = (float)steps / (float)(ks * spw);  // of the warps' steps
+    const int rg = gv::kWarps / ks;
+    if (granules_per_cta < rg) used *= (float)granules_per_cta / (float)rg;
+    if (ks < 4) used *= 0.5f;
+    if (used >= best - 0.01f) {
+      best = used > best ? used : best;
+      a.KS = ks;
+    }
+  }
 }
 
-template <W4 kFmt, bool kBf16, int kTiles>
-static cudaError_t launch_gemv(const GemvArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
-  constexpr int kMaxSmem = 8 * kTiles * ((kTiles == 1 ? 32 : 16) * gv::kStep * 2 + 64);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(gemv_kernel<kFmt, kBf16, kTiles>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e != cudaSuccess) return e;
+// Rows of x per tile, as many as fit beside the rings.  row_bytes: shared memory of one row of x; fixed: of the
+// sums; slot_bytes: of a ring's slot.  Returns the dynamic shared memory.
+static size_t set_smem(GemvArgs& a, int rows, size_t row_bytes, size_t fixed, int slot_bytes) {
+  fixed += (size_t)gv::kWarps * gv::kDepth * slot_bytes;
+  const int fit = (int)((gv::kSmem - fixed) / row_bytes);  // at least 1 at K = 16384
+  a.tile_rows = fit < gv::kRows ? fit : gv::kRows;
+  if (rows < a.tile_rows) a.tile_rows = rows;
+  return fixed + a.tile_rows * row_bytes;
+}
+
+template <W4 kFmt, bool kBf16, bool kZeros>
+static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, int num_sms, cudaStream_t st) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {  // the opt-in shared-memory size, once per device
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(gemv_kernel<kFmt, kBf16, kZeros>, cudaFuncAttributeMaxDynamicSharedMemorySize, gv::kSmem);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) done[dev] = true;
+    }
   }
-  gemv_kernel<kFmt, kBf16, kTiles><<<grid, gv::kThreads, smem, st>>>(a);
+  const unsigned grid = (unsigned)(ctas < num_sms ? ctas : num_sms);
+  gemv_kernel<kFmt, kBf16, kZeros><<<grid, gv::kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -485,32 +599,34 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
   a.st = p.status;
-  const int touched = p.R < p.E ? p.R : p.E;  // at most
-  const bool wide = p.R > 8 * p.E;            // some expert has more than 8 rows: tiles of 16
-  const int rows = wide ? 16 : 8;
-  a.KS = pick_ks(touched, p.N, p.num_sms, wide ? 4 : 8);
-  const int RG = gv::kWarps / a.KS;
-  const dim3 grid((p.N / 16 + RG - 1) / RG, touched + p.R / rows);
-  const size_t smem = set_slab(a, rows, 16);
-  return wide ? launch_gemv<W4::kNvfp4, false, 2>(a, grid, smem, st)
-              : launch_gemv<W4::kNvfp4, false, 1>(a, grid, smem, st);
+  const int granules = (p.N / 16 + gv::kRg - 1) / gv::kRg;
+  const int touched = p.R < p.E ? p.R : p.E;
+  set_steps(a, (long long)touched * granules / p.num_sms);
+  a.pitch = p.K * 2 + 16;  // rows 16 bytes apart in the banks: the lanes' 32-byte pieces of two rows never collide
+  const size_t smem = set_smem(a, p.R, a.pitch, 0, Step<W4::kNvfp4, false>::kBytes);
+  return launch_gemv<W4::kNvfp4, true, false>(a, (long long)(touched + p.R / a.tile_rows) * granules, smem, p.num_sms, st);
 }
 
-template <W4 kFmt, bool kBf16>
+template <W4 kFmt, bool kBf16, bool kZeros>
 static cudaError_t launch_int4(GemvArgs& a, int num_sms, cudaStream_t st) {
-  const bool wide = a.T > 8;
-  a.KS = pick_ks(1, a.N, num_sms, wide ? 4 : 8);
-  const int RG = gv::kWarps / a.KS;
-  const dim3 grid((a.N / 16 + RG - 1) / RG);
-  const size_t smem = set_slab(a, a.T, 64);
-  return wide ? launch_gemv<kFmt, kBf16, 2>(a, grid, smem, st) : launch_gemv<kFmt, kBf16, 1>(a, grid, smem, st);
+  const int granules = (a.N / 16 + gv::kRg - 1) / gv::kRg;
+  a.pitch = a.K * 2 + 64;  // the lanes' 16-byte pieces of two rows never collide
+  const size_t sums = (size_t)a.K / 128 * int4_groups(kFmt) * gv::kRows * 4;
+  const size_t smem = set_smem(a, a.T, a.pitch, sums, Step<kFmt, kZeros>::kBytes);
+  a.tiles = (a.T + a.tile_rows - 1) / a.tile_rows;
+  a.tile_rows = (a.T + a.tiles - 1) / a.tiles;
+  set_steps(a, (long long)granules * a.tiles / num_sms);
+  return launch_gemv<kFmt, kBf16, kZeros>(a, (long long)granules * a.tiles, smem, num_sms, st);
+}
+template <W4 kFmt>
+static cudaError_t launch_int4(GemvArgs& a, const Int4Product& p, cudaStream_t st) {
+  if (p.act_f16) return p.zeros ? launch_int4<kFmt, false, true>(a, p.num_sms, st) : launch_int4<kFmt, false, false>(a, p.num_sms, st);
+  return p.zeros ? launch_int4<kFmt, true, true>(a, p.num_sms, st) : launch_int4<kFmt, true, false>(a, p.num_sms, st);
 }
 
 cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st) {
   GemvArgs a{};
-  a.codes = p.codes;
-  a.scales = p.scales;
-  a.zeros = p.zeros;
+  a.packed = p.packed;
   a.T = p.T;
   a.N = p.N;
   a.K = p.K;
@@ -519,18 +635,19 @@ cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st) {
   a.out = p.out;
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
-  if (p.act_f16)
-    return p.group == 32   ? launch_int4<W4::kInt4G32, false>(a, p.num_sms, st)
-           : p.group == 64 ? launch_int4<W4::kInt4G64, false>(a, p.num_sms, st)
-                           : launch_int4<W4::kInt4G128, false>(a, p.num_sms, st);
-  return p.group == 32   ? launch_int4<W4::kInt4G32, true>(a, p.num_sms, st)
-         : p.group == 64 ? launch_int4<W4::kInt4G64, true>(a, p.num_sms, st)
-                         : launch_int4<W4::kInt4G128, true>(a, p.num_sms, st);
+  return p.group == 32   ? launch_int4<W4::kInt4G32>(a, p, st)
+         : p.group == 64 ? launch_int4<W4::kInt4G64>(a, p, st)
+                         : launch_int4<W4::kInt4G128>(a, p, st);
 }
 
 // ---------------------------------------------------------------------------
-// INT4 packer: one thread per 16-byte code segment.
+// INT4 packer (the layout is described at Step).
 // ---------------------------------------------------------------------------
+size_t int4_packed_bytes(int N, int K, int group, bool zeros) {
+  const size_t blocks = (size_t)((N + 31) / 32) * (K / 128);
+  return blocks * (2048 + (128 / group) * (zeros ? 96 : 64));
+}
+
 __device__ __forceinline__ uint32_t int4_word(uint32_t w) {  // canonical nibble m = element m
   uint32_t o = 0;
 #pragma unroll
@@ -538,56 +655,48 @@ __device__ __forceinline__ uint32_t int4_word(uint32_t w) {  // canonical nibble
   return o;
 }
 
-__global__ void pack_int4_codes_kernel(const uint8_t* __restrict__ w_q, uint8_t* __restrict__ codes, int N, int K) {
-  const size_t s = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int nch = K / kChunk;
-  if (s >= (size_t)N / 16 * nch * 32) return;
-  const int lane = (int)(s & 31);
-  const size_t rc = s >> 5;
-  const int c = (int)(rc % nch);
-  const size_t rg = rc / nch;
-  const int t = lane & 3;
-  uint32_t o[4];
+// One CTA a block of 32 rows x 128 elements; rows past the matrix hold zeros.
+__global__ void pack_int4_kernel(const uint8_t* __restrict__ w_q, const uint16_t* __restrict__ scale,
+                                 const uint8_t* __restrict__ zero, int f16, int N, int K, int group,
+                                 uint8_t* __restrict__ packed, int* __restrict__ bad) {
+  const int G = 128 / group, steps = K / 128;
+  const int step = blockIdx.x % steps, granule = blockIdx.x / steps;
+  uint8_t* dst = packed + (size_t)blockIdx.x * (2048 + G * (zero ? 96 : 64));
+  const int tid = threadIdx.x;  // 128 threads: segment [group q][chunk h][lane]
+  {
+    const int q = tid >> 6, h = (tid >> 5) & 1, lane = tid & 31;
+    uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const size_t n = 16 * rg + (lane >> 2) + 8 * (i >> 1);
-    const int k = 64 * c + 32 * (i & 1) + 8 * t;
-    o[i] = int4_word(*reinterpret_cast<const uint32_t*>(w_q + n * (size_t)(K / 2) + k / 2));
+    for (int i = 0; i < 4; ++i) {
+      const int n = 32 * granule + 16 * q + (lane >> 2) + 8 * (i >> 1);
+      const int k = 128 * step + 64 * h + 32 * (i & 1) + 8 * (lane & 3);
+      o[i] = n < N ? int4_word(*reinterpret_cast<const uint32_t*>(w_q + (size_t)n * (K / 2) + k / 2)) : 0u;
+    }
+    *reinterpret_cast<uint4*>(dst + tid * 16) = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  *reinterpret_cast<uint4*>(codes + s * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-__global__ void pack_int4_scales_kernel(const uint16_t* __restrict__ scale, const uint8_t* __restrict__ zero, int f16,
-                                        int N, int K, int group, uint16_t* __restrict__ scales,
-                                        uint8_t* __restrict__ zeros, int* __restrict__ bad) {
-  const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;  // canonical [N][K/group]
-  const int ng = K / group;
-  if (i >= (size_t)N * ng) return;
-  const size_t n = i / ng;
-  const int grp = (int)(i - n * ng);
-  const int G = 128 / group, step = grp / G, gi = grp - step * G;
-  const size_t o = ((((n >> 4) * (K / 128) + step) * 8 + (n & 7)) * G + gi) * 2 + ((n >> 3) & 1);
-  const uint16_t s = scale[i];
   const uint16_t inf = f16 ? 0x7C00u : 0x7F80u;
-  bool b = (s & inf) == inf;
-  scales[o] = s;
-  if (zero) {
-    const uint8_t z = zero[i];
-    b |= z > 15;
-    zeros[o] = z;
+  for (int i = tid; i < 32 * G; i += 128) {  // [q][r][group][half]
+    const int hf = i & 1, gi = (i >> 1) % G, r = (i >> 1) / G % 8, q = i / (16 * G);
+    const int n = 32 * granule + 16 * q + 8 * hf + r;
+    const size_t src = (size_t)n * (K / group) + step * G + gi;
+    const uint16_t s = n < N ? scale[src] : 0;
+    reinterpret_cast<uint16_t*>(dst + 2048)[i] = s;
+    bool b = (s & inf) == inf;
+    if (zero) {
+      const uint8_t z = n < N ? zero[src] : 0;
+      dst[2048 + 64 * G + i] = z;
+      b |= z > 15;
+    }
+    if (b) atomicAdd(bad, 1);
   }
-  if (b) atomicAdd(bad, 1);
 }
 
 cudaError_t launch_pack_int4(const uint8_t* w_q, const void* scale, const uint8_t* zero, int act_f16, int N, int K,
-                             int group, uint8_t* codes, void* scales, uint8_t* zeros, int* bad, cudaStream_t st) {
+                             int group, uint8_t* packed, int* bad, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(bad, 0, sizeof(int), st);
   if (e != cudaSuccess) return e;
-  const int thr = 256;
-  const size_t nseg = (size_t)N * K / 32, ns = (size_t)N * (K / group);
-  pack_int4_codes_kernel<<<(unsigned)((nseg + thr - 1) / thr), thr, 0, st>>>(w_q, codes, N, K);
-  pack_int4_scales_kernel<<<(unsigned)((ns + thr - 1) / thr), thr, 0, st>>>(
-      static_cast<const uint16_t*>(scale), zero, act_f16, N, K, group, static_cast<uint16_t*>(scales), zeros, bad);
+  pack_int4_kernel<<<(unsigned)((N + 31) / 32 * (K / 128)), 128, 0, st>>>(w_q, static_cast<const uint16_t*>(scale), zero,
+                                                                          act_f16, N, K, group, packed, bad);
   return cudaGetLastError();
 }
 

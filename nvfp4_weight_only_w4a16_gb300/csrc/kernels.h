@@ -194,9 +194,8 @@ constexpr int kGemvMaxRows = 4096;  // grid limit of launch_grouped_gemv
 
 // y [T][N] = x [T][K] times an INT4 matrix with group scales and zero points.
 struct Int4Product {
-  const uint8_t* codes;    // packed, see gemv.cu
-  const void* scales;
-  const uint8_t* zeros;    // NULL: every zero point is 8
+  const uint8_t* packed;   // see gemv.cu
+  bool zeros;              // the matrix has zero points; else each is 8
   int N, K, group;
   int T;                   // 1..16
   int act_f16;             // x and the scales are FP16, else BF16
@@ -208,10 +207,11 @@ struct Int4Product {
   int num_sms;
 };
 cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st);
-// Canonical INT4 (w_q [N][K/2], scale [N][K/group] 16-bit, zero [N][K/group] or NULL) into the layout of
-// gemv.cu; bad [1] receives the number of scales that are not finite and zero points above 15.
+size_t int4_packed_bytes(int N, int K, int group, bool zeros);
+// Canonical INT4 (w_q [N][K/2], scale [N][K/group] 16-bit, zero [N][K/group] or NULL) into that layout; bad [1]
+// receives the number of scales that are not finite and zero points above 15.
 cudaError_t launch_pack_int4(const uint8_t* w_q, const void* scale, const uint8_t* zero, int act_f16, int N, int K,
-                             int group, uint8_t* codes, void* scales, uint8_t* zeros, int* bad, cudaStream_t st);
+                             int group, uint8_t* packed, int* bad, cudaStream_t st);
 // E matrices [N][K] into E linear_layout(Np, K) blobs one after another.
 cudaError_t launch_pack_grouped(const uint8_t* w_q, const uint8_t* w_s, uint8_t* blob, int E, int N, int Np, int K,
                                 cudaStream_t st);

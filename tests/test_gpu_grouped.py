@@ -15,6 +15,7 @@ from tests.products import DEV, bound, check, f64, nvfp4, nvfp4_values
 
 pytestmark = pytest.mark.gpu
 FORWARD = [P.PATH_DECODE, P.PATH_PREFILL]
+FP16_ROWS = {P.PATH_DECODE: 2.0 ** -38, P.PATH_PREFILL: 0.0}   # the streaming kernel multiplies FP16 rows
 CODE = P.STATUS_CODE
 
 
@@ -53,7 +54,7 @@ def status_ok(h):
     assert st == 0, (P.STATUS[st], h.lib.nvfp4_moe_last_error(h.h).decode())
 
 
-def verify(ex, counts, got, x, backward, first=0, fp16_rows=False):
+def verify(ex, counts, got, x, backward, first=0, fp16_rows=0.0):
     got, x = f64(got), f64(x)
     r = first
     for e, m in enumerate(counts):
@@ -89,7 +90,7 @@ def test_forward(E, N, K, counts, path, out_f32):
     x, out = rows_of(R, K), blank(R, N, ex.dtype)
     ex.h.nvfp4_grouped_forward(x, offsets_of(counts), out)
     status_ok(ex.h)
-    verify(ex, counts, out, x, False, fp16_rows=path == P.PATH_DECODE)
+    verify(ex, counts, out, x, False, fp16_rows=FP16_ROWS[path])
 
 
 @pytest.mark.parametrize("out_f32", [False, True])
@@ -115,7 +116,7 @@ def test_rows_apart_and_a_first_offset(path):
     dy, dx = rows_of(R, 144, pad=8), blank(R, 256, ex.dtype, pad=64)
     ex.h.nvfp4_grouped_backward(dy, off, dx)
     status_ok(ex.h)
-    verify(ex, counts, out, x, False, first, fp16_rows=path == P.PATH_DECODE)
+    verify(ex, counts, out, x, False, first, fp16_rows=FP16_ROWS[path])
     verify(ex, counts, dx, dy, True, first)
     for t, n in ((out, 144), (dx, 256)):   # the gaps between rows are not written
         whole = torch.as_strided(t, (R, t.stride(0) - n), (t.stride(0), 1), n)[:-1]
@@ -206,7 +207,7 @@ def test_captured_and_replayed_with_other_rows_and_offsets(path):
         dx.fill_(float("nan"))
         graph.replay()
         torch.cuda.synchronize()
-        verify(ex, counts, out, x, False, fp16_rows=path == P.PATH_DECODE)
+        verify(ex, counts, out, x, False, fp16_rows=FP16_ROWS[path])
         verify(ex, counts, dx, x, True)
     status_ok(ex.h)
 
@@ -225,7 +226,7 @@ def test_two_streams_share_a_handle():
     torch.cuda.synchronize()
     status_ok(ex.h)
     for path, counts, x, off, out, stream in jobs:
-        verify(ex, counts, out, x, False, fp16_rows=path == P.PATH_DECODE)
+        verify(ex, counts, out, x, False, fp16_rows=FP16_ROWS[path])
 
 
 def test_output_offsets_beyond_32_bits():

@@ -24,10 +24,16 @@ class Matrix:
         q = torch.from_numpy(rng.integers(0, 256, (N, K // 2), dtype=np.uint8)).to(DEV)
         scale = torch.from_numpy(rng.uniform(-0.1, 0.1, (N, K // group))).to(DEV).to(t)
         zero = torch.from_numpy(rng.integers(0, 16, (N, K // group), dtype=np.uint8)).to(DEV) if zeros else None
-        self.w = int4_values(q.cpu().numpy(), f64(scale), None if zero is None else zero.cpu().numpy(), group)
+        self.set_values(q, scale, zero, group)
         self.h = P.Int4Linear(N, K, group, max_tokens=max_tokens, act_f16=f16, out_f32=out_f32)
         self.h.nvfp4_int4_pack(q, scale, zero)
         self.N, self.K, self.act, self.dtype = N, K, t, torch.float32 if out_f32 else t
+
+
+    def set_values(self, q, scale, zero, group):
+        q, scale, zero = q.cpu().numpy(), f64(scale), None if zero is None else zero.cpu().numpy()
+        self.w = int4_values(q, scale, zero, group)
+        self.terms = int4_values(q, scale, zero, group, sign=1.0)
 
 
 def rows_of(m, T, seed=1, pad=0):
@@ -47,7 +53,7 @@ def run(m, x, pad=0, stream=None):
 
 def verify(m, x, got):
     y = f64(x) @ m.w.T
-    check(f64(got), y, bound(y, f64(x), m.w, m.dtype))
+    check(f64(got), y, bound(y, f64(x), m.w, m.dtype, fp16_rows=2.0 ** -34, terms=m.terms, rounds=2))
 
 
 @pytest.mark.parametrize("f16", [False, True])
@@ -128,7 +134,7 @@ def test_packing_again_replaces_the_zero_points():
     q = torch.from_numpy(rng.integers(0, 256, (32, 128), dtype=np.uint8)).to(DEV)
     scale = torch.from_numpy(rng.uniform(0.01, 0.1, (32, 4))).to(DEV).to(torch.bfloat16)
     m.h.nvfp4_int4_pack(q, scale)
-    m.w = int4_values(q.cpu().numpy(), f64(scale), None, 64)
+    m.set_values(q, scale, None, 64)
     x = rows_of(m, 3)
     verify(m, x, run(m, x))
 

@@ -41,7 +41,7 @@ def test_grouped_create_rejects_bad_shapes(lib, kw):
 
 @pytest.mark.parametrize("kw", [
     dict(out_features=0), dict(out_features=40), dict(out_features=(1 << 20) + 16), dict(in_features=64),
-    dict(in_features=200), dict(in_features=65664), dict(group_size=16), dict(group_size=48), dict(group_size=256),
+    dict(in_features=200), dict(in_features=16512), dict(group_size=16), dict(group_size=48), dict(group_size=256),
     dict(max_tokens=0), dict(max_tokens=17),
 ])
 def test_int4_create_rejects_bad_shapes(lib, kw):
