@@ -500,7 +500,7 @@ nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uin
  * Products are exact in FP32 and accumulated in FP32; one rounding to BF16 at
  * the end.  The forward takes the streaming kernel for few rows (by default up
  * to 4 per expert on average, nvfp4_moe_set_path forces either; the streaming
- * kernel takes at most 4096 rows), the tcgen05 GEMM above; the backward always
+ * kernel takes at most 2048 rows), the tcgen05 GEMM above; the backward always
  * the GEMM. */
 nvfp4_moe_status nvfp4_grouped_forward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* x, int64_t ldx,
                                        void* out, int64_t ldo, cudaStream_t stream);

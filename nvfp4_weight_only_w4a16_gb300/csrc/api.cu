@@ -972,7 +972,7 @@ nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t*
   if (ldi < wi || ldo < wo || ldi % 8 || ldo % 8 || ldi > (1 << 24) || ldo > (1 << 24))
     return bad(NVFP4_MOE_ERR_INVALID_ARG, "a row stride is below the row length, above 2^24 or no multiple of 8");
   if (!backward && h->path == NVFP4_MOE_PATH_DECODE && R > kGemvMaxRows)
-    return bad(NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "the decode path takes at most 4096 rows");
+    return bad(NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "the decode path takes at most 2048 rows");
   const bool stream = !backward && (h->path == NVFP4_MOE_PATH_DECODE ||
                                     (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= 4 * E));
   DeviceGuard g(h->cfg.device);

@@ -36,8 +36,8 @@ constexpr int kStep = 128;
 constexpr int kRg = 2;            // 16-row groups a warp multiplies with the same x: two chains of MMAs
 constexpr int kRows = 8;          // rows of x at a time: the MMA's N
 constexpr int kDepth = 3;         // steps in flight per warp, kRg KB of codes each
-constexpr int kSmem = 190 * 1024; // of rings and x
-constexpr int kStageBatch = 8;    // 16-byte pieces of x a thread holds while its row's maximum is found
+constexpr int kMaxTiles = 256 + kGemvMaxRows / 2;  // NVFP4: of a call; all but an expert's last have 2 rows or more
+constexpr int smem_for(bool nvfp4) { return (nvfp4 ? 180 : 190) * 1024; }  // of rings and x; the rest is static
 }  // namespace gv
 
 enum class W4 { kNvfp4, kInt4G32, kInt4G64, kInt4G128 };
@@ -236,119 +236,105 @@ __device__ __forceinline__ float2 pow2_pair(int e) {
   const int a = e >> 1, b = e - a;
   return make_float2(__int_as_float((127 + a) << 23), __int_as_float((127 + b) << 23));
 }
+// p such that a row whose largest finite magnitude has these FP32 bits lies below 2^14 times 2^p
+// (in [2^13, 2^14) unless it is below FP32's normal range).
+__device__ __forceinline__ int row_exponent(unsigned bits) { return bits ? (int)(bits >> 23) - 140 : 0; }
 
-// x rows row0 .. row0 + rows - 1 into shared memory as FP16 times 2^-p per row, xexp[r] = p; INT4: elements 2, 3,
-// 6 and 7 of every 8 times another 2^-4, and 2^-24 times the sums over each group of 128 / G elements into
-// sums[group][8].  down[r] is 2^-p and xexp[r] = p.  amax: one word per row, zero on entry and on exit.  Every
-// thread of the CTA calls it; its last writes are not yet visible to the others.
+// x rows into shared memory as FP16 times 2^-p per row; INT4: elements 2, 3, 6 and 7 of every 8 times another
+// 2^-4, and 2^-24 times the sums over each group of the matrix into sums[group][8].  In two parts: start() copies the
+// rows as they are, finish() -- once the copies have landed -- finds each row's p and converts in place.  A thread
+// handles the same 16-byte pieces throughout, so nothing but the maxima passes between threads.  (Small loops on
+// purpose: a call's first use of its code comes from memory, and this runs before any product.)
 template <W4 kFmt, bool kBf16>
-__device__ __forceinline__ void stage_x(const GemvArgs& a, int row0, int rows, uint8_t* xs, float* sums, unsigned* amax,
-                                        int* xexp, float2* down) {
-  constexpr int kLanes = kFmt == W4::kNvfp4 ? 1 : 16 / int4_groups(kFmt);  // threads (of 8 elements) per group
-  const int per = a.K / 8;  // 16-byte pieces of a row
-  const int total = rows * per;
-  const auto piece = [&](int i) {
-    const int r = i / per;
-    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (long long)(row0 + r) * a.ldx) +
-                 (i - r * per));
-  };
-  const auto value = [](uint32_t w, int hi) {
+struct Stage {
+  uint8_t* xs;
+  int pitch, per, rows;  // 16-byte pieces of a row
+  int r0, p0, dr, dp;    // the thread's first piece, and the step from one to the next
+  __device__ __forceinline__ Stage(const GemvArgs& a, uint8_t* x) : xs(x), pitch(a.pitch), per(a.K / 8), rows(0) {
+    r0 = (int)threadIdx.x / per, p0 = (int)threadIdx.x - r0 * per;
+    dr = gv::kThreads / per, dp = gv::kThreads - dr * per;
+  }
+  __device__ __forceinline__ void next(int& r, int& p) const {
+    r += dr, p += dp;
+    if (p >= per) p -= per, ++r;
+  }
+  __device__ __forceinline__ void start(const GemvArgs& a, int row0, int n) {
+    rows = n;
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(xs);
+    int r = r0, p = p0;
+#pragma unroll 1
+    for (; r < rows; next(r, p))
+      copy16(d + r * pitch + p * 16, static_cast<const uint8_t*>(a.x) + ((long long)(row0 + r) * a.ldx + 8 * p) * 2);
+  }
+  static __device__ __forceinline__ float value(uint32_t w, int hi) {
     return kBf16 ? __uint_as_float(hi ? w & 0xFFFF0000u : w << 16)
                  : __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xFFFFu)));
-  };
-  const auto store = [&](int i, bool ok, const uint4& v) {  // whole warps: lanes with nothing to store take part in the sums
-    const int r = i / per, p = i - r * per;
-    const float2 f2 = down[r];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-    float sum = 0.f;
+  }
+  // amax: the rows' largest finite magnitudes, zero on entry.  The barrier after the writes is the caller's.
+  __device__ __forceinline__ void finish(float* sums, unsigned* amax) {
+    const int lane = threadIdx.x & 31;
+    int r = r0, p = p0;
+#pragma unroll 1
+    for (int i = threadIdx.x & ~31; i < rows * per; i += gv::kThreads, next(r, p)) {  // whole warps
+      unsigned m = 0;  // FP32 bits order like the magnitudes
+      if (r < rows) {
+        const uint4 v = *reinterpret_cast<const uint4*>(xs + r * pitch + p * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      __half2 h = __floats2half2_rn(value(w[j], 0) * f2.x * f2.y, value(w[j], 1) * f2.x * f2.y);
-      if (kFmt != W4::kNvfp4) {
-        if (j & 1) h = __hmul2(h, __float2half2_rn(0.0625f));  // what the MMA multiplies with q 2^-20
-        const float2 f = __half22float2(h);
-        sum += (j & 1 ? 16.0f : 1.0f) * (f.x + f.y);
-      }
-      o[j] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    if (ok) *reinterpret_cast<uint4*>(xs + r * a.pitch + p * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-    if (kFmt != W4::kNvfp4) {  // a group's threads are neighbours (K is a multiple of 128)
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, kLanes);
-      if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = sum * 0x1p-24f;
-    }
-  };
-  // rows in batches whose pieces all threads hold at once (whole rows, so that their maxima are known)
-  const int batch_rows = max(1, gv::kStageBatch * gv::kThreads / per);
-  for (int rb = 0; rb < rows; rb += batch_rows) {
-    const int i0 = rb * per, i1 = min(total, (rb + batch_rows) * per);
-    const bool held = i1 - i0 <= gv::kStageBatch * gv::kThreads;
-    uint4 v[gv::kStageBatch];
-    for (int b0 = i0; b0 < i1; b0 += gv::kStageBatch * gv::kThreads) {
-#pragma unroll
-      for (int b = 0; b < gv::kStageBatch; ++b) {
-        const int i = b0 + b * gv::kThreads + (int)threadIdx.x;
-        v[b] = i < i1 ? piece(i) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int b = 0; b < gv::kStageBatch; ++b) {
-        const int i = b0 + b * gv::kThreads + (int)threadIdx.x;
-        if (b0 + b * gv::kThreads >= i1) break;
-        unsigned m = 0;  // largest finite magnitude, as FP32 bits, which order like the values
-        if (i < i1) {
-          const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const unsigned lo = __float_as_uint(fabsf(value(w[j], 0))), hi = __float_as_uint(fabsf(value(w[j], 1)));
-            if (lo < 0x7F800000u) m = max(m, lo);
-            if (hi < 0x7F800000u) m = max(m, hi);
-          }
-        }
-        const int r = i < i1 ? i / per : -1;
-        const int r0 = __shfl_sync(0xffffffffu, r, 0);
-        if (__all_sync(0xffffffffu, r == r0 || r < 0)) {  // one atomic per warp where its lanes share a row
-          m = __reduce_max_sync(0xffffffffu, m);
-          if ((threadIdx.x & 31) == 0 && r >= 0) atomicMax(amax + r, m);
-        } else if (r >= 0) {
-          atomicMax(amax + r, m);
+        for (int j = 0; j < 8; ++j) {
+          const unsigned b = __float_as_uint(fabsf(value(w[j >> 1], j & 1)));
+          if (b < 0x7F800000u) m = max(m, b);
         }
       }
-    }
-    __syncthreads();
-    const int r = rb + (int)threadIdx.x;
-    if (r < min(rows, rb + batch_rows)) {
-      xexp[r] = prescale_exp(__uint_as_float(amax[r]));
-      down[r] = pow2_pair(-xexp[r]);
-    }
-    __syncthreads();
-    if (r < min(rows, rb + batch_rows)) amax[r] = 0u;
-    for (int b0 = i0; b0 < i1; b0 += gv::kStageBatch * gv::kThreads) {
+      // rows are multiples of 16 pieces: half a warp is always in one row
 #pragma unroll
-      for (int b = 0; b < gv::kStageBatch; ++b) {
-        const int i = b0 + b * gv::kThreads + (int)threadIdx.x;
-        if (b0 + b * gv::kThreads >= i1) break;
-        const bool ok = i < i1;  // i1 - i0 is a multiple of 16: a group's threads are all in or all out
-        store(ok ? i : i0, ok, held ? v[b] : piece(ok ? i : i0));
+      for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if ((lane & 15) == 0 && r < rows) atomicMax(amax + r, m);
+    }
+    __syncthreads();
+    constexpr int kLanes = kFmt == W4::kNvfp4 ? 1 : 16 / int4_groups(kFmt);  // threads per group
+    r = r0, p = p0;
+#pragma unroll 1
+    for (int i = threadIdx.x & ~31; i < rows * per; i += gv::kThreads, next(r, p)) {
+      const bool ok = r < rows;
+      uint4* at = reinterpret_cast<uint4*>(xs + (ok ? r : 0) * pitch + p * 16);
+      const uint4 v = *at;
+      const float2 f2 = pow2_pair(-row_exponent(amax[ok ? r : 0]));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[4];
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __half2 h = __floats2half2_rn(value(w[j], 0) * f2.x * f2.y, value(w[j], 1) * f2.x * f2.y);
+        if (kFmt != W4::kNvfp4) {
+          if (j & 1) h = __hmul2(h, __float2half2_rn(0.0625f));  // what the MMA multiplies with q 2^-20
+          const float2 f = __half22float2(h);
+          sum += (j & 1 ? 16.0f : 1.0f) * (f.x + f.y);
+        }
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if (ok) *at = make_uint4(o[0], o[1], o[2], o[3]);
+      if (kFmt != W4::kNvfp4) {  // a group's pieces belong to neighbouring lanes
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = sum * 0x1p-24f;
       }
     }
   }
-}
+};
 
 template <W4 kFmt, bool kBf16, bool kZeros>
 __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   using S = Step<kFmt, kZeros>;
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the group sums
-  __shared__ unsigned amax[gv::kRows];
-  __shared__ int xexp[gv::kRows];
-  __shared__ float2 down[gv::kRows];
-  __shared__ int tile_of[257];  // NVFP4: x tiles before expert e
-  __shared__ int wsum[8];
+  __shared__ unsigned amax[2][gv::kRows];                  // of this tile and, zero, of the next
+  __shared__ short tile_expert[gv::kMaxTiles];             // NVFP4
+  __shared__ int tile_row0[gv::kMaxTiles], wsum[8];
   __shared__ float red[2][gv::kWarps][4 * gv::kRg][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int tiles = a.tiles;
-  if (threadIdx.x < gv::kRows) amax[threadIdx.x] = 0u;
+  if (threadIdx.x < 2 * gv::kRows) amax[0][threadIdx.x] = 0u;
   if (S::kNv) {  // tiles of at most tile_rows rows of one expert; thread i looks at expert i
     const int i = threadIdx.x;
     const int o0 = i < a.E ? __ldg(a.offsets + i) : 0, o1 = i < a.E ? __ldg(a.offsets + i + 1) : 0;
@@ -365,13 +351,17 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       if (threadIdx.x == 0 && blockIdx.x == 0) report(a.st, kFlagBounds, 920);
       return;
     }
-    if (i < 256) {
-      for (int w = 0; w < warp; ++w) before += wsum[w];
-      tile_of[i + 1] = before;
+    tiles = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += wsum[w];
+      tiles += wsum[w];
     }
-    if (i == 0) tile_of[0] = 0;
+    for (int k = 0; k < nt; ++k) {
+      tile_expert[before - nt + k] = (short)i;
+      tile_row0[before - nt + k] = o0 + k * a.tile_rows;
+    }
     __syncthreads();
-    tiles = tile_of[256];
   }
   const int steps = a.K / gv::kStep, rgroups = a.N / 16;
   const int granules = (rgroups + gv::kRg - 1) / gv::kRg;  // of a matrix
@@ -379,49 +369,58 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   const int ks = warp % a.KS, wg = warp / a.KS;
   // this CTA's run of granules.  NVFP4: tile * granules + granule, over all CTAs.  INT4: CTAs c, c + 1, ..
   // c + tiles - 1 take the same granules for one tile of x each, so that they share the weights in L2
-  int u0, u1, tile = S::kNv ? -1 : (int)blockIdx.x % tiles;
+  int tile = 0, left = 0x7FFFFFFF;  // the tile at the run's next granule, and how many it has from there on
+  int u0, u1;
   {
     const int n = S::kNv ? (int)gridDim.x : (int)gridDim.x / tiles;
     const int c = S::kNv ? (int)blockIdx.x : (int)blockIdx.x / tiles;
-    const long long all = S::kNv ? (long long)tiles * granules : granules;
-    u0 = (int)(all * c / n);
-    u1 = c < n ? (int)(all * (c + 1) / n) : u0;
-  }
-  if (u0 >= u1) return;
-  const auto expert_of = [&](int t) {  // the expert with tile_of[e] <= t < tile_of[e + 1]
-    int e = 0, hi = 256;
-    while (hi - e > 1) {
-      const int mid = (e + hi) >> 1;
-      if (tile_of[mid] <= t) e = mid;
-      else hi = mid;
+    const int all = S::kNv ? tiles * granules : granules;
+    const int base = all / n, extra = all - base * n;
+    u0 = c * base + min(c, extra);
+    u1 = c < n ? u0 + base + (c < extra ? 1 : 0) : u0;
+    if (u0 >= u1) return;
+    if (S::kNv) {
+      tile = u0 / granules;
+      left = granules - (u0 - tile * granules);
+    } else {
+      tile = (int)blockIdx.x % tiles;
     }
-    return e;
+  }
+  uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kBytes;
+  float* sums = reinterpret_cast<float*>(xs + (size_t)a.tile_rows * a.pitch);
+  Stage<kFmt, kBf16> stage(a, xs);
+  int row0, rows;
+  const auto tile_rows = [&] {  // the rows of `tile`
+    row0 = S::kNv ? tile_row0[tile] : tile * a.tile_rows;
+    rows = min(a.tile_rows, (S::kNv ? __ldg(a.offsets + tile_expert[tile] + 1) : a.T) - row0);
   };
+  tile_rows();
+  stage.start(a, row0, rows);
+  copies_commit();
 
   // ---- the copy side: the warp's next step to copy is number lk of its my_steps in the granule it is at; lnext is
   // where the next batch of granules starts, lleft how many granules the tile has from there on ----
   const int my_steps = (steps - ks + a.KS - 1) / a.KS;
   uint8_t* ring = smem + warp * (gv::kDepth * S::kBytes);
   const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
-  int lnext = u0, lk = 0, lslot = 0, lleft = 0;
-  const uint8_t *lbase = nullptr, *pc = nullptr, *ps = nullptr;
+  int lnext = u0, lk = 0, lslot = 0, lleft = left, ltile = tile;
+  const uint8_t *pc = nullptr, *ps = nullptr;
   const int row_block = a.K / kChunk * kTileBytes;
   const int dstep = a.KS * S::kStride;
   const auto next_granule = [&] {  // point the copies at the warp's next granule; false: it has no more
     while (my_steps > 0 && lnext < u1) {
-      if (S::kNv && lleft == 0) {  // a new tile: its expert
-        const int t = lnext / granules;
-        lleft = granules - (lnext - t * granules);
-        lbase = a.blob + (size_t)expert_of(t) * a.expert_stride + (size_t)ks * S::kStride;
+      if (lleft == 0) {
+        ++ltile;
+        lleft = granules;
       }
-      const int n = S::kNv ? min(RG, min(lleft, u1 - lnext)) : min(RG, u1 - lnext);
+      const int n = min(RG, min(lleft, u1 - lnext));
       const int g = (S::kNv ? granules - lleft : lnext) + wg;
-      const bool mine = wg < n;  // the last batch of a tile or of the run may leave warps idle
       lnext += n;
       lleft -= n;
-      if (mine) {
+      if (wg < n) {  // the last batch of a tile or of the run may leave warps idle
         if (S::kNv) {
-          const uint8_t* p = lbase + (size_t)(g >> 2) * row_block;
+          const uint8_t* p = a.blob + (size_t)tile_expert[ltile] * a.expert_stride + (size_t)ks * S::kStride +
+                             (size_t)(g >> 2) * row_block;
           pc = p + (g & 3) * 1024 + lane * 16;
           ps = p + kTileCodes + (g & 3) * 128 + (lane >> 3) * kTileBytes + (lane & 7) * 16;
         } else {
@@ -432,57 +431,50 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     }
     return false;
   };
-  bool more = next_granule();
+  bool more = true;
   const auto copy_next = [&] {  // one group, empty past the end
+    if (more && lk == 0) more = next_granule();
     if (more) {
       S::copy(pc, ps, ring_addr + lslot * S::kBytes, lane);
       lslot = lslot == gv::kDepth - 1 ? 0 : lslot + 1;
       pc += dstep;
       ps += dstep;
-      if (++lk == my_steps) {
-        lk = 0;
-        more = next_granule();
-      }
+      if (++lk == my_steps) lk = 0;
     }
     copies_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int d = 0; d < gv::kDepth; ++d) copy_next();
 
   // ---- the product side ----
-  uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kBytes;
-  float* sums = reinterpret_cast<float*>(xs + (size_t)a.tile_rows * a.pitch);
-  int row0 = 0, rows = 0;
+  asm volatile("cp.async.wait_group %0;" ::"n"(gv::kDepth) : "memory");  // x, the first group
   float gs = 1.0f;
   const uint8_t* xl0 = nullptr;
-  // a lane whose token does not exist reads the last one's row: its column of the products is not stored
-  const auto aim_x = [&] {
-    xl0 = xs + min(lane >> 2, rows - 1) * a.pitch + (lane & 3) * (S::kNv ? 32 : 16) + ks * 256;
-  };
-  if (!S::kNv) {
-    row0 = tile * a.tile_rows;
-    rows = min(a.tile_rows, a.T - row0);
-    stage_x<kFmt, kBf16>(a, row0, rows, xs, sums, amax, xexp, down);
-    __syncthreads();
-    aim_x();
-  }
   const float* sl0 = sums + ks * (S::kGroups * gv::kRows) + 2 * (lane & 3);
-  int phase = 0, left = 0, slot = 0;
+  int phase = 0, tphase = 0, slot = 0;
+  bool fresh = true;  // x of `tile` is still to be converted
   for (int u = u0; u < u1;) {
-    if (S::kNv && left == 0) {  // the next tile: its expert, its rows of x
-      if (tile >= 0) __syncthreads();  // every warp is done with the last one's
-      tile = u / granules;
-      left = granules - (u - tile * granules);
-      const int e = expert_of(tile);
-      const int r0 = __ldg(a.offsets + e), r1 = __ldg(a.offsets + e + 1);
-      row0 = r0 + (tile - tile_of[e]) * a.tile_rows;
-      rows = min(a.tile_rows, r1 - row0);
-      gs = __ldg(a.gscale + e);
-      stage_x<kFmt, true>(a, row0, rows, xs, sums, amax, xexp, down);
-      __syncthreads();
-      aim_x();
+    if (left == 0) {  // the next tile: its rows of x
+      ++tile;
+      left = granules;
+      tile_rows();
+      __syncthreads();  // every warp is done with the last one's
+      tphase ^= 1;
+      stage.start(a, row0, rows);
+      copies_commit();
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fresh = true;
     }
-    const int n = S::kNv ? min(RG, min(left, u1 - u)) : min(RG, u1 - u);
+    if (fresh) {
+      stage.finish(sums, amax[tphase]);
+      if (threadIdx.x < gv::kRows) amax[tphase ^ 1][threadIdx.x] = 0u;
+      if (S::kNv) gs = __ldg(a.gscale + tile_expert[tile]);
+      // a lane whose token does not exist reads the last one's row: its column of the products is not stored
+      xl0 = xs + min(lane >> 2, rows - 1) * a.pitch + (lane & 3) * (S::kNv ? 32 : 16) + ks * 256;
+      __syncthreads();
+      fresh = false;
+    }
+    const int n = min(RG, min(left, u1 - u));
     const int g0 = S::kNv ? granules - left : u;
     float acc[gv::kRg][4];
 #pragma unroll
@@ -492,9 +484,10 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     if (wg < n) {
       const uint8_t* xl = xl0;
       const float* sl = sl0;
+#pragma unroll 1
       for (int k = 0; k < my_steps; ++k) {
         copies_wait();
-        __syncwarp();  // the other lanes' copies (the scales) too
+        __syncwarp();  // the other lanes' copies too
         S w;
         w.read(ring + slot * S::kBytes, lane);
         slot = slot == gv::kDepth - 1 ? 0 : slot + 1;
@@ -510,7 +503,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       const int rg = (g0 + granule) * gv::kRg + (s >> 2), r = 2 * (lane & 3) + (s & 1);
       if (r < rows && rg < rgroups) {
         const long long o = (long long)(row0 + r) * a.ldo + 16 * rg + (lane >> 2) + 8 * ((s >> 1) & 1);
-        const float2 up = pow2_pair(S::kNv ? xexp[r] : xexp[r] + 24);
+        const float2 up = pow2_pair(row_exponent(amax[tphase][r]) + (S::kNv ? 0 : 24));
         y = y * up.x * up.y;
         if (S::kNv) y *= gs;
         if (a.out_f32) static_cast<float*>(a.out)[o] = y;
@@ -554,9 +547,9 @@ static void set_steps(GemvArgs& a, long long granules_per_cta) {
 
 // Rows of x per tile, as many as fit beside the rings.  row_bytes: shared memory of one row of x; fixed: of the
 // sums; slot_bytes: of a ring's slot.  Returns the dynamic shared memory.
-static size_t set_smem(GemvArgs& a, int rows, size_t row_bytes, size_t fixed, int slot_bytes) {
+static size_t set_smem(GemvArgs& a, int rows, size_t row_bytes, size_t fixed, int slot_bytes, int smem) {
   fixed += (size_t)gv::kWarps * gv::kDepth * slot_bytes;
-  const int fit = (int)((gv::kSmem - fixed) / row_bytes);  // at least 1 at K = 16384
+  const int fit = (int)((smem - fixed) / row_bytes);  // at least 1 at K = 16384
   a.tile_rows = fit < gv::kRows ? fit : gv::kRows;
   if (rows < a.tile_rows) a.tile_rows = rows;
   return fixed + a.tile_rows * row_bytes;
@@ -572,7 +565,8 @@ static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, i
   {  // the opt-in shared-memory size, once per device
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(gemv_kernel<kFmt, kBf16, kZeros>, cudaFuncAttributeMaxDynamicSharedMemorySize, gv::kSmem);
+      e = cudaFuncSetAttribute(gemv_kernel<kFmt, kBf16, kZeros>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               gv::smem_for(kFmt == W4::kNvfp4));
       if (e != cudaSuccess) return e;
       if (dev < 64) done[dev] = true;
     }
@@ -581,6 +575,10 @@ static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, i
   gemv_kernel<kFmt, kBf16, kZeros><<<grid, gv::kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
+
+// the longest row of x: two of them fit beside the rings (kMaxTiles), or one with its sums
+static_assert(gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kBytes + 2 * (16384 * 2 + 16) <= gv::smem_for(true), "x");
+static_assert(gv::kWarps * gv::kDepth * Step<W4::kInt4G32, true>::kBytes + 16384 * 2 + 64 + 16384 <= gv::smem_for(false), "x");
 
 cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   const int Np = (p.N + 127) / 128 * 128;
@@ -603,7 +601,7 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   const int touched = p.R < p.E ? p.R : p.E;
   set_steps(a, (long long)touched * granules / p.num_sms);
   a.pitch = p.K * 2 + 16;  // rows 16 bytes apart in the banks: the lanes' 32-byte pieces of two rows never collide
-  const size_t smem = set_smem(a, p.R, a.pitch, 0, Step<W4::kNvfp4, false>::kBytes);
+  const size_t smem = set_smem(a, p.R, a.pitch, 0, Step<W4::kNvfp4, false>::kBytes, gv::smem_for(true));
   return launch_gemv<W4::kNvfp4, true, false>(a, (long long)(touched + p.R / a.tile_rows) * granules, smem, p.num_sms, st);
 }
 
@@ -612,7 +610,7 @@ static cudaError_t launch_int4(GemvArgs& a, int num_sms, cudaStream_t st) {
   const int granules = (a.N / 16 + gv::kRg - 1) / gv::kRg;
   a.pitch = a.K * 2 + 64;  // the lanes' 16-byte pieces of two rows never collide
   const size_t sums = (size_t)a.K / 128 * int4_groups(kFmt) * gv::kRows * 4;
-  const size_t smem = set_smem(a, a.T, a.pitch, sums, Step<kFmt, kZeros>::kBytes);
+  const size_t smem = set_smem(a, a.T, a.pitch, sums, Step<kFmt, kZeros>::kBytes, gv::smem_for(false));
   a.tiles = (a.T + a.tile_rows - 1) / a.tile_rows;
   a.tile_rows = (a.T + a.tiles - 1) / a.tiles;
   set_steps(a, (long long)granules * a.tiles / num_sms);

@@ -190,7 +190,7 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
                                 const CUtensorMap& rows_map, cudaStream_t st);
 // The forward for few rows, streamed through registers (gemv.cu).
 cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st);
-constexpr int kGemvMaxRows = 4096;  // grid limit of launch_grouped_gemv
+constexpr int kGemvMaxRows = 2048;  // of launch_grouped_gemv (its tile table)
 
 // y [T][N] = x [T][K] times an INT4 matrix with group scales and zero points.
 struct Int4Product {
