@@ -136,14 +136,21 @@ def _ptr(t):
 
 def _rows(t, cols, dtype, what):
     """(address, row stride) of a CUDA matrix [rows][cols] whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor")
     if t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype:
         raise ValueError(f"{what}: expected [rows][{cols}] {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if t.stride(1) != 1:
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    ld, one = t.stride()
+    if one != 1:
         raise ValueError(f"{what}: expected contiguous rows")
     # a single row has no stride to speak of
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else -(-cols // 8) * 8
+    return t.data_ptr(), ld if t.shape[0] > 1 else -(-cols // 8) * 8
+
+
+def _raw_stream(stream, device):
+    """The handle of `stream`, or of the device's current one, without a Stream object."""
+    import torch
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 def _host_ptr(t):
@@ -370,6 +377,8 @@ class Grouped(MoELayer):
         self.out_f32 = out_f32
         self.E, self.N, self.K = num_experts, out_features, in_features
         self.device = device
+        import torch
+        self._int32, self._act, self._out = torch.int32, torch.bfloat16, torch.float32 if out_f32 else torch.bfloat16
         h = ctypes.c_void_p()
         st = self.lib.nvfp4_grouped_create(ctypes.byref(self.cfg), ctypes.byref(h))
         if st != 0:
@@ -387,14 +396,17 @@ class Grouped(MoELayer):
         self._check(st, "nvfp4_grouped_pack")
 
     def _product(self, fn, what, x, offsets, out, wi, wo, stream):
-        import torch
-        if offsets.dtype != torch.int32 or offsets.shape != (self.E + 1,):
-            raise ValueError(f"{what}: expected int32 offsets [{self.E + 1}]")
-        if x.shape[0] != out.shape[0]:
-            raise ValueError(f"{what}: the input has {x.shape[0]} rows, the output {out.shape[0]}")
-        xp, ldx = _rows(x, wi, torch.bfloat16, what)
-        op, ldo = _rows(out, wo, torch.float32 if self.out_f32 else torch.bfloat16, what)
-        self._check(fn(self.h, x.shape[0], _ptr(offsets), xp, ldx, op, ldo, _stream(stream, self.device)), what)
+        if offsets.dtype != self._int32 or offsets.numel() != self.E + 1 or not offsets.is_contiguous() \
+                or not offsets.is_cuda:
+            raise ValueError(f"{what}: expected contiguous CUDA int32 offsets [{self.E + 1}]")
+        xp, ldx = _rows(x, wi, self._act, what)
+        op, ldo = _rows(out, wo, self._out, what)
+        R = x.shape[0]
+        if R != out.shape[0]:
+            raise ValueError(f"{what}: the input has {R} rows, the output {out.shape[0]}")
+        st = fn(self.h, R, offsets.data_ptr(), xp, ldx, op, ldo, _raw_stream(stream, self.device))
+        if st:
+            self._check(st, what)
         return out
 
     def nvfp4_grouped_forward(self, x, offsets, out, stream=None):
@@ -426,21 +438,20 @@ class Int4Linear(MoELayer):
         self.out_f32, self.act_f16 = out_f32, act_f16
         self.N, self.K, self.group = out_features, in_features, group_size
         self.device = device
+        import torch
+        self._act = torch.float16 if act_f16 else torch.bfloat16
+        self._out = torch.float32 if out_f32 else self._act
         h = ctypes.c_void_p()
         st = self.lib.nvfp4_int4_create(ctypes.byref(self.cfg), ctypes.byref(h))
         if st != 0:
             raise Nvfp4MoeError(st, "nvfp4_int4_create: " + self.lib.nvfp4_moe_status_string(st).decode())
         self.h = h
 
-    def _act(self):
-        import torch
-        return torch.float16 if self.act_f16 else torch.bfloat16
-
     def nvfp4_int4_pack(self, w_q, scale, zero=None, stream=None):
         """w_q [N][K/2] uint8, scale [N][K/group] in x's type, zero [N][K/group] uint8 or None (8 everywhere)."""
         import torch
         groups = (self.N, self.K // self.group)
-        for t, shape, dt in ((w_q, (self.N, self.K // 2), torch.uint8), (scale, groups, self._act()),
+        for t, shape, dt in ((w_q, (self.N, self.K // 2), torch.uint8), (scale, groups, self._act),
                              (zero, groups, torch.uint8)):
             if t is not None and (tuple(t.shape) != shape or t.dtype != dt):
                 raise ValueError(f"nvfp4_int4_pack: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
@@ -449,13 +460,14 @@ class Int4Linear(MoELayer):
 
     def nvfp4_int4_forward(self, x, out, stream=None):
         """out [T][N] = x [T][K] times the matrix, T <= max_tokens."""
-        import torch
-        if x.shape[0] != out.shape[0]:
-            raise ValueError(f"nvfp4_int4_forward: x has {x.shape[0]} rows, out {out.shape[0]}")
-        xp, ldx = _rows(x, self.K, self._act(), "nvfp4_int4_forward")
-        op, ldo = _rows(out, self.N, torch.float32 if self.out_f32 else self._act(), "nvfp4_int4_forward")
-        st = self.lib.nvfp4_int4_forward(self.h, x.shape[0], xp, ldx, op, ldo, _stream(stream, self.device))
-        self._check(st, "nvfp4_int4_forward")
+        xp, ldx = _rows(x, self.K, self._act, "nvfp4_int4_forward")
+        op, ldo = _rows(out, self.N, self._out, "nvfp4_int4_forward")
+        T = x.shape[0]
+        if T != out.shape[0]:
+            raise ValueError(f"nvfp4_int4_forward: x has {T} rows, out {out.shape[0]}")
+        st = self.lib.nvfp4_int4_forward(self.h, T, xp, ldx, op, ldo, _raw_stream(stream, self.device))
+        if st:
+            self._check(st, "nvfp4_int4_forward")
         return out
 
     def nvfp4_moe_debug_packed_blob(self, stream=None):

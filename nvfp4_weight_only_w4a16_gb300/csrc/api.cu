@@ -1146,6 +1146,7 @@ nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t
   p.ldo = ldo;
   p.out_f32 = h->i4.out_f32;
   p.num_sms = h->num_sms;
+  p.status = h->ws.status;
   cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
   const nvfp4_moe_status s = take_events(h, ev);
   if (s != NVFP4_MOE_OK) return s;

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 
 namespace nvfp4moe {
 
@@ -99,6 +100,7 @@ struct Step {
   static constexpr int kCodes = gv::kRg * 1024;
   static constexpr int kZeroOff = kCodes + 64 * kGroups;
   static constexpr int kBytes = kNv ? kCodes + 256 : kZeroOff + (kZeros ? 32 * kGroups : 0);  // of a slot
+  static constexpr int kSlot = (kBytes + 127) & ~127;  // slots start on 128 bytes: off it, a read of 512 takes a turn more
   static constexpr int kStride = kNv ? 2 * kTileBytes : kBytes;  // in memory, from a step to the next
   uint4 c[gv::kRg][2];                     // the lane's codes
   uint32_t s[gv::kRg][kNv ? 2 : kGroups];  // INT4: {row r, row r + 8} 16-bit scales per group
@@ -242,9 +244,8 @@ __device__ __forceinline__ int row_exponent(unsigned bits) { return bits ? (int)
 
 // x rows into shared memory as FP16 times 2^-p per row; INT4: elements 2, 3, 6 and 7 of every 8 times another
 // 2^-4, and 2^-24 times the sums over each group of the matrix into sums[group][8].  In two parts: start() copies the
-// rows as they are, finish() -- once the copies have landed -- finds each row's p and converts in place.  A thread
-// handles the same 16-byte pieces throughout, so nothing but the maxima passes between threads.  (Small loops on
-// purpose: a call's first use of its code comes from memory, and this runs before any product.)
+// rows as they are (bulk copies, by one thread), finish() waits for them, finds each row's p and converts in place.
+// (Small loops on purpose: a call's first use of its code comes from memory, and this runs before any product.)
 template <W4 kFmt, bool kBf16>
 struct Stage {
   uint8_t* xs;
@@ -258,24 +259,25 @@ struct Stage {
     r += dr, p += dp;
     if (p >= per) p -= per, ++r;
   }
-  __device__ __forceinline__ void start(const GemvArgs& a, int row0, int n) {
-    rows = n;
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(xs);
-    int r = r0, p = p0;
+  __device__ __forceinline__ void start(const GemvArgs& a, int row0, uint64_t* bar) {  // one thread
+    mbar_arrive_expect_tx(bar, (uint32_t)(rows * per * 16));
 #pragma unroll 1
-    for (; r < rows; next(r, p))
-      copy16(d + r * pitch + p * 16, static_cast<const uint8_t*>(a.x) + ((long long)(row0 + r) * a.ldx + 8 * p) * 2);
+    for (int r = 0; r < rows; ++r)
+      bulk_g2s(xs + r * pitch, static_cast<const uint16_t*>(a.x) + (long long)(row0 + r) * a.ldx, (uint32_t)(per * 16), bar);
   }
   static __device__ __forceinline__ float value(uint32_t w, int hi) {
     return kBf16 ? __uint_as_float(hi ? w & 0xFFFF0000u : w << 16)
                  : __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xFFFFu)));
   }
-  // amax: the rows' largest finite magnitudes, zero on entry.  The barrier after the writes is the caller's.
-  __device__ __forceinline__ void finish(float* sums, unsigned* amax) {
+  // amax: the rows' largest finite magnitudes, zero on entry.  False, in every thread, when the copies did not land
+  // in time (reported).  The barrier after the writes is the caller's.
+  __device__ __forceinline__ bool finish(float* sums, unsigned* amax, uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         DeviceStatus* st) {
+    const bool landed = mbar_wait(bar, parity, abort, st, 921);
     const int lane = threadIdx.x & 31;
     int r = r0, p = p0;
 #pragma unroll 1
-    for (int i = threadIdx.x & ~31; i < rows * per; i += gv::kThreads, next(r, p)) {  // whole warps
+    for (int i = threadIdx.x & ~31; landed && i < rows * per; i += gv::kThreads, next(r, p)) {  // whole warps
       unsigned m = 0;  // FP32 bits order like the magnitudes
       if (r < rows) {
         const uint4 v = *reinterpret_cast<const uint4*>(xs + r * pitch + p * 16);
@@ -291,7 +293,7 @@ struct Stage {
       for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
       if ((lane & 15) == 0 && r < rows) atomicMax(amax + r, m);
     }
-    __syncthreads();
+    if (__syncthreads_or(!landed)) return false;
     constexpr int kLanes = kFmt == W4::kNvfp4 ? 1 : 16 / int4_groups(kFmt);  // threads per group
     r = r0, p = p0;
 #pragma unroll 1
@@ -320,22 +322,32 @@ struct Stage {
         if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = sum * 0x1p-24f;
       }
     }
+    return true;
   }
 };
 
 template <W4 kFmt, bool kBf16, bool kZeros>
 __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   using S = Step<kFmt, kZeros>;
-  extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the group sums
+  extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the group sums
   __shared__ unsigned amax[2][gv::kRows];                  // of this tile and, zero, of the next
   __shared__ short tile_expert[gv::kMaxTiles];             // NVFP4
   __shared__ int tile_row0[gv::kMaxTiles], wsum[8];
+  __shared__ uint64_t x_bar;  // x rows landed
+  __shared__ int abort_flag;
   __shared__ float red[2][gv::kWarps][4 * gv::kRg][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int tiles = a.tiles;
   if (threadIdx.x < 2 * gv::kRows) amax[0][threadIdx.x] = 0u;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(&x_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   if (S::kNv) {  // tiles of at most tile_rows rows of one expert; thread i looks at expert i
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int i = threadIdx.x;
     const int o0 = i < a.E ? __ldg(a.offsets + i) : 0, o1 = i < a.E ? __ldg(a.offsets + i + 1) : 0;
     const bool bad = o0 < 0 || o1 < o0 || o1 > a.R;
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       tile = (int)blockIdx.x % tiles;
     }
   }
-  uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kBytes;
+  uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kSlot;
   float* sums = reinterpret_cast<float*>(xs + (size_t)a.tile_rows * a.pitch);
   Stage<kFmt, kBf16> stage(a, xs);
   int row0, rows;
@@ -395,13 +407,13 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     rows = min(a.tile_rows, (S::kNv ? __ldg(a.offsets + tile_expert[tile] + 1) : a.T) - row0);
   };
   tile_rows();
-  stage.start(a, row0, rows);
-  copies_commit();
+  stage.rows = rows;
+  if (S::kNv && threadIdx.x == 0) stage.start(a, row0, &x_bar);
 
   // ---- the copy side: the warp's next step to copy is number lk of its my_steps in the granule it is at; lnext is
   // where the next batch of granules starts, lleft how many granules the tile has from there on ----
   const int my_steps = (steps - ks + a.KS - 1) / a.KS;
-  uint8_t* ring = smem + warp * (gv::kDepth * S::kBytes);
+  uint8_t* ring = smem + warp * (gv::kDepth * S::kSlot);
   const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
   int lnext = u0, lk = 0, lslot = 0, lleft = left, ltile = tile;
   const uint8_t *pc = nullptr, *ps = nullptr;
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   const auto copy_next = [&] {  // one group, empty past the end
     if (more && lk == 0) more = next_granule();
     if (more) {
-      S::copy(pc, ps, ring_addr + lslot * S::kBytes, lane);
+      S::copy(pc, ps, ring_addr + lslot * S::kSlot, lane);
       lslot = lslot == gv::kDepth - 1 ? 0 : lslot + 1;
       pc += dstep;
       ps += dstep;
@@ -447,7 +459,12 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   for (int d = 0; d < gv::kDepth; ++d) copy_next();
 
   // ---- the product side ----
-  asm volatile("cp.async.wait_group %0;" ::"n"(gv::kDepth) : "memory");  // x, the first group
+  if (!S::kNv) {  // the weights, which no kernel writes, are on their way; x may still be in the making
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (threadIdx.x == 0) stage.start(a, row0, &x_bar);
+  }
+  __syncthreads();  // the barrier is initialised
   float gs = 1.0f;
   const uint8_t* xl0 = nullptr;
   const float* sl0 = sums + ks * (S::kGroups * gv::kRows) + 2 * (lane & 3);
@@ -460,13 +477,18 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       tile_rows();
       __syncthreads();  // every warp is done with the last one's
       tphase ^= 1;
-      stage.start(a, row0, rows);
-      copies_commit();
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      stage.rows = rows;
+      if (threadIdx.x == 0) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the reads of the last x, before the copies
+        stage.start(a, row0, &x_bar);
+      }
       fresh = true;
     }
     if (fresh) {
-      stage.finish(sums, amax[tphase]);
+      if (!stage.finish(sums, amax[tphase], &x_bar, (uint32_t)tphase, &abort_flag, a.st)) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+      }
       if (threadIdx.x < gv::kRows) amax[tphase ^ 1][threadIdx.x] = 0u;
       if (S::kNv) gs = __ldg(a.gscale + tile_expert[tile]);
       // a lane whose token does not exist reads the last one's row: its column of the products is not stored
@@ -489,7 +511,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
         copies_wait();
         __syncwarp();  // the other lanes' copies too
         S w;
-        w.read(ring + slot * S::kBytes, lane);
+        w.read(ring + slot * S::kSlot, lane);
         slot = slot == gv::kDepth - 1 ? 0 : slot + 1;
         __syncwarp();  // read by all before it is filled again
         copy_next();
@@ -571,14 +593,22 @@ static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, i
       if (dev < 64) done[dev] = true;
     }
   }
-  const unsigned grid = (unsigned)(ctas < num_sms ? ctas : num_sms);
-  gemv_kernel<kFmt, kBf16, kZeros><<<grid, gv::kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(ctas < num_sms ? ctas : num_sms));
+  cfg.blockDim = dim3(gv::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<kFmt, kBf16, kZeros>, a);
 }
 
 // the longest row of x: two of them fit beside the rings (kMaxTiles), or one with its sums
-static_assert(gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kBytes + 2 * (16384 * 2 + 16) <= gv::smem_for(true), "x");
-static_assert(gv::kWarps * gv::kDepth * Step<W4::kInt4G32, true>::kBytes + 16384 * 2 + 64 + 16384 <= gv::smem_for(false), "x");
+static_assert(gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kSlot + 2 * (16384 * 2 + 16) <= gv::smem_for(true), "x");
+static_assert(gv::kWarps * gv::kDepth * Step<W4::kInt4G32, true>::kSlot + 16384 * 2 + 64 + 16384 <= gv::smem_for(false), "x");
 
 cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   const int Np = (p.N + 127) / 128 * 128;
@@ -601,7 +631,7 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   const int touched = p.R < p.E ? p.R : p.E;
   set_steps(a, (long long)touched * granules / p.num_sms);
   a.pitch = p.K * 2 + 16;  // rows 16 bytes apart in the banks: the lanes' 32-byte pieces of two rows never collide
-  const size_t smem = set_smem(a, p.R, a.pitch, 0, Step<W4::kNvfp4, false>::kBytes, gv::smem_for(true));
+  const size_t smem = set_smem(a, p.R, a.pitch, 0, Step<W4::kNvfp4, false>::kSlot, gv::smem_for(true));
   return launch_gemv<W4::kNvfp4, true, false>(a, (long long)(touched + p.R / a.tile_rows) * granules, smem, p.num_sms, st);
 }
 
@@ -610,7 +640,7 @@ static cudaError_t launch_int4(GemvArgs& a, int num_sms, cudaStream_t st) {
   const int granules = (a.N / 16 + gv::kRg - 1) / gv::kRg;
   a.pitch = a.K * 2 + 64;  // the lanes' 16-byte pieces of two rows never collide
   const size_t sums = (size_t)a.K / 128 * int4_groups(kFmt) * gv::kRows * 4;
-  const size_t smem = set_smem(a, a.T, a.pitch, sums, Step<kFmt, kZeros>::kBytes, gv::smem_for(false));
+  const size_t smem = set_smem(a, a.T, a.pitch, sums, Step<kFmt, kZeros>::kSlot, gv::smem_for(false));
   a.tiles = (a.T + a.tile_rows - 1) / a.tile_rows;
   a.tile_rows = (a.T + a.tiles - 1) / a.tiles;
   set_steps(a, (long long)granules * a.tiles / num_sms);
@@ -624,6 +654,7 @@ static cudaError_t launch_int4(GemvArgs& a, const Int4Product& p, cudaStream_t s
 
 cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st) {
   GemvArgs a{};
+  a.st = p.status;
   a.packed = p.packed;
   a.T = p.T;
   a.N = p.N;

@@ -153,7 +153,6 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   const int first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
   volatile int* abort_flag = &ctl.abort_flag;
 
-  for (int i = threadIdx.x; i <= a.E; i += gg::kThreads) ctl.off[i] = a.offsets[i];
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.raw_stages; ++s) {
       mbar_init(ctl.raw_full + s, 1);
@@ -184,6 +183,9 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
   }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int i = threadIdx.x; i <= a.E; i += gg::kThreads) ctl.off[i] = a.offsets[i];
   __syncthreads();
   if (warp == 0) {  // token tiles per expert, 8 experts a lane; offsets that do not ascend within 0..R give no tile
     int n[8], sum = 0;
@@ -518,12 +520,14 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   cfg.blockDim = dim3(gg::kThreads);
   cfg.dynamicSmemBytes = gg::kSmemMax;
   cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)t.ctas;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)t.ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, grouped_kernel(backward, t.ctas == 2), rows_map, a);
 }
 

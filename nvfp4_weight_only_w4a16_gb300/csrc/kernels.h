@@ -205,6 +205,7 @@ struct Int4Product {
   long long ldo;
   int out_f32;
   int num_sms;
+  DeviceStatus* status;
 };
 cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st);
 size_t int4_packed_bytes(int N, int K, int group, bool zeros);

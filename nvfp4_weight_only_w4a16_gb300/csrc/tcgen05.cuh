@@ -57,6 +57,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// Programmatic dependent launch: a kernel launched with that attribute may start while its
+// predecessor in the stream ends.  It waits here before it touches anything the predecessor
+// may write or read; what no kernel writes (packed weights) may be read before.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the successor's launch begin; its own wait still holds it until this grid has completed.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- CTA pairs (a cluster of two on neighbouring multiprocessors) -----------
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
