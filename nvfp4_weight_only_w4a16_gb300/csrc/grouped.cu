@@ -20,10 +20,10 @@
 // halves of the MMA read.  kCtas = 1, 128 features, where there is no second block
 // to pair with.
 //
-// One CTA per multiprocessor, 24 warps: 0 packed-weight producer (bulk copies into
+// One CTA per multiprocessor, 24 or 32 warps: 0 packed-weight producer (bulk copies into
 // a ring), 1 MMA issuer (the pair's first CTA), 2 row producer (TMA, zero fill past
-// the matrix), 4-7 epilogue (TMEM -> gs -> shared -> 16-byte stores), 8-23
-// dequantisers in two teams that take turns.  Two accumulator buffers of 256
+// the matrix), 4-7 epilogue (TMEM -> gs -> shared -> 16-byte stores), the
+// rest dequantisers, in two or three teams of 8 that take turns.  Two accumulator buffers of 256
 // columns: the epilogue of a unit overlaps the next one's MMAs.  The row offsets
 // are read on the device; every CTA derives the same unit list from them, so
 // nothing is written but the output.
@@ -36,8 +36,8 @@
 namespace nvfp4moe {
 
 namespace gg {
-constexpr int kThreads = 768;
-constexpr int kTeamWarps = 8, kDequantWarps = 2 * kTeamWarps, kEpiWarps = 4;
+constexpr int kTeamWarps = 8, kEpiWarps = 4;
+__host__ __device__ constexpr int threads(int teams) { return 32 * (8 + teams * kTeamWarps); }
 constexpr int kPairBytes = 2 * kTileBytes;  // one 128 x 128 weight square, packed
 constexpr int kHalfBytes = 16384;           // half a square in BF16: 64 long in the reduction
 constexpr int kMaxStages = 6, kMaxRaw = 16;
@@ -64,46 +64,56 @@ struct GroupedArgs {
   int out_f32;
   int tile_rows;           // rows per token tile, a multiple of 64 up to 256
   int box;                 // rows per TMA box, divides tile_rows / kCtas
+  // ring depths.  A parity wait must not run two phases ahead: a team meets every raw slot again itself (raw_stages
+  // is a multiple of the teams; bulk copies may land out of order); the operand stages are freed in order, so that
+  // as many stages as teams are enough for them
   int stages, raw_stages;
   DeviceStatus* st;
   int fault;
+  uint32_t zero;           // 0, unknown to the compiler
 };
 
 struct GroupedCtl {
   int off[257];
-  int tile[257];  // token tiles before expert e; tile[E] = all
+  int tile[257];   // token tiles before expert e; tile[E] = all
+  short per[256];  // rows per tile of expert e: its tiles are of one size, so that none is a small remainder
   uint64_t raw_full[gg::kMaxRaw], raw_empty[gg::kMaxRaw];
-  uint64_t a_full[gg::kMaxStages], b_full[gg::kMaxStages], empty[gg::kMaxStages];
+  uint64_t full[gg::kMaxStages], empty[gg::kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
   int abort_flag;
 };
 static_assert(sizeof(GroupedCtl) <= gg::kCtlBytes, "control block");
 
-struct GroupedUnit {
-  int e, row0, rows, nb;
-};
-
+// The units of one CTA (pair): first, first + stride, ..; unit u is feature block(s) u % NU of token tile u / NU.
 template <int kCtas>
-__device__ __forceinline__ GroupedUnit grouped_unit(const GroupedCtl& c, const GroupedArgs& a, int u) {
-  const int t = u / a.NU;
-  int lo = 0, hi = a.E;  // the expert e with tile[e] <= t < tile[e + 1]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (c.tile[mid] <= t) lo = mid;
-    else hi = mid;
+struct GroupedUnits {
+  int u, stride, nu, t, nb, dt, dnb, e;
+  __device__ __forceinline__ GroupedUnits(const GroupedCtl& c, const GroupedArgs& a, int first, int step)
+      : u(first), stride(step), nu(a.NU) {
+    t = u / nu, nb = u - t * nu;
+    dt = stride / nu, dnb = stride - dt * nu;
+    e = 0;
+    int hi = a.E;  // the expert e with tile[e] <= t < tile[e + 1]
+    while (hi - e > 1) {
+      const int mid = (e + hi) >> 1;
+      if (c.tile[mid] <= t) e = mid;
+      else hi = mid;
+    }
   }
-  const int m = c.off[lo + 1] - c.off[lo], nt = c.tile[lo + 1] - c.tile[lo], j = t - c.tile[lo];
-  // an expert's tiles are of one size, so that none is a small remainder
-  constexpr int kRound = 16 * kCtas - 1;
-  const int per = ((m + nt - 1) / nt + kRound) & ~kRound;
-  GroupedUnit r;
-  r.e = lo;
-  r.row0 = c.off[lo] + j * per;
-  r.rows = min(per, m - j * per);
-  r.nb = (u - t * a.NU) * kCtas;
-  return r;
-}
+  __device__ __forceinline__ void next(const GroupedCtl& c, int total) {
+    u += stride, t += dt, nb += dnb;
+    if (nb >= nu) nb -= nu, ++t;
+    if (u < total)
+      while (c.tile[e + 1] <= t) ++e;
+  }
+  __device__ __forceinline__ int block() const { return nb * kCtas; }
+  __device__ __forceinline__ int rows(const GroupedCtl& c, int& row0) const {
+    const int per = c.per[e], j = (t - c.tile[e]) * per;
+    row0 = c.off[e] + j;
+    return min(per, c.off[e + 1] - c.off[e] - j);
+  }
+};
 
 // M-major A operand, 128B swizzle: 64 M elements by 8 reduction rows per 1024-byte
 // atom, the next 8 rows 1024 B on, the next 64 M elements one panel (64 rows x
@@ -136,8 +146,8 @@ __device__ __forceinline__ void dequant16_bf16(uint32_t c0, uint32_t c1, uint32_
   for (int i = 0; i < 4; ++i) o[4 + i] = scaled_pair_bf16(v[i], s);
 }
 
-template <bool kBackward, int kCtas>
-__global__ void __launch_bounds__(gg::kThreads, 1)
+template <bool kBackward, int kCtas, int kTeams>
+__global__ void __launch_bounds__(gg::threads(kTeams), 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap, GroupedArgs a) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -147,10 +157,11 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   const int b_half = a.tile_rows / kCtas * 128;
   const int stage_bytes = 2 * gg::kHalfBytes + 2 * b_half;
   uint8_t* raw = ring + a.stages * stage_bytes;
-  const uint32_t ring_addr = smem_u32(ring);
+  const uint32_t ring_addr = smem_u32(ring), raw_addr = smem_u32(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
   const int first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
+  constexpr int kRound = 16 * kCtas;  // the MMA's columns come in these
   volatile int* abort_flag = &ctl.abort_flag;
 
   if (threadIdx.x == 0) {
@@ -159,8 +170,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       mbar_init(ctl.raw_empty + s, gg::kTeamWarps);
     }
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(ctl.a_full + s, kCtas * gg::kTeamWarps);  // waited for by the pair's first CTA
-      mbar_init(ctl.b_full + s, 1);                          // the same
+      mbar_init(ctl.full + s, kCtas * gg::kTeamWarps + 1);  // waited for by the pair's first CTA
       mbar_init(ctl.empty + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -185,7 +195,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int i = threadIdx.x; i <= a.E; i += gg::kThreads) ctl.off[i] = a.offsets[i];
+  for (int i = threadIdx.x; i <= a.E; i += gg::threads(kTeams)) ctl.off[i] = a.offsets[i];
   __syncthreads();
   if (warp == 0) {  // token tiles per expert, 8 experts a lane; offsets that do not ascend within 0..R give no tile
     int n[8], sum = 0;
@@ -196,6 +206,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       const int m = e < a.E ? ctl.off[e + 1] - ctl.off[e] : 0;
       bad |= e < a.E && ctl.off[e + 1] < ctl.off[e];
       n[i] = (m + a.tile_rows - 1) / a.tile_rows;
+      if (e < a.E && n[i] > 0) ctl.per[e] = (short)(((m + n[i] - 1) / n[i] + kRound - 1) & ~(kRound - 1));
       sum += n[i];
     }
     bad = __any_sync(0xffffffffu, bad);
@@ -221,6 +232,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
   const int total = ctl.tile[a.E] * a.NU;
+  const int squares = first < total ? ((total - first - 1) / stride + 1) * a.steps : 0;  // of this CTA
 
   if (warp == 0) {
     if (lane == 0) {
@@ -228,39 +240,39 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       uint32_t it = 0;
       RingPos p;
       bool ok = true;
-      for (int u = first; u < total && ok && a.fault != 1; u += stride) {
-        const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
+      for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok && a.fault != 1; w.next(ctl, total)) {
         // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
-        const int nb = min(w.nb + rank, a.NB - 1);
+        const int nb = min(w.block() + rank, a.NB - 1);
         const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)nb * a.block_stride;
-        for (int s = 0; s < a.steps; ++s, ++it, p.step(a.raw_stages)) {
+        for (int s = 0; s < a.steps; ++s, ++it, p.step(a.raw_stages), src += a.step_stride) {
           if (!mbar_wait(ctl.raw_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 911)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(ctl.raw_full + p.slot, gg::kPairBytes);
-          bulk_g2s(raw + p.slot * gg::kPairBytes, src + (size_t)s * a.step_stride, gg::kPairBytes, ctl.raw_full + p.slot);
+          bulk_g2s(raw + p.slot * gg::kPairBytes, src, gg::kPairBytes, ctl.raw_full + p.slot);
         }
       }
       if (!ok) drain_copies(ctl.raw_full, it, a.raw_stages);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer: the whole warp walks the loop, one lane issues ----------------
-    uint32_t j = 0;
-    RingPos p;
+    // ---------------- MMA issuer: the whole warp walks the loop, one lane issues.  Every instruction here counts:
+    // the loop shares its scheduler with four dequantisers ----------------
     if (rank == 0) {
-      for (int u = first; u < total; u += stride, ++j) {
-        const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
+      uint32_t j = 0;
+      RingPos p;
+      bool ok = true;
+      for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok; w.next(ctl, total), ++j) {
+        int row0;
         const uint32_t idesc =
-            idesc_bf16(128 * kCtas, (w.rows + 16 * kCtas - 1) & ~(16 * kCtas - 1)) | (kBackward ? 1u << 15 : 0u);
+            idesc_bf16(128 * kCtas, (w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) | (kBackward ? 1u << 15 : 0u);
         const uint32_t buf = j & 1u;
-        if (!mbar_wait_cluster(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
+        if (!warp_wait(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * 256u;
-        bool ok = true;
-        for (int s = 0; s < a.steps; ++s, p.step(a.stages)) {
-          if (!mbar_wait_cluster(ctl.b_full + p.slot, p.phase, abort_flag, a.st, 913) ||
-              !mbar_wait_cluster(ctl.a_full + p.slot, p.phase, abort_flag, a.st, 914)) {
+        uint32_t acc = 0;
+        for (int s = a.steps; s > 0; --s, p.step(a.stages)) {
+          if (!warp_wait(ctl.full + p.slot, p.phase, abort_flag, a.st, 913)) {
             ok = false;
             break;
           }
@@ -273,107 +285,100 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
             for (int kk = 0; kk < 8; ++kk) {  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
               const uint64_t ak = ad + (uint32_t)(kk >> 2) * (gg::kHalfBytes >> 4) + (kBackward ? 128u : 2u) * (kk & 3);
               const uint64_t bk = bd + (uint32_t)(kk >> 2) * (uint32_t)(b_half >> 4) + 2u * (kk & 3);
-              if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, (s | kk) != 0 ? 1u : 0u);
-              else umma_bf16(d, ak, bk, idesc, (s | kk) != 0 ? 1u : 0u);
+              if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, kk ? 1u : acc);
+              else umma_bf16(d, ak, bk, idesc, kk ? 1u : acc);
             }
             if (kCtas == 2) umma_commit_pair(ctl.empty + p.slot);
             else umma_commit(ctl.empty + p.slot);
+            if (s == 1) {
+              if (kCtas == 2) umma_commit_pair(ctl.acc_full + buf);
+              else umma_commit(ctl.acc_full + buf);
+            }
           }
+          acc = 1;
           __syncwarp();
         }
-        if (!ok) break;
-        if (elect_one()) {
-          if (kCtas == 2) umma_commit_pair(ctl.acc_full + buf);
-          else umma_commit(ctl.acc_full + buf);
-        }
-        __syncwarp();
       }
     }
   } else if (warp == 2) {
     // ---------------- rows of x (dy): this CTA's half of the tile, boxes of 64 reduction elements ----------------
-    uint32_t it = 0;
     RingPos p;
     bool ok = true;
-    for (int u = first; u < total && ok && a.fault != 1; u += stride) {
-      const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
-      const int share = ((w.rows + 16 * kCtas - 1) & ~(16 * kCtas - 1)) / kCtas;
+    for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok && a.fault != 1; w.next(ctl, total)) {
+      int row0;
+      const int share = ((w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) / kCtas;
       const int nbox = (share + a.box - 1) / a.box;
-      const int row0 = w.row0 + rank * share;
-      for (int s = 0; s < a.steps; ++s, ++it, p.step(a.stages)) {
-        if (!mbar_wait(ctl.empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 915)) {
+      row0 += rank * share;
+      for (int s = 0; s < a.steps; ++s, p.step(a.stages)) {
+        if (!warp_wait(ctl.empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 915)) {
           ok = false;
           break;
         }
         if (elect_one()) {
           uint8_t* dst = ring + p.slot * stage_bytes + 2 * gg::kHalfBytes;
-          if (rank == 0) mbar_arrive_expect_tx(ctl.b_full + p.slot, (uint32_t)(kCtas * 2 * nbox * a.box) * 128u);
-          const uint32_t bar = kCtas == 2 ? map_rank(ctl.b_full + p.slot, 0) : 0u;
+          uint64_t* bar = ctl.full + p.slot;
+          if (rank == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kCtas * 2 * nbox * a.box) * 128u);
+          const uint32_t bar0 = kCtas == 2 ? map_rank(bar, 0) : 0u;
           for (int h = 0; h < 2; ++h)
             for (int b = 0; b < nbox; ++b) {
-              if (kCtas == 2) tma_2d_pair(dst + h * b_half + b * a.box * 128, &tmap, s * 128 + h * 64, row0 + b * a.box, bar);
-              else tma_2d(dst + h * b_half + b * a.box * 128, &tmap, s * 128 + h * 64, row0 + b * a.box, ctl.b_full + p.slot);
+              uint8_t* to = dst + h * b_half + b * a.box * 128;
+              if (kCtas == 2) tma_2d_pair(to, &tmap, s * 128 + h * 64, row0 + b * a.box, bar0);
+              else tma_2d(to, &tmap, s * 128 + h * 64, row0 + b * a.box, bar);
             }
         }
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
-      if (rank == 0) drain_copies(ctl.b_full, it, a.stages);
-      else
-        for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // its copies complete on the first CTA's barriers
-    }
+    if (!ok)  // given up: the copies in flight land within microseconds (their barrier also counts the dequantisers)
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   } else if (warp >= 8) {
-    // ---------------- dequantisers: two teams take turns at the squares; warp w of a team takes one 16-row
+    // ---------------- dequantisers: the teams take turns at the squares; warp w of a team takes one 16-row
     // sub-block of each half, so that its waits and its fence are paid once for 64 weights a lane ----------------
     const int team = (warp - 8) >> 3, w = (warp - 8) & 7, q = lane & 3;
-    const int slot = seg_pos(lane);
     // forward: half h is tile h (K elements 64 h ..), all 128 rows; backward: rows 64 h .. of both tiles
     const int r = (kBackward ? (w & 3) * 16 : w * 16) + (lane >> 2);
-    const uint32_t dst0 = (kBackward ? (uint32_t)(w >> 2) * 8192u : 0u) + (uint32_t)r * 128u;
+    const uint32_t dst0 = ring_addr + (kBackward ? (uint32_t)(w >> 2) * 8192u : 0u) + (uint32_t)r * 128u;
     const uint32_t x0 = (uint32_t)((2 * q) ^ (r & 7)) * 16u, x1 = (uint32_t)((2 * q + 1) ^ (r & 7)) * 16u;
+    const uint32_t sub = (uint32_t)(kBackward ? (w >> 2) * kTileBytes + (w & 3) * 512 : w * 512) + seg_pos(lane) * 16;
+    const uint32_t ssub = (uint32_t)(kBackward ? (w >> 2) * kTileBytes + (w & 3) * 64 : w * 64) + kTileCodes + seg_pos(lane) * 2;
+    const uint32_t raw_empty0 = smem_u32(ctl.raw_empty);
+    const uint32_t full0 = kCtas == 2 ? map_rank(ctl.full, 0) : 0u;  // the pair's first CTA's
     RingPos pr, pa;
-    int mine = 0;  // team of the current square
-    bool ok = true;
-    for (int u = first; u < total && ok; u += stride) {
-      for (int s = 0; s < a.steps; ++s, mine ^= 1, pr.step(a.raw_stages), pa.step(a.stages)) {
-        if (mine != team) continue;
-        if (!mbar_wait(ctl.raw_full + pr.slot, pr.phase, abort_flag, a.st, 916)) {
-          ok = false;
-          break;
-        }
-        uint4 c[2];
-        uint32_t sc[2];
+    pr.slot = pa.slot = team;  // at most the ring's depth
+    for (int i = team; i < squares; i += kTeams, pr.step(a.raw_stages, kTeams), pa.step(a.stages, kTeams)) {
+      if (!warp_wait(ctl.raw_full + pr.slot, pr.phase, abort_flag, a.st, 916)) break;
+      uint4 c[2];
+      uint32_t sc[2];
+      const uint32_t pair = raw_addr + pr.slot * gg::kPairBytes;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* tile = raw + pr.slot * gg::kPairBytes + (kBackward ? w >> 2 : h) * kTileBytes;
-          const int sb = kBackward ? 4 * h + (w & 3) : w;
-          c[h] = *reinterpret_cast<const uint4*>(tile + sb * 512 + slot * 16);
-          sc[h] = *reinterpret_cast<const uint16_t*>(tile + kTileCodes + sb * 64 + slot * 2);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ctl.raw_empty + pr.slot);
-        if (!mbar_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) {
-          ok = false;
-          break;
-        }
+      for (int h = 0; h < 2; ++h) {
+        c[h] = lds128(pair + h * (kBackward ? 4 * 512 : kTileBytes) + sub);
+        sc[h] = lds16(pair + h * (kBackward ? 4 * 64 : kTileBytes) + ssub);
+      }
+      // The packed slot goes back.  A read that is merely issued can be overtaken by the refill (measured: wrong
+      // 16-row groups), so the address of the arrival takes in what was read, masked by an argument that is zero.
+      const uint32_t seen = (c[0].x | c[0].y | c[0].z | c[0].w | c[1].x | c[1].y | c[1].z | c[1].w | sc[0] | sc[1]) & a.zero;
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + seen);
+      if (!warp_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
+      const uint32_t st = dst0 + (uint32_t)(pa.slot * stage_bytes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
-          const uint32_t p = ring_addr + (uint32_t)(pa.slot * stage_bytes + h * gg::kHalfBytes) + dst0;
-          uint32_t o[8];
-          dequant16_bf16(c[h].x, c[h].y, s2, o);
-          sts128(p + x0, o[0], o[1], o[2], o[3]);
-          sts128(p + x1, o[4], o[5], o[6], o[7]);
-          dequant16_bf16(c[h].z, c[h].w, s2 >> 16, o);
-          sts128(p + 1024u + x0, o[0], o[1], o[2], o[3]);
-          sts128(p + 1024u + x1, o[4], o[5], o[6], o[7]);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          if (kCtas == 2 && rank) mbar_arrive_cluster(map_rank(ctl.a_full + pa.slot, 0));
-          else mbar_arrive(ctl.a_full + pa.slot);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
+        const uint32_t p = st + h * gg::kHalfBytes;
+        uint32_t o[8];
+        dequant16_bf16(c[h].x, c[h].y, s2, o);
+        sts128(p + x0, o[0], o[1], o[2], o[3]);
+        sts128(p + x1, o[4], o[5], o[6], o[7]);
+        dequant16_bf16(c[h].z, c[h].w, s2 >> 16, o);
+        sts128(p + 1024u + x0, o[0], o[1], o[2], o[3]);
+        sts128(p + 1024u + x1, o[4], o[5], o[6], o[7]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + pa.slot * 8);
+        else mbar_arrive(ctl.full + pa.slot);
       }
     }
   } else if (warp >= 4) {
@@ -382,16 +387,17 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
     const int quarter = warp & 3;
     uint8_t* buf_s = smem + gg::kCtlBytes + quarter * gg::kEpiBytes;
     uint32_t j = 0;
-    for (int u = first; u < total; u += stride, ++j) {
-      const GroupedUnit w = grouped_unit<kCtas>(ctl, a, u);
+    for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total; w.next(ctl, total), ++j) {
+      int row0;
+      const int rows = w.rows(ctl, row0);
       const float gs = __ldg(a.gscale + w.e);
       const uint32_t buf = j & 1u;
-      if (!mbar_wait(ctl.acc_full + buf, (j >> 1) & 1u, abort_flag, a.st, 918)) break;
+      if (!warp_wait(ctl.acc_full + buf, (j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
       const uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * 256u;
-      const int f0 = 128 * (w.nb + rank) + 32 * quarter;  // beyond n_out for a block computed twice
+      const int f0 = 128 * (w.block() + rank) + 32 * quarter;  // beyond n_out for a block computed twice
       if (f0 < a.n_out) {
-        for (int col = 0; col < w.rows; col += 32) {
+        for (int col = 0; col < rows; col += 32) {
           uint32_t v[2][16];
           tmem_ld16_nw(t + (uint32_t)col, v[0]);
           tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);  // past the tile's last column: unwritten columns, not stored
@@ -407,8 +413,8 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int row = 4 * i + (lane >> 3), f = f0 + 4 * (lane & 7), rr = col + 16 * hh + row;
-                if (rr < w.rows && f < a.n_out)
-                  *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (long long)(w.row0 + rr) * a.ldo + f) =
+                if (rr < rows && f < a.n_out)
+                  *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (long long)(row0 + rr) * a.ldo + f) =
                       *reinterpret_cast<const uint4*>(buf_s + row * 128 + (lane & 7) * 16);
               }
             }
@@ -422,8 +428,8 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row = 8 * i + (lane >> 2), f = f0 + 8 * (lane & 3), rr = col + row;
-              if (rr < w.rows && f < a.n_out)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)(w.row0 + rr) * a.ldo + f) =
+              if (rr < rows && f < a.n_out)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)(row0 + rr) * a.ldo + f) =
                     *reinterpret_cast<const uint4*>(buf_s + row * 64 + (lane & 3) * 16);
             }
           }
@@ -449,9 +455,13 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
 }
 
 typedef void (*GroupedKernel)(const CUtensorMap, GroupedArgs);
-static GroupedKernel grouped_kernel(bool backward, bool pair) {
-  return backward ? (pair ? grouped_gemm_kernel<true, 2> : grouped_gemm_kernel<true, 1>)
-                  : (pair ? grouped_gemm_kernel<false, 2> : grouped_gemm_kernel<false, 1>);
+template <int kTeams>
+static GroupedKernel grouped_kernel_of(bool backward, bool pair) {
+  return backward ? (pair ? grouped_gemm_kernel<true, 2, kTeams> : grouped_gemm_kernel<true, 1, kTeams>)
+                  : (pair ? grouped_gemm_kernel<false, 2, kTeams> : grouped_gemm_kernel<false, 1, kTeams>);
+}
+static GroupedKernel grouped_kernel(bool backward, bool pair, int teams) {
+  return teams == 3 ? grouped_kernel_of<3>(backward, pair) : grouped_kernel_of<2>(backward, pair);
 }
 
 // The opt-in shared-memory size, once per device.
@@ -464,8 +474,8 @@ static cudaError_t set_grouped_attrs() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && dev < kCached && done[dev]) return cudaSuccess;
-  for (int i = 0; i < 4; ++i) {
-    e = cudaFuncSetAttribute((const void*)grouped_kernel(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+  for (int i = 0; i < 8; ++i) {
+    e = cudaFuncSetAttribute((const void*)grouped_kernel(i & 1, i & 2, 2 + (i >> 2)), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              gg::kSmemMax);
     if (e != cudaSuccess) return e;
   }
@@ -481,6 +491,14 @@ GroupedTiling grouped_tiling(int E, int R, int out_blocks) {
   const int avg = R / E;
   t.tile_rows = avg > 64 ? 256 : avg > 32 ? 128 : 64;
   t.box = t.tile_rows / t.ctas < 64 ? t.tile_rows / t.ctas : 64;
+  // three teams of dequantisers where weights are the bound, and their rings fit; see GroupedArgs for the depths
+  const int stage = 2 * gg::kHalfBytes + 2 * (t.tile_rows / t.ctas) * 128;
+  const int room = gg::kSmemMax - 1024 - gg::kRingOff;
+  t.teams = 3 * stage + 3 * gg::kPairBytes <= room ? 3 : 2;
+  t.stages = t.teams == 2 ? (room - 2 * gg::kPairBytes) / stage : 4 * stage + 6 * gg::kPairBytes <= room ? 4 : 3;
+  t.raw_stages = (room - t.stages * stage) / gg::kPairBytes;
+  if (t.raw_stages > gg::kMaxRaw) t.raw_stages = gg::kMaxRaw;
+  t.raw_stages -= t.raw_stages % t.teams;
   return t;
 }
 
@@ -510,14 +528,11 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   a.fault = p.fault;
   a.tile_rows = t.tile_rows;
   a.box = t.box;
-  const int stage = 2 * gg::kHalfBytes + 2 * (t.tile_rows / t.ctas) * 128;
-  const int room = gg::kSmemMax - 1024 - gg::kRingOff;
-  a.stages = stage > 49152 ? (room - 2 * gg::kPairBytes) / stage : 4;
-  const int left = (room - a.stages * stage) / gg::kPairBytes;
-  a.raw_stages = left < gg::kMaxRaw ? left : gg::kMaxRaw;
+  a.stages = t.stages;
+  a.raw_stages = t.raw_stages;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.num_sms / t.ctas * t.ctas));
-  cfg.blockDim = dim3(gg::kThreads);
+  cfg.blockDim = dim3(gg::threads(t.teams));
   cfg.dynamicSmemBytes = gg::kSmemMax;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
@@ -528,7 +543,7 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_kernel(backward, t.ctas == 2), rows_map, a);
+  return cudaLaunchKernelEx(&cfg, grouped_kernel(backward, t.ctas == 2, t.teams), rows_map, a);
 }
 
 }  // namespace nvfp4moe

@@ -19,6 +19,9 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
+  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(addr) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(smem_u32(bar)),
                "r"(bytes)
@@ -83,35 +86,10 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
 // which waits about 2000 cycles for every earlier access of the thread: what is
 // published this way is read by the tensor cores of the writer's own
 // multiprocessor (its operand, behind fence.proxy.async) or is tensor memory
-// that tcgen05.fence orders.
+// that tcgen05.fence orders.  The waits on such barriers are plain ones for the same
+// reason: a cluster-scope acquire invalidates the L1 cache each time.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait for a barrier that the other CTA of the pair arrives at too.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                                  DeviceStatus* st, unsigned where) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 0;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 63u) == 63u) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
-        *abort_flag = 1;
-        report(st, kFlagTimeout, where);
-        return false;
-      }
-    }
-  }
 }
 // tma_2d whose bytes complete on a barrier of either CTA of the pair (cluster address).
 __device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -138,6 +116,18 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// mbar_wait by a whole warp: one answer for all lanes, and they come out together, as .aligned instructions need.
+// The waiting itself is out of line, so that the usual case is a test and a vote.
+[[maybe_unused]] static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st,
+                                            unsigned where) {
+  return mbar_wait(bar, parity, abort_flag, st, where);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st,
+                                          unsigned where) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_slow(bar, parity, abort_flag, st, where));
+}
+
 // True in one lane of a converged warp.  A loop that the whole warp runs, with
 // this around the instructions that one thread issues, keeps descriptors and
 // addresses in uniform registers; under `lane == 0` they are moved there one
@@ -152,8 +142,9 @@ __device__ __forceinline__ bool elect_one() {
 struct RingPos {
   int slot = 0;
   uint32_t phase = 0;
-  __device__ __forceinline__ void step(int n) {
-    if (++slot == n) slot = 0, phase ^= 1u;
+  __device__ __forceinline__ void step(int n, int by = 1) {  // by <= n
+    slot += by;
+    if (slot >= n) slot -= n, phase ^= 1u;
   }
 };
 
@@ -231,6 +222,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
