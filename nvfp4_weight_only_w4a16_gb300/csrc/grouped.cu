@@ -21,7 +21,7 @@
 // to pair with.
 //
 // One CTA per multiprocessor, 24 or 32 warps: 0 packed-weight producer (bulk copies into
-// a ring), 1 MMA issuer (the pair's first CTA), 2 row producer (TMA, zero fill past
+// a ring), 1 MMA issuer (the pair's first CTA; for narrow tiles 3 too), 2 row producer (TMA, zero fill past
 // the matrix), 4-7 epilogue (TMEM -> gs -> shared -> 16-byte stores), the
 // rest dequantisers, in two or three teams of 8 that take turns.  Two accumulator buffers of 256
 // columns: the epilogue of a unit overlaps the next one's MMAs.  The row offsets
@@ -37,14 +37,38 @@ namespace nvfp4moe {
 
 namespace gg {
 constexpr int kTeamWarps = 8, kEpiWarps = 4;
-__host__ __device__ constexpr int threads(int teams) { return 32 * (8 + teams * kTeamWarps); }
 constexpr int kPairBytes = 2 * kTileBytes;  // one 128 x 128 weight square, packed
 constexpr int kHalfBytes = 16384;           // half a square in BF16: 64 long in the reduction
-constexpr int kMaxStages = 6, kMaxRaw = 16;
 constexpr int kSmemMax = 232448;
 constexpr int kCtlBytes = 4096;             // tables and barriers in front of the rings
 constexpr int kEpiBytes = 2048;             // per epilogue warp
 constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
+constexpr int kRoom = kSmemMax - 1024 - kRingOff;  // for the rings
+
+// What follows from the CTAs of a unit (1 or 2) and the rows of a token tile (64, 128 or 256): MMA issuers, teams of
+// dequantisers, ring depths.  With up to 64 rows the MMAs are so short that issuing them sets the pace, so two warps
+// take turns at the steps, each into an accumulator of its own.  Three teams where their packed slots fit, else two.
+// A parity wait must not run two phases ahead of its barrier: a team meets every packed slot again itself (their
+// number is a multiple of the teams; bulk copies may land out of order); one issuer frees the operand stages in order,
+// so that as many stages as teams are enough for them; with two, the issuers and teams too must meet their own stages
+// again.
+template <int kCtas, int kTile>
+struct Plan {
+  static constexpr int kBHalf = kTile / kCtas * 128;             // half a stage's rows: this CTA's share of the tile
+  static constexpr int kStage = 2 * kHalfBytes + 2 * kBHalf;     // the operand's two halves, then the rows'
+  static constexpr int kIssuers = kCtas == 2 && kTile == 64 ? 2 : 1;
+  static constexpr int kTeams = kIssuers == 1 && 3 * kStage + 3 * kPairBytes <= kRoom ? 3 : 2;
+  static constexpr int kStages = kIssuers == 2 ? 4
+                                 : kTeams == 2 ? (kRoom - 2 * kPairBytes) / kStage
+                                 : 4 * kStage + 6 * kPairBytes <= kRoom ? 4 : 3;
+  static constexpr int kRaw = (kRoom - kStages * kStage) / kPairBytes / kTeams * kTeams;  // packed slots
+  static constexpr int kThreads = 32 * (8 + kTeams * kTeamWarps);
+  static constexpr int kBox = kTile / kCtas < 64 ? kTile / kCtas : 64;  // rows per TMA box
+  static_assert(kStages >= kTeams && kRaw >= kTeams && kRaw % kTeams == 0 && kStages * kStage + kRaw * kPairBytes <= kRoom, "rings");
+  static_assert(kIssuers == 1 || (kStages % 2 == 0 && kStages % kTeams == 0 && kTile <= 128), "two issuers");
+  static_assert(kStage % 1024 == 0 && kBHalf % 1024 == 0, "128B-swizzled tiles");
+};
+constexpr int kMaxStages = 4, kMaxRaw = 6;
 }  // namespace gg
 
 struct GroupedArgs {
@@ -62,12 +86,6 @@ struct GroupedArgs {
   void* out;
   long long ldo;
   int out_f32;
-  int tile_rows;           // rows per token tile, a multiple of 64 up to 256
-  int box;                 // rows per TMA box, divides tile_rows / kCtas
-  // ring depths.  A parity wait must not run two phases ahead: a team meets every raw slot again itself (raw_stages
-  // is a multiple of the teams; bulk copies may land out of order); the operand stages are freed in order, so that
-  // as many stages as teams are enough for them
-  int stages, raw_stages;
   DeviceStatus* st;
   int fault;
   uint32_t zero;           // 0, unknown to the compiler
@@ -146,17 +164,17 @@ __device__ __forceinline__ void dequant16_bf16(uint32_t c0, uint32_t c1, uint32_
   for (int i = 0; i < 4; ++i) o[4 + i] = scaled_pair_bf16(v[i], s);
 }
 
-template <bool kBackward, int kCtas, int kTeams>
-__global__ void __launch_bounds__(gg::threads(kTeams), 1)
+template <bool kBackward, int kCtas, int kTile>
+__global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap, GroupedArgs a) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   GroupedCtl& ctl = *reinterpret_cast<GroupedCtl*>(smem);
   uint8_t* ring = smem + gg::kRingOff;
-  // a stage: the operand's two halves, then the rows' two halves (this CTA's share of the tile)
-  const int b_half = a.tile_rows / kCtas * 128;
-  const int stage_bytes = 2 * gg::kHalfBytes + 2 * b_half;
-  uint8_t* raw = ring + a.stages * stage_bytes;
+  using Plan = gg::Plan<kCtas, kTile>;
+  constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kStages = Plan::kStages, kRaw = Plan::kRaw;
+  static_assert(kStages <= gg::kMaxStages && kRaw <= gg::kMaxRaw, "barriers");
+  uint8_t* raw = ring + kStages * Plan::kStage;
   const uint32_t ring_addr = smem_u32(ring), raw_addr = smem_u32(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
@@ -165,16 +183,16 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
   volatile int* abort_flag = &ctl.abort_flag;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.raw_stages; ++s) {
+    for (int s = 0; s < kRaw; ++s) {
       mbar_init(ctl.raw_full + s, 1);
       mbar_init(ctl.raw_empty + s, gg::kTeamWarps);
     }
-    for (int s = 0; s < a.stages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(ctl.full + s, kCtas * gg::kTeamWarps + 1);  // waited for by the pair's first CTA
       mbar_init(ctl.empty + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(ctl.acc_full + b, 1);
+      mbar_init(ctl.acc_full + b, kIssuers);
       mbar_init(ctl.acc_empty + b, kCtas * gg::kEpiWarps);
     }
     ctl.abort_flag = 0;
@@ -195,7 +213,7 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int i = threadIdx.x; i <= a.E; i += gg::threads(kTeams)) ctl.off[i] = a.offsets[i];
+  for (int i = threadIdx.x; i <= a.E; i += Plan::kThreads) ctl.off[i] = a.offsets[i];
   __syncthreads();
   if (warp == 0) {  // token tiles per expert, 8 experts a lane; offsets that do not ascend within 0..R give no tile
     int n[8], sum = 0;
@@ -205,7 +223,7 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
       const int e = 8 * lane + i;
       const int m = e < a.E ? ctl.off[e + 1] - ctl.off[e] : 0;
       bad |= e < a.E && ctl.off[e + 1] < ctl.off[e];
-      n[i] = (m + a.tile_rows - 1) / a.tile_rows;
+      n[i] = (m + kTile - 1) / kTile;
       if (e < a.E && n[i] > 0) ctl.per[e] = (short)(((m + n[i] - 1) / n[i] + kRound - 1) & ~(kRound - 1));
       sum += n[i];
     }
@@ -244,7 +262,7 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
         // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
         const int nb = min(w.block() + rank, a.NB - 1);
         const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)nb * a.block_stride;
-        for (int s = 0; s < a.steps; ++s, ++it, p.step(a.raw_stages), src += a.step_stride) {
+        for (int s = 0; s < a.steps; ++s, ++it, p.step(kRaw), src += a.step_stride) {
           if (!mbar_wait(ctl.raw_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 911)) {
             ok = false;
             break;
@@ -253,51 +271,56 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
           bulk_g2s(raw + p.slot * gg::kPairBytes, src, gg::kPairBytes, ctl.raw_full + p.slot);
         }
       }
-      if (!ok) drain_copies(ctl.raw_full, it, a.raw_stages);
+      if (!ok) drain_copies(ctl.raw_full, it, kRaw);
     }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer: the whole warp walks the loop, one lane issues.  Every instruction here counts:
-    // the loop shares its scheduler with four dequantisers ----------------
+  } else if (warp == 1 || (kIssuers == 2 && warp == 3)) {
+    // ---------------- MMA issuers: the whole warp walks the loop, one lane issues.  Issuer h takes every kIssuers-th
+    // square of the CTA's sequence, into its own accumulator ----------------
     if (rank == 0) {
+      const int h = warp >> 1;  // 0, 1
       uint32_t j = 0;
-      RingPos p;
+      int base = 0;  // squares before the unit
       bool ok = true;
-      for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok; w.next(ctl, total), ++j) {
+      for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok; w.next(ctl, total), ++j, base += a.steps) {
         int row0;
         const uint32_t idesc =
             idesc_bf16(128 * kCtas, (w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) | (kBackward ? 1u << 15 : 0u);
         const uint32_t buf = j & 1u;
         if (!warp_wait(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * 256u;
+        const uint32_t d = tmem + buf * 256u + (uint32_t)h * 128u;
+        const int end = base + a.steps;
         uint32_t acc = 0;
-        for (int s = a.steps; s > 0; --s, p.step(a.stages)) {
-          if (!warp_wait(ctl.full + p.slot, p.phase, abort_flag, a.st, 913)) {
+        for (int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base; i < end; i += kIssuers) {
+          const int slot = i % kStages;
+          if (!warp_wait(ctl.full + slot, (uint32_t)(i / kStages) & 1u, abort_flag, a.st, 913)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = ring_addr + (uint32_t)(p.slot * stage_bytes);
+          const uint32_t st = ring_addr + (uint32_t)(slot * Plan::kStage);
           const uint64_t ad = kBackward ? sw128_desc_mn(st) : sw128_desc(st);
           const uint64_t bd = sw128_desc(st + 2 * gg::kHalfBytes);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
               const uint64_t ak = ad + (uint32_t)(kk >> 2) * (gg::kHalfBytes >> 4) + (kBackward ? 128u : 2u) * (kk & 3);
-              const uint64_t bk = bd + (uint32_t)(kk >> 2) * (uint32_t)(b_half >> 4) + 2u * (kk & 3);
+              const uint64_t bk = bd + (uint32_t)(kk >> 2) * (uint32_t)(Plan::kBHalf >> 4) + 2u * (kk & 3);
               if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, kk ? 1u : acc);
               else umma_bf16(d, ak, bk, idesc, kk ? 1u : acc);
             }
-            if (kCtas == 2) umma_commit_pair(ctl.empty + p.slot);
-            else umma_commit(ctl.empty + p.slot);
-            if (s == 1) {
-              if (kCtas == 2) umma_commit_pair(ctl.acc_full + buf);
-              else umma_commit(ctl.acc_full + buf);
-            }
+            if (kCtas == 2) umma_commit_pair(ctl.empty + slot);
+            else umma_commit(ctl.empty + slot);
           }
           acc = 1;
           __syncwarp();
         }
+        if (!ok) break;
+        if (elect_one()) {  // (an issuer without a square in the unit: nothing to wait for, and its accumulator is not read)
+          if (kCtas == 2) umma_commit_pair(ctl.acc_full + buf);
+          else umma_commit(ctl.acc_full + buf);
+        }
+        __syncwarp();
       }
     }
   } else if (warp == 2) {
@@ -307,23 +330,23 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
     for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok && a.fault != 1; w.next(ctl, total)) {
       int row0;
       const int share = ((w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) / kCtas;
-      const int nbox = (share + a.box - 1) / a.box;
+      const int nbox = (share + Plan::kBox - 1) / Plan::kBox;
       row0 += rank * share;
-      for (int s = 0; s < a.steps; ++s, p.step(a.stages)) {
+      for (int s = 0; s < a.steps; ++s, p.step(kStages)) {
         if (!warp_wait(ctl.empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 915)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          uint8_t* dst = ring + p.slot * stage_bytes + 2 * gg::kHalfBytes;
+          uint8_t* dst = ring + p.slot * Plan::kStage + 2 * gg::kHalfBytes;
           uint64_t* bar = ctl.full + p.slot;
-          if (rank == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kCtas * 2 * nbox * a.box) * 128u);
+          if (rank == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kCtas * 2 * nbox * Plan::kBox) * 128u);
           const uint32_t bar0 = kCtas == 2 ? map_rank(bar, 0) : 0u;
           for (int h = 0; h < 2; ++h)
             for (int b = 0; b < nbox; ++b) {
-              uint8_t* to = dst + h * b_half + b * a.box * 128;
-              if (kCtas == 2) tma_2d_pair(to, &tmap, s * 128 + h * 64, row0 + b * a.box, bar0);
-              else tma_2d(to, &tmap, s * 128 + h * 64, row0 + b * a.box, bar);
+              uint8_t* to = dst + h * Plan::kBHalf + b * Plan::kBox * 128;
+              if (kCtas == 2) tma_2d_pair(to, &tmap, s * 128 + h * 64, row0 + b * Plan::kBox, bar0);
+              else tma_2d(to, &tmap, s * 128 + h * 64, row0 + b * Plan::kBox, bar);
             }
         }
         __syncwarp();
@@ -345,7 +368,7 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
     const uint32_t full0 = kCtas == 2 ? map_rank(ctl.full, 0) : 0u;  // the pair's first CTA's
     RingPos pr, pa;
     pr.slot = pa.slot = team;  // at most the ring's depth
-    for (int i = team; i < squares; i += kTeams, pr.step(a.raw_stages, kTeams), pa.step(a.stages, kTeams)) {
+    for (int i = team; i < squares; i += kTeams, pr.step(kRaw, kTeams), pa.step(kStages, kTeams)) {
       if (!warp_wait(ctl.raw_full + pr.slot, pr.phase, abort_flag, a.st, 916)) break;
       uint4 c[2];
       uint32_t sc[2];
@@ -361,7 +384,7 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + seen);
       if (!warp_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
-      const uint32_t st = dst0 + (uint32_t)(pa.slot * stage_bytes);
+      const uint32_t st = dst0 + (uint32_t)(pa.slot * Plan::kStage);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
@@ -394,14 +417,27 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
       const uint32_t buf = j & 1u;
       if (!warp_wait(ctl.acc_full + buf, (j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
-      const uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * 256u;
+      uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * 256u;
+      if (kIssuers == 2 && a.steps == 1) t += (j & 1u) * 128u;  // unit j's only square is the CTA's j-th
       const int f0 = 128 * (w.block() + rank) + 32 * quarter;  // beyond n_out for a block computed twice
       if (f0 < a.n_out) {
         for (int col = 0; col < rows; col += 32) {
           uint32_t v[2][16];
+          if (kIssuers == 2 && a.steps > 1) {  // the sum of both issuers' accumulators
+            uint32_t v1[2][16];
+            tmem_ld16_nw(t + (uint32_t)col, v[0]);
+            tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);
+            tmem_ld16_nw(t + (uint32_t)col + 128u, v1[0]);
+            tmem_ld16_nw(t + (uint32_t)col + 144u, v1[1]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i >> 4][i & 15] = __float_as_uint(__uint_as_float(v[i >> 4][i & 15]) + __uint_as_float(v1[i >> 4][i & 15]));
+          } else {
           tmem_ld16_nw(t + (uint32_t)col, v[0]);
           tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);  // past the tile's last column: unwritten columns, not stored
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          }
           if (a.out_f32) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
@@ -455,14 +491,17 @@ __global__ void __launch_bounds__(gg::threads(kTeams), 1)
 }
 
 typedef void (*GroupedKernel)(const CUtensorMap, GroupedArgs);
-template <int kTeams>
-static GroupedKernel grouped_kernel_of(bool backward, bool pair) {
-  return backward ? (pair ? grouped_gemm_kernel<true, 2, kTeams> : grouped_gemm_kernel<true, 1, kTeams>)
-                  : (pair ? grouped_gemm_kernel<false, 2, kTeams> : grouped_gemm_kernel<false, 1, kTeams>);
+struct GroupedVariant {
+  GroupedKernel fn[2];  // forward, backward
+  int ctas, tile_rows, threads, box;
+};
+template <int kCtas, int kTile>
+static constexpr GroupedVariant grouped_variant() {
+  using Plan = gg::Plan<kCtas, kTile>;
+  return {{grouped_gemm_kernel<false, kCtas, kTile>, grouped_gemm_kernel<true, kCtas, kTile>}, kCtas, kTile, Plan::kThreads, Plan::kBox};
 }
-static GroupedKernel grouped_kernel(bool backward, bool pair, int teams) {
-  return teams == 3 ? grouped_kernel_of<3>(backward, pair) : grouped_kernel_of<2>(backward, pair);
-}
+static const GroupedVariant kGroupedVariants[] = {grouped_variant<1, 64>(), grouped_variant<1, 128>(), grouped_variant<1, 256>(),
+                                                  grouped_variant<2, 64>(), grouped_variant<2, 128>(), grouped_variant<2, 256>()};
 
 // The opt-in shared-memory size, once per device.
 static cudaError_t set_grouped_attrs() {
@@ -474,8 +513,8 @@ static cudaError_t set_grouped_attrs() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && dev < kCached && done[dev]) return cudaSuccess;
-  for (int i = 0; i < 8; ++i) {
-    e = cudaFuncSetAttribute((const void*)grouped_kernel(i & 1, i & 2, 2 + (i >> 2)), cudaFuncAttributeMaxDynamicSharedMemorySize,
+  for (int i = 0; i < 12; ++i) {
+    e = cudaFuncSetAttribute((const void*)kGroupedVariants[i >> 1].fn[i & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
                              gg::kSmemMax);
     if (e != cudaSuccess) return e;
   }
@@ -484,21 +523,12 @@ static cudaError_t set_grouped_attrs() {
 }
 
 GroupedTiling grouped_tiling(int E, int R, int out_blocks) {
-  GroupedTiling t;
-  t.ctas = out_blocks > 1 ? 2 : 1;
-  // rows per token tile: wide tiles dequantise a weight square once for many rows, narrow ones leave
-  // shared memory for a deeper packed ring, which the few-rows end needs to stream weights
+  // pairs where there are two feature blocks to pair; rows per token tile: wide tiles dequantise a weight square
+  // once for many rows, narrow ones leave shared memory for deeper rings, which the few-rows end needs
   const int avg = R / E;
-  t.tile_rows = avg > 64 ? 256 : avg > 32 ? 128 : 64;
-  t.box = t.tile_rows / t.ctas < 64 ? t.tile_rows / t.ctas : 64;
-  // three teams of dequantisers where weights are the bound, and their rings fit; see GroupedArgs for the depths
-  const int stage = 2 * gg::kHalfBytes + 2 * (t.tile_rows / t.ctas) * 128;
-  const int room = gg::kSmemMax - 1024 - gg::kRingOff;
-  t.teams = 3 * stage + 3 * gg::kPairBytes <= room ? 3 : 2;
-  t.stages = t.teams == 2 ? (room - 2 * gg::kPairBytes) / stage : 4 * stage + 6 * gg::kPairBytes <= room ? 4 : 3;
-  t.raw_stages = (room - t.stages * stage) / gg::kPairBytes;
-  if (t.raw_stages > gg::kMaxRaw) t.raw_stages = gg::kMaxRaw;
-  t.raw_stages -= t.raw_stages % t.teams;
+  GroupedTiling t;
+  t.variant = (out_blocks > 1 ? 3 : 0) + (avg > 64 ? 2 : avg > 32 ? 1 : 0);
+  t.box = kGroupedVariants[t.variant].box;
   return t;
 }
 
@@ -516,7 +546,8 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   a.E = p.E;
   a.R = p.R;
   a.NB = backward ? p.K / 128 : Np / 128;
-  a.NU = (a.NB + t.ctas - 1) / t.ctas;
+  const GroupedVariant& v = kGroupedVariants[t.variant];
+  a.NU = (a.NB + v.ctas - 1) / v.ctas;
   a.steps = backward ? Np / 128 : p.K / 128;
   a.block_stride = backward ? (size_t)gg::kPairBytes : row_block;
   a.step_stride = backward ? row_block : (size_t)gg::kPairBytes;
@@ -526,24 +557,20 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   a.out_f32 = p.out_f32;
   a.st = p.status;
   a.fault = p.fault;
-  a.tile_rows = t.tile_rows;
-  a.box = t.box;
-  a.stages = t.stages;
-  a.raw_stages = t.raw_stages;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.num_sms / t.ctas * t.ctas));
-  cfg.blockDim = dim3(gg::threads(t.teams));
+  cfg.gridDim = dim3((unsigned)(p.num_sms / v.ctas * v.ctas));
+  cfg.blockDim = dim3(v.threads);
   cfg.dynamicSmemBytes = gg::kSmemMax;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)t.ctas;
+  at[0].val.clusterDim.x = (unsigned)v.ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_kernel(backward, t.ctas == 2, t.teams), rows_map, a);
+  return cudaLaunchKernelEx(&cfg, v.fn[backward], rows_map, a);
 }
 
 }  // namespace nvfp4moe

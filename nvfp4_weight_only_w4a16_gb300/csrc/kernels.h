@@ -180,12 +180,8 @@ struct GroupedProduct {
 };
 // How launch_grouped_gemm cuts a product whose output has out_blocks blocks of 128 features.
 struct GroupedTiling {
-  int ctas;       // 2: pairs of CTAs on 256 features, 1: single ones
-  int tile_rows;  // rows per tile
-  int box;        // rows per TMA box
-  int teams;      // of dequantisers, 2 or 3
-  int stages;     // operand stages
-  int raw_stages; // packed ring
+  int variant;  // of the kernel: CTAs per unit and rows per token tile
+  int box;      // rows per TMA box
 };
 GroupedTiling grouped_tiling(int E, int R, int out_blocks);
 // rows_map: in as [R][K or N] BF16, box {64, tiling.box}, 128B swizzle.
