@@ -43,6 +43,7 @@ constexpr int kSmemMax = 232448;
 constexpr int kCtlBytes = 4096;             // tables and barriers in front of the rings
 constexpr int kEpiBytes = 2048;             // per epilogue warp
 constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
+constexpr int kMaxStages = 4, kMaxRaw = 20;
 constexpr int kRoom = kSmemMax - 1024 - kRingOff;  // for the rings
 
 // What follows from the CTAs of a unit (1 or 2) and the rows of a token tile (64, 128 or 256): MMA issuers, teams of
@@ -52,23 +53,32 @@ constexpr int kRoom = kSmemMax - 1024 - kRingOff;  // for the rings
 // number is a multiple of the teams; bulk copies may land out of order); one issuer frees the operand stages in order,
 // so that as many stages as teams are enough for them; with two, the issuers and teams too must meet their own stages
 // again.
-template <int kCtas, int kTile>
+//
+// The forward's operand goes to tensor memory where that has room beside the accumulators, that is for tiles of up to
+// 128 rows: with the operand in shared memory its bandwidth is the bound there (per square 256 of 128-byte accesses to
+// write it, 256 to read it, and 400 for the rest, against some 390 cycles that the packed bytes take from memory; 64
+// rows an expert, E 128, N 1536, K 4096: 150 us).  The transposed operand would have to cross the lanes to get there.
+template <bool kBackward, int kCtas, int kTile>
 struct Plan {
+  static constexpr bool kTmemA = !kBackward && kCtas == 2 && kTile <= 128;
   static constexpr int kBHalf = kTile / kCtas * 128;             // half a stage's rows: this CTA's share of the tile
-  static constexpr int kStage = 2 * kHalfBytes + 2 * kBHalf;     // the operand's two halves, then the rows'
+  static constexpr int kStageA = kTmemA ? 0 : 2 * kHalfBytes;
+  static constexpr int kStage = kStageA + 2 * kBHalf;            // the operand's two halves, then the rows'
   static constexpr int kIssuers = kCtas == 2 && kTile == 64 ? 2 : 1;
-  static constexpr int kTeams = kIssuers == 1 && 3 * kStage + 3 * kPairBytes <= kRoom ? 3 : 2;
-  static constexpr int kStages = kIssuers == 2 ? 4
+  static constexpr int kTeams = !kTmemA && kIssuers == 1 && 3 * kStage + 3 * kPairBytes <= kRoom ? 3 : 2;
+  static constexpr int kStages = kTmemA || kIssuers == 2 ? 4
                                  : kTeams == 2 ? (kRoom - 2 * kPairBytes) / kStage
                                  : 4 * kStage + 6 * kPairBytes <= kRoom ? 4 : 3;
-  static constexpr int kRaw = (kRoom - kStages * kStage) / kPairBytes / kTeams * kTeams;  // packed slots
+  static constexpr int kFit = (kRoom - kStages * kStage) / kPairBytes;
+  static constexpr int kRaw = (kFit < kMaxRaw ? kFit : kMaxRaw) / kTeams * kTeams;  // packed slots
+  // tensor memory: buffer b, issuer h at b kAccBuf + h kAccIssuer; operand stages of 64 columns from kOperand on
+  static constexpr uint32_t kAccBuf = kTmemA ? 128 : 256, kAccIssuer = kAccBuf / 2, kOperand = 256;
   static constexpr int kThreads = 32 * (8 + kTeams * kTeamWarps);
   static constexpr int kBox = kTile / kCtas < 64 ? kTile / kCtas : 64;  // rows per TMA box
   static_assert(kStages >= kTeams && kRaw >= kTeams && kRaw % kTeams == 0 && kStages * kStage + kRaw * kPairBytes <= kRoom, "rings");
   static_assert(kIssuers == 1 || (kStages % 2 == 0 && kStages % kTeams == 0 && kTile <= 128), "two issuers");
   static_assert(kStage % 1024 == 0 && kBHalf % 1024 == 0, "128B-swizzled tiles");
 };
-constexpr int kMaxStages = 4, kMaxRaw = 6;
 }  // namespace gg
 
 struct GroupedArgs {
@@ -164,14 +174,28 @@ __device__ __forceinline__ void dequant16_bf16(uint32_t c0, uint32_t c1, uint32_
   for (int i = 0; i < 4; ++i) o[4 + i] = scaled_pair_bf16(v[i], s);
 }
 
+// 32 registers into 32 columns of the thread's lane, waited for.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&o)[4][8]) {
+  const uint32_t* w = o[0];
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]), "r"(w[17]), "r"(w[18]),
+      "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]),
+      "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 template <bool kBackward, int kCtas, int kTile>
-__global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
+__global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap, GroupedArgs a) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   GroupedCtl& ctl = *reinterpret_cast<GroupedCtl*>(smem);
   uint8_t* ring = smem + gg::kRingOff;
-  using Plan = gg::Plan<kCtas, kTile>;
+  using Plan = gg::Plan<kBackward, kCtas, kTile>;
   constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kStages = Plan::kStages, kRaw = Plan::kRaw;
   static_assert(kStages <= gg::kMaxStages && kRaw <= gg::kMaxRaw, "barriers");
   uint8_t* raw = ring + kStages * Plan::kStage;
@@ -288,7 +312,7 @@ __global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
         const uint32_t buf = j & 1u;
         if (!warp_wait(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * 256u + (uint32_t)h * 128u;
+        const uint32_t d = tmem + buf * Plan::kAccBuf + (uint32_t)h * Plan::kAccIssuer;
         const int end = base + a.steps;
         uint32_t acc = 0;
         for (int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base; i < end; i += kIssuers) {
@@ -300,13 +324,15 @@ __global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
           tc_fence_after();
           const uint32_t st = ring_addr + (uint32_t)(slot * Plan::kStage);
           const uint64_t ad = kBackward ? sw128_desc_mn(st) : sw128_desc(st);
-          const uint64_t bd = sw128_desc(st + 2 * gg::kHalfBytes);
+          const uint64_t bd = sw128_desc(st + Plan::kStageA);
+          const uint32_t at = tmem + Plan::kOperand + (uint32_t)slot * 64u;  // 8 columns per 16 elements
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
               const uint64_t ak = ad + (uint32_t)(kk >> 2) * (gg::kHalfBytes >> 4) + (kBackward ? 128u : 2u) * (kk & 3);
               const uint64_t bk = bd + (uint32_t)(kk >> 2) * (uint32_t)(Plan::kBHalf >> 4) + 2u * (kk & 3);
-              if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, kk ? 1u : acc);
+              if (Plan::kTmemA) umma_ts_pair(d, at + 8u * kk, bk, idesc, kk ? 1u : acc);
+              else if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, kk ? 1u : acc);
               else umma_bf16(d, ak, bk, idesc, kk ? 1u : acc);
             }
             if (kCtas == 2) umma_commit_pair(ctl.empty + slot);
@@ -338,7 +364,7 @@ __global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
           break;
         }
         if (elect_one()) {
-          uint8_t* dst = ring + p.slot * Plan::kStage + 2 * gg::kHalfBytes;
+          uint8_t* dst = ring + p.slot * Plan::kStage + Plan::kStageA;
           uint64_t* bar = ctl.full + p.slot;
           if (rank == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kCtas * 2 * nbox * Plan::kBox) * 128u);
           const uint32_t bar0 = kCtas == 2 ? map_rank(bar, 0) : 0u;
@@ -365,39 +391,65 @@ __global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
     const uint32_t sub = (uint32_t)(kBackward ? (w >> 2) * kTileBytes + (w & 3) * 512 : w * 512) + seg_pos(lane) * 16;
     const uint32_t ssub = (uint32_t)(kBackward ? (w >> 2) * kTileBytes + (w & 3) * 64 : w * 64) + kTileCodes + seg_pos(lane) * 2;
     const uint32_t raw_empty0 = smem_u32(ctl.raw_empty);
+    // tensor-memory operand: the thread's row in a packed square, and its place in an operand stage
+    const int tr = 32 * (w & 3) + lane;
+    const uint32_t row_c = (uint32_t)((w >> 2) * kTileBytes + (tr >> 4) * 512 + ((tr >> 3) & 1) * 8);
+    const uint32_t row_s = (uint32_t)((w >> 2) * kTileBytes + kTileCodes + (tr >> 4) * 64 + ((tr >> 3) & 1));
+    const uint32_t t_row = tmem + ((uint32_t)(32 * (w & 3)) << 16) + Plan::kOperand + 32u * (uint32_t)(w >> 2);
     const uint32_t full0 = kCtas == 2 ? map_rank(ctl.full, 0) : 0u;  // the pair's first CTA's
     RingPos pr, pa;
     pr.slot = pa.slot = team;  // at most the ring's depth
     for (int i = team; i < squares; i += kTeams, pr.step(kRaw, kTeams), pa.step(kStages, kTeams)) {
       if (!warp_wait(ctl.raw_full + pr.slot, pr.phase, abort_flag, a.st, 916)) break;
-      uint4 c[2];
-      uint32_t sc[2];
       const uint32_t pair = raw_addr + pr.slot * gg::kPairBytes;
+      if constexpr (Plan::kTmemA) {
+        // thread = one weight row of half w / 4, which is its TMEM lane: groups of 16 elements, 8 bytes and a scale each
+        uint2 c[4];
+        uint32_t sc[4], seen = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        c[h] = lds128(pair + h * (kBackward ? 4 * 512 : kTileBytes) + sub);
-        sc[h] = lds16(pair + h * (kBackward ? 4 * 64 : kTileBytes) + ssub);
-      }
-      // The packed slot goes back.  A read that is merely issued can be overtaken by the refill (measured: wrong
-      // 16-row groups), so the address of the arrival takes in what was read, masked by an argument that is zero.
-      const uint32_t seen = (c[0].x | c[0].y | c[0].z | c[0].w | c[1].x | c[1].y | c[1].z | c[1].w | sc[0] | sc[1]) & a.zero;
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + seen);
-      if (!warp_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
-      const uint32_t st = dst0 + (uint32_t)(pa.slot * Plan::kStage);
+        for (int g = 0; g < 4; ++g) {
+          c[g] = lds64(pair + row_c + (uint32_t)(seg_pos(4 * (lane & 7) + g) * 16));
+          sc[g] = lds8(pair + row_s + (uint32_t)(seg_pos(4 * (lane & 7) + g) * 2));
+          seen |= c[g].x | c[g].y | sc[g];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + (seen & a.zero));  // see below
+        if (!warp_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
+        tc_fence_after();
+        uint32_t o[4][8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
-        const uint32_t p = st + h * gg::kHalfBytes;
-        uint32_t o[8];
-        dequant16_bf16(c[h].x, c[h].y, s2, o);
-        sts128(p + x0, o[0], o[1], o[2], o[3]);
-        sts128(p + x1, o[4], o[5], o[6], o[7]);
-        dequant16_bf16(c[h].z, c[h].w, s2 >> 16, o);
-        sts128(p + 1024u + x0, o[0], o[1], o[2], o[3]);
-        sts128(p + 1024u + x1, o[4], o[5], o[6], o[7]);
+        for (int g = 0; g < 4; ++g) dequant16_bf16(c[g].x, c[g].y, e4m3x2_to_f16x2(sc[g]), o[g]);
+        tmem_st32(t_row + (uint32_t)pa.slot * 64u, o);
+        tc_fence_before();
+      } else {
+        uint4 c[2];
+        uint32_t sc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          c[h] = lds128(pair + h * (kBackward ? 4 * 512 : kTileBytes) + sub);
+          sc[h] = lds16(pair + h * (kBackward ? 4 * 64 : kTileBytes) + ssub);
+        }
+        // The packed slot goes back.  A read that is merely issued can be overtaken by the refill (measured: wrong
+        // 16-row groups), so the address of the arrival takes in what was read, masked by an argument that is zero.
+        const uint32_t seen = (c[0].x | c[0].y | c[0].z | c[0].w | c[1].x | c[1].y | c[1].z | c[1].w | sc[0] | sc[1]) & a.zero;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + seen);
+        if (!warp_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
+        const uint32_t st = dst0 + (uint32_t)(pa.slot * Plan::kStage);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
+          const uint32_t p = st + h * gg::kHalfBytes;
+          uint32_t o[8];
+          dequant16_bf16(c[h].x, c[h].y, s2, o);
+          sts128(p + x0, o[0], o[1], o[2], o[3]);
+          sts128(p + x1, o[4], o[5], o[6], o[7]);
+          dequant16_bf16(c[h].z, c[h].w, s2 >> 16, o);
+          sts128(p + 1024u + x0, o[0], o[1], o[2], o[3]);
+          sts128(p + 1024u + x1, o[4], o[5], o[6], o[7]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
         if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + pa.slot * 8);
@@ -417,8 +469,8 @@ __global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
       const uint32_t buf = j & 1u;
       if (!warp_wait(ctl.acc_full + buf, (j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
-      uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * 256u;
-      if (kIssuers == 2 && a.steps == 1) t += (j & 1u) * 128u;  // unit j's only square is the CTA's j-th
+      uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * Plan::kAccBuf;
+      if (kIssuers == 2 && a.steps == 1) t += (j & 1u) * Plan::kAccIssuer;  // unit j's only square is the CTA's j-th
       const int f0 = 128 * (w.block() + rank) + 32 * quarter;  // beyond n_out for a block computed twice
       if (f0 < a.n_out) {
         for (int col = 0; col < rows; col += 32) {
@@ -427,8 +479,8 @@ __global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
             uint32_t v1[2][16];
             tmem_ld16_nw(t + (uint32_t)col, v[0]);
             tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);
-            tmem_ld16_nw(t + (uint32_t)col + 128u, v1[0]);
-            tmem_ld16_nw(t + (uint32_t)col + 144u, v1[1]);
+            tmem_ld16_nw(t + (uint32_t)col + Plan::kAccIssuer, v1[0]);
+            tmem_ld16_nw(t + (uint32_t)col + Plan::kAccIssuer + 16u, v1[1]);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -493,12 +545,15 @@ __global__ void __launch_bounds__(gg::Plan<kCtas, kTile>::kThreads, 1)
 typedef void (*GroupedKernel)(const CUtensorMap, GroupedArgs);
 struct GroupedVariant {
   GroupedKernel fn[2];  // forward, backward
-  int ctas, tile_rows, threads, box;
+  int threads[2];
+  int ctas, box;
 };
 template <int kCtas, int kTile>
 static constexpr GroupedVariant grouped_variant() {
-  using Plan = gg::Plan<kCtas, kTile>;
-  return {{grouped_gemm_kernel<false, kCtas, kTile>, grouped_gemm_kernel<true, kCtas, kTile>}, kCtas, kTile, Plan::kThreads, Plan::kBox};
+  return {{grouped_gemm_kernel<false, kCtas, kTile>, grouped_gemm_kernel<true, kCtas, kTile>},
+          {gg::Plan<false, kCtas, kTile>::kThreads, gg::Plan<true, kCtas, kTile>::kThreads},
+          kCtas,
+          gg::Plan<false, kCtas, kTile>::kBox};
 }
 static const GroupedVariant kGroupedVariants[] = {grouped_variant<1, 64>(), grouped_variant<1, 128>(), grouped_variant<1, 256>(),
                                                   grouped_variant<2, 64>(), grouped_variant<2, 128>(), grouped_variant<2, 256>()};
@@ -559,7 +614,7 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   a.fault = p.fault;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.num_sms / v.ctas * v.ctas));
-  cfg.blockDim = dim3(v.threads);
+  cfg.blockDim = dim3(v.threads[backward]);
   cfg.dynamicSmemBytes = gg::kSmemMax;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
