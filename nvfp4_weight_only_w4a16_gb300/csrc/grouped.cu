@@ -277,26 +277,27 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
   const int squares = first < total ? ((total - first - 1) / stride + 1) * a.steps : 0;  // of this CTA
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- packed weights of this CTA's 128 features ----------------
-      uint32_t it = 0;
-      RingPos p;
-      bool ok = true;
-      for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok && a.fault != 1; w.next(ctl, total)) {
-        // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
-        const int nb = min(w.block() + rank, a.NB - 1);
-        const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)nb * a.block_stride;
-        for (int s = 0; s < a.steps; ++s, ++it, p.step(kRaw), src += a.step_stride) {
-          if (!mbar_wait(ctl.raw_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 911)) {
-            ok = false;
-            break;
-          }
+    // ---------------- packed weights of this CTA's 128 features ----------------
+    uint32_t it = 0;
+    RingPos p;
+    bool ok = true;
+    for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok && a.fault != 1; w.next(ctl, total)) {
+      // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
+      const int nb = min(w.block() + rank, a.NB - 1);
+      const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)nb * a.block_stride;
+      for (int s = 0; s < a.steps; ++s, ++it, p.step(kRaw), src += a.step_stride) {
+        if (!warp_wait(ctl.raw_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 911)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           mbar_arrive_expect_tx(ctl.raw_full + p.slot, gg::kPairBytes);
           bulk_g2s(raw + p.slot * gg::kPairBytes, src, gg::kPairBytes, ctl.raw_full + p.slot);
         }
+        __syncwarp();
       }
-      if (!ok) drain_copies(ctl.raw_full, it, kRaw);
     }
+    if (!ok && lane == 0) drain_copies(ctl.raw_full, it, kRaw);
   } else if (warp == 1 || (kIssuers == 2 && warp == 3)) {
     // ---------------- MMA issuers: the whole warp walks the loop, one lane issues.  Issuer h takes every kIssuers-th
     // square of the CTA's sequence, into its own accumulator ----------------
