@@ -20,10 +20,10 @@
 // halves of the MMA read.  kCtas = 1, 128 features, where there is no second block
 // to pair with.
 //
-// One CTA per multiprocessor, 24 or 32 warps: 0 packed-weight producer (bulk copies into
+// One CTA per multiprocessor, 24 warps: 0 packed-weight producer (bulk copies into
 // a ring), 1 MMA issuer (the pair's first CTA; for narrow tiles 3 too), 2 row producer (TMA, zero fill past
 // the matrix), 4-7 epilogue (TMEM -> gs -> shared -> 16-byte stores), the
-// rest dequantisers, in two or three teams of 8 that take turns.  Two accumulator buffers of 256
+// rest dequantisers, in two teams of 8 that take turns.  Two accumulator buffers of 256
 // columns: the epilogue of a unit overlaps the next one's MMAs.  The row offsets
 // are read on the device; every CTA derives the same unit list from them, so
 // nothing is written but the output.
@@ -36,48 +36,54 @@
 namespace nvfp4moe {
 
 namespace gg {
-constexpr int kTeamWarps = 8, kEpiWarps = 4;
+constexpr int kTeams = 2, kTeamWarps = 8, kEpiWarps = 4;
+constexpr int kThreads = 32 * (8 + kTeams * kTeamWarps);
 constexpr int kPairBytes = 2 * kTileBytes;  // one 128 x 128 weight square, packed
 constexpr int kHalfBytes = 16384;           // half a square in BF16: 64 long in the reduction
 constexpr int kSmemMax = 232448;
 constexpr int kCtlBytes = 4096;             // tables and barriers in front of the rings
 constexpr int kEpiBytes = 2048;             // per epilogue warp
 constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
-constexpr int kMaxStages = 4, kMaxRaw = 20;
+constexpr int kMaxStages = 8, kMaxRaw = 16;
 constexpr int kRoom = kSmemMax - 1024 - kRingOff;  // for the rings
 
-// What follows from the CTAs of a unit (1 or 2) and the rows of a token tile (64, 128 or 256): MMA issuers, teams of
-// dequantisers, ring depths.  With up to 64 rows the MMAs are so short that issuing them sets the pace, so two warps
-// take turns at the steps, each into an accumulator of its own.  Three teams where their packed slots fit, else two.
-// A parity wait must not run two phases ahead of its barrier: a team meets every packed slot again itself (their
-// number is a multiple of the teams; bulk copies may land out of order); one issuer frees the operand stages in order,
-// so that as many stages as teams are enough for them; with two, the issuers and teams too must meet their own stages
-// again.
+// What follows from the CTAs of a unit (1 or 2) and the rows of a token tile (64, 128 or 256): MMA issuers and ring
+// depths.
+//
+// With up to 64 rows the MMAs are so short that issuing them sets the pace, so two warps take turns at the squares,
+// each into an accumulator of its own.
 //
 // The forward's operand goes to tensor memory where that has room beside the accumulators, that is for tiles of up to
 // 128 rows: with the operand in shared memory its bandwidth is the bound there (per square 256 of 128-byte accesses to
-// write it, 256 to read it, and 400 for the rest, against some 390 cycles that the packed bytes take from memory; 64
-// rows an expert, E 128, N 1536, K 4096: 150 us).  The transposed operand would have to cross the lanes to get there.
+// write it, 256 to read it, and 400 for the rest, against some 390 cycles that the packed bytes take from memory).
+// The transposed operand would have to cross the lanes to get there.
+//
+// The rows have a ring of their own, deeper than the operand's: they come from L2 some 1500 cycles after they are asked
+// for, and with the operand's 4 stages that alone made a square cost 670 cycles (64 rows an expert, E 128, N 1536,
+// K 4096: 115 us with no conversion, no MMA and no weights, of 149).
+//
+// A parity wait must not run two phases ahead of its barrier: a team meets every packed slot again itself (their
+// number is even; bulk copies may land out of order), and so does one of two issuers every stage; one issuer frees
+// the operand stages in order, so that two of them are enough for two teams.
 template <bool kBackward, int kCtas, int kTile>
 struct Plan {
   static constexpr bool kTmemA = !kBackward && kCtas == 2 && kTile <= 128;
-  static constexpr int kBHalf = kTile / kCtas * 128;             // half a stage's rows: this CTA's share of the tile
-  static constexpr int kStageA = kTmemA ? 0 : 2 * kHalfBytes;
-  static constexpr int kStage = kStageA + 2 * kBHalf;            // the operand's two halves, then the rows'
   static constexpr int kIssuers = kCtas == 2 && kTile == 64 ? 2 : 1;
-  static constexpr int kTeams = !kTmemA && kIssuers == 1 && 3 * kStage + 3 * kPairBytes <= kRoom ? 3 : 2;
-  static constexpr int kStages = kTmemA || kIssuers == 2 ? 4
-                                 : kTeams == 2 ? (kRoom - 2 * kPairBytes) / kStage
-                                 : 4 * kStage + 6 * kPairBytes <= kRoom ? 4 : 3;
-  static constexpr int kFit = (kRoom - kStages * kStage) / kPairBytes;
-  static constexpr int kRaw = (kFit < kMaxRaw ? kFit : kMaxRaw) / kTeams * kTeams;  // packed slots
+  static constexpr int kABytes = kTmemA ? 0 : 2 * kHalfBytes;  // an operand stage in shared memory: a square
+  static constexpr int kBHalf = kTile / kCtas * 128;           // half a row stage: this CTA's share of the tile
+  static constexpr int kBBytes = 2 * kBHalf;
+  static constexpr int kStagesA = kTmemA || kTile == 64 ? 4 : kCtas == 1 && kTile == 256 ? 2 : 3;
+  static constexpr int kStagesB = kTmemA ? (kTile == 64 ? 8 : 6)
+                                  : kCtas == 2 ? (kTile == 64 ? 6 : kTile == 128 ? 5 : 3)
+                                               : (kTile == 64 ? 4 : kTile == 128 ? 3 : 2);
+  static constexpr int kRings = kStagesA * kABytes + kStagesB * kBBytes;
+  static constexpr int kRaw = (kRoom - kRings) / kPairBytes / kTeams * kTeams;  // packed slots
+  static constexpr int kBox = kTile / kCtas < 64 ? kTile / kCtas : 64;          // rows per TMA box
   // tensor memory: buffer b, issuer h at b kAccBuf + h kAccIssuer; operand stages of 64 columns from kOperand on
   static constexpr uint32_t kAccBuf = kTmemA ? 128 : 256, kAccIssuer = kAccBuf / 2, kOperand = 256;
-  static constexpr int kThreads = 32 * (8 + kTeams * kTeamWarps);
-  static constexpr int kBox = kTile / kCtas < 64 ? kTile / kCtas : 64;  // rows per TMA box
-  static_assert(kStages >= kTeams && kRaw >= kTeams && kRaw % kTeams == 0 && kStages * kStage + kRaw * kPairBytes <= kRoom, "rings");
-  static_assert(kIssuers == 1 || (kStages % 2 == 0 && kStages % kTeams == 0 && kTile <= 128), "two issuers");
-  static_assert(kStage % 1024 == 0 && kBHalf % 1024 == 0, "128B-swizzled tiles");
+  static_assert(kRaw >= kTeams && kRaw <= kMaxRaw && kStagesA <= kMaxStages && kStagesB <= kMaxStages && kStagesA >= kTeams, "rings");
+  static_assert(kIssuers == 1 || (kStagesA % 2 == 0 && kStagesB % 2 == 0 && kStagesA % kTeams == 0), "two issuers");
+  static_assert(kBHalf % 1024 == 0, "128B-swizzled tiles");
 };
 }  // namespace gg
 
@@ -106,7 +112,7 @@ struct GroupedCtl {
   int tile[257];   // token tiles before expert e; tile[E] = all
   short per[256];  // rows per tile of expert e: its tiles are of one size, so that none is a small remainder
   uint64_t raw_full[gg::kMaxRaw], raw_empty[gg::kMaxRaw];
-  uint64_t full[gg::kMaxStages], empty[gg::kMaxStages];
+  uint64_t a_full[gg::kMaxStages], a_empty[gg::kMaxStages], b_full[gg::kMaxStages], b_empty[gg::kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
   int abort_flag;
@@ -189,17 +195,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&o)[4]
 }
 
 template <bool kBackward, int kCtas, int kTile>
-__global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1)
+__global__ void __launch_bounds__(gg::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap, GroupedArgs a) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   GroupedCtl& ctl = *reinterpret_cast<GroupedCtl*>(smem);
   uint8_t* ring = smem + gg::kRingOff;
   using Plan = gg::Plan<kBackward, kCtas, kTile>;
-  constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kStages = Plan::kStages, kRaw = Plan::kRaw;
-  static_assert(kStages <= gg::kMaxStages && kRaw <= gg::kMaxRaw, "barriers");
-  uint8_t* raw = ring + kStages * Plan::kStage;
-  const uint32_t ring_addr = smem_u32(ring), raw_addr = smem_u32(raw);
+  constexpr int kIssuers = Plan::kIssuers, kTeams = gg::kTeams, kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB,
+                kRaw = Plan::kRaw;
+  uint8_t* ring_b = ring + kStagesA * Plan::kABytes;
+  uint8_t* raw = ring + Plan::kRings;
+  const uint32_t ring_addr = smem_u32(ring), ring_b_addr = smem_u32(ring_b), raw_addr = smem_u32(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
   const int first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
@@ -211,9 +218,13 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
       mbar_init(ctl.raw_full + s, 1);
       mbar_init(ctl.raw_empty + s, gg::kTeamWarps);
     }
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(ctl.full + s, kCtas * gg::kTeamWarps + 1);  // waited for by the pair's first CTA
-      mbar_init(ctl.empty + s, 1);
+    for (int s = 0; s < kStagesA; ++s) {
+      mbar_init(ctl.a_full + s, kCtas * gg::kTeamWarps);  // waited for by the pair's first CTA
+      mbar_init(ctl.a_empty + s, 1);
+    }
+    for (int s = 0; s < kStagesB; ++s) {
+      mbar_init(ctl.b_full + s, 1);  // the same
+      mbar_init(ctl.b_empty + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(ctl.acc_full + b, kIssuers);
@@ -237,7 +248,7 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int i = threadIdx.x; i <= a.E; i += Plan::kThreads) ctl.off[i] = a.offsets[i];
+  for (int i = threadIdx.x; i <= a.E; i += gg::kThreads) ctl.off[i] = a.offsets[i];
   __syncthreads();
   if (warp == 0) {  // token tiles per expert, 8 experts a lane; offsets that do not ascend within 0..R give no tile
     int n[8], sum = 0;
@@ -317,16 +328,17 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
         const int end = base + a.steps;
         uint32_t acc = 0;
         for (int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base; i < end; i += kIssuers) {
-          const int slot = i % kStages;
-          if (!warp_wait(ctl.full + slot, (uint32_t)(i / kStages) & 1u, abort_flag, a.st, 913)) {
+          const int sa = i % kStagesA, sb = i % kStagesB;
+          if (!warp_wait(ctl.b_full + sb, (uint32_t)(i / kStagesB) & 1u, abort_flag, a.st, 913) ||
+              !warp_wait(ctl.a_full + sa, (uint32_t)(i / kStagesA) & 1u, abort_flag, a.st, 914)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = ring_addr + (uint32_t)(slot * Plan::kStage);
+          const uint32_t st = ring_addr + (uint32_t)(sa * Plan::kABytes);
           const uint64_t ad = kBackward ? sw128_desc_mn(st) : sw128_desc(st);
-          const uint64_t bd = sw128_desc(st + Plan::kStageA);
-          const uint32_t at = tmem + Plan::kOperand + (uint32_t)slot * 64u;  // 8 columns per 16 elements
+          const uint64_t bd = sw128_desc(ring_b_addr + (uint32_t)(sb * Plan::kBBytes));
+          const uint32_t at = tmem + Plan::kOperand + (uint32_t)sa * 64u;  // 8 columns per 16 elements
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
@@ -336,8 +348,13 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
               else if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, kk ? 1u : acc);
               else umma_bf16(d, ak, bk, idesc, kk ? 1u : acc);
             }
-            if (kCtas == 2) umma_commit_pair(ctl.empty + slot);
-            else umma_commit(ctl.empty + slot);
+            if (kCtas == 2) {
+              umma_commit_pair(ctl.b_empty + sb);
+              umma_commit_pair(ctl.a_empty + sa);
+            } else {
+              umma_commit(ctl.b_empty + sb);
+              umma_commit(ctl.a_empty + sa);
+            }
           }
           acc = 1;
           __syncwarp();
@@ -352,6 +369,7 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
     }
   } else if (warp == 2) {
     // ---------------- rows of x (dy): this CTA's half of the tile, boxes of 64 reduction elements ----------------
+    uint32_t it = 0;
     RingPos p;
     bool ok = true;
     for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok && a.fault != 1; w.next(ctl, total)) {
@@ -359,14 +377,14 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
       const int share = ((w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) / kCtas;
       const int nbox = (share + Plan::kBox - 1) / Plan::kBox;
       row0 += rank * share;
-      for (int s = 0; s < a.steps; ++s, p.step(kStages)) {
-        if (!warp_wait(ctl.empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 915)) {
+      for (int s = 0; s < a.steps; ++s, ++it, p.step(kStagesB)) {
+        if (!warp_wait(ctl.b_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 915)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          uint8_t* dst = ring + p.slot * Plan::kStage + Plan::kStageA;
-          uint64_t* bar = ctl.full + p.slot;
+          uint8_t* dst = ring_b + p.slot * Plan::kBBytes;
+          uint64_t* bar = ctl.b_full + p.slot;
           if (rank == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kCtas * 2 * nbox * Plan::kBox) * 128u);
           const uint32_t bar0 = kCtas == 2 ? map_rank(bar, 0) : 0u;
           for (int h = 0; h < 2; ++h)
@@ -379,8 +397,11 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
         __syncwarp();
       }
     }
-    if (!ok)  // given up: the copies in flight land within microseconds (their barrier also counts the dequantisers)
-      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    if (!ok && lane == 0) {
+      if (rank == 0) drain_copies(ctl.b_full, it, kStagesB);
+      else
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // its copies complete on the first CTA's barriers
+    }
   } else if (warp >= 8) {
     // ---------------- dequantisers: the teams take turns at the squares; warp w of a team takes one 16-row
     // sub-block of each half, so that its waits and its fence are paid once for 64 weights a lane ----------------
@@ -397,10 +418,10 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
     const uint32_t row_c = (uint32_t)((w >> 2) * kTileBytes + (tr >> 4) * 512 + ((tr >> 3) & 1) * 8);
     const uint32_t row_s = (uint32_t)((w >> 2) * kTileBytes + kTileCodes + (tr >> 4) * 64 + ((tr >> 3) & 1));
     const uint32_t t_row = tmem + ((uint32_t)(32 * (w & 3)) << 16) + Plan::kOperand + 32u * (uint32_t)(w >> 2);
-    const uint32_t full0 = kCtas == 2 ? map_rank(ctl.full, 0) : 0u;  // the pair's first CTA's
+    const uint32_t full0 = kCtas == 2 ? map_rank(ctl.a_full, 0) : 0u;  // the pair's first CTA's
     RingPos pr, pa;
     pr.slot = pa.slot = team;  // at most the ring's depth
-    for (int i = team; i < squares; i += kTeams, pr.step(kRaw, kTeams), pa.step(kStages, kTeams)) {
+    for (int i = team; i < squares; i += kTeams, pr.step(kRaw, kTeams), pa.step(kStagesA, kTeams)) {
       if (!warp_wait(ctl.raw_full + pr.slot, pr.phase, abort_flag, a.st, 916)) break;
       const uint32_t pair = raw_addr + pr.slot * gg::kPairBytes;
       if constexpr (Plan::kTmemA) {
@@ -415,7 +436,7 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + (seen & a.zero));  // see below
-        if (!warp_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
+        if (!warp_wait(ctl.a_empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
         tc_fence_after();
         uint32_t o[4][8];
 #pragma unroll
@@ -435,8 +456,8 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
         const uint32_t seen = (c[0].x | c[0].y | c[0].z | c[0].w | c[1].x | c[1].y | c[1].z | c[1].w | sc[0] | sc[1]) & a.zero;
         __syncwarp();
         if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + seen);
-        if (!warp_wait(ctl.empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
-        const uint32_t st = dst0 + (uint32_t)(pa.slot * Plan::kStage);
+        if (!warp_wait(ctl.a_empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
+        const uint32_t st = dst0 + (uint32_t)(pa.slot * Plan::kABytes);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
@@ -454,7 +475,7 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
       __syncwarp();
       if (lane == 0) {
         if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + pa.slot * 8);
-        else mbar_arrive(ctl.full + pa.slot);
+        else mbar_arrive(ctl.a_full + pa.slot);
       }
     }
   } else if (warp >= 4) {
@@ -546,13 +567,11 @@ __global__ void __launch_bounds__(gg::Plan<kBackward, kCtas, kTile>::kThreads, 1
 typedef void (*GroupedKernel)(const CUtensorMap, GroupedArgs);
 struct GroupedVariant {
   GroupedKernel fn[2];  // forward, backward
-  int threads[2];
   int ctas, box;
 };
 template <int kCtas, int kTile>
 static constexpr GroupedVariant grouped_variant() {
   return {{grouped_gemm_kernel<false, kCtas, kTile>, grouped_gemm_kernel<true, kCtas, kTile>},
-          {gg::Plan<false, kCtas, kTile>::kThreads, gg::Plan<true, kCtas, kTile>::kThreads},
           kCtas,
           gg::Plan<false, kCtas, kTile>::kBox};
 }
@@ -615,7 +634,7 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   a.fault = p.fault;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.num_sms / v.ctas * v.ctas));
-  cfg.blockDim = dim3(v.threads[backward]);
+  cfg.blockDim = dim3(gg::kThreads);
   cfg.dynamicSmemBytes = gg::kSmemMax;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
