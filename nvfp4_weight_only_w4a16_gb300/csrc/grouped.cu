@@ -23,7 +23,7 @@
 // One CTA per multiprocessor, 24 warps: 0 packed-weight producer (bulk copies into
 // a ring), 1 MMA issuer (the pair's first CTA; for narrow tiles 3 too), 2 row producer (TMA, zero fill past
 // the matrix), 4-7 epilogue (TMEM -> gs -> shared -> 16-byte stores), the
-// rest dequantisers, in two teams of 8 that take turns.  Two accumulator buffers of 256
+// rest dequantisers, in teams that take turns.  Two accumulator buffers of 256
 // columns: the epilogue of a unit overlaps the next one's MMAs.  The row offsets
 // are read on the device; every CTA derives the same unit list from them, so
 // nothing is written but the output.
@@ -36,8 +36,8 @@
 namespace nvfp4moe {
 
 namespace gg {
-constexpr int kTeams = 2, kTeamWarps = 8, kEpiWarps = 4;
-constexpr int kThreads = 32 * (8 + kTeams * kTeamWarps);
+constexpr int kDequantWarps = 16, kEpiWarps = 4;
+constexpr int kThreads = 32 * (8 + kDequantWarps);
 constexpr int kPairBytes = 2 * kTileBytes;  // one 128 x 128 weight square, packed
 constexpr int kHalfBytes = 16384;           // half a square in BF16: 64 long in the reduction
 constexpr int kSmemMax = 232448;
@@ -62,9 +62,13 @@ constexpr int kRoom = kSmemMax - 1024 - kRingOff;  // for the rings
 // for, and with the operand's 4 stages that alone made a square cost 670 cycles (64 rows an expert, E 128, N 1536,
 // K 4096: 115 us with no conversion, no MMA and no weights, of 149).
 //
+// The dequantisers work in teams that take turns at the squares.  Half of what a warp spends on a square is waiting for
+// and signalling barriers, so small teams with more of a square to each warp are better: four teams of four warps where
+// there are four operand stages and packed slots for them, else two of eight.
+//
 // A parity wait must not run two phases ahead of its barrier: a team meets every packed slot again itself (their
-// number is even; bulk copies may land out of order), and so does one of two issuers every stage; one issuer frees
-// the operand stages in order, so that two of them are enough for two teams.
+// number is a multiple of the teams; bulk copies may land out of order), and so does one of two issuers every stage;
+// one issuer frees the operand stages in order, so that as many of them as teams are enough.
 template <bool kBackward, int kCtas, int kTile>
 struct Plan {
   static constexpr bool kTmemA = !kBackward && kCtas == 2 && kTile <= 128;
@@ -77,7 +81,9 @@ struct Plan {
                                   : kCtas == 2 ? (kTile == 64 ? 6 : kTile == 128 ? 5 : 3)
                                                : (kTile == 64 ? 4 : kTile == 128 ? 3 : 2);
   static constexpr int kRings = kStagesA * kABytes + kStagesB * kBBytes;
-  static constexpr int kRaw = (kRoom - kRings) / kPairBytes / kTeams * kTeams;  // packed slots
+  static constexpr int kFit = (kRoom - kRings) / kPairBytes;
+  static constexpr int kTeams = kStagesA == 4 && kFit >= 4 ? 4 : 2, kTeamWarps = kDequantWarps / kTeams;
+  static constexpr int kRaw = kFit / kTeams * kTeams;  // packed slots
   static constexpr int kBox = kTile / kCtas < 64 ? kTile / kCtas : 64;          // rows per TMA box
   // tensor memory: buffer b, issuer h at b kAccBuf + h kAccIssuer; operand stages of 64 columns from kOperand on
   static constexpr uint32_t kAccBuf = kTmemA ? 128 : 256, kAccIssuer = kAccBuf / 2, kOperand = 256;
@@ -180,7 +186,7 @@ __device__ __forceinline__ void dequant16_bf16(uint32_t c0, uint32_t c1, uint32_
   for (int i = 0; i < 4; ++i) o[4 + i] = scaled_pair_bf16(v[i], s);
 }
 
-// 32 registers into 32 columns of the thread's lane, waited for.
+// 32 registers into 32 columns of the thread's lane; the caller waits.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&o)[4][8]) {
   const uint32_t* w = o[0];
   asm volatile(
@@ -191,7 +197,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&o)[4]
       "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]),
       "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 template <bool kBackward, int kCtas, int kTile>
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   GroupedCtl& ctl = *reinterpret_cast<GroupedCtl*>(smem);
   uint8_t* ring = smem + gg::kRingOff;
   using Plan = gg::Plan<kBackward, kCtas, kTile>;
-  constexpr int kIssuers = Plan::kIssuers, kTeams = gg::kTeams, kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB,
+  constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kTeamWarps = Plan::kTeamWarps, kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB,
                 kRaw = Plan::kRaw;
   uint8_t* ring_b = ring + kStagesA * Plan::kABytes;
   uint8_t* raw = ring + Plan::kRings;
@@ -216,10 +221,10 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(ctl.raw_full + s, 1);
-      mbar_init(ctl.raw_empty + s, gg::kTeamWarps);
+      mbar_init(ctl.raw_empty + s, kTeamWarps);
     }
     for (int s = 0; s < kStagesA; ++s) {
-      mbar_init(ctl.a_full + s, kCtas * gg::kTeamWarps);  // waited for by the pair's first CTA
+      mbar_init(ctl.a_full + s, kCtas * kTeamWarps);  // waited for by the pair's first CTA
       mbar_init(ctl.a_empty + s, 1);
     }
     for (int s = 0; s < kStagesB; ++s) {
@@ -403,72 +408,91 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // its copies complete on the first CTA's barriers
     }
   } else if (warp >= 8) {
-    // ---------------- dequantisers: the teams take turns at the squares; warp w of a team takes one 16-row
-    // sub-block of each half, so that its waits and its fence are paid once for 64 weights a lane ----------------
-    const int team = (warp - 8) >> 3, w = (warp - 8) & 7, q = lane & 3;
-    // forward: half h is tile h (K elements 64 h ..), all 128 rows; backward: rows 64 h .. of both tiles
-    const int r = (kBackward ? (w & 3) * 16 : w * 16) + (lane >> 2);
-    const uint32_t dst0 = ring_addr + (kBackward ? (uint32_t)(w >> 2) * 8192u : 0u) + (uint32_t)r * 128u;
-    const uint32_t x0 = (uint32_t)((2 * q) ^ (r & 7)) * 16u, x1 = (uint32_t)((2 * q + 1) ^ (r & 7)) * 16u;
-    const uint32_t sub = (uint32_t)(kBackward ? (w >> 2) * kTileBytes + (w & 3) * 512 : w * 512) + seg_pos(lane) * 16;
-    const uint32_t ssub = (uint32_t)(kBackward ? (w >> 2) * kTileBytes + (w & 3) * 64 : w * 64) + kTileCodes + seg_pos(lane) * 2;
+    // ---------------- dequantisers: the teams take turns at the squares.  A square's work is 8 shares (share w: in
+    // shared memory one 16-row sub-block of each half, in tensor memory 32 rows of one half); a warp takes kShares of
+    // them, w and w + 4, so that its waits and its fence are paid once ----------------
+    constexpr int kShares = 8 / kTeamWarps;
+    const int team = (warp - 8) / kTeamWarps, w0 = (warp - 8) % kTeamWarps, q = lane & 3;
     const uint32_t raw_empty0 = smem_u32(ctl.raw_empty);
-    // tensor-memory operand: the thread's row in a packed square, and its place in an operand stage
-    const int tr = 32 * (w & 3) + lane;
-    const uint32_t row_c = (uint32_t)((w >> 2) * kTileBytes + (tr >> 4) * 512 + ((tr >> 3) & 1) * 8);
-    const uint32_t row_s = (uint32_t)((w >> 2) * kTileBytes + kTileCodes + (tr >> 4) * 64 + ((tr >> 3) & 1));
-    const uint32_t t_row = tmem + ((uint32_t)(32 * (w & 3)) << 16) + Plan::kOperand + 32u * (uint32_t)(w >> 2);
     const uint32_t full0 = kCtas == 2 ? map_rank(ctl.a_full, 0) : 0u;  // the pair's first CTA's
     RingPos pr, pa;
     pr.slot = pa.slot = team;  // at most the ring's depth
     for (int i = team; i < squares; i += kTeams, pr.step(kRaw, kTeams), pa.step(kStagesA, kTeams)) {
       if (!warp_wait(ctl.raw_full + pr.slot, pr.phase, abort_flag, a.st, 916)) break;
       const uint32_t pair = raw_addr + pr.slot * gg::kPairBytes;
+      // The packed slot goes back as soon as it has been read.  A read that is merely issued can be overtaken by the
+      // refill (measured: wrong 16-row groups), so the address of the arrival takes in what was read, masked by an
+      // argument that is zero.
+      uint32_t seen = 0;
       if constexpr (Plan::kTmemA) {
-        // thread = one weight row of half w / 4, which is its TMEM lane: groups of 16 elements, 8 bytes and a scale each
-        uint2 c[4];
-        uint32_t sc[4], seen = 0;
+        // thread = one weight row, its TMEM lane: per half 4 groups of 16 elements, 8 bytes and a scale each
+        const int r = 32 * (w0 & 3) + lane;
+        uint2 c[kShares][4];
+        uint32_t sc[kShares][4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          c[g] = lds64(pair + row_c + (uint32_t)(seg_pos(4 * (lane & 7) + g) * 16));
-          sc[g] = lds8(pair + row_s + (uint32_t)(seg_pos(4 * (lane & 7) + g) * 2));
-          seen |= c[g].x | c[g].y | sc[g];
+        for (int k = 0; k < kShares; ++k) {
+          const uint32_t tile = pair + (uint32_t)(((w0 + 4 * k) >> 2) * kTileBytes);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int slot = seg_pos(4 * (lane & 7) + g);
+            c[k][g] = lds64(tile + (r >> 4) * 512 + ((r >> 3) & 1) * 8 + slot * 16);
+            sc[k][g] = lds8(tile + kTileCodes + (r >> 4) * 64 + ((r >> 3) & 1) + slot * 2);
+            seen |= c[k][g].x | c[k][g].y | sc[k][g];
+          }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + (seen & a.zero));  // see below
+        if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + (seen & a.zero));
         if (!warp_wait(ctl.a_empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
         tc_fence_after();
-        uint32_t o[4][8];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) dequant16_bf16(c[g].x, c[g].y, e4m3x2_to_f16x2(sc[g]), o[g]);
-        tmem_st32(t_row + (uint32_t)pa.slot * 64u, o);
+        for (int k = 0; k < kShares; ++k) {
+          uint32_t o[4][8];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) dequant16_bf16(c[k][g].x, c[k][g].y, e4m3x2_to_f16x2(sc[k][g]), o[g]);
+          tmem_st32(tmem + ((uint32_t)(32 * (w0 & 3)) << 16) + Plan::kOperand + (uint32_t)pa.slot * 64u +
+                        32u * (uint32_t)((w0 + 4 * k) >> 2),
+                    o);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
       } else {
-        uint4 c[2];
-        uint32_t sc[2];
+        uint4 c[kShares][2];
+        uint32_t sc[kShares][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          c[h] = lds128(pair + h * (kBackward ? 4 * 512 : kTileBytes) + sub);
-          sc[h] = lds16(pair + h * (kBackward ? 4 * 64 : kTileBytes) + ssub);
+        for (int k = 0; k < kShares; ++k) {
+          const int w = w0 + 4 * k;
+          // forward: half h is tile h (K elements 64 h ..), all 128 rows; backward: rows 64 h .. of both tiles
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t tile = pair + (uint32_t)((kBackward ? w >> 2 : h) * kTileBytes);
+            const int sb = kBackward ? 4 * h + (w & 3) : w;
+            c[k][h] = lds128(tile + sb * 512 + seg_pos(lane) * 16);
+            sc[k][h] = lds16(tile + kTileCodes + sb * 64 + seg_pos(lane) * 2);
+            seen |= c[k][h].x | c[k][h].y | c[k][h].z | c[k][h].w | sc[k][h];
+          }
         }
-        // The packed slot goes back.  A read that is merely issued can be overtaken by the refill (measured: wrong
-        // 16-row groups), so the address of the arrival takes in what was read, masked by an argument that is zero.
-        const uint32_t seen = (c[0].x | c[0].y | c[0].z | c[0].w | c[1].x | c[1].y | c[1].z | c[1].w | sc[0] | sc[1]) & a.zero;
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + seen);
+        if (lane == 0) mbar_arrive_at(raw_empty0 + pr.slot * 8 + (seen & a.zero));
         if (!warp_wait(ctl.a_empty + pa.slot, pa.phase ^ 1u, abort_flag, a.st, 917)) break;
-        const uint32_t st = dst0 + (uint32_t)(pa.slot * Plan::kABytes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t s2 = e4m3x2_to_f16x2(sc[h]);
-          const uint32_t p = st + h * gg::kHalfBytes;
-          uint32_t o[8];
-          dequant16_bf16(c[h].x, c[h].y, s2, o);
-          sts128(p + x0, o[0], o[1], o[2], o[3]);
-          sts128(p + x1, o[4], o[5], o[6], o[7]);
-          dequant16_bf16(c[h].z, c[h].w, s2 >> 16, o);
-          sts128(p + 1024u + x0, o[0], o[1], o[2], o[3]);
-          sts128(p + 1024u + x1, o[4], o[5], o[6], o[7]);
+        for (int k = 0; k < kShares; ++k) {
+          const int w = w0 + 4 * k;
+          const int r = (kBackward ? (w & 3) * 16 : w * 16) + (lane >> 2);
+          const uint32_t x0 = (uint32_t)((2 * q) ^ (r & 7)) * 16u, x1 = (uint32_t)((2 * q + 1) ^ (r & 7)) * 16u;
+          const uint32_t st = ring_addr + (uint32_t)(pa.slot * Plan::kABytes) + (kBackward ? (uint32_t)(w >> 2) * 8192u : 0u) +
+                              (uint32_t)r * 128u;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t s2 = e4m3x2_to_f16x2(sc[k][h]);
+            const uint32_t p = st + h * gg::kHalfBytes;
+            uint32_t o[8];
+            dequant16_bf16(c[k][h].x, c[k][h].y, s2, o);
+            sts128(p + x0, o[0], o[1], o[2], o[3]);
+            sts128(p + x1, o[4], o[5], o[6], o[7]);
+            dequant16_bf16(c[k][h].z, c[k][h].w, s2 >> 16, o);
+            sts128(p + 1024u + x0, o[0], o[1], o[2], o[3]);
+            sts128(p + 1024u + x1, o[4], o[5], o[6], o[7]);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
