@@ -124,12 +124,29 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
-// mbar_wait by a whole warp: one answer for all lanes, and they come out together, as .aligned instructions need.
-// The waiting itself is out of line, so that the usual case is a test and a vote.
-[[maybe_unused]] static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st,
-                                            unsigned where) {
-  return mbar_wait(bar, parity, abort_flag, st, where);
+// The bounded wait out of line, and asleep: the test suspends the thread for up to a millisecond at a time, where
+// mbar_wait's short ones keep issuing (its waiting warps took a quarter of a multiprocessor's instructions).
+[[maybe_unused]] static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                                    DeviceStatus* st, unsigned where) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      report(st, kFlagTimeout, where);
+      return false;
+    }
+  }
 }
+// The wait of a whole warp: one answer for all lanes, and they come out together, as .aligned instructions need.  The
+// usual case is a test and a vote.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st,
                                           unsigned where) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
