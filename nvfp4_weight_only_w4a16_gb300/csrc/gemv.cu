@@ -23,6 +23,11 @@
 // masked in place, are the FP16 subnormal q 2^-24, or q 2^-20 one nibble higher,
 // which x's matching elements, staged times 2^-4, make good.  The zero point comes
 // off a group's FP32 sum with the sum of x over the group, which is staged too.
+// The tensor core aligns what it adds by exponents that a subnormal does not show, and
+// truncates there: with FP16's 11 significant bits and an FP32 result that was seen
+// (1.2e-6 of the result's norm; 0.5e-6 for BF16, whose sums need fewer bits), so that
+// case (kCenter) makes q - 8 of every code, a normal number, at one more instruction a
+// pair (1024 | q, less 1032), and takes z - 8 off the sums.
 #include <mutex>
 
 #include "common.cuh"
@@ -76,6 +81,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t hsub2_u32(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
@@ -171,7 +182,7 @@ __device__ __forceinline__ float byte_of(uint32_t v, int i) {  // 0..255, exactl
 
 // acc += the step's (16 kRg) x 8 products.  xl: the lane's x row at the step's first element and the lane's
 // position in it; sl: the lane's group sums of x at the step's first group (INT4).
-template <W4 kFmt, bool kBf16, bool kZeros>
+template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
 __device__ __forceinline__ void use_step(const Step<kFmt, kZeros>& w, const uint8_t* xl, const float* sl,
                                          float (&acc)[gv::kRg][4]) {
   uint32_t x[2][8];
@@ -215,13 +226,21 @@ __device__ __forceinline__ void use_step(const Step<kFmt, kZeros>& w, const uint
           const uint32_t l = run & 1 ? c.y : c.x, h = run & 1 ? c.w : c.z;
           const uint32_t* xr = x[run >> 1] + 4 * (run & 1);
           const uint32_t l8 = l >> 8, h8 = h >> 8;
-          mma_16816(part, l & 0x000F000Fu, h & 0x000F000Fu, l & 0x00F000F0u, h & 0x00F000F0u, xr[0], xr[1]);
-          mma_16816(part, l8 & 0x000F000Fu, h8 & 0x000F000Fu, l8 & 0x00F000F0u, h8 & 0x00F000F0u, xr[2], xr[3]);
+          // kCenter: 1024 | q less 1032, and 1024 | 16 q less 1152 (0x6400 = 1024, 0x6408 = 1032, 0x6480 = 1152)
+          const auto lo = [](uint32_t w) {
+            return kCenter ? hsub2_u32((w & 0x000F000Fu) | 0x64006400u, 0x64086408u) : w & 0x000F000Fu;
+          };
+          const auto hi = [](uint32_t w) {
+            return kCenter ? hsub2_u32((w & 0x00F000F0u) | 0x64006400u, 0x64806480u) : w & 0x00F000F0u;
+          };
+          mma_16816(part, lo(l), lo(h), hi(l), hi(h), xr[0], xr[1]);
+          mma_16816(part, lo(l8), lo(h8), hi(l8), hi(h8), xr[2], xr[3]);
         }
-        float z0 = 8.0f, z1 = 8.0f;
+        constexpr float kOff = kCenter ? 8.0f : 0.0f;
+        float z0 = 8.0f - kOff, z1 = 8.0f - kOff;
         if (kZeros) {
           const uint32_t zz = w.z[q][g >> 1] >> (16 * (g & 1));
-          z0 = byte_of(zz, 0), z1 = byte_of(zz, 1);
+          z0 = byte_of(zz, 0) - kOff, z1 = byte_of(zz, 1) - kOff;
         }
         const float s0 = scale_of<kBf16>(w.s[q][g], 0), s1 = scale_of<kBf16>(w.s[q][g], 1);
         acc[q][0] = fmaf(s0, fmaf(-z0, sx.x, part[0]), acc[q][0]);
@@ -243,10 +262,10 @@ __device__ __forceinline__ float2 pow2_pair(int e) {
 __device__ __forceinline__ int row_exponent(unsigned bits) { return bits ? (int)(bits >> 23) - 140 : 0; }
 
 // x rows into shared memory as FP16 times 2^-p per row; INT4: elements 2, 3, 6 and 7 of every 8 times another
-// 2^-4, and 2^-24 times the sums over each group of the matrix into sums[group][8].  In two parts: start() copies the
+// 2^-4, and 2^-24 (kCenter: 1) times the sums over each group of the matrix into sums[group][8].  In two parts: start() copies the
 // rows as they are (bulk copies, by one thread), finish() waits for them, finds each row's p and converts in place.
 // (Small loops on purpose: a call's first use of its code comes from memory, and this runs before any product.)
-template <W4 kFmt, bool kBf16>
+template <W4 kFmt, bool kBf16, bool kCenter>
 struct Stage {
   uint8_t* xs;
   int pitch, per, rows;  // 16-byte pieces of a row
@@ -319,14 +338,14 @@ struct Stage {
       if (kFmt != W4::kNvfp4) {  // a group's pieces belong to neighbouring lanes
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = sum * 0x1p-24f;
+        if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = kCenter ? sum : sum * 0x1p-24f;
       }
     }
     return true;
   }
 };
 
-template <W4 kFmt, bool kBf16, bool kZeros>
+template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
 __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   using S = Step<kFmt, kZeros>;
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the group sums
@@ -400,7 +419,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   }
   uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kSlot;
   float* sums = reinterpret_cast<float*>(xs + (size_t)a.tile_rows * a.pitch);
-  Stage<kFmt, kBf16> stage(a, xs);
+  Stage<kFmt, kBf16, kCenter> stage(a, xs);
   int row0, rows;
   const auto tile_rows = [&] {  // the rows of `tile`
     row0 = S::kNv ? tile_row0[tile] : tile * a.tile_rows;
@@ -515,7 +534,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
         slot = slot == gv::kDepth - 1 ? 0 : slot + 1;
         __syncwarp();  // read by all before it is filled again
         copy_next();
-        use_step<kFmt, kBf16, kZeros>(w, xl, sl, acc);
+        use_step<kFmt, kBf16, kZeros, kCenter>(w, xl, sl, acc);
         xl += a.KS * 256;
         sl += a.KS * (S::kGroups * gv::kRows);
       }
@@ -525,7 +544,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       const int rg = (g0 + granule) * gv::kRg + (s >> 2), r = 2 * (lane & 3) + (s & 1);
       if (r < rows && rg < rgroups) {
         const long long o = (long long)(row0 + r) * a.ldo + 16 * rg + (lane >> 2) + 8 * ((s >> 1) & 1);
-        const float2 up = pow2_pair(row_exponent(amax[tphase][r]) + (S::kNv ? 0 : 24));
+        const float2 up = pow2_pair(row_exponent(amax[tphase][r]) + (S::kNv || kCenter ? 0 : 24));
         y = y * up.x * up.y;
         if (S::kNv) y *= gs;
         if (a.out_f32) static_cast<float*>(a.out)[o] = y;
@@ -577,7 +596,7 @@ static size_t set_smem(GemvArgs& a, int rows, size_t row_bytes, size_t fixed, in
   return fixed + a.tile_rows * row_bytes;
 }
 
-template <W4 kFmt, bool kBf16, bool kZeros>
+template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
 static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, int num_sms, cudaStream_t st) {
   static std::mutex mu;
   static bool done[64] = {};
@@ -587,7 +606,7 @@ static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, i
   {  // the opt-in shared-memory size, once per device
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(gemv_kernel<kFmt, kBf16, kZeros>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(gemv_kernel<kFmt, kBf16, kZeros, kCenter>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                gv::smem_for(kFmt == W4::kNvfp4));
       if (e != cudaSuccess) return e;
       if (dev < 64) done[dev] = true;
@@ -603,7 +622,7 @@ static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, i
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<kFmt, kBf16, kZeros>, a);
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<kFmt, kBf16, kZeros, kCenter>, a);
 }
 
 // the longest row of x: two of them fit beside the rings (kMaxTiles), or one with its sums
@@ -632,10 +651,10 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   set_steps(a, (long long)touched * granules / p.num_sms);
   a.pitch = p.K * 2 + 16;  // rows 16 bytes apart in the banks: the lanes' 32-byte pieces of two rows never collide
   const size_t smem = set_smem(a, p.R, a.pitch, 0, Step<W4::kNvfp4, false>::kSlot, gv::smem_for(true));
-  return launch_gemv<W4::kNvfp4, true, false>(a, (long long)(touched + p.R / a.tile_rows) * granules, smem, p.num_sms, st);
+  return launch_gemv<W4::kNvfp4, true, false, false>(a, (long long)(touched + p.R / a.tile_rows) * granules, smem, p.num_sms, st);
 }
 
-template <W4 kFmt, bool kBf16, bool kZeros>
+template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
 static cudaError_t launch_int4(GemvArgs& a, int num_sms, cudaStream_t st) {
   const int granules = (a.N / 16 + gv::kRg - 1) / gv::kRg;
   a.pitch = a.K * 2 + 64;  // the lanes' 16-byte pieces of two rows never collide
@@ -644,12 +663,15 @@ static cudaError_t launch_int4(GemvArgs& a, int num_sms, cudaStream_t st) {
   a.tiles = (a.T + a.tile_rows - 1) / a.tile_rows;
   a.tile_rows = (a.T + a.tiles - 1) / a.tiles;
   set_steps(a, (long long)granules * a.tiles / num_sms);
-  return launch_gemv<kFmt, kBf16, kZeros>(a, (long long)granules * a.tiles, smem, num_sms, st);
+  return launch_gemv<kFmt, kBf16, kZeros, kCenter>(a, (long long)granules * a.tiles, smem, num_sms, st);
 }
 template <W4 kFmt>
 static cudaError_t launch_int4(GemvArgs& a, const Int4Product& p, cudaStream_t st) {
-  if (p.act_f16) return p.zeros ? launch_int4<kFmt, false, true>(a, p.num_sms, st) : launch_int4<kFmt, false, false>(a, p.num_sms, st);
-  return p.zeros ? launch_int4<kFmt, true, true>(a, p.num_sms, st) : launch_int4<kFmt, true, false>(a, p.num_sms, st);
+  if (p.act_f16 && p.out_f32)
+    return p.zeros ? launch_int4<kFmt, false, true, true>(a, p.num_sms, st) : launch_int4<kFmt, false, false, true>(a, p.num_sms, st);
+  if (p.act_f16)
+    return p.zeros ? launch_int4<kFmt, false, true, false>(a, p.num_sms, st) : launch_int4<kFmt, false, false, false>(a, p.num_sms, st);
+  return p.zeros ? launch_int4<kFmt, true, true, false>(a, p.num_sms, st) : launch_int4<kFmt, true, false, false>(a, p.num_sms, st);
 }
 
 cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st) {

@@ -321,16 +321,20 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       const int h = warp >> 1;  // 0, 1
       uint32_t j = 0;
       int base = 0;  // squares before the unit
+      // FP32 results: the two halves of the reduction into an accumulator each, summed in the epilogue, in place of
+      // two units' accumulators.  The tensor core truncates where it adds (1e-6 of the result's norm after 4096 terms
+      // in one accumulator), and BF16's rounding hides that.
+      const bool halves = kIssuers == 1 && a.out_f32;
       bool ok = true;
       for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok; w.next(ctl, total), ++j, base += a.steps) {
         int row0;
         const uint32_t idesc =
             idesc_bf16(128 * kCtas, (w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) | (kBackward ? 1u << 15 : 0u);
-        const uint32_t buf = j & 1u;
-        if (!warp_wait(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
+        const uint32_t buf = halves ? 0u : j & 1u;
+        if (!warp_wait(ctl.acc_empty + buf, ((halves ? j : j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * Plan::kAccBuf + (uint32_t)h * Plan::kAccIssuer;
-        const int end = base + a.steps;
+        uint32_t d = tmem + buf * Plan::kAccBuf + (uint32_t)h * Plan::kAccIssuer;
+        const int end = base + a.steps, second = halves && a.steps > 1 ? base + a.steps / 2 : end;
         uint32_t acc = 0;
         for (int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base; i < end; i += kIssuers) {
           const int sa = i % kStagesA, sb = i % kStagesB;
@@ -340,6 +344,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
             break;
           }
           tc_fence_after();
+          if (i == second) d += Plan::kAccBuf, acc = 0;
           const uint32_t st = ring_addr + (uint32_t)(sa * Plan::kABytes);
           const uint64_t ad = kBackward ? sw128_desc_mn(st) : sw128_desc(st);
           const uint64_t bd = sw128_desc(ring_b_addr + (uint32_t)(sb * Plan::kBBytes));
@@ -512,8 +517,9 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       int row0;
       const int rows = w.rows(ctl, row0);
       const float gs = __ldg(a.gscale + w.e);
-      const uint32_t buf = j & 1u;
-      if (!warp_wait(ctl.acc_full + buf, (j >> 1) & 1u, abort_flag, a.st, 918)) break;
+      const bool halves = kIssuers == 1 && a.out_f32;  // see the issuers
+      const uint32_t buf = halves ? 0u : j & 1u;
+      if (!warp_wait(ctl.acc_full + buf, (halves ? j : j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
       uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * Plan::kAccBuf;
       if (kIssuers == 2 && a.steps == 1) t += (j & 1u) * Plan::kAccIssuer;  // unit j's only square is the CTA's j-th
@@ -521,12 +527,13 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       if (f0 < a.n_out) {
         for (int col = 0; col < rows; col += 32) {
           uint32_t v[2][16];
-          if (kIssuers == 2 && a.steps > 1) {  // the sum of both issuers' accumulators
+          if ((kIssuers == 2 || halves) && a.steps > 1) {  // the sum of two accumulators
+            constexpr uint32_t kOther = kIssuers == 2 ? Plan::kAccIssuer : Plan::kAccBuf;
             uint32_t v1[2][16];
             tmem_ld16_nw(t + (uint32_t)col, v[0]);
             tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);
-            tmem_ld16_nw(t + (uint32_t)col + Plan::kAccIssuer, v1[0]);
-            tmem_ld16_nw(t + (uint32_t)col + Plan::kAccIssuer + 16u, v1[1]);
+            tmem_ld16_nw(t + (uint32_t)col + kOther, v1[0]);
+            tmem_ld16_nw(t + (uint32_t)col + kOther + 16u, v1[1]);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
             for (int i = 0; i < 32; ++i)
