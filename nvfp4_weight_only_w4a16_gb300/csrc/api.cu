@@ -973,8 +973,11 @@ nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t*
     return bad(NVFP4_MOE_ERR_INVALID_ARG, "a row stride is below the row length, above 2^24 or no multiple of 8");
   if (!backward && h->path == NVFP4_MOE_PATH_DECODE && R > kGemvMaxRows)
     return bad(NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "the decode path takes at most 2048 rows");
+  // AUTO streams the weights through the row kernel up to 8 rows an expert: at 128 experts of 1536 x 4096 it takes 70,
+  // 102, 122 and 167 us at 1, 4, 8 and 12 rows an expert, the GEMM 105, 144, 155 and 154; at 32 of 1024 x 1024 the two
+  // meet at 8 as well (25.5 and 24.6).
   const bool stream = !backward && (h->path == NVFP4_MOE_PATH_DECODE ||
-                                    (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= 4 * E));
+                                    (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= 8 * E));
   DeviceGuard g(h->cfg.device);
   const GroupedTiling tiling = grouped_tiling(E, R, backward ? K / 128 : (N + 127) / 128);
   CUtensorMap map{};

@@ -15,6 +15,13 @@
 // kWarps / KS at a time, of which each is shared by KS warps that take every KS-th
 // 128-element step of K and are summed through shared memory in a fixed order, one
 // barrier each time.  The rings run ahead across that, and across new rows of x.
+// Rows of x that do not fit beside the rings are spread over a cluster (INT4): each
+// of its CTAs takes a slice of K, and sends its sums to the CTA that stores them,
+// which adds them in a fixed order one batch later.  (8192 x 8192, 16 tokens: 28 us
+// against 36 as tiles of 4 rows, each with the weights converted again; 4096 x 16384:
+// 26 against 49.  16 rows at a time instead of twice 8 was slower, 18 us against 15
+// for 4096 x 4096: work per weight and token outweighs the conversion, and the
+// shorter slices need more batches.)
 //
 // Both formats run on FP16 operands.  x enters as FP16 times a power of two per row
 // that brings its largest finite magnitude into [2^13, 2^14); what that drops lies
@@ -40,10 +47,12 @@ namespace gv {
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kStep = 128;
 constexpr int kRg = 2;            // 16-row groups a warp multiplies with the same x: two chains of MMAs
-constexpr int kRows = 8;          // rows of x at a time: the MMA's N
+constexpr int kRows = 8;          // rows of x in one MMA: its N
+constexpr int kShared = 32 * 32 * 4;  // bytes of a batch's sums, where a cluster adds them: 4 granules'
+constexpr int kMaxCluster = 8;
 constexpr int kDepth = 3;         // steps in flight per warp, kRg KB of codes each
 constexpr int kMaxTiles = 256 + kGemvMaxRows / 2;  // NVFP4: of a call; all but an expert's last have 2 rows or more
-constexpr int smem_for(bool nvfp4) { return (nvfp4 ? 180 : 190) * 1024; }  // of rings and x; the rest is static
+constexpr int smem_for(bool nvfp4) { return (nvfp4 ? 180 : 192) * 1024; }  // of rings and x; the rest is static
 }  // namespace gv
 
 enum class W4 { kNvfp4, kInt4G32, kInt4G64, kInt4G128 };
@@ -63,9 +72,10 @@ struct GemvArgs {
   int T;
   // both
   int N, K;
-  int KS;          // warps along K per granule: 1, 2, 4, 8, 16
-  int tile_rows;   // rows of x per tile, up to 8
+  int S;           // CTAs of a cluster, which share K (1 for NVFP4)
   int tiles;       // INT4: ceil(T / tile_rows)
+  int KS;          // warps along the CTA's slice of K per granule: 1, 2, 4, 8, 16
+  int tile_rows;   // rows of x per tile, up to 8
   int pitch;       // bytes of one x row in shared memory
   const void* x;
   long long ldx;
@@ -261,78 +271,84 @@ __device__ __forceinline__ float2 pow2_pair(int e) {
 // (in [2^13, 2^14) unless it is below FP32's normal range).
 __device__ __forceinline__ int row_exponent(unsigned bits) { return bits ? (int)(bits >> 23) - 140 : 0; }
 
+// sum + the two halves of w times s (FP16), in FP32.
+__device__ __forceinline__ float add_halves(float sum, uint32_t w, uint16_t s) {
+  asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %1;\n fma.rn.f32.f16 %0, l, %2, %0;\n fma.rn.f32.f16 %0, h, %2, %0;\n}"
+      : "+f"(sum)
+      : "r"(w), "h"(s));
+  return sum;
+}
+
 // x rows into shared memory as FP16 times 2^-p per row; INT4: elements 2, 3, 6 and 7 of every 8 times another
-// 2^-4, and 2^-24 (kCenter: 1) times the sums over each group of the matrix into sums[group][8].  In two parts: start() copies the
-// rows as they are (bulk copies, by one thread), finish() waits for them, finds each row's p and converts in place.
+// 2^-4, and 2^-24 (kCenter: 1) times the sums over each group of the matrix into sums[group][8].  In two parts:
+// start() copies the rows as they are (bulk copies, by one thread), finish() waits for them, finds each row's p and
+// converts in place; a row's 16-byte pieces are shared by kWarps / rows warps.
 // (Small loops on purpose: a call's first use of its code comes from memory, and this runs before any product.)
 template <W4 kFmt, bool kBf16, bool kCenter>
 struct Stage {
   uint8_t* xs;
-  int pitch, per, rows;  // 16-byte pieces of a row
-  int r0, p0, dr, dp;    // the thread's first piece, and the step from one to the next
-  __device__ __forceinline__ Stage(const GemvArgs& a, uint8_t* x) : xs(x), pitch(a.pitch), per(a.K / 8), rows(0) {
-    r0 = (int)threadIdx.x / per, p0 = (int)threadIdx.x - r0 * per;
-    dr = gv::kThreads / per, dp = gv::kThreads - dr * per;
-  }
-  __device__ __forceinline__ void next(int& r, int& p) const {
-    r += dr, p += dp;
-    if (p >= per) p -= per, ++r;
-  }
+  int pitch, per, rows;  // pieces of a row (of the CTA's slice)
+  int first;             // element the slice begins at
+  __device__ __forceinline__ Stage(const GemvArgs& a, uint8_t* x, int step0, int steps)
+      : xs(x), pitch(a.pitch), per(steps * (gv::kStep / 8)), rows(0), first(step0 * gv::kStep) {}
   __device__ __forceinline__ void start(const GemvArgs& a, int row0, uint64_t* bar) {  // one thread
     mbar_arrive_expect_tx(bar, (uint32_t)(rows * per * 16));
 #pragma unroll 1
     for (int r = 0; r < rows; ++r)
-      bulk_g2s(xs + r * pitch, static_cast<const uint16_t*>(a.x) + (long long)(row0 + r) * a.ldx, (uint32_t)(per * 16), bar);
+      bulk_g2s(xs + r * pitch, static_cast<const uint16_t*>(a.x) + (long long)(row0 + r) * a.ldx + first, (uint32_t)(per * 16), bar);
   }
   static __device__ __forceinline__ float value(uint32_t w, int hi) {
     return kBf16 ? __uint_as_float(hi ? w & 0xFFFF0000u : w << 16)
                  : __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xFFFFu)));
   }
-  // amax: the rows' largest finite magnitudes, zero on entry.  False, in every thread, when the copies did not land
-  // in time (reported).  The barrier after the writes is the caller's.
+  // amax: the rows' largest finite magnitudes (FP32 bits, which order alike), zero on entry.  False, in every thread,
+  // when the copies did not land in time (reported).  The barrier after the writes is the caller's.
   __device__ __forceinline__ bool finish(float* sums, unsigned* amax, uint64_t* bar, uint32_t parity, volatile int* abort,
                                          DeviceStatus* st) {
     const bool landed = mbar_wait(bar, parity, abort, st, 921);
-    const int lane = threadIdx.x & 31;
-    int r = r0, p = p0;
-#pragma unroll 1
-    for (int i = threadIdx.x & ~31; landed && i < rows * per; i += gv::kThreads, next(r, p)) {  // whole warps
-      unsigned m = 0;  // FP32 bits order like the magnitudes
-      if (r < rows) {
-        const uint4 v = *reinterpret_cast<const uint4*>(xs + r * pitch + p * 16);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const unsigned b = __float_as_uint(fabsf(value(w[j >> 1], j & 1)));
-          if (b < 0x7F800000u) m = max(m, b);
-        }
+    const int lane = threadIdx.x & 31, warps = gv::kWarps / rows, r = (int)(threadIdx.x >> 5) / warps;
+    const int p0 = ((int)(threadIdx.x >> 5) - r * warps) * 32, dp = warps * 32;
+    uint8_t* row = xs + r * pitch;
+    if (landed && r < rows) {
+      constexpr unsigned kInf = kBf16 ? 0x7F80u : 0x7C00u;
+      unsigned m = 0;
+#pragma unroll 2
+      for (int p = p0 + lane; p < per; p += dp) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + p * 16);
+        m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+        m = __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
       }
-      // rows are multiples of 16 pieces: half a warp is always in one row
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      if ((lane & 15) == 0 && r < rows) atomicMax(amax + r, m);
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+      if (m >= kInf) {  // once more, of the finite ones
+        m = 0;
+#pragma unroll 1
+        for (int i = 8 * (p0 + lane); i < 8 * per; i += i % 8 == 7 ? 8 * dp - 7 : 1) {
+          const unsigned e = reinterpret_cast<const uint16_t*>(row)[i] & 0x7FFFu;
+          if (e < kInf) m = max(m, e);
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+      }
+      if (lane == 0) atomicMax(amax + r, __float_as_uint(value(m, 0)));
     }
     if (__syncthreads_or(!landed)) return false;
+    if (r >= rows) return true;
     constexpr int kLanes = kFmt == W4::kNvfp4 ? 1 : 16 / int4_groups(kFmt);  // threads per group
-    r = r0, p = p0;
+    const float2 f2 = pow2_pair(-row_exponent(amax[r]));
 #pragma unroll 1
-    for (int i = threadIdx.x & ~31; i < rows * per; i += gv::kThreads, next(r, p)) {
-      const bool ok = r < rows;
-      uint4* at = reinterpret_cast<uint4*>(xs + (ok ? r : 0) * pitch + p * 16);
+    for (int p = p0 + lane; p - lane < per; p += dp) {  // whole warps, for the shuffles
+      const bool ok = p < per;  // rows are multiples of 16 pieces, so half a warp is in or out
+      uint4* at = reinterpret_cast<uint4*>(row + (ok ? p : 0) * 16);
       const uint4 v = *at;
-      const float2 f2 = pow2_pair(-row_exponent(amax[ok ? r : 0]));
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t o[4];
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        __half2 h = __floats2half2_rn(value(w[j], 0) * f2.x * f2.y, value(w[j], 1) * f2.x * f2.y);
-        if (kFmt != W4::kNvfp4) {
-          if (j & 1) h = __hmul2(h, __float2half2_rn(0.0625f));  // what the MMA multiplies with q 2^-20
-          const float2 f = __half22float2(h);
-          sum += (j & 1 ? 16.0f : 1.0f) * (f.x + f.y);
-        }
+        // odd pairs of INT4: what the MMA multiplies with q 2^-20
+        const float f = kFmt != W4::kNvfp4 && (j & 1) ? f2.y * 0.0625f : f2.y;
+        const __half2 h = __floats2half2_rn(value(w[j], 0) * f2.x * f, value(w[j], 1) * f2.x * f);
         o[j] = *reinterpret_cast<const uint32_t*>(&h);
+        if (kFmt != W4::kNvfp4) sum = add_halves(sum, o[j], j & 1 ? 0x4C00u : 0x3C00u);  // times 16, 1
       }
       if (ok) *at = make_uint4(o[0], o[1], o[2], o[3]);
       if (kFmt != W4::kNvfp4) {  // a group's pieces belong to neighbouring lanes
@@ -348,13 +364,14 @@ struct Stage {
 template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
 __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   using S = Step<kFmt, kZeros>;
-  extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the group sums
-  __shared__ unsigned amax[2][gv::kRows];                  // of this tile and, zero, of the next
-  __shared__ short tile_expert[gv::kMaxTiles];             // NVFP4
-  __shared__ int tile_row0[gv::kMaxTiles], wsum[8];
+  constexpr int kSums = 4 * gv::kRg;                // of a lane
+  extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the cluster's and the group sums
+  __shared__ unsigned amax[2][gv::kRows];           // of this tile and, zero, of the next
+  __shared__ short tile_expert[S::kNv ? gv::kMaxTiles : 1];
+  __shared__ int tile_row0[S::kNv ? gv::kMaxTiles : 1], wsum[8];
   __shared__ uint64_t x_bar;  // x rows landed
   __shared__ int abort_flag;
-  __shared__ float red[2][gv::kWarps][4 * gv::kRg][32];
+  __shared__ float red[2][gv::kWarps][kSums][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int tiles = a.tiles;
@@ -394,17 +411,20 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     }
     __syncthreads();
   }
-  const int steps = a.K / gv::kStep, rgroups = a.N / 16;
+  const int rank = S::kNv || a.S == 1 ? 0 : (int)cluster_rank();
+  const int all_steps = a.K / gv::kStep, rgroups = a.N / 16;
+  const int step0 = S::kNv ? 0 : rank * (all_steps / a.S) + min(rank, all_steps % a.S);  // this CTA's slice of K
+  const int steps = S::kNv ? all_steps : all_steps / a.S + (rank < all_steps % a.S);
   const int granules = (rgroups + gv::kRg - 1) / gv::kRg;  // of a matrix
   const int RG = gv::kWarps / a.KS;                        // granules at a time
   const int ks = warp % a.KS, wg = warp / a.KS;
-  // this CTA's run of granules.  NVFP4: tile * granules + granule, over all CTAs.  INT4: CTAs c, c + 1, ..
+  // this CTA's run of granules.  NVFP4: tile * granules + granule, over all CTAs.  INT4: clusters c, c + 1, ..
   // c + tiles - 1 take the same granules for one tile of x each, so that they share the weights in L2
   int tile = 0, left = 0x7FFFFFFF;  // the tile at the run's next granule, and how many it has from there on
   int u0, u1;
   {
-    const int n = S::kNv ? (int)gridDim.x : (int)gridDim.x / tiles;
-    const int c = S::kNv ? (int)blockIdx.x : (int)blockIdx.x / tiles;
+    const int n = S::kNv ? (int)gridDim.x : (int)gridDim.x / a.S / tiles;
+    const int c = S::kNv ? (int)blockIdx.x : (int)blockIdx.x / a.S / tiles;
     const int all = S::kNv ? tiles * granules : granules;
     const int base = all / n, extra = all - base * n;
     u0 = c * base + min(c, extra);
@@ -414,12 +434,14 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       tile = u0 / granules;
       left = granules - (u0 - tile * granules);
     } else {
-      tile = (int)blockIdx.x % tiles;
+      tile = (int)blockIdx.x / a.S % tiles;
     }
   }
+  if (!S::kNv && a.S > 1) cluster_arrive();  // the first batch waits for it: every CTA has begun
   uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kSlot;
-  float* sums = reinterpret_cast<float*>(xs + (size_t)a.tile_rows * a.pitch);
-  Stage<kFmt, kBf16, kCenter> stage(a, xs);
+  float* shared = reinterpret_cast<float*>(xs + (size_t)a.tile_rows * a.pitch);  // S > 1: [2][source][kShared / S]
+  float* sums = shared + (!S::kNv && a.S > 1 ? 2 * gv::kShared / 4 : 0);
+  Stage<kFmt, kBf16, kCenter> stage(a, xs, step0, steps);
   int row0, rows;
   const auto tile_rows = [&] {  // the rows of `tile`
     row0 = S::kNv ? tile_row0[tile] : tile * a.tile_rows;
@@ -455,7 +477,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
           pc = p + (g & 3) * 1024 + lane * 16;
           ps = p + kTileCodes + (g & 3) * 128 + (lane >> 3) * kTileBytes + (lane & 7) * 16;
         } else {
-          pc = a.packed + ((size_t)g * steps + ks) * S::kStride + lane * 16;
+          pc = a.packed + ((size_t)g * all_steps + step0 + ks) * S::kStride + lane * 16;
         }
         return true;
       }
@@ -489,6 +511,28 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   const float* sl0 = sums + ks * (S::kGroups * gv::kRows) + 2 * (lane & 3);
   int phase = 0, tphase = 0, slot = 0;
   bool fresh = true;  // x of `tile` is still to be converted
+  bool dead = false;  // its copy did not land
+  float2 up = make_float2(1.0f, 1.0f);  // the power of two of row 2 (lane & 3) + (warp & 1), the one whose sums the lane adds
+  // y, the lane's sum s (row group, element of the accumulator) of a granule, into out
+  const auto store = [&](int granule, int s, float y) {
+    const int rg = granule * gv::kRg + (s >> 2), r = 2 * (lane & 3) + (s & 1);
+    if (r < rows && rg < rgroups) {
+      const long long o = (long long)(row0 + r) * a.ldo + 16 * rg + (lane >> 2) + 8 * ((s >> 1) & 1);
+      if (a.out_f32) static_cast<float*>(a.out)[o] = y;
+      else if (S::kNv || kBf16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
+      else static_cast<__half*>(a.out)[o] = __float2half_rn(y);
+    }
+  };
+  // S > 1: row j of a batch's sums is added and stored by CTA j % S, from what every CTA has put into its `shared`
+  int pg0 = 0, pj = 0;  // the batch before: its first granule, its rows
+  const auto add_shared = [&] {
+    const float* from = shared + (phase ^ 1) * (gv::kShared / 4) + lane;
+    for (int j = rank + a.S * warp; j < pj; j += a.S * gv::kWarps) {
+      float y = 0.f;
+      for (int c = 0; c < a.S; ++c) y += from[(c * (gv::kShared / 128 / a.S) + j / a.S) * 32];
+      if (!dead) store(pg0 + j / kSums, j % kSums, y);
+    }
+  };
   for (int u = u0; u < u1;) {
     if (left == 0) {  // the next tile: its rows of x
       ++tile;
@@ -505,11 +549,12 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     }
     if (fresh) {
       if (!stage.finish(sums, amax[tphase], &x_bar, (uint32_t)tphase, &abort_flag, a.st)) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        return;
+        dead = true;
+        if (S::kNv || a.S == 1) break;  // a cluster's others wait for this CTA's sums, which then count for nothing
       }
       if (threadIdx.x < gv::kRows) amax[tphase ^ 1][threadIdx.x] = 0u;
       if (S::kNv) gs = __ldg(a.gscale + tile_expert[tile]);
+      up = pow2_pair(row_exponent(amax[tphase][2 * (lane & 3) + (warp & 1)]) + (S::kNv || kCenter ? 0 : 24));
       // a lane whose token does not exist reads the last one's row: its column of the products is not stored
       xl0 = xs + min(lane >> 2, rows - 1) * a.pitch + (lane & 3) * (S::kNv ? 32 : 16) + ks * 256;
       __syncthreads();
@@ -517,12 +562,8 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     }
     const int n = min(RG, min(left, u1 - u));
     const int g0 = S::kNv ? granules - left : u;
-    float acc[gv::kRg][4];
-#pragma unroll
-    for (int q = 0; q < gv::kRg; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[q][i] = 0.f;
-    if (wg < n) {
+    float acc[gv::kRg][4] = {};
+    if (wg < n && !dead) {
       const uint8_t* xl = xl0;
       const float* sl = sl0;
 #pragma unroll 1
@@ -539,41 +580,47 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
         sl += a.KS * (S::kGroups * gv::kRows);
       }
     }
-    // the batch's sums into out: slot s of a lane is row group s / 4, element s % 4 of the accumulator
-    const auto store = [&](int granule, int s, float y) {
-      const int rg = (g0 + granule) * gv::kRg + (s >> 2), r = 2 * (lane & 3) + (s & 1);
-      if (r < rows && rg < rgroups) {
-        const long long o = (long long)(row0 + r) * a.ldo + 16 * rg + (lane >> 2) + 8 * ((s >> 1) & 1);
-        const float2 up = pow2_pair(row_exponent(amax[tphase][r]) + (S::kNv || kCenter ? 0 : 24));
-        y = y * up.x * up.y;
-        if (S::kNv) y *= gs;
-        if (a.out_f32) static_cast<float*>(a.out)[o] = y;
-        else if (S::kNv || kBf16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
-        else static_cast<__half*>(a.out)[o] = __float2half_rn(y);
-      }
-    };
-    float(*part)[4 * gv::kRg][32] = red[phase];
-    phase ^= 1;  // the next batch's sums go to the other buffer: one barrier a batch
+    // the batch's sums into out; the next batch's go to the other buffer: one barrier a batch
+    const bool cluster = !S::kNv && a.S > 1;
+    float(*part)[kSums][32] = red[phase];
 #pragma unroll
-    for (int s = 0; s < 4 * gv::kRg; ++s) part[warp][s][lane] = acc[s >> 2][s & 3];
+    for (int s = 0; s < kSums; ++s) part[warp][s][lane] = acc[s >> 2][s & 3];
+    if (cluster) {
+      cluster_wait();  // the last batch's sums are there, and those of the one before are read
+      add_shared();
+    }
     __syncthreads();
-    for (int j = warp; j < 4 * gv::kRg * n; j += gv::kWarps) {
-      const int g = j / (4 * gv::kRg), s = j % (4 * gv::kRg);
+    static_assert(gv::kWarps % kSums == 0, "a warp's rows j are all even or all odd");
+    for (int j = warp; j < kSums * n; j += gv::kWarps) {
+      const int g = j / kSums, s = j % kSums;
       float y = 0.f;
       for (int w = 0; w < a.KS; ++w) y += part[g * a.KS + w][s][lane];
-      store(g, s, y);
+      y = y * up.x * up.y;
+      if (S::kNv) y *= gs;
+      if (cluster)
+        st_cluster(shared + phase * (gv::kShared / 4) + (rank * (gv::kShared / 128 / a.S) + j / a.S) * 32 + lane, j % a.S, y);
+      else store(g0 + g, s, y);
     }
+    if (cluster) {
+      cluster_arrive();
+      pg0 = g0, pj = kSums * n;
+    }
+    phase ^= 1;
     u += n;
     left -= n;
   }
+  if (!S::kNv && a.S > 1) {
+    cluster_wait();
+    add_shared();
+  }
+  if (dead) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Warps along K: few, for few barriers, but as many as keep every warp busy with the CTA's share of granules.
-static void set_steps(GemvArgs& a, long long granules_per_cta) {
-  const int steps = a.K / gv::kStep;
+static void set_steps(GemvArgs& a, int steps, long long granules_per_cta, int least = 1) {
   if (granules_per_cta < 1) granules_per_cta = 1;
   float best = 0.f;
-  for (int ks = gv::kWarps; ks >= 1; ks /= 2) {
+  for (int ks = gv::kWarps; ks >= least; ks /= 2) {
     const int spw = (steps + ks - 1) / ks;
     float used = (float)steps / (float)(ks * spw);  // of the warps' steps
     const int rg = gv::kWarps / ks;
@@ -586,48 +633,47 @@ static void set_steps(GemvArgs& a, long long granules_per_cta) {
   }
 }
 
-// Rows of x per tile, as many as fit beside the rings.  row_bytes: shared memory of one row of x; fixed: of the
-// sums; slot_bytes: of a ring's slot.  Returns the dynamic shared memory.
-static size_t set_smem(GemvArgs& a, int rows, size_t row_bytes, size_t fixed, int slot_bytes, int smem) {
-  fixed += (size_t)gv::kWarps * gv::kDepth * slot_bytes;
-  const int fit = (int)((smem - fixed) / row_bytes);  // at least 1 at K = 16384
-  a.tile_rows = fit < gv::kRows ? fit : gv::kRows;
-  if (rows < a.tile_rows) a.tile_rows = rows;
-  return fixed + a.tile_rows * row_bytes;
-}
-
+// The kernel over as many clusters of a.S CTAs as there are granules (of all tiles), or as run at a time.
 template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
-static cudaError_t launch_gemv(const GemvArgs& a, long long ctas, size_t smem, int num_sms, cudaStream_t st) {
+static cudaError_t launch_gemv(const GemvArgs& a, long long granules, size_t smem, int num_sms, cudaStream_t st) {
   static std::mutex mu;
-  static bool done[64] = {};
+  static int fit[64][gv::kMaxCluster + 1] = {};  // clusters that run at a time, by device and size; 0: not known yet
+  const auto kernel = gemv_kernel<kFmt, kBf16, kZeros, kCenter>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  {  // the opt-in shared-memory size, once per device
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(gemv_kernel<kFmt, kBf16, kZeros, kCenter>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               gv::smem_for(kFmt == W4::kNvfp4));
-      if (e != cudaSuccess) return e;
-      if (dev < 64) done[dev] = true;
-    }
-  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(ctas < num_sms ? ctas : num_sms));
+  cfg.gridDim = dim3((unsigned)(num_sms / a.S * a.S));
   cfg.blockDim = dim3(gv::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<kFmt, kBf16, kZeros, kCenter>, a);
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)a.S;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.S > 1 ? 2 : 1;
+  int n = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64) n = fit[dev][a.S];
+    if (n == 0) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, gv::smem_for(kFmt == W4::kNvfp4));
+      if (e == cudaSuccess && a.S > 1) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (a.S == 1) n = num_sms;
+      if (n < 1) n = 1;
+      if (dev < 64) fit[dev][a.S] = n;
+    }
+  }
+  cfg.gridDim = dim3((unsigned)(granules < n ? granules : n) * a.S);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// the longest row of x: two of them fit beside the rings (kMaxTiles), or one with its sums
+// NVFP4: two of the longest rows of x fit beside the rings (kMaxTiles).
 static_assert(gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kSlot + 2 * (16384 * 2 + 16) <= gv::smem_for(true), "x");
-static_assert(gv::kWarps * gv::kDepth * Step<W4::kInt4G32, true>::kSlot + 16384 * 2 + 64 + 16384 <= gv::smem_for(false), "x");
 
 cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   const int Np = (p.N + 127) / 128 * 128;
@@ -646,24 +692,42 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
   a.st = p.status;
+  a.S = 1;
   const int granules = (p.N / 16 + gv::kRg - 1) / gv::kRg;
   const int touched = p.R < p.E ? p.R : p.E;
-  set_steps(a, (long long)touched * granules / p.num_sms);
+  set_steps(a, p.K / gv::kStep, (long long)touched * granules / p.num_sms);
   a.pitch = p.K * 2 + 16;  // rows 16 bytes apart in the banks: the lanes' 32-byte pieces of two rows never collide
-  const size_t smem = set_smem(a, p.R, a.pitch, 0, Step<W4::kNvfp4, false>::kSlot, gv::smem_for(true));
-  return launch_gemv<W4::kNvfp4, true, false, false>(a, (long long)(touched + p.R / a.tile_rows) * granules, smem, p.num_sms, st);
+  const size_t rings = (size_t)gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kSlot;
+  const int fit = (int)((gv::smem_for(true) - rings) / a.pitch);
+  a.tile_rows = fit < gv::kRows ? fit : gv::kRows;
+  if (p.R < a.tile_rows) a.tile_rows = p.R;
+  return launch_gemv<W4::kNvfp4, true, false, false>(a, (long long)(touched + p.R / a.tile_rows) * granules,
+                                                     rings + (size_t)a.tile_rows * a.pitch, p.num_sms, st);
 }
+
+// Shared memory of a CTA that takes `steps` steps of K for `rows` rows of x.
+template <W4 kFmt, bool kZeros>
+static constexpr size_t int4_smem(int rows, int steps, bool cluster) {
+  return (size_t)gv::kWarps * gv::kDepth * Step<kFmt, kZeros>::kSlot + (size_t)rows * (steps * 256 + 64) +
+         (size_t)steps * int4_groups(kFmt) * gv::kRows * 4 + (cluster ? 2 * gv::kShared : 0);
+}
+static_assert(int4_smem<W4::kInt4G32, true>(gv::kRows, 16384 / gv::kStep / gv::kMaxCluster, true) <= gv::smem_for(false), "x");
 
 template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
 static cudaError_t launch_int4(GemvArgs& a, int num_sms, cudaStream_t st) {
-  const int granules = (a.N / 16 + gv::kRg - 1) / gv::kRg;
-  a.pitch = a.K * 2 + 64;  // the lanes' 16-byte pieces of two rows never collide
-  const size_t sums = (size_t)a.K / 128 * int4_groups(kFmt) * gv::kRows * 4;
-  const size_t smem = set_smem(a, a.T, a.pitch, sums, Step<kFmt, kZeros>::kSlot, gv::smem_for(false));
-  a.tiles = (a.T + a.tile_rows - 1) / a.tile_rows;
+  const int granules = (a.N / 16 + gv::kRg - 1) / gv::kRg, steps = a.K / gv::kStep;
+  a.tiles = (a.T + gv::kRows - 1) / gv::kRows;
   a.tile_rows = (a.T + a.tiles - 1) / a.tiles;
-  set_steps(a, (long long)granules * a.tiles / num_sms);
-  return launch_gemv<kFmt, kBf16, kZeros, kCenter>(a, (long long)granules * a.tiles, smem, num_sms, st);
+  int per = steps;
+  a.S = 1;
+  while (int4_smem<kFmt, kZeros>(a.tile_rows, per, a.S > 1) > (size_t)gv::smem_for(false)) {  // at kMaxCluster it fits
+    a.S *= 2;
+    per = (steps + a.S - 1) / a.S;
+  }
+  a.pitch = per * 256 + 64;  // the lanes' 16-byte pieces of two rows never collide
+  set_steps(a, steps / a.S, (long long)granules * a.tiles * a.S / num_sms, a.S > 1 ? 4 : 1);  // 4: a batch fits into kShared
+  return launch_gemv<kFmt, kBf16, kZeros, kCenter>(a, (long long)granules * a.tiles,
+                                                   int4_smem<kFmt, kZeros>(a.tile_rows, per, a.S > 1), num_sms, st);
 }
 template <W4 kFmt>
 static cudaError_t launch_int4(GemvArgs& a, const Int4Product& p, cudaStream_t st) {

@@ -629,11 +629,14 @@ static cudaError_t set_grouped_attrs() {
 }
 
 GroupedTiling grouped_tiling(int E, int R, int out_blocks) {
-  // pairs where there are two feature blocks to pair; rows per token tile: wide tiles dequantise a weight square
-  // once for many rows, narrow ones leave shared memory for deeper rings, which the few-rows end needs
+  // Pairs where there are two feature blocks to pair. Rows per token tile: a wide tile dequantises a weight square
+  // once for many rows, a narrow one leaves shared memory for deeper rings. At 128 experts of 1536 x 4096, counts
+  // spread by half around the mean (sigma 0.5), forward / backward, us for tiles of 64, 128 and 256 rows: 32 rows an
+  // expert 143 / 140, 145 / 146, 187 / 171; 48 167 / 171, 146 / 153, 190 / 175; 96 262 / 260, 172 / 193, 198 / 190;
+  // 112 285 / 286, 184 / 204, 200 / 195; 144 345 / 352, 209 / 234, 209 / 205; 256 559 / 573, 332 / 374, 282 / 273.
   const int avg = R / E;
   GroupedTiling t;
-  t.variant = (out_blocks > 1 ? 3 : 0) + (avg > 64 ? 2 : avg > 32 ? 1 : 0);
+  t.variant = (out_blocks > 1 ? 3 : 0) + (avg > 112 ? 2 : avg > 32 ? 1 : 0);
   t.box = kGroupedVariants[t.variant].box;
   return t;
 }

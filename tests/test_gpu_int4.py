@@ -74,6 +74,19 @@ def test_shapes(N, K, T):
     verify(m, x, run(m, x))
 
 
+@pytest.mark.parametrize("T,N,K,group,f16", [(16, 4848, 4096, 32, False), (16, 1056, 8320, 32, True), (9, 304, 4224, 64, True),
+                                             (16, 208, 16384, 32, False), (8, 272, 16384, 128, False), (10, 16, 2560, 64, True),
+                                             (5, 96, 12416, 32, True), (16, 2080, 2176, 128, False)])
+@pytest.mark.parametrize("out_f32", [False, True])
+def test_rows_that_share_a_cluster(T, N, K, group, f16, out_f32):
+    m = Matrix(N, K, group, True, f16, out_f32=out_f32)
+    x = rows_of(m, T)
+    x *= torch.exp2(torch.arange(K, device=DEV) // 128 % 5 - 2.0).to(m.act)    # slices of different size
+    got = run(m, x)
+    verify(m, x, got)
+    assert torch.equal(got, run(m, x))
+
+
 def test_wide_matrix():
     m = Matrix(12576, 4096, 128, True, False)
     x = rows_of(m, 2)
