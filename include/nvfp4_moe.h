@@ -497,11 +497,12 @@ nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uin
  *   out, dx  BF16 or FP32 (config.out_dtype) DEVICE, 16-byte aligned; must not
  *            overlap the input
  *   ld*      at least the row length, a multiple of 8, at most 2^24
- * Products are exact in FP32 and accumulated in FP32; one rounding to BF16 at
- * the end.  The forward takes the streaming kernel for few rows (by default up
- * to 4 per expert on average, nvfp4_moe_set_path forces either; the streaming
- * kernel takes at most 2048 rows), the tcgen05 GEMM above; the backward always
- * the GEMM. */
+ * Products are exact and accumulated in FP32; one rounding to BF16 at the end.
+ * The forward takes the streaming kernel for few rows (by default up to 8 per
+ * expert on average; nvfp4_moe_set_path forces either; the streaming kernel takes
+ * at most 2048 rows), the tcgen05 GEMM above; the backward always the GEMM.  The
+ * streaming kernel multiplies x as FP16 times a power of two per row: what lies
+ * 2^-38 below a row's largest magnitude is rounded away. */
 nvfp4_moe_status nvfp4_grouped_forward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* x, int64_t ldx,
                                        void* out, int64_t ldo, cudaStream_t stream);
 nvfp4_moe_status nvfp4_grouped_backward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* dy, int64_t ld_dy,
@@ -546,10 +547,13 @@ nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* 
 
 /* out [T][N] as above, 1 <= T <= max_tokens; x [T][K] and out DEVICE, 16-byte
  * aligned, rows ldx / ldo elements apart (at least the row length, a multiple
- * of 8, at most 2^24), not overlapping.  The products (q - z) * x are exact and
- * summed in FP32, each group's sum times its scale in FP32, one rounding at
- * the end.  Enqueued on `stream`; no host synchronisation, no allocation and
- * no workspace: calls on one handle may overlap and be captured. */
+ * of 8, at most 2^24), not overlapping.  Per group sum q x and z sum x are formed
+ * in FP32 (q x exactly), their difference times the scale is added in FP32, and
+ * the result rounded once.  x is multiplied as FP16 times a power of two per token
+ * (FP16 x too): what lies 2^-34 below a token's largest magnitude is rounded away.
+ * A token with an infinity or a NaN has NaN and infinite outputs.  Enqueued on
+ * `stream`; no host synchronisation, no allocation and no workspace: calls on one
+ * handle may overlap and be captured. */
 nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t ldx, void* out, int64_t ldo,
                                     cudaStream_t stream);
 

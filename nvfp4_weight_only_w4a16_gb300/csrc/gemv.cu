@@ -187,7 +187,7 @@ __device__ __forceinline__ float scale_of(uint32_t v, int hi) {
   return __half2float(__ushort_as_half((unsigned short)(hi ? v >> 16 : v & 0xFFFFu)));
 }
 __device__ __forceinline__ float byte_of(uint32_t v, int i) {  // 0..255, exactly
-  return __uint_as_float(0x4B000000u | ((v >> (8 * i)) & 0xFFu)) - 8388608.0f;
+  return __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7440 + i)) - 8388608.0f;
 }
 
 // acc += the step's (16 kRg) x 8 products.  xl: the lane's x row at the step's first element and the lane's
@@ -249,8 +249,7 @@ __device__ __forceinline__ void use_step(const Step<kFmt, kZeros>& w, const uint
         constexpr float kOff = kCenter ? 8.0f : 0.0f;
         float z0 = 8.0f - kOff, z1 = 8.0f - kOff;
         if (kZeros) {
-          const uint32_t zz = w.z[q][g >> 1] >> (16 * (g & 1));
-          z0 = byte_of(zz, 0) - kOff, z1 = byte_of(zz, 1) - kOff;
+          z0 = byte_of(w.z[q][g >> 1], 2 * (g & 1)) - kOff, z1 = byte_of(w.z[q][g >> 1], 2 * (g & 1) + 1) - kOff;
         }
         const float s0 = scale_of<kBf16>(w.s[q][g], 0), s1 = scale_of<kBf16>(w.s[q][g], 1);
         acc[q][0] = fmaf(s0, fmaf(-z0, sx.x, part[0]), acc[q][0]);
@@ -668,6 +667,7 @@ static cudaError_t launch_gemv(const GemvArgs& a, long long granules, size_t sme
       if (dev < 64) fit[dev][a.S] = n;
     }
   }
+  if (n < a.tiles) n = a.tiles;  // one for each tile of x at least
   cfg.gridDim = dim3((unsigned)(granules < n ? granules : n) * a.S);
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }

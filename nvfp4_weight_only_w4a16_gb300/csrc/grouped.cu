@@ -21,12 +21,12 @@
 // to pair with.
 //
 // One CTA per multiprocessor, 24 warps: 0 packed-weight producer (bulk copies into
-// a ring), 1 MMA issuer (the pair's first CTA; for narrow tiles 3 too), 2 row producer (TMA, zero fill past
-// the matrix), 4-7 epilogue (TMEM -> gs -> shared -> 16-byte stores), the
-// rest dequantisers, in teams that take turns.  Two accumulator buffers of 256
-// columns: the epilogue of a unit overlaps the next one's MMAs.  The row offsets
-// are read on the device; every CTA derives the same unit list from them, so
-// nothing is written but the output.
+// a ring), 1 MMA issuer (the pair's first CTA; for narrow tiles 3 too), 2 row
+// producer (TMA, zero fill past the matrix), 4-7 epilogue (TMEM -> gs -> shared ->
+// 16-byte stores), the rest dequantisers, in teams that take turns.  Two accumulator
+// buffers: the epilogue of a unit overlaps the next one's MMAs.  The row offsets are
+// read on the device; every CTA derives the same unit list from them, so nothing is
+// written but the output.
 #include <mutex>
 
 #include "common.cuh"
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   GroupedCtl& ctl = *reinterpret_cast<GroupedCtl*>(smem);
   uint8_t* ring = smem + gg::kRingOff;
   using Plan = gg::Plan<kBackward, kCtas, kTile>;
-  constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kTeamWarps = Plan::kTeamWarps, kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB,
-                kRaw = Plan::kRaw;
+  constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kTeamWarps = Plan::kTeamWarps;
+  constexpr int kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB, kRaw = Plan::kRaw;
   uint8_t* ring_b = ring + kStagesA * Plan::kABytes;
   uint8_t* raw = ring + Plan::kRings;
   const uint32_t ring_addr = smem_u32(ring), ring_b_addr = smem_u32(ring_b), raw_addr = smem_u32(raw);
@@ -539,9 +539,9 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
             for (int i = 0; i < 32; ++i)
               v[i >> 4][i & 15] = __float_as_uint(__uint_as_float(v[i >> 4][i & 15]) + __uint_as_float(v1[i >> 4][i & 15]));
           } else {
-          tmem_ld16_nw(t + (uint32_t)col, v[0]);
-          tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);  // past the tile's last column: unwritten columns, not stored
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            tmem_ld16_nw(t + (uint32_t)col, v[0]);
+            tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);  // past the tile's last column: unwritten columns, not stored
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           }
           if (a.out_f32) {
 #pragma unroll

@@ -77,6 +77,11 @@ CASES = [
     (2, 144, 1024, [600, 33]),
     (1, 1040, 4224, [19]),
     (256, 48, 128, [1 if e % 3 else 0 for e in range(255)] + [70]),
+    # averages and numbers of feature blocks that lead to each tile of the GEMM, one CTA and two
+    (3, 128, 128, [40, 128, 31]),
+    (3, 272, 256, [129, 1, 60]),
+    (2, 96, 384, [300, 90]),
+    (2, 528, 128, [0, 513]),
 ]
 
 
@@ -283,6 +288,67 @@ def test_bounded_wait_reports_a_timeout():
     out = ex.h.nvfp4_grouped_forward(x, off, blank(40, 128, ex.dtype))
     status_ok(ex.h)
     verify(ex, counts, out, x, False)
+
+
+@pytest.mark.parametrize("path,N,K", [(P.PATH_DECODE, 48, 16384), (P.PATH_PREFILL, 48, 16384), (P.PATH_PREFILL, 16384, 128)])
+def test_the_longest_sums(path, N, K):
+    counts = [9, 1, 20]
+    ex = Experts(3, N, K, 30, out_f32=True)
+    ex.h.nvfp4_moe_set_path(path)
+    x, dy, off = rows_of(30, K), rows_of(30, N), offsets_of(counts)
+    out = ex.h.nvfp4_grouped_forward(x, off, blank(30, N, ex.dtype))
+    dx = ex.h.nvfp4_grouped_backward(dy, off, blank(30, K, ex.dtype))
+    status_ok(ex.h)
+    verify(ex, counts, out, x, False, fp16_rows=FP16_ROWS[path])
+    verify(ex, counts, dx, dy, True)
+
+
+@pytest.mark.parametrize("counts", [[30, 0, 34, 17], [100, 130, 3, 60], [256, 700, 1, 90]])   # each tile of the GEMM
+@pytest.mark.parametrize("out_f32", [False, True])
+def test_many_units_a_multiprocessor(counts, out_f32):
+    """Rings that wrap many times: right, and the same bits each time."""
+    ex = Experts(4, 2064, 2048, 1100, out_f32=out_f32)
+    ex.h.nvfp4_moe_set_path(P.PATH_PREFILL)
+    R = sum(counts)
+    off = offsets_of(counts)
+    for wi, wo, run, backward in ((2048, 2064, ex.h.nvfp4_grouped_forward, False),
+                                  (2064, 2048, ex.h.nvfp4_grouped_backward, True)):
+        x = rows_of(R, wi)
+        first = run(x, off, blank(R, wo, ex.dtype))
+        verify(ex, counts, first, x, backward)
+        for _ in range(5):
+            assert torch.equal(run(x, off, blank(R, wo, ex.dtype)), first)
+    status_ok(ex.h)
+
+
+def test_bounded_waits_of_a_pair_report_a_timeout():
+    ex = Experts(2, 272, 256, 200)
+    ex.h.nvfp4_moe_set_path(P.PATH_PREFILL)
+    x, off, counts = rows_of(200, 256), offsets_of([130, 70]), [130, 70]
+    dy = rows_of(200, 272)
+    ex.h.nvfp4_moe_debug_set_fault(1)
+    for run, rows, n in ((ex.h.nvfp4_grouped_forward, x, 272), (ex.h.nvfp4_grouped_backward, dy, 256)):
+        run(rows, off, blank(200, n, ex.dtype))
+        assert P.STATUS[ex.h.nvfp4_moe_get_status()[0]] == "NVFP4_MOE_ERR_TIMEOUT"
+    ex.h.nvfp4_moe_debug_set_fault(0)
+    out = ex.h.nvfp4_grouped_forward(x, off, blank(200, 272, ex.dtype))
+    dx = ex.h.nvfp4_grouped_backward(dy, off, blank(200, 256, ex.dtype))
+    status_ok(ex.h)
+    verify(ex, counts, out, x, False)
+    verify(ex, counts, dx, dy, True)
+
+
+def test_stage_times_count_the_products():
+    ex = Experts(2, 128, 256, 40)
+    x, off = rows_of(40, 256), offsets_of([30, 10])
+    ex.h.nvfp4_moe_set_profiling(True)
+    for path in FORWARD:
+        ex.h.nvfp4_moe_set_path(path)
+        ex.h.nvfp4_grouped_forward(x, off, blank(40, 128, ex.dtype))
+    ms, n = ex.h.nvfp4_moe_get_stage_times()
+    assert n == 2 and ms[2] > 0 and ms[2] < 1000
+    ex.h.nvfp4_moe_set_profiling(False)
+    status_ok(ex.h)
 
 
 def test_refusals():
