@@ -93,6 +93,10 @@ struct Plan {
 };
 }  // namespace gg
 
+// The result's type, where the kernel knows it: with tiles of 256 rows that is 1 to 2% faster, with fewer, where the
+// dequantisers' code sets the pace, up to 4% slower.
+enum class Out { kBf16, kF32, kEither };
+
 struct GroupedArgs {
   const uint8_t* blob;
   size_t expert_stride;
@@ -199,7 +203,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&o)[4]
       : "memory");
 }
 
-template <bool kBackward, int kCtas, int kTile>
+template <bool kBackward, int kCtas, int kTile, Out kOut>
 __global__ void __launch_bounds__(gg::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap, GroupedArgs a) {
   extern __shared__ uint8_t smem_dyn[];
@@ -208,6 +212,11 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   uint8_t* ring = smem + gg::kRingOff;
   using Plan = gg::Plan<kBackward, kCtas, kTile>;
   constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kTeamWarps = Plan::kTeamWarps;
+  // FP32 results: the two halves of the reduction into an accumulator each, summed in the epilogue, in place of two
+  // units' accumulators.  The tensor core truncates where it adds (1e-6 of the result's norm after 4096 terms in one
+  // accumulator), and BF16's rounding hides that.
+  const bool f32 = kOut == Out::kF32 || (kOut == Out::kEither && a.out_f32);
+  const bool halves = kIssuers == 1 && f32;
   constexpr int kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB, kRaw = Plan::kRaw;
   uint8_t* ring_b = ring + kStagesA * Plan::kABytes;
   uint8_t* raw = ring + Plan::kRings;
@@ -321,10 +330,6 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       const int h = warp >> 1;  // 0, 1
       uint32_t j = 0;
       int base = 0;  // squares before the unit
-      // FP32 results: the two halves of the reduction into an accumulator each, summed in the epilogue, in place of
-      // two units' accumulators.  The tensor core truncates where it adds (1e-6 of the result's norm after 4096 terms
-      // in one accumulator), and BF16's rounding hides that.
-      const bool halves = kIssuers == 1 && a.out_f32;
       bool ok = true;
       for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok; w.next(ctl, total), ++j, base += a.steps) {
         int row0;
@@ -334,40 +339,44 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         if (!warp_wait(ctl.acc_empty + buf, ((halves ? j : j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
         uint32_t d = tmem + buf * Plan::kAccBuf + (uint32_t)h * Plan::kAccIssuer;
-        const int end = base + a.steps, second = halves && a.steps > 1 ? base + a.steps / 2 : end;
+        const int end = base + a.steps;
+        int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base;
+        int stop = halves && a.steps > 1 ? base + a.steps / 2 : end;
         uint32_t acc = 0;
-        for (int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base; i < end; i += kIssuers) {
-          const int sa = i % kStagesA, sb = i % kStagesB;
-          if (!warp_wait(ctl.b_full + sb, (uint32_t)(i / kStagesB) & 1u, abort_flag, a.st, 913) ||
-              !warp_wait(ctl.a_full + sa, (uint32_t)(i / kStagesA) & 1u, abort_flag, a.st, 914)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (i == second) d += Plan::kAccBuf, acc = 0;
-          const uint32_t st = ring_addr + (uint32_t)(sa * Plan::kABytes);
-          const uint64_t ad = kBackward ? sw128_desc_mn(st) : sw128_desc(st);
-          const uint64_t bd = sw128_desc(ring_b_addr + (uint32_t)(sb * Plan::kBBytes));
-          const uint32_t at = tmem + Plan::kOperand + (uint32_t)sa * 64u;  // 8 columns per 16 elements
-          if (elect_one()) {
+        for (; ok; stop = end, d += Plan::kAccBuf, acc = 0) {  // once or twice (a test in the loop itself cost 1.5%)
+          for (; i < stop; i += kIssuers) {
+            const int sa = i % kStagesA, sb = i % kStagesB;
+            if (!warp_wait(ctl.b_full + sb, (uint32_t)(i / kStagesB) & 1u, abort_flag, a.st, 913) ||
+                !warp_wait(ctl.a_full + sa, (uint32_t)(i / kStagesA) & 1u, abort_flag, a.st, 914)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t st = ring_addr + (uint32_t)(sa * Plan::kABytes);
+            const uint64_t ad = kBackward ? sw128_desc_mn(st) : sw128_desc(st);
+            const uint64_t bd = sw128_desc(ring_b_addr + (uint32_t)(sb * Plan::kBBytes));
+            const uint32_t at = tmem + Plan::kOperand + (uint32_t)sa * 64u;  // 8 columns per 16 elements
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
-              const uint64_t ak = ad + (uint32_t)(kk >> 2) * (gg::kHalfBytes >> 4) + (kBackward ? 128u : 2u) * (kk & 3);
-              const uint64_t bk = bd + (uint32_t)(kk >> 2) * (uint32_t)(Plan::kBHalf >> 4) + 2u * (kk & 3);
-              if (Plan::kTmemA) umma_ts_pair(d, at + 8u * kk, bk, idesc, kk ? 1u : acc);
-              else if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, kk ? 1u : acc);
-              else umma_bf16(d, ak, bk, idesc, kk ? 1u : acc);
+              for (int kk = 0; kk < 8; ++kk) {  // 16 reduction elements: 32 B along a row, or 16 rows of 128 B
+                const uint64_t ak = ad + (uint32_t)(kk >> 2) * (gg::kHalfBytes >> 4) + (kBackward ? 128u : 2u) * (kk & 3);
+                const uint64_t bk = bd + (uint32_t)(kk >> 2) * (uint32_t)(Plan::kBHalf >> 4) + 2u * (kk & 3);
+                if (Plan::kTmemA) umma_ts_pair(d, at + 8u * kk, bk, idesc, kk ? 1u : acc);
+                else if (kCtas == 2) umma_bf16_pair(d, ak, bk, idesc, kk ? 1u : acc);
+                else umma_bf16(d, ak, bk, idesc, kk ? 1u : acc);
+              }
+              if (kCtas == 2) {
+                umma_commit_pair(ctl.b_empty + sb);
+                umma_commit_pair(ctl.a_empty + sa);
+              } else {
+                umma_commit(ctl.b_empty + sb);
+                umma_commit(ctl.a_empty + sa);
+              }
             }
-            if (kCtas == 2) {
-              umma_commit_pair(ctl.b_empty + sb);
-              umma_commit_pair(ctl.a_empty + sa);
-            } else {
-              umma_commit(ctl.b_empty + sb);
-              umma_commit(ctl.a_empty + sa);
-            }
+            acc = 1;
+            __syncwarp();
           }
-          acc = 1;
-          __syncwarp();
+          if (stop == end) break;
         }
         if (!ok) break;
         if (elect_one()) {  // (an issuer without a square in the unit: nothing to wait for, and its accumulator is not read)
@@ -517,7 +526,6 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       int row0;
       const int rows = w.rows(ctl, row0);
       const float gs = __ldg(a.gscale + w.e);
-      const bool halves = kIssuers == 1 && a.out_f32;  // see the issuers
       const uint32_t buf = halves ? 0u : j & 1u;
       if (!warp_wait(ctl.acc_full + buf, (halves ? j : j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
@@ -529,21 +537,21 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
           uint32_t v[2][16];
           if ((kIssuers == 2 || halves) && a.steps > 1) {  // the sum of two accumulators
             constexpr uint32_t kOther = kIssuers == 2 ? Plan::kAccIssuer : Plan::kAccBuf;
-            uint32_t v1[2][16];
-            tmem_ld16_nw(t + (uint32_t)col, v[0]);
-            tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);
-            tmem_ld16_nw(t + (uint32_t)col + kOther, v1[0]);
-            tmem_ld16_nw(t + (uint32_t)col + kOther + 16u, v1[1]);
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              v[i >> 4][i & 15] = __float_as_uint(__uint_as_float(v[i >> 4][i & 15]) + __uint_as_float(v1[i >> 4][i & 15]));
+            for (int hh = 0; hh < 2; ++hh) {  // 16 columns at a time: all 32 of both would spill
+              uint32_t v1[16];
+              tmem_ld16_nw(t + (uint32_t)col + 16u * hh, v[hh]);
+              tmem_ld16_nw(t + (uint32_t)col + 16u * hh + kOther, v1);
+              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[hh][i] = __float_as_uint(__uint_as_float(v[hh][i]) + __uint_as_float(v1[i]));
+            }
           } else {
             tmem_ld16_nw(t + (uint32_t)col, v[0]);
             tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);  // past the tile's last column: unwritten columns, not stored
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           }
-          if (a.out_f32) {
+          if (f32) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               __syncwarp();
@@ -597,12 +605,14 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
 
 typedef void (*GroupedKernel)(const CUtensorMap, GroupedArgs);
 struct GroupedVariant {
-  GroupedKernel fn[2];  // forward, backward
+  GroupedKernel fn[2][2];  // forward, backward; BF16, FP32
   int ctas, box;
 };
 template <int kCtas, int kTile>
 static constexpr GroupedVariant grouped_variant() {
-  return {{grouped_gemm_kernel<false, kCtas, kTile>, grouped_gemm_kernel<true, kCtas, kTile>},
+  constexpr Out b = kTile == 256 ? Out::kBf16 : Out::kEither, f = kTile == 256 ? Out::kF32 : Out::kEither;
+  return {{{grouped_gemm_kernel<false, kCtas, kTile, b>, grouped_gemm_kernel<false, kCtas, kTile, f>},
+           {grouped_gemm_kernel<true, kCtas, kTile, b>, grouped_gemm_kernel<true, kCtas, kTile, f>}},
           kCtas,
           gg::Plan<false, kCtas, kTile>::kBox};
 }
@@ -619,8 +629,8 @@ static cudaError_t set_grouped_attrs() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && dev < kCached && done[dev]) return cudaSuccess;
-  for (int i = 0; i < 12; ++i) {
-    e = cudaFuncSetAttribute((const void*)kGroupedVariants[i >> 1].fn[i & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
+  for (int i = 0; i < 24; ++i) {
+    e = cudaFuncSetAttribute((const void*)kGroupedVariants[i >> 2].fn[i & 1][(i >> 1) & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
                              gg::kSmemMax);
     if (e != cudaSuccess) return e;
   }
@@ -679,7 +689,7 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, v.fn[backward], rows_map, a);
+  return cudaLaunchKernelEx(&cfg, v.fn[backward][p.out_f32 != 0], rows_map, a);
 }
 
 }  // namespace nvfp4moe
