@@ -979,7 +979,8 @@ nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t*
   const bool stream = !backward && (h->path == NVFP4_MOE_PATH_DECODE ||
                                     (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= 8 * E));
   DeviceGuard g(h->cfg.device);
-  const GroupedTiling tiling = grouped_tiling(E, R, backward ? K / 128 : (N + 127) / 128);
+  const GroupedTiling tiling = grouped_tiling(E, R, backward ? K / 128 : (N + 127) / 128, backward ? (N + 127) / 128 : K / 128,
+                                              h->num_sms);
   CUtensorMap map{};
   if (!stream &&
       !encode_rows_map(&map, const_cast<void*>(in), (uint64_t)R, (uint64_t)wi, (uint32_t)tiling.box, (uint64_t)ldi))

@@ -20,6 +20,11 @@
 // halves of the MMA read.  kCtas = 1, 128 features, where there is no second block
 // to pair with.
 //
+// kSplit: where there are few units, a cluster of 2 or 4 CTAs takes one unit, a
+// share of the reduction each.  Then each puts its sums into its shared memory (the
+// rings, which are done with), and adds and stores every S-th row from all of theirs,
+// in a fixed order.
+//
 // One CTA per multiprocessor, 24 warps: 0 packed-weight producer (bulk copies into
 // a ring), 1 MMA issuer (the pair's first CTA; for narrow tiles 3 too), 2 row
 // producer (TMA, zero fill past the matrix), 4-7 epilogue (TMEM -> gs -> shared ->
@@ -45,6 +50,7 @@ constexpr int kCtlBytes = 4096;             // tables and barriers in front of t
 constexpr int kEpiBytes = 2048;             // per epilogue warp
 constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
 constexpr int kMaxStages = 8, kMaxRaw = 16;
+constexpr int kMaxSplit = 4;                // CTAs that share a unit
 constexpr int kRoom = kSmemMax - 1024 - kRingOff;  // for the rings
 
 // What follows from the CTAs of a unit (1 or 2) and the rows of a token tile (64, 128 or 256): MMA issuers and ring
@@ -106,6 +112,7 @@ struct GroupedArgs {
   int NB;                  // 128-feature output blocks
   int NU;                  // work units across the features: NB or, in pairs, half of it
   int steps;               // 128-long reduction steps
+  int split;               // CTAs that share a unit's (kSplit), else 1
   size_t block_stride;     // bytes from one output block's first square to the next one's
   size_t step_stride;      // bytes from one reduction step's square to the next
   int n_out;               // output features
@@ -203,7 +210,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&o)[4]
       : "memory");
 }
 
-template <bool kBackward, int kCtas, int kTile, Out kOut>
+template <bool kBackward, int kCtas, int kTile, Out kOut, bool kSplit>
 __global__ void __launch_bounds__(gg::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap, GroupedArgs a) {
   extern __shared__ uint8_t smem_dyn[];
@@ -216,14 +223,19 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   // units' accumulators.  The tensor core truncates where it adds (1e-6 of the result's norm after 4096 terms in one
   // accumulator), and BF16's rounding hides that.
   const bool f32 = kOut == Out::kF32 || (kOut == Out::kEither && a.out_f32);
-  const bool halves = kIssuers == 1 && f32;
+  const bool halves = kIssuers == 1 && f32 && !kSplit;  // (split: already fewer terms each)
   constexpr int kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB, kRaw = Plan::kRaw;
   uint8_t* ring_b = ring + kStagesA * Plan::kABytes;
   uint8_t* raw = ring + Plan::kRings;
   const uint32_t ring_addr = smem_u32(ring), ring_b_addr = smem_u32(ring_b), raw_addr = smem_u32(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(!kSplit || kCtas == 1, "a cluster is a pair or shares a unit");
   const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
-  const int first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
+  const int first = kSplit ? blockIdx.x / a.split : blockIdx.x / kCtas;
+  const int stride = kSplit ? gridDim.x / a.split : gridDim.x / kCtas;  // split: no CTA has a second unit
+  const int part = kSplit ? (int)cluster_rank() : 0;
+  const int step0 = kSplit ? part * a.steps / a.split : 0;  // this CTA's steps of the reduction
+  const int steps = kSplit ? (part + 1) * a.steps / a.split - step0 : a.steps;
   constexpr int kRound = 16 * kCtas;  // the MMA's columns come in these
   volatile int* abort_flag = &ctl.abort_flag;
 
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
   const int total = ctl.tile[a.E] * a.NU;
-  const int squares = first < total ? ((total - first - 1) / stride + 1) * a.steps : 0;  // of this CTA
+  const int squares = first < total ? ((total - first - 1) / stride + 1) * steps : 0;  // of this CTA
 
   if (warp == 0) {
     // ---------------- packed weights of this CTA's 128 features ----------------
@@ -309,8 +321,9 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
     for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok && a.fault != 1; w.next(ctl, total)) {
       // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
       const int nb = min(w.block() + rank, a.NB - 1);
-      const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)nb * a.block_stride;
-      for (int s = 0; s < a.steps; ++s, ++it, p.step(kRaw), src += a.step_stride) {
+      const uint8_t* src = a.blob + (size_t)w.e * a.expert_stride + (size_t)nb * a.block_stride +
+                           (kSplit ? (size_t)step0 * a.step_stride : 0);
+      for (int s = 0; s < steps; ++s, ++it, p.step(kRaw), src += a.step_stride) {
         if (!warp_wait(ctl.raw_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 911)) {
           ok = false;
           break;
@@ -331,7 +344,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       uint32_t j = 0;
       int base = 0;  // squares before the unit
       bool ok = true;
-      for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok; w.next(ctl, total), ++j, base += a.steps) {
+      for (GroupedUnits<kCtas> w(ctl, a, first, stride); w.u < total && ok; w.next(ctl, total), ++j, base += steps) {
         int row0;
         const uint32_t idesc =
             idesc_bf16(128 * kCtas, (w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) | (kBackward ? 1u << 15 : 0u);
@@ -339,9 +352,9 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         if (!warp_wait(ctl.acc_empty + buf, ((halves ? j : j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
         uint32_t d = tmem + buf * Plan::kAccBuf + (uint32_t)h * Plan::kAccIssuer;
-        const int end = base + a.steps;
+        const int end = base + steps;
         int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base;
-        int stop = halves && a.steps > 1 ? base + a.steps / 2 : end;
+        int stop = halves && steps > 1 ? base + steps / 2 : end;
         uint32_t acc = 0;
         for (; ok; stop = end, d += Plan::kAccBuf, acc = 0) {  // once or twice (a test in the loop itself cost 1.5%)
           for (; i < stop; i += kIssuers) {
@@ -396,7 +409,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       const int share = ((w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) / kCtas;
       const int nbox = (share + Plan::kBox - 1) / Plan::kBox;
       row0 += rank * share;
-      for (int s = 0; s < a.steps; ++s, ++it, p.step(kStagesB)) {
+      for (int s = step0; s < step0 + steps; ++s, ++it, p.step(kStagesB)) {
         if (!warp_wait(ctl.b_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 915)) {
           ok = false;
           break;
@@ -516,6 +529,9 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         else mbar_arrive(ctl.a_full + pa.slot);
       }
     }
+  } else if (warp >= 4 && kSplit) {
+    if (first < total && !warp_wait(ctl.acc_full, 0, abort_flag, a.st, 918) && lane == 0) ctl.abort_flag = 1;
+    tc_fence_after();
   } else if (warp >= 4) {
     // ---------------- epilogue: warp w reads TMEM lanes 32 (w % 4) .., one output feature a lane, and turns
     // 32 (FP32: 16) rows x 32 features through shared memory into 16-byte stores ----------------
@@ -530,12 +546,12 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       if (!warp_wait(ctl.acc_full + buf, (halves ? j : j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
       uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * Plan::kAccBuf;
-      if (kIssuers == 2 && a.steps == 1) t += (j & 1u) * Plan::kAccIssuer;  // unit j's only square is the CTA's j-th
+      if (kIssuers == 2 && steps == 1) t += (j & 1u) * Plan::kAccIssuer;  // unit j's only square is the CTA's j-th
       const int f0 = 128 * (w.block() + rank) + 32 * quarter;  // beyond n_out for a block computed twice
       if (f0 < a.n_out) {
         for (int col = 0; col < rows; col += 32) {
           uint32_t v[2][16];
-          if ((kIssuers == 2 || halves) && a.steps > 1) {  // the sum of two accumulators
+          if ((kIssuers == 2 || halves) && steps > 1) {  // the sum of two accumulators
             constexpr uint32_t kOther = kIssuers == 2 ? Plan::kAccIssuer : Plan::kAccBuf;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {  // 16 columns at a time: all 32 of both would spill
@@ -596,6 +612,48 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (kCtas == 2) cluster_sync_all();  // neither CTA leaves while the other may still signal it
+  if constexpr (kSplit) {
+    GroupedUnits<kCtas> w(ctl, a, first, stride);
+    int row0 = 0;
+    const int rows = first < total ? w.rows(ctl, row0) : 0;
+    float* sums = reinterpret_cast<float*>(ring);  // [row][128 features]; the copies and MMAs are done with the rings
+    if (warp >= 4 && warp < 8 && rows && !*abort_flag) {
+      tc_fence_after();
+      const uint32_t t = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      for (int col = 0; col < rows; col += 16) {
+        uint32_t v[16];
+        tmem_ld16_nw(t + (uint32_t)col, v);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[(col + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
+      }
+      tc_fence_before();
+    }
+    cluster_sync_all();
+    const int f = 128 * w.block() + 4 * lane;
+    if (rows && f < a.n_out) {
+      const float gs = __ldg(a.gscale + w.e);
+      for (int r = warp * a.split + part; r < rows; r += gg::kThreads / 32 * a.split) {
+        float4 v[gg::kMaxSplit], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < gg::kMaxSplit; ++c)
+          if (c < a.split) v[c] = ld_cluster(sums + r * 128 + 4 * lane, c);
+#pragma unroll
+        for (int c = 0; c < gg::kMaxSplit; ++c)
+          if (c < a.split) y.x += v[c].x, y.y += v[c].y, y.z += v[c].z, y.w += v[c].w;
+        y.x *= gs, y.y *= gs, y.z *= gs, y.w *= gs;
+        const long long o = (long long)(row0 + r) * a.ldo + f;
+        if (f32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = y;
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while its sums are read
+  }
   if (warp == 1) {
     tc_fence_after();
     if (kCtas == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -608,16 +666,19 @@ struct GroupedVariant {
   GroupedKernel fn[2][2];  // forward, backward; BF16, FP32
   int ctas, box;
 };
-template <int kCtas, int kTile>
+template <int kCtas, int kTile, bool kSplit>
 static constexpr GroupedVariant grouped_variant() {
-  constexpr Out b = kTile == 256 ? Out::kBf16 : Out::kEither, f = kTile == 256 ? Out::kF32 : Out::kEither;
-  return {{{grouped_gemm_kernel<false, kCtas, kTile, b>, grouped_gemm_kernel<false, kCtas, kTile, f>},
-           {grouped_gemm_kernel<true, kCtas, kTile, b>, grouped_gemm_kernel<true, kCtas, kTile, f>}},
+  constexpr bool known = kTile == 256 && !kSplit;
+  constexpr Out b = known ? Out::kBf16 : Out::kEither, f = known ? Out::kF32 : Out::kEither;
+  return {{{grouped_gemm_kernel<false, kCtas, kTile, b, kSplit>, grouped_gemm_kernel<false, kCtas, kTile, f, kSplit>},
+           {grouped_gemm_kernel<true, kCtas, kTile, b, kSplit>, grouped_gemm_kernel<true, kCtas, kTile, f, kSplit>}},
           kCtas,
           gg::Plan<false, kCtas, kTile>::kBox};
 }
-static const GroupedVariant kGroupedVariants[] = {grouped_variant<1, 64>(), grouped_variant<1, 128>(), grouped_variant<1, 256>(),
-                                                  grouped_variant<2, 64>(), grouped_variant<2, 128>(), grouped_variant<2, 256>()};
+static const GroupedVariant kGroupedVariants[] = {
+    grouped_variant<1, 64, false>(), grouped_variant<1, 128, false>(), grouped_variant<1, 256, false>(),
+    grouped_variant<2, 64, false>(), grouped_variant<2, 128, false>(), grouped_variant<2, 256, false>(),
+    grouped_variant<1, 64, true>(),  grouped_variant<1, 128, true>(),  grouped_variant<1, 256, true>()};
 
 // The opt-in shared-memory size, once per device.
 static cudaError_t set_grouped_attrs() {
@@ -629,7 +690,7 @@ static cudaError_t set_grouped_attrs() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && dev < kCached && done[dev]) return cudaSuccess;
-  for (int i = 0; i < 24; ++i) {
+  for (int i = 0; i < 36; ++i) {
     e = cudaFuncSetAttribute((const void*)kGroupedVariants[i >> 2].fn[i & 1][(i >> 1) & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
                              gg::kSmemMax);
     if (e != cudaSuccess) return e;
@@ -638,7 +699,7 @@ static cudaError_t set_grouped_attrs() {
   return cudaSuccess;
 }
 
-GroupedTiling grouped_tiling(int E, int R, int out_blocks) {
+GroupedTiling grouped_tiling(int E, int R, int out_blocks, int steps, int num_sms) {
   // Pairs where there are two feature blocks to pair. Rows per token tile: a wide tile dequantises a weight square
   // once for many rows, a narrow one leaves shared memory for deeper rings. At 128 experts of 1536 x 4096, counts
   // spread by half around the mean (sigma 0.5), forward / backward, us for tiles of 64, 128 and 256 rows: 32 rows an
@@ -646,7 +707,18 @@ GroupedTiling grouped_tiling(int E, int R, int out_blocks) {
   // 112 285 / 286, 184 / 204, 200 / 195; 144 345 / 352, 209 / 234, 209 / 205; 256 559 / 573, 332 / 374, 282 / 273.
   const int avg = R / E;
   GroupedTiling t;
-  t.variant = (out_blocks > 1 ? 3 : 0) + (avg > 112 ? 2 : avg > 32 ? 1 : 0);
+  const int width = avg > 112 ? 2 : avg > 32 ? 1 : 0;  // of a tile: 64, 128, 256 rows
+  // Units too few for half of the multiprocessors share them, as long as a CTA keeps two squares: one expert of
+  // 4096 x 4096, 32 rows, 17.7 us as pairs, 13.6 and 10.4 with 2 and 4 CTAs a unit; 2048 x 4096, 64 rows, 18.2, 14.4 and
+  // 10.8 (8: 16.9, too few clusters of that size run at a time; of 4, 36 on 152 multiprocessors, and with 37 the time
+  // goes from 10.8 to 19.0: hence 15/16).
+  const int groups = E < R ? E : R;  // with rows: a unit each, and one for every further full tile, at most
+  const long long units = (long long)((R - groups) / (64 << width) + groups) * out_blocks;
+  t.units = (int)(units < num_sms ? units : num_sms);
+  t.split = 1;
+  while (t.split < gg::kMaxSplit && units * 2 * t.split <= (t.split == 1 ? num_sms : num_sms * 15 / 16) && 4 * t.split <= steps)
+    t.split *= 2;
+  t.variant = width + (t.split > 1 ? 6 : out_blocks > 1 ? 3 : 0);
   t.box = kGroupedVariants[t.variant].box;
   return t;
 }
@@ -668,6 +740,7 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   const GroupedVariant& v = kGroupedVariants[t.variant];
   a.NU = (a.NB + v.ctas - 1) / v.ctas;
   a.steps = backward ? Np / 128 : p.K / 128;
+  a.split = t.split;
   a.block_stride = backward ? (size_t)gg::kPairBytes : row_block;
   a.step_stride = backward ? row_block : (size_t)gg::kPairBytes;
   a.n_out = backward ? p.K : p.N;
@@ -677,13 +750,13 @@ cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const Gr
   a.st = p.status;
   a.fault = p.fault;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.num_sms / v.ctas * v.ctas));
+  cfg.gridDim = dim3((unsigned)(t.split > 1 ? t.units * t.split : p.num_sms / v.ctas * v.ctas));
   cfg.blockDim = dim3(gg::kThreads);
   cfg.dynamicSmemBytes = gg::kSmemMax;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)v.ctas;
+  at[0].val.clusterDim.x = (unsigned)(t.split > 1 ? t.split : v.ctas);
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;

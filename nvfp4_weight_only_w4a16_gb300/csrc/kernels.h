@@ -182,8 +182,11 @@ struct GroupedProduct {
 struct GroupedTiling {
   int variant;  // of the kernel: CTAs per unit and rows per token tile
   int box;      // rows per TMA box
+  int split;    // CTAs that share a unit's reduction, or 1
+  int units;    // split > 1: at most so many, whatever the offsets
 };
-GroupedTiling grouped_tiling(int E, int R, int out_blocks);
+// out_blocks, steps: 128-long blocks of the result's rows and of the reduction.
+GroupedTiling grouped_tiling(int E, int R, int out_blocks, int steps, int num_sms);
 // rows_map: in as [R][K or N] BF16, box {64, tiling.box}, 128B swizzle.
 cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const GroupedTiling& tiling,
                                 const CUtensorMap& rows_map, cudaStream_t st);

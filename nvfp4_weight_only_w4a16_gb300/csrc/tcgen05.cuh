@@ -88,6 +88,14 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(const float* p, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_rank(p, rank)), "f"(v) : "memory");
 }
+// 16 bytes of the same shared variable in CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(map_rank(p, rank)));
+  return v;
+}
 // Arrive at a barrier of either CTA of the pair.  Not a cluster-scope release,
 // which waits about 2000 cycles for every earlier access of the thread: what is
 // published this way is read by the tensor cores of the writer's own

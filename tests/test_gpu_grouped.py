@@ -321,6 +321,40 @@ def test_many_units_a_multiprocessor(counts, out_f32):
     status_ok(ex.h)
 
 
+@pytest.mark.parametrize("E,N,K,counts", [
+    (1, 2048, 2048, [1]), (1, 4096, 4096, [33]), (1, 4112, 2176, [70]), (1, 1040, 4224, [300]), (2, 272, 2048, [0, 5]),
+    (3, 528, 1152, [64, 1, 129]), (2, 128, 4096, [65, 31]), (1, 144, 640, [513]), (4, 1024, 512, [2, 0, 3, 1])])
+@pytest.mark.parametrize("out_f32", [False, True])
+def test_clusters_that_share_a_reduction(E, N, K, counts, out_f32):
+    """Few units, long sums: each shared by 2 or 4 CTAs."""
+    R = sum(counts) + 3
+    ex = Experts(E, N, K, R, out_f32=out_f32)
+    ex.h.nvfp4_moe_set_path(P.PATH_PREFILL)
+    off = offsets_of(counts, 2)
+    for wi, wo, run, backward in ((K, N, ex.h.nvfp4_grouped_forward, False), (N, K, ex.h.nvfp4_grouped_backward, True)):
+        x = rows_of(R, wi)
+        first = run(x, off, blank(R, wo, ex.dtype, pad=8))
+        status_ok(ex.h)
+        verify(ex, counts, first, x, backward, first=2)
+        for _ in range(3):
+            assert torch.equal(run(x, off, blank(R, wo, ex.dtype))[2:-1], first[2:-1])
+    status_ok(ex.h)
+
+
+def test_bounded_waits_of_a_cluster_report_a_timeout():
+    ex = Experts(1, 1024, 1024, 40)
+    ex.h.nvfp4_moe_set_path(P.PATH_PREFILL)
+    x, dy, off = rows_of(40, 1024), rows_of(40, 1024, 5), offsets_of([40])
+    ex.h.nvfp4_moe_debug_set_fault(1)
+    for run, rows in ((ex.h.nvfp4_grouped_forward, x), (ex.h.nvfp4_grouped_backward, dy)):
+        run(rows, off, blank(40, 1024, ex.dtype))
+        assert P.STATUS[ex.h.nvfp4_moe_get_status()[0]] == "NVFP4_MOE_ERR_TIMEOUT"
+    ex.h.nvfp4_moe_debug_set_fault(0)
+    out = ex.h.nvfp4_grouped_forward(x, off, blank(40, 1024, ex.dtype))
+    status_ok(ex.h)
+    verify(ex, [40], out, x, False)
+
+
 def test_bounded_waits_of_a_pair_report_a_timeout():
     ex = Experts(2, 272, 256, 200)
     ex.h.nvfp4_moe_set_path(P.PATH_PREFILL)
