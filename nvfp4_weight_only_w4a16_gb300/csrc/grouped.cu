@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   // FP32 results: the two halves of the reduction into an accumulator each, summed in the epilogue, in place of two
   // units' accumulators.  The tensor core truncates where it adds (1e-6 of the result's norm after 4096 terms in one
   // accumulator), and BF16's rounding hides that.
-  const bool f32 = kOut == Out::kF32 || (kOut == Out::kEither && a.out_f32);
-  const bool halves = kIssuers == 1 && f32 && !kSplit;  // (split: already fewer terms each)
+  const auto f32 = [&] { return kOut == Out::kF32 || (kOut == Out::kEither && a.out_f32); };
+  const auto halves = [&] { return kIssuers == 1 && !kSplit && f32(); };  // (split: already fewer terms each)
   constexpr int kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB, kRaw = Plan::kRaw;
   uint8_t* ring_b = ring + kStagesA * Plan::kABytes;
   uint8_t* raw = ring + Plan::kRings;
@@ -348,13 +348,13 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         int row0;
         const uint32_t idesc =
             idesc_bf16(128 * kCtas, (w.rows(ctl, row0) + kRound - 1) & ~(kRound - 1)) | (kBackward ? 1u << 15 : 0u);
-        const uint32_t buf = halves ? 0u : j & 1u;
-        if (!warp_wait(ctl.acc_empty + buf, ((halves ? j : j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
+        const uint32_t buf = halves() ? 0u : j & 1u;
+        if (!warp_wait(ctl.acc_empty + buf, ((halves() ? j : j >> 1) & 1u) ^ 1u, abort_flag, a.st, 912)) break;
         tc_fence_after();
         uint32_t d = tmem + buf * Plan::kAccBuf + (uint32_t)h * Plan::kAccIssuer;
         const int end = base + steps;
         int i = kIssuers == 2 ? base + ((base ^ h) & 1) : base;
-        int stop = halves && steps > 1 ? base + steps / 2 : end;
+        int stop = halves() && steps > 1 ? base + steps / 2 : end;
         uint32_t acc = 0;
         for (; ok; stop = end, d += Plan::kAccBuf, acc = 0) {  // once or twice (a test in the loop itself cost 1.5%)
           for (; i < stop; i += kIssuers) {
@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       int row0;
       const int rows = w.rows(ctl, row0);
       const float gs = __ldg(a.gscale + w.e);
-      const uint32_t buf = halves ? 0u : j & 1u;
-      if (!warp_wait(ctl.acc_full + buf, (halves ? j : j >> 1) & 1u, abort_flag, a.st, 918)) break;
+      const uint32_t buf = halves() ? 0u : j & 1u;
+      if (!warp_wait(ctl.acc_full + buf, (halves() ? j : j >> 1) & 1u, abort_flag, a.st, 918)) break;
       tc_fence_after();
       uint32_t t = tmem + ((uint32_t)(32 * quarter) << 16) + buf * Plan::kAccBuf;
       if (kIssuers == 2 && steps == 1) t += (j & 1u) * Plan::kAccIssuer;  // unit j's only square is the CTA's j-th
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
       if (f0 < a.n_out) {
         for (int col = 0; col < rows; col += 32) {
           uint32_t v[2][16];
-          if ((kIssuers == 2 || halves) && steps > 1) {  // the sum of two accumulators
+          if ((kIssuers == 2 || halves()) && steps > 1) {  // the sum of two accumulators
             constexpr uint32_t kOther = kIssuers == 2 ? Plan::kAccIssuer : Plan::kAccBuf;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {  // 16 columns at a time: all 32 of both would spill
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
             tmem_ld16_nw(t + (uint32_t)col + 16u, v[1]);  // past the tile's last column: unwritten columns, not stored
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           }
-          if (f32) {
+          if (f32()) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               __syncwarp();
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
           if (c < a.split) y.x += v[c].x, y.y += v[c].y, y.z += v[c].z, y.w += v[c].w;
         y.x *= gs, y.y *= gs, y.z *= gs, y.w *= gs;
         const long long o = (long long)(row0 + r) * a.ldo + f;
-        if (f32) {
+        if (f32()) {
           *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = y;
         } else {
           const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
