@@ -1050,8 +1050,8 @@ nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uin
     return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "grouped_pack: misaligned input");
   DeviceGuard g(h->cfg.device);
   const int E = h->cfg.num_experts;
-  std::vector<float> gs((size_t)E);
-  cudaError_t e = cudaMemcpyAsync(gs.data(), gscale, sizeof(float) * E, cudaMemcpyDeviceToHost, st);
+  float gs[256];
+  cudaError_t e = cudaMemcpyAsync(gs, gscale, sizeof(float) * E, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(h, e, "grouped_pack: reading gscale");
   for (int i = 0; i < E; ++i)

@@ -7,6 +7,8 @@ float64: the roundings that lie on its way, each at most half a step (BF16 2^-8
 of the value) plus the products' FP32 summation, carried through the absolute
 values of everything behind them; second-order terms are covered by 2% on top.
 """
+import threading
+
 import numpy as np
 import pytest
 
@@ -258,5 +260,46 @@ def test_products_that_feed_each_other_without_a_kernel_between(R, path):
     for _ in range(10):
         assert all(torch.equal(u, v) for u, v in zip(chain(False), want))
     for h in (a, b, lin):
+        assert h.nvfp4_moe_get_status()[0] == 0
+        h.close()
+
+
+def test_host_threads_share_handles():
+    """Calls on one handle from several host threads, each on a stream of its own: as if made one after the other."""
+    P.build()
+    rng = np.random.default_rng(8)
+    E, n, k = 4, 512, 1024
+    g = P.Grouped(E, n, k, 200)
+    g.nvfp4_grouped_pack(_t(rng.integers(0, 256, (E, n, k // 2), dtype=np.uint8)),
+                         _t(rng.integers(0, 0x40, (E, n, k // 16), dtype=np.uint8)), torch.full((E,), 0.02, device=DEV))
+    lin = P.Int4Linear(n, k, 64)
+    lin.nvfp4_int4_pack(_t(rng.integers(0, 256, (n, k // 2), dtype=np.uint8)),
+                        torch.from_numpy(rng.uniform(-0.01, 0.01, (n, k // 64))).to(DEV).to(BF16))
+    off = [_t(np.array(o, np.int32)) for o in ([0, 3, 3, 20, 24], [0, 100, 100, 130, 200])]
+    xs = [torch.from_numpy(rng.standard_normal((r, k))).to(DEV).to(BF16) for r in (24, 200, 13)]
+    dy = torch.from_numpy(rng.standard_normal((200, n))).to(DEV).to(BF16)
+    new = lambda r, c: torch.empty((r, c), dtype=BF16, device=DEV)
+    jobs = [lambda s: g.nvfp4_grouped_forward(xs[0], off[0], new(24, n), stream=s),
+            lambda s: g.nvfp4_grouped_forward(xs[1], off[1], new(200, n), stream=s),
+            lambda s: g.nvfp4_grouped_backward(dy, off[1], new(200, k), stream=s),
+            lambda s: lin.nvfp4_int4_forward(xs[2], new(13, n), stream=s)]
+    want = [j(None) for j in jobs]
+    torch.cuda.synchronize()
+    got = [None] * len(jobs)
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            outs = [jobs[i](s) for _ in range(50)]
+            s.synchronize()
+        got[i] = all(torch.equal(o, want[i]) for o in outs)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got == [True] * len(jobs)
+    for h in (g, lin):
         assert h.nvfp4_moe_get_status()[0] == 0
         h.close()
