@@ -18,7 +18,7 @@
 // features (128 each) of one tile of up to 256 rows, M = 256 MMAs: each CTA
 // dequantises its own 128 x 128 squares and loads half of the rows, which both
 // halves of the MMA read.  kCtas = 1, 128 features, where there is no second block
-// to pair with.
+// to pair with or nothing to gain from it (grouped_tiling).
 //
 // kSplit: where there are few units, a cluster of 2 or 4 CTAs takes one unit, a
 // share of the reduction each.  Then each puts its sums into its shared memory (the
@@ -700,11 +700,11 @@ static cudaError_t set_grouped_attrs() {
 }
 
 GroupedTiling grouped_tiling(int E, int R, int out_blocks, int steps, int num_sms) {
-  // Pairs where there are two feature blocks to pair. Rows per token tile: a wide tile dequantises a weight square
-  // once for many rows, a narrow one leaves shared memory for deeper rings. At 128 experts of 1536 x 4096, counts
-  // spread by half around the mean (sigma 0.5), forward / backward, us for tiles of 64, 128 and 256 rows: 32 rows an
-  // expert 143 / 140, 145 / 146, 187 / 171; 48 167 / 171, 146 / 153, 190 / 175; 96 262 / 260, 172 / 193, 198 / 190;
-  // 112 285 / 286, 184 / 204, 200 / 195; 144 345 / 352, 209 / 234, 209 / 205; 256 559 / 573, 332 / 374, 282 / 273.
+  // Rows per token tile: a wide tile dequantises a weight square once for many rows, a narrow one leaves shared memory
+  // for deeper rings.  At 128 experts of 1536 x 4096, counts spread by half around the mean (sigma 0.5), forward /
+  // backward, us for tiles of 64, 128 and 256 rows: 32 rows an expert 143 / 140, 145 / 146, 187 / 171; 48 167 / 171,
+  // 146 / 153, 190 / 175; 96 262 / 260, 172 / 193, 198 / 190; 112 285 / 286, 184 / 204, 200 / 195; 144 345 / 352,
+  // 209 / 234, 209 / 205; 256 559 / 573, 332 / 374, 282 / 273.
   const int avg = R / E;
   GroupedTiling t;
   const int width = avg > 112 ? 2 : avg > 32 ? 1 : 0;  // of a tile: 64, 128, 256 rows
@@ -718,7 +718,11 @@ GroupedTiling grouped_tiling(int E, int R, int out_blocks, int steps, int num_sm
   t.split = 1;
   while (t.split < gg::kMaxSplit && units * 2 * t.split <= (t.split == 1 ? num_sms : num_sms * 15 / 16) && 4 * t.split <= steps)
     t.split *= 2;
-  t.variant = width + (t.split > 1 ? 6 : out_blocks > 1 ? 3 : 0);
+  // Pairs only where there are more units than multiprocessors or tiles of 128 rows and more, for which they halve the
+  // reads of the rows: 8 experts of 272 x 256, 4 rows each, 7.0 us as pairs, 6.3 without; of 1024 x 1024, 16 rows, 9.0
+  // and 8.8; but 2 of 4096 x 4096, 100 rows, 18.6 and 21.4.
+  const bool pairs = out_blocks > 1 && (width > 0 || units > num_sms);
+  t.variant = width + (t.split > 1 ? 6 : pairs ? 3 : 0);
   t.box = kGroupedVariants[t.variant].box;
   return t;
 }

@@ -321,6 +321,23 @@ def test_many_units_a_multiprocessor(counts, out_f32):
     status_ok(ex.h)
 
 
+@pytest.mark.parametrize("out_f32", [False, True])
+def test_narrow_tiles_on_pairs(out_f32):
+    """More units than multiprocessors, few rows each: two MMA issuers a pair."""
+    counts = [7, 0, 61, 64, 1, 16, 17, 3, 0, 40, 65, 2, 9, 33, 0, 12, 5, 28, 31, 90]
+    ex = Experts(20, 1040, 1152, sum(counts), out_f32=out_f32)
+    ex.h.nvfp4_moe_set_path(P.PATH_PREFILL)
+    off, R = offsets_of(counts), sum(counts)
+    for wi, wo, run, backward in ((1152, 1040, ex.h.nvfp4_grouped_forward, False),
+                                  (1040, 1152, ex.h.nvfp4_grouped_backward, True)):
+        x = rows_of(R, wi)
+        first = run(x, off, blank(R, wo, ex.dtype))
+        verify(ex, counts, first, x, backward)
+        for _ in range(5):
+            assert torch.equal(run(x, off, blank(R, wo, ex.dtype)), first)
+    status_ok(ex.h)
+
+
 @pytest.mark.parametrize("E,N,K,counts", [
     (1, 2048, 2048, [1]), (1, 4096, 4096, [33]), (1, 4112, 2176, [70]), (1, 1040, 4224, [300]), (2, 272, 2048, [0, 5]),
     (3, 528, 1152, [64, 1, 129]), (2, 128, 4096, [65, 31]), (1, 144, 640, [513]), (4, 1024, 512, [2, 0, 3, 1])])
