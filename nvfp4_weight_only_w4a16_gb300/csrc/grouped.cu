@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         }
       }
     }
+    __syncwarp();
     cluster_sync_all();  // no CTA leaves while its sums are read
   }
   if (warp == 1) {
