@@ -23,6 +23,7 @@ struct nvfp4_moe {
   enum Kind { kLayerOrLinear, kGrouped, kInt4 } kind = kLayerOrLinear;
   nvfp4_int4_config i4{};
   size_t product_bytes = 0;  // a product handle's packed matrix (matrices)
+  size_t l2_bytes = 0;       // a product handle's device's L2
   bool i4_zeros = false;     // INT4: the last pack had zero points
   RouteParams rp{};     // scoring rule (nvfp4_moe_set_scoring); rp.bias points at `bias` when set
   float* bias = nullptr;  // [num_experts] device copy of the choice bias
@@ -929,6 +930,9 @@ nvfp4_moe_status create_product(nvfp4_moe::Kind kind, int device, size_t bytes, 
   if (fp && !strcmp(fp, "prefill")) h->path = NVFP4_MOE_PATH_PREFILL;
   DeviceGuard g(device);
   cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device);
+  int l2 = 0;
+  cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, device);
+  h->l2_bytes = (size_t)l2;
   h->ws_bytes = sizeof(DeviceStatus);
   if (cudaMalloc(&h->blob, bytes) != cudaSuccess || cudaMalloc(&h->gscale, sizeof(float) * n_scales) != cudaSuccess ||
       cudaMalloc(&h->ws_mem, h->ws_bytes) != cudaSuccess) {
@@ -998,6 +1002,7 @@ nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t*
   p.out = out;
   p.ldo = ldo;
   p.out_f32 = h->cfg.out_dtype == NVFP4_MOE_OUT_F32;
+  p.once = h->product_bytes > h->l2_bytes;
   p.num_sms = h->num_sms;
   p.status = h->ws.status;
   p.fault = h->fault;
@@ -1149,6 +1154,7 @@ nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t
   p.out = out;
   p.ldo = ldo;
   p.out_f32 = h->i4.out_f32;
+  p.once = h->product_bytes > h->l2_bytes;
   p.num_sms = h->num_sms;
   p.status = h->ws.status;
   cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};

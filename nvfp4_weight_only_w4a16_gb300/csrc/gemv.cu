@@ -82,6 +82,7 @@ struct GemvArgs {
   void* out;
   long long ldo;
   int out_f32;
+  bool once;       // the weights do not outlast the call in L2
   DeviceStatus* st;
 };
 
@@ -99,8 +100,18 @@ __device__ __forceinline__ uint32_t hsub2_u32(uint32_t a, uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// The weights' L2 policy.  Matrices larger than L2 are gone before the next call reads them again: L2 gives their lines
+// up first, and need not write back or drop what else it holds for them (128 experts of 1536 x 4096, 128 rows, 51.5 ->
+// 50.3 us, behind 256 MB of written lines 65 -> 57; INT4 131072 x 4096 47.1 -> 46.2 and 63 -> 55).  Smaller ones may
+// still be there (INT4 12576 x 4096: 8.0 us, 8.4 with their lines given up).
+__device__ __forceinline__ uint64_t weight_policy(bool once) {
+  uint64_t first, normal;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+  return once ? first : normal;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() {  // all but the latest kDepth - 1 groups have landed
@@ -128,18 +139,18 @@ struct Step {
   uint32_t z[gv::kRg][(kGroups + 1) / 2];  // INT4: {r, r + 8} bytes per group
 
   // Start the copy of a step into a slot.  c: the lane's place in the codes; s (NVFP4): lanes 0..15's in the scales.
-  static __device__ __forceinline__ void copy(const uint8_t* c, const uint8_t* s, uint32_t slot, int lane) {
+  static __device__ __forceinline__ void copy(const uint8_t* c, const uint8_t* s, uint32_t slot, int lane, uint64_t policy) {
     const uint32_t d = slot + lane * 16;
     if (kNv) {
-      copy16(d, c);
-      copy16(d + 512, c + 512);
-      copy16(d + 1024, c + kTileBytes);
-      copy16(d + 1536, c + kTileBytes + 512);
-      if (lane < 16) copy16(d + kCodes, s);
+      copy16(d, c, policy);
+      copy16(d + 512, c + 512, policy);
+      copy16(d + 1024, c + kTileBytes, policy);
+      copy16(d + 1536, c + kTileBytes + 512, policy);
+      if (lane < 16) copy16(d + kCodes, s, policy);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) copy16(d + 512 * i, c + 512 * i);
-      if (lane < (kBytes - kCodes) / 16) copy16(d + kCodes, c + kCodes);
+      for (int i = 0; i < 4; ++i) copy16(d + 512 * i, c + 512 * i, policy);
+      if (lane < (kBytes - kCodes) / 16) copy16(d + kCodes, c + kCodes, policy);
     }
   }
   // The lane's part of a landed step.
@@ -484,10 +495,11 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     return false;
   };
   bool more = true;
+  const uint64_t policy = weight_policy(a.once);
   const auto copy_next = [&] {  // one group, empty past the end
     if (more && lk == 0) more = next_granule();
     if (more) {
-      S::copy(pc, ps, ring_addr + lslot * S::kSlot, lane);
+      S::copy(pc, ps, ring_addr + lslot * S::kSlot, lane, policy);
       lslot = lslot == gv::kDepth - 1 ? 0 : lslot + 1;
       pc += dstep;
       ps += dstep;
@@ -691,6 +703,7 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   a.out = p.out;
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
+  a.once = p.once;
   a.st = p.status;
   a.S = 1;
   const int granules = (p.N / 16 + gv::kRg - 1) / gv::kRg;
@@ -750,6 +763,7 @@ cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st) {
   a.out = p.out;
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
+  a.once = p.once;
   return p.group == 32   ? launch_int4<W4::kInt4G32>(a, p, st)
          : p.group == 64 ? launch_int4<W4::kInt4G64>(a, p, st)
                          : launch_int4<W4::kInt4G128>(a, p, st);

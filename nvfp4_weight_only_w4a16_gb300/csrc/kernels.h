@@ -174,6 +174,7 @@ struct GroupedProduct {
   void* out;               // BF16 or FP32 [R][N] (backward [R][K])
   long long ldo;
   int out_f32;
+  bool once;               // all the matrices' bytes are more than L2 holds
   int num_sms;
   DeviceStatus* status;
   int fault;
@@ -206,6 +207,7 @@ struct Int4Product {
   void* out;               // [T][N], ldo elements apart: FP32, or x's type
   long long ldo;
   int out_f32;
+  bool once;               // all the matrices' bytes are more than L2 holds
   int num_sms;
   DeviceStatus* status;
 };
