@@ -514,7 +514,7 @@ nvfp4_moe_status nvfp4_grouped_backward(nvfp4_moe_t h, int R, const int32_t* off
  *   out[t][n] = sum_k s[n][k/g] * (q[n][k] - z[n][k/g]) * x[t][k]
  * q 0..15, one scale and one zero point per g consecutive elements of a row.
  * An INT4 handle is an nvfp4_moe_t with the same calls as a grouped one;
- * nvfp4_moe_set_path and nvfp4_moe_debug_set_fault have no effect on it.
+ * nvfp4_moe_set_path has no effect on it.
  * ------------------------------------------------------------------------- */
 typedef enum nvfp4_moe_act_dtype {
   NVFP4_MOE_ACT_BF16 = 0,

@@ -1157,6 +1157,7 @@ nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t
   p.once = h->product_bytes > h->l2_bytes;
   p.num_sms = h->num_sms;
   p.status = h->ws.status;
+  p.fault = h->fault;
   cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
   const nvfp4_moe_status s = take_events(h, ev);
   if (s != NVFP4_MOE_OK) return s;

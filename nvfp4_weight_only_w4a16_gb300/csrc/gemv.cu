@@ -84,6 +84,7 @@ struct GemvArgs {
   int out_f32;
   bool once;       // the weights do not outlast the call in L2
   DeviceStatus* st;
+  int fault;       // 1: x is not copied, so that the wait for it ends with a timeout
 };
 
 // D += A B (m16n8k16, FP16 in, FP32 out); not volatile, so that the two row groups' chains interleave.
@@ -302,6 +303,7 @@ struct Stage {
   __device__ __forceinline__ Stage(const GemvArgs& a, uint8_t* x, int step0, int steps)
       : xs(x), pitch(a.pitch), per(steps * (gv::kStep / 8)), rows(0), first(step0 * gv::kStep) {}
   __device__ __forceinline__ void start(const GemvArgs& a, int row0, uint64_t* bar) {  // one thread
+    if (a.fault == 1) return;
     mbar_arrive_expect_tx(bar, (uint32_t)(rows * per * 16));
 #pragma unroll 1
     for (int r = 0; r < rows; ++r)
@@ -624,7 +626,10 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     cluster_wait();
     add_shared();
   }
-  if (dead) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (dead) {
+    if (threadIdx.x == 0 && a.fault != 1) drain_copies(&x_bar, (uint32_t)tphase + 1, 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
 }
 
 // Warps along K: few, for few barriers, but as many as keep every warp busy with the CTA's share of granules.
@@ -704,6 +709,7 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
   a.once = p.once;
+  a.fault = p.fault;
   a.st = p.status;
   a.S = 1;
   const int granules = (p.N / 16 + gv::kRg - 1) / gv::kRg;
@@ -764,6 +770,7 @@ cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st) {
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
   a.once = p.once;
+  a.fault = p.fault;
   return p.group == 32   ? launch_int4<W4::kInt4G32>(a, p, st)
          : p.group == 64 ? launch_int4<W4::kInt4G64>(a, p, st)
                          : launch_int4<W4::kInt4G128>(a, p, st);

@@ -210,6 +210,7 @@ struct Int4Product {
   bool once;               // all the matrices' bytes are more than L2 holds
   int num_sms;
   DeviceStatus* status;
+  int fault;
 };
 cudaError_t launch_int4_gemv(const Int4Product& p, cudaStream_t st);
 size_t int4_packed_bytes(int N, int K, int group, bool zeros);

@@ -358,6 +358,20 @@ def test_clusters_that_share_a_reduction(E, N, K, counts, out_f32):
     status_ok(ex.h)
 
 
+def test_bounded_wait_of_the_streaming_kernel_reports_a_timeout():
+    ex = Experts(3, 272, 512, 40)
+    ex.h.nvfp4_moe_set_path(P.PATH_DECODE)
+    counts = [1, 20, 9]
+    x, off = rows_of(30, 512), offsets_of(counts)
+    ex.h.nvfp4_moe_debug_set_fault(1)
+    ex.h.nvfp4_grouped_forward(x, off, blank(30, 272, ex.dtype))
+    assert P.STATUS[ex.h.nvfp4_moe_get_status()[0]] == "NVFP4_MOE_ERR_TIMEOUT"
+    ex.h.nvfp4_moe_debug_set_fault(0)
+    out = ex.h.nvfp4_grouped_forward(x, off, blank(30, 272, ex.dtype))
+    status_ok(ex.h)
+    verify(ex, counts, out, x, False, fp16_rows=FP16_ROWS[P.PATH_DECODE])
+
+
 def test_bounded_waits_of_a_cluster_report_a_timeout():
     ex = Experts(1, 1024, 1024, 40)
     ex.h.nvfp4_moe_set_path(P.PATH_PREFILL)

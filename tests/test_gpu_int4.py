@@ -141,6 +141,18 @@ def test_captured_and_on_two_streams():
         verify(m, a, b)
 
 
+@pytest.mark.parametrize("T,K", [(3, 512), (16, 8320)])   # one CTA a slice, and a cluster
+def test_bounded_wait_reports_a_timeout(T, K):
+    m = Matrix(272, K, 64, True, False)
+    x = rows_of(m, T)
+    m.h.nvfp4_moe_debug_set_fault(1)
+    m.h.nvfp4_int4_forward(x, torch.empty((T, 272), dtype=m.dtype, device=DEV))
+    assert P.STATUS[m.h.nvfp4_moe_get_status()[0]] == "NVFP4_MOE_ERR_TIMEOUT"
+    m.h.nvfp4_moe_debug_set_fault(0)
+    verify(m, x, run(m, x))
+    assert m.h.nvfp4_moe_get_status()[0] == 0
+
+
 def test_packing_again_replaces_the_zero_points():
     m = Matrix(32, 256, 64, True, False)
     rng = np.random.default_rng(5)
