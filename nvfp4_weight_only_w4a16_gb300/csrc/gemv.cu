@@ -538,11 +538,13 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   };
   // S > 1: row j of a batch's sums is added and stored by CTA j % S, from what every CTA has put into its `shared`
   int pg0 = 0, pj = 0;  // the batch before: its first granule, its rows
+  const int slog = 31 - __clz(a.S);  // a source has 32 / S rows of `shared`
+  static_assert(gv::kShared == 32 * 128, "rows");
   const auto add_shared = [&] {
     const float* from = shared + (phase ^ 1) * (gv::kShared / 4) + lane;
     for (int j = rank + a.S * warp; j < pj; j += a.S * gv::kWarps) {
       float y = 0.f;
-      for (int c = 0; c < a.S; ++c) y += from[(c * (gv::kShared / 128 / a.S) + j / a.S) * 32];
+      for (int c = 0; c < a.S; ++c) y += from[((c << (5 - slog)) + (j >> slog)) * 32];
       if (!dead) store(pg0 + j / kSums, j % kSums, y);
     }
   };
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       y = y * up.x * up.y;
       if (S::kNv) y *= gs;
       if (cluster)
-        st_cluster(shared + phase * (gv::kShared / 4) + (rank * (gv::kShared / 128 / a.S) + j / a.S) * 32 + lane, j % a.S, y);
+        st_cluster(shared + phase * (gv::kShared / 4) + ((rank << (5 - slog)) + (j >> slog)) * 32 + lane, j & (a.S - 1), y);
       else store(g0 + g, s, y);
     }
     if (cluster) {
