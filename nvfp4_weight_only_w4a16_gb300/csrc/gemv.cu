@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   __shared__ unsigned amax[2][gv::kRows];           // of this tile and, zero, of the next
   __shared__ short tile_expert[S::kNv ? gv::kMaxTiles : 1];
   __shared__ int tile_row0[S::kNv ? gv::kMaxTiles : 1], wsum[8];
+  __shared__ uint8_t tile_count[S::kNv ? gv::kMaxTiles : 1];  // its rows
   __shared__ uint64_t x_bar;  // x rows landed
   __shared__ int abort_flag;
   __shared__ float red[2][gv::kWarps][kSums][32];
@@ -393,11 +394,14 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     mbar_init(&x_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (S::kNv) {  // tiles of at most tile_rows rows of one expert; thread i looks at expert i
+  if (S::kNv) {
+    // Tiles of at most tile_rows rows of one expert; thread i looks at expert i.  The offsets are read here alone, with
+    // ordinary loads: the kernel before may write them while this one has begun, so that a read-only load could return
+    // an older line, and two reads that differ would put a tile's rows out of its range.
     grid_dependency_wait();
     grid_launch_dependents();
     const int i = threadIdx.x;
-    const int o0 = i < a.E ? __ldg(a.offsets + i) : 0, o1 = i < a.E ? __ldg(a.offsets + i + 1) : 0;
+    const int o0 = i < a.E ? a.offsets[i] : 0, o1 = i < a.E ? a.offsets[i + 1] : 0;
     const bool bad = o0 < 0 || o1 < o0 || o1 > a.R;
     const int nt = (o1 - o0 + a.tile_rows - 1) / a.tile_rows;
     int before = nt;
@@ -420,6 +424,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     for (int k = 0; k < nt; ++k) {
       tile_expert[before - nt + k] = (short)i;
       tile_row0[before - nt + k] = o0 + k * a.tile_rows;
+      tile_count[before - nt + k] = (uint8_t)min(a.tile_rows, o1 - o0 - k * a.tile_rows);
     }
     __syncthreads();
   }
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   int row0, rows;
   const auto tile_rows = [&] {  // the rows of `tile`
     row0 = S::kNv ? tile_row0[tile] : tile * a.tile_rows;
-    rows = min(a.tile_rows, (S::kNv ? __ldg(a.offsets + tile_expert[tile] + 1) : a.T) - row0);
+    rows = S::kNv ? tile_count[tile] : min(a.tile_rows, a.T - row0);
   };
   tile_rows();
   stage.rows = rows;
