@@ -317,7 +317,9 @@ struct Stage {
   // when the copies did not land in time (reported).  The barrier after the writes is the caller's.
   __device__ __forceinline__ bool finish(float* sums, unsigned* amax, uint64_t* bar, uint32_t parity, volatile int* abort,
                                          DeviceStatus* st) {
-    const bool landed = mbar_wait(bar, parity, abort, st, 921);
+    // one answer for a warp: at the limit one lane may still see the copy and another not, and the reductions below
+    // need them all
+    const bool landed = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, st, 921));
     const int lane = threadIdx.x & 31, warps = gv::kWarps / rows, r = (int)(threadIdx.x >> 5) / warps;
     const int p0 = ((int)(threadIdx.x >> 5) - r * warps) * 32, dp = warps * 32;
     uint8_t* row = xs + r * pitch;

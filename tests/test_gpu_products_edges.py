@@ -66,3 +66,24 @@ def test_offsets_written_by_the_kernel_before(path):
     for handle in (h, lin):
         assert handle.nvfp4_moe_get_status()[0] == 0
         handle.close()
+
+
+@pytest.mark.parametrize("path", [P.PATH_DECODE, P.PATH_PREFILL])
+def test_a_call_behind_one_that_times_out(path):
+    """Every warp of a kernel whose wait has run out leaves it (its copies are held back here), and the call queued
+    behind it, which begins early, computes as if nothing had been."""
+    N, K = 272, 1152
+    h = _experts(3, N, K, 13, out_f32=True)
+    h.nvfp4_moe_set_path(path)
+    off = _t(np.array([0, 5, 5, 13], np.int32))
+    x = _randn(3, 13, K).to(BF16)
+    want = h.nvfp4_grouped_forward(x, off, torch.empty((13, N), device=DEV))
+    assert h.nvfp4_moe_get_status()[0] == 0
+    h.nvfp4_moe_debug_set_fault(1)
+    h.nvfp4_grouped_forward(x, off, torch.empty((13, N), device=DEV))
+    h.nvfp4_moe_debug_set_fault(0)
+    got = h.nvfp4_grouped_forward(x, off, torch.empty((13, N), device=DEV))
+    assert P.STATUS[h.nvfp4_moe_get_status()[0]] == "NVFP4_MOE_ERR_TIMEOUT"
+    assert h.nvfp4_moe_get_status()[0] == 0
+    assert torch.equal(got, want)
+    h.close()
