@@ -131,6 +131,7 @@ struct GroupedCtl {
   uint64_t raw_full[gg::kMaxRaw], raw_empty[gg::kMaxRaw];
   uint64_t a_full[gg::kMaxStages], a_empty[gg::kMaxStages], b_full[gg::kMaxStages], b_empty[gg::kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t mma_done[2];  // every MMA of issuer h has completed
   uint32_t tmem;
   int abort_flag;
 };
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(ctl.acc_full + b, kIssuers);
       mbar_init(ctl.acc_empty + b, kCtas * gg::kEpiWarps);
+      mbar_init(ctl.mma_done + b, 1);
     }
     ctl.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -398,6 +400,14 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         }
         __syncwarp();
       }
+      // MMAs may still be at work where a role has given up: none may outlive the shared and tensor memory it uses
+      if (elect_one()) {
+        if (kCtas == 2) umma_commit_pair_own(ctl.mma_done + h);
+        else umma_commit(ctl.mma_done + h);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(ctl.mma_done + h, 0) && globaltimer_ns() - t0 <= kWaitTimeoutNs) {}
+      }
+      __syncwarp();
     }
   } else if (warp == 2) {
     // ---------------- rows of x (dy): this CTA's half of the tile, boxes of 64 reduction elements ----------------

@@ -137,6 +137,11 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// The same, at the issuing CTA's own barrier alone.
+__device__ __forceinline__ void umma_commit_pair_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
 
 // The bounded wait out of line, and asleep: the test suspends the thread for up to a millisecond at a time, where
 // mbar_wait's short ones keep issuing (its waiting warps took a quarter of a multiprocessor's instructions).
