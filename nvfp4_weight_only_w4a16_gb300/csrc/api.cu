@@ -80,6 +80,7 @@ nvfp4_moe_status fail(nvfp4_moe* h, nvfp4_moe_status s, const std::string& msg) 
 }
 
 nvfp4_moe_status cuda_fail(nvfp4_moe* h, cudaError_t e, const char* where) {
+  cudaGetLastError();  // reported here: left behind, it would be the next kernel launch's
   return fail(h, NVFP4_MOE_ERR_CUDA, std::string(where) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
 }
 
@@ -380,6 +381,7 @@ nvfp4_moe_status create_handle(const nvfp4_moe_config* c, bool linear, int lin_n
   const float ones[3] = {1.0f, 1.0f, 1.0f};
   if (cudaMemset(h->ws_mem, 0, h->ws_bytes) != cudaSuccess ||
       cudaMemcpy(w.ones3, ones, sizeof(ones), cudaMemcpyHostToDevice) != cudaSuccess) {
+    cudaGetLastError();
     nvfp4_moe_destroy(h);
     return NVFP4_MOE_ERR_CUDA;
   }
@@ -408,6 +410,7 @@ void nvfp4_moe_destroy(nvfp4_moe_t h) {
     if (h->gs_eff) cudaFree(h->gs_eff);
     if (h->hbound) cudaFree(h->hbound);
     if (h->ws_mem) cudaFree(h->ws_mem);
+    cudaGetLastError();
   }
   delete h;
 }
@@ -942,6 +945,7 @@ nvfp4_moe_status create_product(nvfp4_moe::Kind kind, int device, size_t bytes, 
   }
   h->ws.status = static_cast<DeviceStatus*>(h->ws_mem);
   if (cudaMemset(h->ws_mem, 0, h->ws_bytes) != cudaSuccess) {
+    cudaGetLastError();
     nvfp4_moe_destroy(h);
     return NVFP4_MOE_ERR_CUDA;
   }

@@ -136,6 +136,12 @@ size_t carve(uint8_t* base, int E, int H, int I, int T, int k, int num_sms, Work
   return r.off;
 }
 
+// A failed CUDA call's status; its error, left behind, would be the next kernel launch's.
+nvfp4_moe_status cuda_error() {
+  cudaGetLastError();
+  return NVFP4_MOE_ERR_CUDA;
+}
+
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
@@ -158,10 +164,10 @@ extern "C" nvfp4_moe_status nvfp4_moe_forward_decode_static(const uint8_t* packe
       !aligned_to(router_logits, logits_dtype == NVFP4_MOE_LOGITS_BF16 ? 2 : 4))
     return NVFP4_MOE_ERR_INVALID_ARG;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_MOE_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_error();
   if (dev < 0 || dev >= kMaxDevices) return NVFP4_MOE_ERR_INVALID_ARG;  // device ordinals 0..63 only
   StaticSetup setup;
-  if (static_setup(dev, &setup) != cudaSuccess) return NVFP4_MOE_ERR_CUDA;
+  if (static_setup(dev, &setup) != cudaSuccess) return cuda_error();
   size_t zero_end = 0;
   if (carve(nullptr, E, H, I, T, top_k, setup.num_sms, nullptr, &zero_end) > kStaticScratchBytes)
     return NVFP4_MOE_ERR_UNSUPPORTED_SHAPE;  // needs more than the static scratch holds
@@ -176,20 +182,20 @@ extern "C" nvfp4_moe_status nvfp4_moe_forward_decode_static(const uint8_t* packe
                                    g_fault.load(), stream)
             : launch_decode_forward(d, packed_experts, gscale, router_logits, x, T, top_k, out, 0, setup.num_sms, ws,
                                     g_fault.load(), stream);
-  return e == cudaSuccess ? NVFP4_MOE_OK : NVFP4_MOE_ERR_CUDA;
+  return e == cudaSuccess ? NVFP4_MOE_OK : cuda_error();
 }
 
 extern "C" nvfp4_moe_status nvfp4_moe_static_get_status(uint32_t* nan_logits) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_MOE_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_error();
   if (dev < 0 || dev >= kMaxDevices) return NVFP4_MOE_ERR_INVALID_ARG;
   StaticSetup setup;
-  if (static_setup(dev, &setup) != cudaSuccess) return NVFP4_MOE_ERR_CUDA;
+  if (static_setup(dev, &setup) != cudaSuccess) return cuda_error();
   DeviceStatus ds{};
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&ds, setup.scratch, sizeof(ds), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(setup.scratch, 0, sizeof(ds));
-  if (e != cudaSuccess) return NVFP4_MOE_ERR_CUDA;
+  if (e != cudaSuccess) return cuda_error();
   if (nan_logits) *nan_logits = ds.nan_logits;
   return nvfp4_moe_decode_status_word(ds.flags);
 }

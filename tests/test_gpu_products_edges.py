@@ -87,3 +87,60 @@ def test_a_call_behind_one_that_times_out(path):
     assert h.nvfp4_moe_get_status()[0] == 0
     assert torch.equal(got, want)
     h.close()
+
+
+class _Capture:
+    """A stream in capture mode, by the driver's own calls: pack, which synchronises, is refused on it."""
+
+    def __init__(self):
+        import ctypes
+        self.cu, self.ctypes = ctypes.CDLL("libcuda.so.1"), ctypes
+        self.stream = torch.cuda.Stream()
+
+    def __enter__(self):
+        assert self.cu.cuStreamBeginCapture_v2(self.ctypes.c_void_p(self.stream.cuda_stream), 2) == 0    # relaxed
+        return self.stream
+
+    def __exit__(self, *exc):
+        graph = self.ctypes.c_void_p()
+        self.cu.cuStreamEndCapture(self.ctypes.c_void_p(self.stream.cuda_stream), self.ctypes.byref(graph))
+        if graph.value:
+            self.cu.cuGraphDestroy(graph)
+
+
+def _packers():
+    """(handle, pack(stream), forward()) of every kind of handle."""
+    P.build()
+    rng = np.random.default_rng(4)
+    q, s = nvfp4(rng, 2, 128, 256)
+    gs = torch.ones((2,), device=DEV)
+    off = _t(np.array([0, 2, 4], np.int32))
+    x, out = _randn(5, 4, 256).to(BF16), torch.empty((4, 128), dtype=BF16, device=DEV)
+    g = P.Grouped(2, 128, 256, 4)
+    gq, gsc = _t(q), _t(s)
+    yield g, lambda st=None: g.nvfp4_grouped_pack(gq, gsc, gs, stream=st), lambda: g.nvfp4_grouped_forward(x, off, out)
+    lin = P.Linear(128, 256, 4)
+    one = torch.ones((1,), device=DEV)
+    yield lin, lambda st=None: lin.nvfp4_linear_pack(gq[0], gsc[0], one, stream=st), lambda: lin.nvfp4_linear_forward(x, out)
+    i4 = P.Int4Linear(128, 256, 64)
+    scale = torch.full((128, 4), 0.5, dtype=BF16, device=DEV)
+    yield i4, lambda st=None: i4.nvfp4_int4_pack(gq[0], scale, stream=st), lambda: i4.nvfp4_int4_forward(x, out)
+    moe = P.MoELayer(2, 128, 128, 4, 1)
+    q13, s13 = nvfp4(rng, 2, 256, 128)
+    q2, s2 = nvfp4(rng, 2, 128, 128)
+    gs3, logits = torch.ones((2, 3), device=DEV), torch.zeros((4, 2), device=DEV)
+    xm, om = x[:, :128].contiguous(), torch.empty((4, 128), dtype=BF16, device=DEV)
+    w = [_t(a) for a in (q13, s13, q2, s2)]
+    yield moe, lambda st=None: moe.nvfp4_moe_pack(*w, gs3, stream=st), lambda: moe.nvfp4_moe_forward(logits, xm, 1, om)
+
+
+@pytest.mark.parametrize("kind", range(4), ids=["grouped", "linear", "int4", "layer"])
+def test_a_refused_call_does_not_fail_the_next(kind):
+    """CUDA keeps the last error until it is asked for: one call's must not come back as another's."""
+    h, pack, forward = list(_packers())[kind]
+    with _Capture() as stream:
+        with pytest.raises(P.Nvfp4MoeError):
+            pack(stream)
+    pack()
+    forward()
+    assert h.nvfp4_moe_get_status()[0] == 0
