@@ -37,7 +37,9 @@
  *     the caller keeps ownership of every pointer it passes;
  *   - work is enqueued on `stream`; only calls documented as synchronous
  *     wait for the GPU;
- *   - shape and pointer errors are detected on the host, before any launch.
+ *   - shape and pointer errors are detected on the host, before any launch, and
+ *     change nothing; a pack that fails for another reason leaves the handle
+ *     unpacked, also where it was packed before.
  */
 #ifndef NVFP4_MOE_H_
 #define NVFP4_MOE_H_

@@ -533,13 +533,13 @@ nvfp4_moe_status nvfp4_moe_pack(nvfp4_moe_t h, const uint8_t* w13_q, const uint8
   DeviceGuard g(h->cfg.device);
   const int E = h->cfg.num_experts + h->cfg.num_shared_experts;
   std::vector<float> gs((size_t)3 * E);
+  h->packed = false;  // until all of it is done
   cudaError_t e = cudaMemcpyAsync(gs.data(), gscale, sizeof(float) * gs.size(), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(h, e, "pack: reading gscale");
   for (size_t i = 0; i < gs.size(); ++i) {
     const float v = gs[i];
     if (!(v > 0.0f) || v != v || v > 3.4e38f) {
-      h->packed = false;
       return fail(h, NVFP4_MOE_ERR_BAD_SCALE,
                   "pack: tensor scale " + std::to_string(i % 3) + " of expert " + std::to_string(i / 3) + " is not finite > 0");
     }
@@ -847,13 +847,12 @@ nvfp4_moe_status nvfp4_linear_pack(nvfp4_moe_t h, const uint8_t* w_q, const uint
     return fail(h, NVFP4_MOE_ERR_INVALID_ARG, "linear_pack: misaligned input");
   DeviceGuard g(h->cfg.device);
   float gs = 0.f;
+  h->packed = false;  // until all of it is done
   cudaError_t e = cudaMemcpyAsync(&gs, gscale, sizeof(float), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(h, e, "linear_pack: reading gscale");
-  if (!(gs > 0.0f) || gs != gs || gs > 3.4e38f) {
-    h->packed = false;
+  if (!(gs > 0.0f) || gs != gs || gs > 3.4e38f)
     return fail(h, NVFP4_MOE_ERR_BAD_SCALE, "linear_pack: the tensor scale is not finite > 0");
-  }
   // the kernels read the down-projection scale of "expert" 0: slot 2 of 3
   const float gs3[3] = {gs, gs, gs};
   e = cudaMemcpyAsync(h->gscale, gs3, sizeof(gs3), cudaMemcpyHostToDevice, st);
@@ -1060,15 +1059,14 @@ nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uin
   DeviceGuard g(h->cfg.device);
   const int E = h->cfg.num_experts;
   float gs[256];
+  h->packed = false;  // until all of it is done
   cudaError_t e = cudaMemcpyAsync(gs, gscale, sizeof(float) * E, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(h, e, "grouped_pack: reading gscale");
   for (int i = 0; i < E; ++i)
-    if (!(gs[i] > 0.0f) || gs[i] > 3.4e38f) {
-      h->packed = false;
+    if (!(gs[i] > 0.0f) || gs[i] > 3.4e38f)
       return fail(h, NVFP4_MOE_ERR_BAD_SCALE,
                   "grouped_pack: the tensor scale of expert " + std::to_string(i) + " is not finite > 0");
-    }
   e = cudaMemcpyAsync(h->gscale, gscale, sizeof(float) * E, cudaMemcpyDeviceToDevice, st);
   if (e == cudaSuccess) e = launch_pack_grouped(w_q, w_s, h->blob, E, h->lin_n, h->cfg.hidden, h->cfg.inter, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);

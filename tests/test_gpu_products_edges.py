@@ -144,3 +144,18 @@ def test_a_refused_call_does_not_fail_the_next(kind):
     pack()
     forward()
     assert h.nvfp4_moe_get_status()[0] == 0
+
+
+@pytest.mark.parametrize("kind", range(4), ids=["grouped", "linear", "int4", "layer"])
+def test_a_pack_that_fails_leaves_the_handle_unpacked(kind):
+    h, pack, forward = list(_packers())[kind]
+    pack()
+    forward()
+    torch.cuda.synchronize()
+    with _Capture() as stream:
+        with pytest.raises(P.Nvfp4MoeError) as ei:
+            pack(stream)
+        assert ei.value.status == CODE["NVFP4_MOE_ERR_CUDA"]
+    with pytest.raises(P.Nvfp4MoeError) as ei:
+        forward()
+    assert ei.value.status == CODE["NVFP4_MOE_ERR_NOT_PACKED"]
