@@ -134,15 +134,15 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _rows(t, cols, dtype, what):
-    """(address, row stride, rows) of a CUDA matrix [rows][cols] whose rows are contiguous.
+def _rows(t, cols, dtype, device, what):
+    """(address, row stride, rows) of a matrix [rows][cols] on cuda:`device` whose rows are contiguous.
 
     Each of a tensor's attributes costs some 0.1 us, and these calls' smallest take 4 us, so none is asked for twice."""
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols or t.dtype != dtype:
         raise ValueError(f"{what}: expected [rows][{cols}] {dtype}, got {tuple(shape)} {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{what}: expected a CUDA tensor on the handle's device, cuda:{device}")
     ld, one = t.stride()
     if one != 1:
         raise ValueError(f"{what}: expected contiguous rows")
@@ -389,17 +389,18 @@ class Grouped(MoELayer):
         import torch
         for t, shape, dt in ((w_q, (self.E, self.N, self.K // 2), torch.uint8),
                              (w_s, (self.E, self.N, self.K // 16), torch.uint8), (gscale, (self.E,), torch.float32)):
-            if tuple(t.shape) != shape or t.dtype != dt:
-                raise ValueError(f"nvfp4_grouped_pack: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
+            if tuple(t.shape) != shape or t.dtype != dt or t.get_device() != self.device:
+                raise ValueError(f"nvfp4_grouped_pack: expected {shape} {dt} on cuda:{self.device}, "
+                                 f"got {tuple(t.shape)} {t.dtype} on {t.device}")
         st = self.lib.nvfp4_grouped_pack(self.h, _ptr(w_q), _ptr(w_s), _ptr(gscale), _stream(stream, self.device))
         self._check(st, "nvfp4_grouped_pack")
 
     def _product(self, fn, what, x, offsets, out, wi, wo, stream):
         if offsets.dtype != self._int32 or offsets.numel() != self.E + 1 or not offsets.is_contiguous() \
-                or not offsets.is_cuda:
-            raise ValueError(f"{what}: expected contiguous CUDA int32 offsets [{self.E + 1}]")
-        xp, ldx, R = _rows(x, wi, self._act, what)
-        op, ldo, Ro = _rows(out, wo, self._out, what)
+                or offsets.get_device() != self.device:
+            raise ValueError(f"{what}: expected contiguous int32 offsets [{self.E + 1}] on cuda:{self.device}")
+        xp, ldx, R = _rows(x, wi, self._act, self.device, what)
+        op, ldo, Ro = _rows(out, wo, self._out, self.device, what)
         if R != Ro:
             raise ValueError(f"{what}: the input has {R} rows, the output {Ro}")
         st = fn(self.h, R, offsets.data_ptr(), xp, ldx, op, ldo,
@@ -453,15 +454,16 @@ class Int4Linear(MoELayer):
         groups = (self.N, self.K // self.group)
         for t, shape, dt in ((w_q, (self.N, self.K // 2), torch.uint8), (scale, groups, self._act),
                              (zero, groups, torch.uint8)):
-            if t is not None and (tuple(t.shape) != shape or t.dtype != dt):
-                raise ValueError(f"nvfp4_int4_pack: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
+            if t is not None and (tuple(t.shape) != shape or t.dtype != dt or t.get_device() != self.device):
+                raise ValueError(f"nvfp4_int4_pack: expected {shape} {dt} on cuda:{self.device}, "
+                                 f"got {tuple(t.shape)} {t.dtype} on {t.device}")
         st = self.lib.nvfp4_int4_pack(self.h, _ptr(w_q), _ptr(scale), _ptr(zero), _stream(stream, self.device))
         self._check(st, "nvfp4_int4_pack")
 
     def nvfp4_int4_forward(self, x, out, stream=None):
         """out [T][N] = x [T][K] times the matrix, T <= max_tokens."""
-        xp, ldx, T = _rows(x, self.K, self._act, "nvfp4_int4_forward")
-        op, ldo, To = _rows(out, self.N, self._out, "nvfp4_int4_forward")
+        xp, ldx, T = _rows(x, self.K, self._act, self.device, "nvfp4_int4_forward")
+        op, ldo, To = _rows(out, self.N, self._out, self.device, "nvfp4_int4_forward")
         if T != To:
             raise ValueError(f"nvfp4_int4_forward: x has {T} rows, out {To}")
         st = self.lib.nvfp4_int4_forward(self.h, T, xp, ldx, op, ldo,
