@@ -553,9 +553,9 @@ nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* 
  * in FP32 (q x exactly), their difference times the scale is added in FP32, and
  * the result rounded once.  x is multiplied as FP16 times a power of two per token
  * (FP16 x too): what lies 2^-34 below a token's largest magnitude is rounded away.
- * A token with an infinity or a NaN has NaN and infinite outputs.  Enqueued on
- * `stream`; no host synchronisation, no allocation and no workspace: calls on one
- * handle may overlap and be captured. */
+ * Infinities and NaNs of x count as in the formula (slower: such a token's outputs
+ * are added up once more).  Enqueued on `stream`; no host synchronisation, no
+ * allocation and no workspace: calls on one handle may overlap and be captured. */
 nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t ldx, void* out, int64_t ldo,
                                     cudaStream_t stream);
 

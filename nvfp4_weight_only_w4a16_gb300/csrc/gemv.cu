@@ -313,10 +313,11 @@ struct Stage {
     return kBf16 ? __uint_as_float(hi ? w & 0xFFFF0000u : w << 16)
                  : __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xFFFFu)));
   }
-  // amax: the rows' largest finite magnitudes (FP32 bits, which order alike), zero on entry.  False, in every thread,
+  // amax: the rows' largest finite magnitudes (FP32 bits, which order alike), zero on entry.  odd: set where one has an
+  // element that is not finite.  False, in every thread,
   // when the copies did not land in time (reported).  The barrier after the writes is the caller's.
-  __device__ __forceinline__ bool finish(float* sums, unsigned* amax, uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         DeviceStatus* st) {
+  __device__ __forceinline__ bool finish(float* sums, unsigned* amax, int* odd, uint64_t* bar, uint32_t parity,
+                                         volatile int* abort, DeviceStatus* st) {
     // one answer for a warp: at the limit one lane may still see the copy and another not, and the reductions below
     // need them all
     const bool landed = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, st, 921));
@@ -341,6 +342,7 @@ struct Stage {
           if (e < kInf) m = max(m, e);
         }
         m = __reduce_max_sync(0xffffffffu, m);
+        if (kFmt != W4::kNvfp4) *odd = 1;
       }
       if (lane == 0) atomicMax(amax + r, __float_as_uint(value(m, 0)));
     }
@@ -375,8 +377,75 @@ struct Stage {
   }
 };
 
+// A CTA's run of granules, u0 .. u1 - 1.  NVFP4: tile * granules + granule, over all CTAs.  INT4: clusters c, c + 1, ..
+// c + tiles - 1 take the same granules for one tile of x each, so that they share the weights in L2.
+template <bool kNv>
+__device__ __forceinline__ void run_of(const GemvArgs& a, int tiles, int granules, int& u0, int& u1) {
+  const int n = kNv ? (int)gridDim.x : (int)gridDim.x / a.S / tiles;
+  const int c = kNv ? (int)blockIdx.x : (int)blockIdx.x / a.S / tiles;
+  const int all = kNv ? tiles * granules : granules;
+  const int base = all / n, extra = all - base * n;
+  u0 = c * base + min(c, extra);
+  u1 = c < n ? u0 + base + (c < extra ? 1 : 0) : u0;
+}
+
+// INT4, where a row of x is not all finite.  With an infinity, sum q x less z sum x is infinity less infinity, but the
+// definition has s (q - z) x, of either sign.  So each thread looks at the results that it has stored, and adds what is
+// not finite of a NaN's row up again, term by term, from x and the packed matrix; all that is finite does not count
+// beside it.  G: groups of 128 elements.
+// Out of line and after all products, so that they do not pay for it: called where a result is stored it cost
+// 131072 x 4096, 4 tokens, 1.6%, a NaN noted there 0.8%, this less than 0.2%.  One thread a result.
+static __device__ __noinline__ void int4_non_finite(const GemvArgs& a, int G, bool bf16, bool zeros) {
+  const unsigned inf = bf16 ? 0x7F80u : 0x7C00u;
+  const auto value = [&](unsigned b) {
+    return bf16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+  };
+  constexpr int kSums = 4 * gv::kRg;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = a.S == 1 ? 0 : (int)cluster_rank();
+  const int rgroups = a.N / 16, granules = (rgroups + gv::kRg - 1) / gv::kRg, RG = gv::kWarps / a.KS;
+  const int row0 = (int)blockIdx.x / a.S % a.tiles * a.tile_rows, rows = min(a.tile_rows, a.T - row0);
+  const int block = 2048 + G * (zeros ? 96 : 64);
+  int u0, u1;
+  run_of<false>(a, a.tiles, granules, u0, u1);
+  for (int u = u0; u < u1; u += RG)
+    for (int j = rank + a.S * warp; j < kSums * min(RG, u1 - u); j += a.S * gv::kWarps) {
+      const int s = j % kSums, rg = (u + j / kSums) * gv::kRg + (s >> 2), t = 2 * (lane & 3) + (s & 1);
+      const int r = lane >> 2, hf = (s >> 1) & 1;  // row r or r + 8 of the 16-row group
+      if (t >= rows || rg >= rgroups) continue;
+      const long long o = (long long)(row0 + t) * a.ldo + 16 * rg + r + 8 * hf;
+      float* const f = static_cast<float*>(a.out) + o;
+      uint16_t* const h = static_cast<uint16_t*>(a.out) + o;
+      const float y = a.out_f32 ? *f : value(*h);
+      if (y == y) continue;
+      const uint16_t* x = static_cast<const uint16_t*>(a.x) + (long long)(row0 + t) * a.ldx;
+      const uint8_t* w = a.packed + (size_t)(rg >> 1) * (a.K / gv::kStep) * block;  // the row's blocks; layout: Step
+      float sum = 0.f;
+      bool any = false;  // else sums of finite values have overflowed, and y stays
+      for (int k = 0; k < a.K && sum == sum; k += 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(x + k);
+        const unsigned p[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+        const unsigned m = __vmaxu2(__vmaxu2(p[0], p[1]), __vmaxu2(p[2], p[3]));
+        if (max(m & 0xFFFFu, m >> 16) < inf) continue;
+        any = true;
+        const uint8_t* b = w + (size_t)(k / gv::kStep) * block;
+        const uint32_t codes = *reinterpret_cast<const uint32_t*>(
+            b + 1024 * (rg & 1) + 512 * ((k >> 6) & 1) + 16 * (4 * r + ((k >> 3) & 3)) + 4 * (2 * hf + ((k >> 5) & 1)));
+        const int at = (((rg & 1) * 8 + r) * G + k % gv::kStep * G / gv::kStep) * 2 + hf;
+        const float scale = value(reinterpret_cast<const uint16_t*>(b + 2048)[at]);
+        const int z = zeros ? b[2048 + 64 * G + at] : 8;
+        for (int e = 0; e < 8; ++e) {  // element 2 i is nibble i, 2 i + 1 nibble 4 + i
+          const unsigned xe = x[k + e];
+          if ((xe & 0x7FFFu) >= inf) sum += scale * (float)((int)(codes >> (4 * ((e >> 1) + 4 * (e & 1))) & 15u) - z) * value(xe);
+        }
+      }
+      if (!any) continue;
+      if (a.out_f32) *f = sum;
+      else *h = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(sum)) : __half_as_ushort(__float2half_rn(sum));
+    }
+}
+
 template <W4 kFmt, bool kBf16, bool kZeros, bool kCenter>
-__global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
+__global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(const __grid_constant__ GemvArgs a) {
   using S = Step<kFmt, kZeros>;
   constexpr int kSums = 4 * gv::kRg;                // of a lane
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, x rows, then (INT4) the cluster's and the group sums
@@ -385,14 +454,14 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   __shared__ int tile_row0[S::kNv ? gv::kMaxTiles : 1], wsum[8];
   __shared__ uint8_t tile_count[S::kNv ? gv::kMaxTiles : 1];  // its rows
   __shared__ uint64_t x_bar;  // x rows landed
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, odd;  // odd: INT4, x is not all finite
   __shared__ float red[2][gv::kWarps][kSums][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int tiles = a.tiles;
   if (threadIdx.x < 2 * gv::kRows) amax[0][threadIdx.x] = 0u;
   if (threadIdx.x == 0) {
-    abort_flag = 0;
+    abort_flag = odd = 0;
     mbar_init(&x_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -437,24 +506,15 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
   const int granules = (rgroups + gv::kRg - 1) / gv::kRg;  // of a matrix
   const int RG = gv::kWarps / a.KS;                        // granules at a time
   const int ks = warp % a.KS, wg = warp / a.KS;
-  // this CTA's run of granules.  NVFP4: tile * granules + granule, over all CTAs.  INT4: clusters c, c + 1, ..
-  // c + tiles - 1 take the same granules for one tile of x each, so that they share the weights in L2
   int tile = 0, left = 0x7FFFFFFF;  // the tile at the run's next granule, and how many it has from there on
   int u0, u1;
-  {
-    const int n = S::kNv ? (int)gridDim.x : (int)gridDim.x / a.S / tiles;
-    const int c = S::kNv ? (int)blockIdx.x : (int)blockIdx.x / a.S / tiles;
-    const int all = S::kNv ? tiles * granules : granules;
-    const int base = all / n, extra = all - base * n;
-    u0 = c * base + min(c, extra);
-    u1 = c < n ? u0 + base + (c < extra ? 1 : 0) : u0;
-    if (u0 >= u1) return;
-    if (S::kNv) {
-      tile = u0 / granules;
-      left = granules - (u0 - tile * granules);
-    } else {
-      tile = (int)blockIdx.x / a.S % tiles;
-    }
+  run_of<S::kNv>(a, tiles, granules, u0, u1);
+  if (u0 >= u1) return;
+  if (S::kNv) {
+    tile = u0 / granules;
+    left = granules - (u0 - tile * granules);
+  } else {
+    tile = (int)blockIdx.x / a.S % tiles;
   }
   if (!S::kNv && a.S > 1) cluster_arrive();  // the first batch waits for it: every CTA has begun
   uint8_t* xs = smem + gv::kWarps * gv::kDepth * S::kSlot;
@@ -552,6 +612,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     for (int j = rank + a.S * warp; j < pj; j += a.S * gv::kWarps) {
       float y = 0.f;
       for (int c = 0; c < a.S; ++c) y += from[((c << (5 - slog)) + (j >> slog)) * 32];
+      if (y != y) odd = 1;  // by another CTA's slice; what this thread writes it reads itself
       if (!dead) store(pg0 + j / kSums, j % kSums, y);
     }
   };
@@ -570,7 +631,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
       fresh = true;
     }
     if (fresh) {
-      if (!stage.finish(sums, amax[tphase], &x_bar, (uint32_t)tphase, &abort_flag, a.st)) {
+      if (!stage.finish(sums, amax[tphase], &odd, &x_bar, (uint32_t)tphase, &abort_flag, a.st)) {
         dead = true;
         if (S::kNv || a.S == 1) break;  // a cluster's others wait for this CTA's sums, which then count for nothing
       }
@@ -635,6 +696,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(GemvArgs a) {
     cluster_wait();
     add_shared();
   }
+  if (!S::kNv && odd) int4_non_finite(a, S::kGroups, kBf16, kZeros);
   if (dead) {
     if (threadIdx.x == 0 && a.fault != 1) drain_copies(&x_bar, (uint32_t)tphase + 1, 1);
     asm volatile("cp.async.wait_all;" ::: "memory");

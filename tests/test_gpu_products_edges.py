@@ -159,3 +159,54 @@ def test_a_pack_that_fails_leaves_the_handle_unpacked(kind):
     with pytest.raises(P.Nvfp4MoeError) as ei:
         forward()
     assert ei.value.status == CODE["NVFP4_MOE_ERR_NOT_PACKED"]
+
+
+def _int4(N, K, group, zeros, f16, out_f32, seed=0):
+    """A packed INT4 handle and its codes less their zero points and scales, in float64."""
+    P.build()
+    rng = np.random.default_rng(seed)
+    t = torch.float16 if f16 else BF16
+    q = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    scale = torch.from_numpy(rng.uniform(-0.1, 0.1, (N, K // group))).to(t)
+    scale[0, 0] = 0.0
+    zero = rng.integers(0, 16, (N, K // group), dtype=np.uint8)
+    h = P.Int4Linear(N, K, group, act_f16=f16, out_f32=out_f32)
+    h.nvfp4_int4_pack(_t(q), scale.to(DEV), _t(zero) if zeros else None)
+    code = np.stack([q & 15, q >> 4], axis=-1).reshape(N, K).astype(np.float64)
+    z = np.repeat(zero.astype(np.float64), group, axis=1) if zeros else 8.0
+    return h, (code - z) * np.repeat(scale.double().numpy(), group, axis=1)
+
+
+@pytest.mark.parametrize("T,N,K,group,zeros,f16,out_f32", [
+    (1, 48, 128, 128, False, False, True), (5, 272, 640, 32, True, True, False), (8, 80, 512, 64, True, False, False),
+    (16, 144, 1024, 64, False, True, True), (3, 64, 384, 32, False, False, False), (10, 80, 640, 128, True, True, True),
+    (16, 208, 8320, 32, True, False, True),      # clusters: each CTA has a slice of the token
+    (12, 48, 16384, 64, False, True, False)])
+def test_int4_infinities_keep_their_sign(T, N, K, group, zeros, f16, out_f32):
+    """A token's infinities give what the definition gives: s (q - z) x is an infinity of the term's sign, NaN where
+    s (q - z) is zero or two terms' signs differ.  Tokens without any are as they were, bit for bit."""
+    h, w = _int4(N, K, group, zeros, f16, out_f32)
+    x = _randn(6, T, K).to(torch.float16 if f16 else BF16)
+    new = lambda: torch.empty((T, N), dtype=torch.float32 if out_f32 else x.dtype, device=DEV)
+    clean = h.nvfp4_int4_forward(x, new())
+    rng = np.random.default_rng(7)
+    inf = float("inf")
+    marks = [[(0, inf)], [(K - 1, -inf)], [(K // 2 + 3, inf), (K // 3, inf)], [(5, inf), (K - 9, -inf)],
+             [(K // 2, inf), (K // 2 + 1, -inf)], [(17, float("nan"))], [(K - 2, inf), (1, float("nan"))]]
+    hit = {}
+    for i, t in enumerate(rng.permutation(T)[:max(1, T - 1)]):
+        for k, v in marks[i % len(marks)]:
+            x[t, k] = v
+        hit[t] = True
+    got = h.nvfp4_int4_forward(x, new())
+    assert h.nvfp4_moe_get_status()[0] == 0
+    xs = x.double().cpu().numpy()
+    for t in range(T):
+        if t not in hit:
+            assert torch.equal(got[t], clean[t])
+            continue
+        k = np.nonzero(~np.isfinite(xs[t]))[0]
+        with np.errstate(invalid="ignore"):
+            want = (w[:, k] * xs[t, k]).sum(axis=1)
+        np.testing.assert_array_equal(got[t].double().cpu().numpy(), want)
+    h.close()
