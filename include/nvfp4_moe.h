@@ -501,8 +501,9 @@ nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uin
  *   ld*      at least the row length, a multiple of 8, at most 2^24
  * Products are exact and accumulated in FP32; one rounding to BF16 at the end.
  * The forward takes the streaming kernel for few rows (by default up to 8 per
- * expert on average; nvfp4_moe_set_path forces either; the streaming kernel takes
- * at most 2048 rows), the tcgen05 GEMM above; the backward always the GEMM.  The
+ * expert on average, fewer where K is above 4096: 5 at 7168, 2 at 16384;
+ * nvfp4_moe_set_path forces either; the streaming kernel takes at most 2048
+ * rows), the tcgen05 GEMM above; the backward always the GEMM.  The
  * streaming kernel multiplies x as FP16 times a power of two per row: what lies
  * 2^-38 below a row's largest magnitude is rounded away. */
 nvfp4_moe_status nvfp4_grouped_forward(nvfp4_moe_t h, int R, const int32_t* offsets, const void* x, int64_t ldx,

@@ -980,11 +980,16 @@ nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t*
     return bad(NVFP4_MOE_ERR_INVALID_ARG, "a row stride is below the row length, above 2^24 or no multiple of 8");
   if (!backward && h->path == NVFP4_MOE_PATH_DECODE && R > kGemvMaxRows)
     return bad(NVFP4_MOE_ERR_UNSUPPORTED_SHAPE, "the decode path takes at most 2048 rows");
-  // AUTO streams the weights through the row kernel up to 8 rows an expert: at 128 experts of 1536 x 4096 it takes 70,
-  // 102, 122 and 167 us at 1, 4, 8 and 12 rows an expert, the GEMM 105, 144, 155 and 154; at 32 of 1024 x 1024 the two
-  // meet at 8 as well (25.5 and 24.6).
+  // AUTO streams the weights through the row kernel as long as an expert's rows, were they even, make one tile of it: 8
+  // up to K = 4096, then as many as fit beside its rings (5 at 7168, 4 at 8192, 2 at 16384).  It reads and converts a
+  // matrix once for each tile, in a little over half of the GEMM's time, so that a second tile loses the gain.  Even
+  // counts, us streamed and as GEMM: 128 experts of 1536 x 4096, 8 rows each 77 and 144; 64 of 2048 x 7168, 5 each 85
+  // and 158, 6 each 154 and 155; of 2048 x 8192, 4 each 97 and 176, 6 each 176 and 176; of 1024 x 16384, 2 each 99 and
+  // 198, 4 each 181 and 198, 8 each 340 and 198; one of 16384 x 16384, 2 rows 29 and 97, 8 rows 90 and 63.  Uneven ones
+  // make more tiles: at these limits, popularity by Zipf's law with 1.1, 112 and 131, 111 and 136, 117 and 128, 109 and
+  // 153.  The host does not see the offsets; all rows with one expert is the worst (1024 of 1536 x 4096: 76 and 31).
   const bool stream = !backward && (h->path == NVFP4_MOE_PATH_DECODE ||
-                                    (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= 8 * E));
+                                    (h->path == NVFP4_MOE_PATH_AUTO && R <= kGemvMaxRows && R <= E * grouped_gemv_tile_rows(K)));
   DeviceGuard g(h->cfg.device);
   const GroupedTiling tiling = grouped_tiling(E, R, backward ? K / 128 : (N + 127) / 128, backward ? (N + 127) / 128 : K / 128,
                                               h->num_sms);

@@ -763,6 +763,13 @@ static cudaError_t launch_gemv(const GemvArgs& a, long long granules, size_t sme
 // NVFP4: two of the longest rows of x fit beside the rings (kMaxTiles).
 static_assert(gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kSlot + 2 * (16384 * 2 + 16) <= gv::smem_for(true), "x");
 
+static int nvfp4_pitch(int K) { return K * 2 + 16; }  // 16 bytes apart in the banks: 32-byte pieces of two rows never collide
+static constexpr size_t kNvfp4Rings = (size_t)gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kSlot;
+int grouped_gemv_tile_rows(int K) {
+  const int fit = (int)((gv::smem_for(true) - kNvfp4Rings) / nvfp4_pitch(K));
+  return fit < gv::kRows ? fit : gv::kRows;
+}
+
 cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   const int Np = (p.N + 127) / 128 * 128;
   GemvArgs a{};
@@ -786,13 +793,11 @@ cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st) {
   const int granules = (p.N / 16 + gv::kRg - 1) / gv::kRg;
   const int touched = p.R < p.E ? p.R : p.E;
   set_steps(a, p.K / gv::kStep, (long long)touched * granules / p.num_sms);
-  a.pitch = p.K * 2 + 16;  // rows 16 bytes apart in the banks: the lanes' 32-byte pieces of two rows never collide
-  const size_t rings = (size_t)gv::kWarps * gv::kDepth * Step<W4::kNvfp4, false>::kSlot;
-  const int fit = (int)((gv::smem_for(true) - rings) / a.pitch);
-  a.tile_rows = fit < gv::kRows ? fit : gv::kRows;
+  a.pitch = nvfp4_pitch(p.K);
+  a.tile_rows = grouped_gemv_tile_rows(p.K);
   if (p.R < a.tile_rows) a.tile_rows = p.R;
   return launch_gemv<W4::kNvfp4, true, false, false>(a, (long long)(touched + p.R / a.tile_rows) * granules,
-                                                     rings + (size_t)a.tile_rows * a.pitch, p.num_sms, st);
+                                                     kNvfp4Rings + (size_t)a.tile_rows * a.pitch, p.num_sms, st);
 }
 
 // Shared memory of a CTA that takes `steps` steps of K for `rows` rows of x.

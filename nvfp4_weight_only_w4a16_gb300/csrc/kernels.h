@@ -191,8 +191,9 @@ GroupedTiling grouped_tiling(int E, int R, int out_blocks, int steps, int num_sm
 // rows_map: in as [R][K or N] BF16, box {64, tiling.box}, 128B swizzle.
 cudaError_t launch_grouped_gemm(const GroupedProduct& p, bool backward, const GroupedTiling& tiling,
                                 const CUtensorMap& rows_map, cudaStream_t st);
-// The forward for few rows, streamed through registers (gemv.cu).
+// The forward for few rows: weights streamed through per-warp rings in shared memory (gemv.cu).
 cudaError_t launch_grouped_gemv(const GroupedProduct& p, cudaStream_t st);
+int grouped_gemv_tile_rows(int K);  // rows of an expert that it multiplies in one pass over the matrix, 2..8
 constexpr int kGemvMaxRows = 2048;  // of launch_grouped_gemv (its tile table)
 
 // y [T][N] = x [T][K] times an INT4 matrix with group scales and zero points.

@@ -210,3 +210,22 @@ def test_int4_infinities_keep_their_sign(T, N, K, group, zeros, f16, out_f32):
             want = (w[:, k] * xs[t, k]).sum(axis=1)
         np.testing.assert_array_equal(got[t].double().cpu().numpy(), want)
     h.close()
+
+
+@pytest.mark.parametrize("K,most", [(4096, 8), (7168, 5), (8192, 4), (12288, 2), (16384, 2)])
+def test_the_default_path_streams_one_tile_an_expert(K, most):
+    """Where an expert's rows no longer fit the streaming kernel's one pass over the matrix, the GEMM takes over.  The
+    two add in different orders, so the bits of an FP32 result tell which one ran."""
+    E, N = 4, 256
+    h = _experts(E, N, K, E * 8 + 4, out_f32=True, seed=K)
+    for R, path in ((E * most, P.PATH_DECODE), (E * most + 4, P.PATH_PREFILL), (E * 8 + 4, P.PATH_PREFILL)):
+        off = _t((np.arange(E + 1) * R // E).astype(np.int32))
+        x = _randn(R, R, K).to(BF16)
+        got = {}
+        for p in (P.PATH_AUTO, P.PATH_DECODE, P.PATH_PREFILL):
+            h.nvfp4_moe_set_path(p)
+            got[p] = h.nvfp4_grouped_forward(x, off, torch.empty((R, N), device=DEV))
+        assert not torch.equal(got[P.PATH_DECODE], got[P.PATH_PREFILL])
+        assert torch.equal(got[P.PATH_AUTO], got[path]), (R, path)
+    assert h.nvfp4_moe_get_status()[0] == 0
+    h.close()
