@@ -394,7 +394,8 @@ __device__ __forceinline__ void run_of(const GemvArgs& a, int tiles, int granule
 // not finite of a NaN's row up again, term by term, from x and the packed matrix; all that is finite does not count
 // beside it.  G: groups of 128 elements.
 // Out of line and after all products, so that they do not pay for it: called where a result is stored it cost
-// 131072 x 4096, 4 tokens, 1.6%, a NaN noted there 0.8%, this less than 0.2%.  One thread a result.
+// 131072 x 4096, 4 tokens, 1.6%, this less than 1%.  One thread a result (with an infinity in every token that product
+// takes 540 us, 4096 x 4096 with one token 30).
 static __device__ __noinline__ void int4_non_finite(const GemvArgs& a, int G, bool bf16, bool zeros) {
   const unsigned inf = bf16 ? 0x7F80u : 0x7C00u;
   const auto value = [&](unsigned b) {
@@ -421,21 +422,26 @@ static __device__ __noinline__ void int4_non_finite(const GemvArgs& a, int G, bo
       const uint8_t* w = a.packed + (size_t)(rg >> 1) * (a.K / gv::kStep) * block;  // the row's blocks; layout: Step
       float sum = 0.f;
       bool any = false;  // else sums of finite values have overflowed, and y stays
-      for (int k = 0; k < a.K && sum == sum; k += 8) {
-        const uint4 v = *reinterpret_cast<const uint4*>(x + k);
-        const unsigned p[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
-        const unsigned m = __vmaxu2(__vmaxu2(p[0], p[1]), __vmaxu2(p[2], p[3]));
+      for (int k0 = 0; k0 < a.K && sum == sum; k0 += 64) {  // a chunk, whose loads overlap
+        uint4 v[8];
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const uint4*>(x + k0)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          m = __vmaxu2(__vmaxu2(m, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu)),
+                       __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
         if (max(m & 0xFFFFu, m >> 16) < inf) continue;
         any = true;
-        const uint8_t* b = w + (size_t)(k / gv::kStep) * block;
-        const uint32_t codes = *reinterpret_cast<const uint32_t*>(
-            b + 1024 * (rg & 1) + 512 * ((k >> 6) & 1) + 16 * (4 * r + ((k >> 3) & 3)) + 4 * (2 * hf + ((k >> 5) & 1)));
-        const int at = (((rg & 1) * 8 + r) * G + k % gv::kStep * G / gv::kStep) * 2 + hf;
-        const float scale = value(reinterpret_cast<const uint16_t*>(b + 2048)[at]);
-        const int z = zeros ? b[2048 + 64 * G + at] : 8;
-        for (int e = 0; e < 8; ++e) {  // element 2 i is nibble i, 2 i + 1 nibble 4 + i
-          const unsigned xe = x[k + e];
-          if ((xe & 0x7FFFu) >= inf) sum += scale * (float)((int)(codes >> (4 * ((e >> 1) + 4 * (e & 1))) & 15u) - z) * value(xe);
+        const uint8_t* b = w + (size_t)(k0 / gv::kStep) * block;
+        for (int k = k0; k < k0 + 64; ++k) {
+          if ((x[k] & 0x7FFFu) < inf) continue;
+          const uint32_t codes = *reinterpret_cast<const uint32_t*>(
+              b + 1024 * (rg & 1) + 512 * ((k >> 6) & 1) + 16 * (4 * r + ((k >> 3) & 3)) + 4 * (2 * hf + ((k >> 5) & 1)));
+          const int code = (int)(codes >> (4 * (((k & 7) >> 1) + 4 * (k & 1)))) & 15;
+          const int at = (((rg & 1) * 8 + r) * G + k % gv::kStep * G / gv::kStep) * 2 + hf;
+          const float scale = value(reinterpret_cast<const uint16_t*>(b + 2048)[at]);
+          sum += scale * (float)(code - (zeros ? b[2048 + 64 * G + at] : 8)) * value(x[k]);
         }
       }
       if (!any) continue;
