@@ -500,6 +500,9 @@ nvfp4_moe_status nvfp4_grouped_pack(nvfp4_moe_t h, const uint8_t* w_q, const uin
  *            overlap the input
  *   ld*      at least the row length, a multiple of 8, at most 2^24
  * Products are exact and accumulated in FP32; one rounding to BF16 at the end.
+ * The tensor cores cut off the bits that an addition drops: an FP32 result is off
+ * by about 1.2e-9 of its norm per term that one accumulator adds.  The GEMM has two,
+ * so 2e-6 at 4096 terms (E4M3 scales over their whole range; FP32 arithmetic 8e-7).
  * The forward takes the streaming kernel for few rows (by default up to 8 per
  * expert on average, fewer where K is above 4096: 5 at 7168, 2 at 16384;
  * nvfp4_moe_set_path forces either; the streaming kernel takes at most 2048
@@ -551,8 +554,10 @@ nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* 
 /* out [T][N] as above, 1 <= T <= max_tokens; x [T][K] and out DEVICE, 16-byte
  * aligned, rows ldx / ldo elements apart (at least the row length, a multiple
  * of 8, at most 2^24), not overlapping.  Per group sum q x and z sum x are formed
- * in FP32 (q x exactly), their difference times the scale is added in FP32, and
- * the result rounded once.  x is multiplied as FP16 times a power of two per token
+ * in FP32 (each q x is exact, their sum is the tensor cores', which cut off what an
+ * addition drops), their difference times the scale is added in FP32, and the result
+ * rounded once: an FP32 result is off by up to 3e-7 of its norm, 1.2e-7 where x is
+ * FP16.  x is multiplied as FP16 times a power of two per token
  * (FP16 x too): what lies 2^-34 below a token's largest magnitude is rounded away.
  * Infinities and NaNs of x count as in the formula (slower: such a token's outputs
  * are added up once more).  Enqueued on `stream`; no host synchronisation, no

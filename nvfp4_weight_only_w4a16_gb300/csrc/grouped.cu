@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
   using Plan = gg::Plan<kBackward, kCtas, kTile>;
   constexpr int kIssuers = Plan::kIssuers, kTeams = Plan::kTeams, kTeamWarps = Plan::kTeamWarps;
   // FP32 results: the two halves of the reduction into an accumulator each, summed in the epilogue, in place of two
-  // units' accumulators.  The tensor core truncates where it adds (1e-6 of the result's norm after 4096 terms in one
-  // accumulator), and BF16's rounding hides that.
+  // units' accumulators.  The tensor core truncates where it adds (4e-6 of the result's norm after 4096 terms in one
+  // accumulator, E4M3 scales over their whole range, 2e-6 in two), and BF16's rounding hides that.
   const auto f32 = [&] { return kOut == Out::kF32 || (kOut == Out::kEither && a.out_f32); };
   const auto halves = [&] { return kIssuers == 1 && !kSplit && f32(); };  // (split: already fewer terms each)
   constexpr int kStagesA = Plan::kStagesA, kStagesB = Plan::kStagesB, kRaw = Plan::kRaw;
