@@ -547,7 +547,8 @@ nvfp4_moe_status nvfp4_int4_create(const nvfp4_int4_config* config, nvfp4_moe_t*
  *   zero  [N][K/g] uint8   zero points 0..15, or NULL: 8 everywhere
  * NVFP4_MOE_ERR_BAD_SCALE, and the handle is left unpacked, for a scale that is
  * not finite or a zero point above 15.  Synchronous.  Inputs may be freed once
- * the call returns. */
+ * the call returns.  Zero points are laid out only where there are any: after a
+ * pack that adds or drops them a captured forward has to be captured again. */
 nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* scale, const uint8_t* zero,
                                  cudaStream_t stream);
 

@@ -17,18 +17,19 @@
 // barrier each time.  The rings run ahead across that, and across new rows of x.
 // Rows of x that do not fit beside the rings are spread over a cluster (INT4): each
 // of its CTAs takes a slice of K, and sends its sums to the CTA that stores them,
-// which adds them in a fixed order one batch later.  (8192 x 8192, 16 tokens: 28 us
-// against 36 as tiles of 4 rows, each with the weights converted again; 4096 x 16384:
-// 26 against 49.  16 rows at a time instead of twice 8 was slower, 18 us against 15
-// for 4096 x 4096: work per weight and token outweighs the conversion, and the
-// shorter slices need more batches.)
+// which adds them in a fixed order one batch later.  (8192 x 8192, groups of 32, 16
+// tokens: 18.6 us against 26.9 as tiles of 4 rows, each with the weights converted
+// again; 4096 x 16384, groups of 64: 18.1 against 42.7.  16 rows at a time instead of
+// twice 8 was a fifth slower in an earlier form of this kernel: work per weight and
+// token outweighs the conversion, and the shorter slices need more batches.)
 //
 // Both formats run on FP16 operands.  x enters as FP16 times a power of two per row
 // that brings its largest finite magnitude into [2^13, 2^14); what that drops lies
-// 2^-37 below the row's maximum.  NVFP4 codes times their scale are exact in FP16
+// 2^-38 below the row's maximum (INT4: 2^-34, see below).  NVFP4 codes times their scale are exact in FP16
 // (at most 6 significant bits).  An INT4 code needs no conversion: its four bits,
 // masked in place, are the FP16 subnormal q 2^-24, or q 2^-20 one nibble higher,
-// which x's matching elements, staged times 2^-4, make good.  The zero point comes
+// which x's matching elements, staged times 2^-4, make good (their smallest step is 2^4
+// times farther up).  The zero point comes
 // off a group's FP32 sum with the sum of x over the group, which is staged too.
 // The tensor core aligns what it adds by exponents that a subnormal does not show, and
 // truncates there: with FP16's 11 significant bits an FP32 result was off by up to 7e-7
