@@ -557,8 +557,8 @@ nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* 
  * of 8, at most 2^24), not overlapping.  Per group sum q x and z sum x are formed
  * in FP32 (each q x is exact, their sum is the tensor cores', which cut off what an
  * addition drops), their difference times the scale is added in FP32, and the result
- * rounded once: an FP32 result is off by up to 3e-7 of its norm, 1.2e-7 where x is
- * FP16.  x is multiplied as FP16 times a power of two per token
+ * rounded once: an FP32 result is off by 1 to 3e-7 of its norm, the more the nearer
+ * the codes are to their zero points; 1e-7 where x is FP16.  x is multiplied as FP16 times a power of two per token
  * (FP16 x too): what lies 2^-34 below a token's largest magnitude is rounded away.
  * Infinities and NaNs of x count as in the formula (slower: such a token's outputs
  * are added up once more).  Enqueued on `stream`; no host synchronisation, no

@@ -27,16 +27,19 @@
 // that brings its largest finite magnitude into [2^13, 2^14); what that drops lies
 // 2^-38 below the row's maximum (INT4: 2^-34, see below).  NVFP4 codes times their scale are exact in FP16
 // (at most 6 significant bits).  An INT4 code needs no conversion: its four bits,
-// masked in place, are the FP16 subnormal q 2^-24, or q 2^-20 one nibble higher,
+// masked in place, are the FP16 subnormal q 2^-22, or q 2^-18 one nibble higher,
 // which x's matching elements, staged times 2^-4, make good (their smallest step is 2^4
-// times farther up).  The zero point comes
-// off a group's FP32 sum with the sum of x over the group, which is staged too.
+// times farther up).  The zero point comes off a group's FP32 sum with the sum of x
+// over the group, which is staged too.
 // The tensor core aligns what it adds by exponents that a subnormal does not show, and
-// truncates there: with FP16's 11 significant bits an FP32 result was off by up to 7e-7
-// of its norm, so that case (kCenter) makes q - 8 of every code, a normal number, at one
-// more instruction a pair (1024 | q, less 1032), and takes z - 8 off the sums: 1e-7.
-// BF16's sums need fewer bits, 2 to 2.7e-7 without, and stay as they are: centred codes
-// cost a quarter to a third there (131072 x 4096, 4 tokens, 46 -> 62 us).
+// truncates there.  So the codes lie as high as FP16's ten low bits allow: the packed
+// words are rotated left by 2 bits, and the second byte comes down by a rotation in place
+// of a shift.  FP32 results of BF16 x are off by 1 to 1.5e-7 of their norm (codes of normal
+// weights; FP32 arithmetic 1 to 4e-7), two bits lower by 4 to 6e-7.  FP16's 11 significant
+// bits still show (2e-7; 7e-7 with codes next to their zero points), so with an FP32 result
+// that case (kCenter) makes q - 8 of every code, a normal number, at one more instruction a
+// pair (1024 | 4 q, less 1056), and takes z - 8 off the sums: 1e-7, and a quarter to a third
+// more time (131072 x 4096, 4 tokens, 46 -> 62 us).
 #include <mutex>
 
 #include "common.cuh"
@@ -126,7 +129,7 @@ __device__ __forceinline__ void copies_wait() {  // all but the latest kDepth - 
 //   their scales 128; a slot holds [chunk][group][512 B] codes (lane t's at seg_pos(t)), then [chunk][group][64 B] scales.
 //   INT4: packed as [N/32][K/128] blocks, one block a slot's contents: [group][chunk][32 lanes][16 B] codes -- lane
 //   4 r + t holds the words of row r's elements 8 t .. 8 t + 7 and 32 + 8 t .. of the chunk, then row r + 8's; nibble i
-//   of a word is element 2 i, nibble 4 + i element 2 i + 1 -- then [group][8 r][128/g][2: row r, row r + 8] 16-bit
+//   of a word is element 2 i, nibble 4 + i element 2 i + 1, and the word is rotated left by 2 bits -- then [group][8 r][128/g][2: row r, row r + 8] 16-bit
 //   scales and, if the matrix has any, zero points alike in bytes.
 template <W4 kFmt, bool kZeros>
 struct Step {
@@ -249,13 +252,13 @@ __device__ __forceinline__ void use_step(const Step<kFmt, kZeros>& w, const uint
           const uint4 c = w.c[q][run >> 1];
           const uint32_t l = run & 1 ? c.y : c.x, h = run & 1 ? c.w : c.z;
           const uint32_t* xr = x[run >> 1] + 4 * (run & 1);
-          const uint32_t l8 = l >> 8, h8 = h >> 8;
-          // kCenter: 1024 | q less 1032, and 1024 | 16 q less 1152 (0x6400 = 1024, 0x6408 = 1032, 0x6480 = 1152)
+          const uint32_t l8 = __byte_perm(l, 0, 0x0321), h8 = __byte_perm(h, 0, 0x0321);  // rotated right by 8
+          // kCenter: 1024 | 4 q less 1056, and 1024 | 64 q less 1536 (0x6400 = 1024, 0x6420 = 1056, 0x6600 = 1536)
           const auto lo = [](uint32_t w) {
-            return kCenter ? hsub2_u32((w & 0x000F000Fu) | 0x64006400u, 0x64086408u) : w & 0x000F000Fu;
+            return kCenter ? hsub2_u32((w & 0x003C003Cu) | 0x64006400u, 0x64206420u) : w & 0x003C003Cu;
           };
           const auto hi = [](uint32_t w) {
-            return kCenter ? hsub2_u32((w & 0x00F000F0u) | 0x64006400u, 0x64806480u) : w & 0x00F000F0u;
+            return kCenter ? hsub2_u32((w & 0x03C003C0u) | 0x64006400u, 0x66006600u) : w & 0x03C003C0u;
           };
           mma_16816(part, lo(l), lo(h), hi(l), hi(h), xr[0], xr[1]);
           mma_16816(part, lo(l8), lo(h8), hi(l8), hi(h8), xr[2], xr[3]);
@@ -293,7 +296,7 @@ __device__ __forceinline__ float add_halves(float sum, uint32_t w, uint16_t s) {
 }
 
 // x rows into shared memory as FP16 times 2^-p per row; INT4: elements 2, 3, 6 and 7 of every 8 times another
-// 2^-4, and 2^-24 (kCenter: 1) times the sums over each group of the matrix into sums[group][8].  In two parts:
+// 2^-4, and 2^-22 (kCenter: 4) times the sums over each group of the matrix into sums[group][8].  In two parts:
 // start() copies the rows as they are (bulk copies, by one thread), finish() waits for them, finds each row's p and
 // converts in place; a row's 16-byte pieces are shared by kWarps / rows warps.
 // (Small loops on purpose: a call's first use of its code comes from memory, and this runs before any product.)
@@ -362,7 +365,7 @@ struct Stage {
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        // odd pairs of INT4: what the MMA multiplies with q 2^-20
+        // odd pairs of INT4: what the MMA multiplies with q 2^-18
         const float f = kFmt != W4::kNvfp4 && (j & 1) ? f2.y * 0.0625f : f2.y;
         const __half2 h = __floats2half2_rn(value(w[j], 0) * f2.x * f, value(w[j], 1) * f2.x * f);
         o[j] = *reinterpret_cast<const uint32_t*>(&h);
@@ -372,7 +375,7 @@ struct Stage {
       if (kFmt != W4::kNvfp4) {  // a group's pieces belong to neighbouring lanes
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = kCenter ? sum : sum * 0x1p-24f;
+        if (ok && p % kLanes == 0) sums[p / kLanes * gv::kRows + r] = sum * (kCenter ? 4.0f : 0x1p-22f);
       }
     }
     return true;
@@ -440,7 +443,7 @@ static __device__ __noinline__ void int4_non_finite(const GemvArgs& a, int G, bo
           if ((x[k] & 0x7FFFu) < inf) continue;
           const uint32_t codes = *reinterpret_cast<const uint32_t*>(
               b + 1024 * (rg & 1) + 512 * ((k >> 6) & 1) + 16 * (4 * r + ((k >> 3) & 3)) + 4 * (2 * hf + ((k >> 5) & 1)));
-          const int code = (int)(codes >> (4 * (((k & 7) >> 1) + 4 * (k & 1)))) & 15;
+          const int code = (int)(__funnelshift_r(codes, codes, 2) >> (4 * (((k & 7) >> 1) + 4 * (k & 1)))) & 15;
           const int at = (((rg & 1) * 8 + r) * G + k % gv::kStep * G / gv::kStep) * 2 + hf;
           const float scale = value(reinterpret_cast<const uint16_t*>(b + 2048)[at]);
           sum += scale * (float)(code - (zeros ? b[2048 + 64 * G + at] : 8)) * value(x[k]);
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1) gemv_kernel(const __grid_cons
       }
       if (threadIdx.x < gv::kRows) amax[tphase ^ 1][threadIdx.x] = 0u;
       if (S::kNv) gs = __ldg(a.gscale + tile_expert[tile]);
-      up = pow2_pair(row_exponent(amax[tphase][2 * (lane & 3) + (warp & 1)]) + (S::kNv || kCenter ? 0 : 24));
+      up = pow2_pair(row_exponent(amax[tphase][2 * (lane & 3) + (warp & 1)]) + (S::kNv ? 0 : kCenter ? -2 : 22));
       // a lane whose token does not exist reads the last one's row: its column of the products is not stored
       xl0 = xs + min(lane >> 2, rows - 1) * a.pitch + (lane & 3) * (S::kNv ? 32 : 16) + ks * 256;
       __syncthreads();
@@ -872,7 +875,7 @@ __device__ __forceinline__ uint32_t int4_word(uint32_t w) {  // canonical nibble
   uint32_t o = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o |= (((w >> (8 * i)) & 0xFu) << (4 * i)) | (((w >> (8 * i + 4)) & 0xFu) << (16 + 4 * i));
-  return o;
+  return __funnelshift_l(o, o, 2);
 }
 
 // One CTA a block of 32 rows x 128 elements; rows past the matrix hold zeros.
