@@ -28,7 +28,11 @@
  * decode forward on pinned host buffers (nvfp4_moe_forward_host).  The 4-bit
  * products a layer is made of are there on their own too: NVFP4 experts over
  * ragged row groups, with the gradient of their input (nvfp4_grouped_*), and
- * a dense linear with INT4 weights and group scales (nvfp4_int4_*).
+ * a dense linear with INT4 weights and group scales (nvfp4_int4_*).  So is what
+ * a block has around them: routing with its gradient (nvfp4_route_*), SwiGLU
+ * with 8-bit checkpoints for its backward pass (nvfp4_swiglu_*), the RMS norm
+ * with the residual's addition (nvfp4_norm_*), whose 8-bit output feeds a dense
+ * linear with 8-bit integers on both sides (nvfp4_int8_*).
  *
  * Conventions for every call:
  *   - returns a status, never throws, never prints unless NVFP4_MOE_LOG=1;
@@ -72,7 +76,8 @@ typedef enum nvfp4_moe_logits_dtype {
 
 typedef enum nvfp4_moe_out_dtype {
   NVFP4_MOE_OUT_BF16 = 0,      /* the layer's output rounded once to BF16 */
-  NVFP4_MOE_OUT_F32 = 1        /* the FP32 combine result, unrounded      */
+  NVFP4_MOE_OUT_F32 = 1,       /* the FP32 combine result, unrounded      */
+  NVFP4_MOE_OUT_F16 = 2        /* FP16: the INT8 linear alone             */
 } nvfp4_moe_out_dtype;
 
 typedef enum nvfp4_moe_score {
@@ -565,6 +570,200 @@ nvfp4_moe_status nvfp4_int4_pack(nvfp4_moe_t h, const uint8_t* w_q, const void* 
  * allocation and no workspace: calls on one handle may overlap and be captured. */
 nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t ldx, void* out, int64_t ldo,
                                     cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Routing on its own: the choice of experts, its weights, the tables that the
+ * grouped products and the combination of their rows read, and the gradient of
+ * the weights.  Per token, over E experts:
+ *   s_e = softmax of the logits, or 1 / (1 + exp(-l_e))    (config.score)
+ *   c_e = s_e + bias_e; the logit itself where there is no bias (both scores
+ *         increase with it)
+ *   groups: E / groups experts that follow one another make a group.  Its value
+ *         is its largest c, or with group_top = 2 the sum of its two largest
+ *         (of s_e + bias_e, the bias being 0 if there is none); experts of the
+ *         top_groups groups of largest value may be chosen.
+ *   choice: the top_k largest c, the largest first
+ *   weight_j = scale * s_j, divided by the sum of the chosen s if renormalize
+ * Among equals the lower index comes first, for groups as for experts.  The
+ * order is that of c, and of the groups' values, evaluated in 64 bits; the
+ * weights are FP32.
+ * A NaN logit has s = 0 and ranks below every number (its group counts it as
+ * -inf), and so does an expert whose bias is NaN; a bias of -inf or of the
+ * type's lowest value keeps an expert behind all others.  Softmax where no
+ * logit is above -inf: s = 1 / E for each -inf; where some are +inf: those share 1.
+ * Renormalised weights whose sum is 0 are scale / top_k each.
+ *
+ * A route handle is an nvfp4_moe_t: nvfp4_moe_destroy, nvfp4_moe_last_error and
+ * nvfp4_moe_get_status (which counts NaN logits) apply to it; the other
+ * operators' calls return NVFP4_MOE_ERR_INVALID_ARG.
+ * ------------------------------------------------------------------------- */
+typedef struct nvfp4_route_config {
+  int num_experts;  /* E: 1..512 */
+  int top_k;        /* 1..16, at most top_groups * E / groups */
+  int groups;       /* 1..32, a divisor of E */
+  int top_groups;   /* 1..groups; groups: no limit */
+  int group_top;    /* 1 or 2; at most E / groups */
+  int score;        /* nvfp4_moe_score */
+  int renormalize;  /* 0 or 1 */
+  float scale;      /* finite */
+  int logits_dtype; /* nvfp4_moe_logits_dtype of the logits and of their gradient */
+  int device;       /* CUDA device ordinal */
+} nvfp4_route_config;
+
+nvfp4_moe_status nvfp4_route_create(const nvfp4_route_config* config, nvfp4_moe_t* out);
+
+/* Enqueued on `stream`; no host synchronisation, no allocation and no
+ * workspace: calls on one handle may overlap and be captured.
+ *   T       0..2^20 tokens; 0 writes zeros to offsets and nothing else
+ *   logits  [T][E] DEVICE, rows ld elements apart (E..2^24)
+ *   bias    [E] float DEVICE, or NULL
+ *   ids     [T][top_k] int32 out   the choice
+ *   weights [T][top_k] float out
+ *   offsets [E+1] int32 out        rows offsets[e] .. offsets[e+1]-1 are e's, as
+ *                                  nvfp4_grouped_forward takes them
+ *   perm    [T*top_k] int32 out    the row at a position: t * top_k + j, ascending
+ *                                  within an expert
+ *   inv     [T*top_k] int32 out    perm's inverse: the position of row t * top_k + j
+ * None of the outputs may overlap another or an input. */
+nvfp4_moe_status nvfp4_route_forward(nvfp4_moe_t h, int T, const void* logits, int64_t ld, const float* bias,
+                                     int32_t* ids, float* weights, int32_t* offsets, int32_t* perm, int32_t* inv,
+                                     cudaStream_t stream);
+
+/* dlogits [T][E] (the logits' type, rows ld_dl apart) from dweights [T][top_k]
+ * for the choice ids, top_k different experts a token; the choice itself is
+ * constant.  An id outside 0..E-1 counts as none.  Softmax whose largest logit is
+ * infinite, NaN logits, and renormalised sigmoids that are all 0 have no gradient
+ * (zeros).  dlogits may be logits. */
+nvfp4_moe_status nvfp4_route_backward(nvfp4_moe_t h, int T, const void* logits, int64_t ld, const int32_t* ids,
+                                      const float* dweights, void* dlogits, int64_t ld_dl, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition:
+ *   sum = x + residual, rounded to the 16-bit type (x itself without a residual)
+ *   y   = weight * sum * rstd, rstd = 1 / sqrt(mean(sum^2) + eps)
+ *   q   = round(127 v / max |v|), v = weight * sum; q_scale = max |y| / 127
+ * so that y is about q * q_scale: the input of nvfp4_int8_forward.  q is the
+ * exactly rounded quotient, ties to even, in -127..127.  A row of zeros has codes
+ * and a scale of 0 (one whose products are all below 2^-149 too); one that is not
+ * finite has codes 0 and a scale of NaN.
+ * Backward, of sum (which is x's and the residual's):
+ *   dx = rstd * (weight * dy) - sum * rstd^3 / H * sum_h(weight * dy * sum) + dsum
+ *   dweight = sum over the rows of dy * sum * rstd
+ * A norm handle is an nvfp4_moe_t like a route handle.
+ * ------------------------------------------------------------------------- */
+typedef struct nvfp4_norm_config {
+  int hidden;    /* H: 8..16384, a multiple of 8 */
+  float eps;     /* >= 0, finite */
+  int act_dtype; /* nvfp4_moe_act_dtype of all rows and of the weight */
+  int device;    /* CUDA device ordinal */
+} nvfp4_norm_config;
+
+/* Synchronous.  The handle holds the workspace of dweight (some H * 2.5 KB). */
+nvfp4_moe_status nvfp4_norm_create(const nvfp4_norm_config* config, nvfp4_moe_t* out);
+
+/* T 0..2^20 rows of H, DEVICE, 16-byte aligned (q: 8), rows ld elements apart: at
+ * least H, a multiple of 8, at most 2^24.
+ *   residual NULL: none, and sum has to be NULL; else sum may be x or residual
+ *   y, q     either may be NULL, not both; y may be x; q_scale [T] float with q
+ *   rstd     [T] float, for the backward pass, or NULL
+ * Otherwise outputs must not overlap inputs or one another.  No host
+ * synchronisation, no allocation and no workspace: calls may overlap and be
+ * captured. */
+nvfp4_moe_status nvfp4_norm_forward(nvfp4_moe_t h, int T, const void* x, int64_t ldx, const void* residual,
+                                    int64_t ld_res, const void* weight, void* sum, int64_t ld_sum, void* y, int64_t ldy,
+                                    int8_t* q, int64_t ldq, float* q_scale, float* rstd, cudaStream_t stream);
+
+/* sum and rstd [T] are the forward's.  dsum: the gradient that reaches sum on its
+ * other way, or NULL.  dx may be dy or dsum.  dweight [H] float (16-byte aligned)
+ * or NULL; it is written, not added to, in an order of summation that depends on
+ * T and H alone.  Calls with a dweight use the handle's workspace: serialise
+ * those on one stream, captured ones too. */
+nvfp4_moe_status nvfp4_norm_backward(nvfp4_moe_t h, int T, const void* dy, int64_t ld_dy, const void* sum,
+                                     int64_t ld_sum, const void* weight, const float* rstd, const void* dsum,
+                                     int64_t ld_dsum, void* dx, int64_t ld_dx, float* dweight, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * SwiGLU between the grouped gate/up and down products, with gate and up kept
+ * for the backward pass in 8 bits (half of what they take):
+ *   h = silu(gate) * up
+ *   codes = round(127 v / peak), scales = peak / 127, peak the largest magnitude of
+ *           128 elements of a row that follow one another (a row's last ones may be
+ *           fewer); exactly rounded, ties to even
+ * Backward, with g and u = codes * scales, s = 1 / (1 + exp(-g)):
+ *   dgate = dh * u * s * (1 + g * (1 - s)),  dup = dh * g * s
+ * A block of 128 that is not finite comes back as NaN.  exp is evaluated to about
+ * 2^-21; all arithmetic is FP32, with one rounding at the end.
+ * A SwiGLU handle is an nvfp4_moe_t like a route handle.
+ * ------------------------------------------------------------------------- */
+typedef struct nvfp4_swiglu_config {
+  int inter;     /* I: 16..16384, a multiple of 16 */
+  int act_dtype; /* nvfp4_moe_act_dtype of all rows */
+  int device;    /* CUDA device ordinal */
+} nvfp4_swiglu_config;
+
+nvfp4_moe_status nvfp4_swiglu_create(const nvfp4_swiglu_config* config, nvfp4_moe_t* out);
+
+/* R 0..2^24 rows of I, DEVICE, 16-byte aligned, rows ld elements apart: at least I,
+ * a multiple of 8, at most 2^24 (gate and up may be halves of one matrix).
+ *   codes  [R][2][I] int8 out (gate, up), 16-byte aligned, and
+ *   scales [R][2][ceil(I / 128)] float out; or both NULL: nothing is kept
+ * h may be gate or up; otherwise outputs must not overlap inputs or one another.
+ * No host synchronisation, no allocation and no workspace: calls may overlap and
+ * be captured. */
+nvfp4_moe_status nvfp4_swiglu_forward(nvfp4_moe_t h, int R, const void* gate, int64_t ld_gate, const void* up,
+                                      int64_t ld_up, void* out, int64_t ld_out, int8_t* codes, float* scales,
+                                      cudaStream_t stream);
+/* The same conditions; dgate or dup may be dh. */
+nvfp4_moe_status nvfp4_swiglu_backward(nvfp4_moe_t h, int R, const int8_t* codes, const float* scales, const void* dh,
+                                       int64_t ld_dh, void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup,
+                                       cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense linear with 8-bit integers on both sides, a scale per token and per output:
+ *   out[t][n] = x_scale[t] * w_scale[n] * sum_k x[t][k] w[n][k] + bias[n]
+ * The sum is exact; it, and the product of the scales, are rounded to FP32, their
+ * product with the bias added is rounded once more, and once to the result's type.
+ * An INT8 handle is an nvfp4_moe_t with the same calls as an INT4 one.
+ * ------------------------------------------------------------------------- */
+typedef struct nvfp4_int8_config {
+  int out_features; /* N: 16..2^20, a multiple of 16 */
+  int in_features;  /* K: 16..16384, a multiple of 16 */
+  int max_tokens;   /* largest T of any forward, 1..2^20 */
+  int out_dtype;    /* nvfp4_moe_out_dtype */
+  int device;       /* CUDA device ordinal */
+} nvfp4_int8_config;
+
+/* Allocate an INT8 handle: the packed matrix (N*K bytes, both rounded up to
+ * multiples of 128) on config->device.  Synchronous.  *out is NULL on failure. */
+nvfp4_moe_status nvfp4_int8_create(const nvfp4_int8_config* config, nvfp4_moe_t* out);
+
+/* Copy the matrix into the handle's device layout.  DEVICE inputs:
+ *   w       [N][K] int8   (16-byte aligned), -128..127
+ *   w_scale [N] float     finite, else NVFP4_MOE_ERR_BAD_SCALE and the handle is
+ *                         left unpacked
+ *   bias    [N] float, or NULL: none
+ * Synchronous.  Inputs may be freed once the call returns.  After a pack that adds
+ * or drops the bias a captured forward has to be captured again. */
+nvfp4_moe_status nvfp4_int8_pack(nvfp4_moe_t h, const int8_t* w, const float* w_scale, const float* bias,
+                                 cudaStream_t stream);
+
+/* Activations for the forward from 16-bit ones: x [T][K] of x_dtype
+ * (nvfp4_moe_act_dtype), 16-byte aligned, rows ldx elements apart (at least K, a
+ * multiple of 8, at most 2^24); q [T][K] int8, 8-byte aligned, rows ldq apart (the
+ * same), q_scale [T] float: round(127 x / max |x|) and max |x| / 127 per row, as in
+ * nvfp4_norm_forward.  T 0..2^20.  May overlap other calls and be captured. */
+nvfp4_moe_status nvfp4_int8_quantize(nvfp4_moe_t h, int T, const void* x, int x_dtype, int64_t ldx, int8_t* q,
+                                     int64_t ldq, float* q_scale, cudaStream_t stream);
+
+/* out [T][N] as above, 0 <= T <= max_tokens; x [T][K] int8 and out DEVICE, 16-byte
+ * aligned, rows ldx / ldo elements apart (at least the row length, ldx a multiple
+ * of 16 and ldo of 8, at most 2^24), not overlapping; x_scale [T] float, whose NaNs
+ * and infinities reach their row.  Enqueued on `stream`; no host synchronisation,
+ * no allocation and no workspace: calls on one handle may overlap and be captured
+ * (above 16 tokens the tensor descriptor over x is encoded on the host, so a
+ * captured graph replays with the pointers it was captured with). */
+nvfp4_moe_status nvfp4_int8_forward(nvfp4_moe_t h, int T, const int8_t* x, int64_t ldx, const float* x_scale, void* out,
+                                    int64_t ldo, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -55,6 +55,27 @@ class Int4Config(ctypes.Structure):
                 ("device", ctypes.c_int)]
 
 
+class Int8Config(ctypes.Structure):
+    _fields_ = [("out_features", ctypes.c_int), ("in_features", ctypes.c_int), ("max_tokens", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("device", ctypes.c_int)]
+
+
+class RouteConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("score", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("scale", ctypes.c_float), ("logits_dtype", ctypes.c_int),
+                ("device", ctypes.c_int)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int), ("eps", ctypes.c_float), ("act_dtype", ctypes.c_int),
+                ("device", ctypes.c_int)]
+
+
+class SwiGLUConfig(ctypes.Structure):
+    _fields_ = [("inter", ctypes.c_int), ("act_dtype", ctypes.c_int), ("device", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -62,7 +83,7 @@ def header_functions():
     """Names of the functions include/nvfp4_moe.h declares."""
     with open(HEADER) as f:
         text = f.read()
-    return sorted(set(re.findall(r"\b(nvfp4_(?:moe|linear|grouped|int4)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(nvfp4_(?:moe|linear|grouped|int4|int8|route|norm|swiglu)_[a-z_0-9]+)\s*\(", text)))
 
 
 def load_library(path: str | None = None):
@@ -114,6 +135,19 @@ def load_library(path: str | None = None):
         "nvfp4_int4_create": (i, [ctypes.POINTER(Int4Config), ctypes.POINTER(vp)]),
         "nvfp4_int4_pack": (i, [vp, vp, vp, vp, vp]),
         "nvfp4_int4_forward": (i, [vp, i, vp, ll, vp, ll, vp]),
+        "nvfp4_int8_create": (i, [ctypes.POINTER(Int8Config), ctypes.POINTER(vp)]),
+        "nvfp4_int8_pack": (i, [vp, vp, vp, vp, vp]),
+        "nvfp4_int8_quantize": (i, [vp, i, vp, i, ll, vp, ll, vp, vp]),
+        "nvfp4_int8_forward": (i, [vp, i, vp, ll, vp, vp, ll, vp]),
+        "nvfp4_route_create": (i, [ctypes.POINTER(RouteConfig), ctypes.POINTER(vp)]),
+        "nvfp4_route_forward": (i, [vp, i, vp, ll, vp, vp, vp, vp, vp, vp, vp]),
+        "nvfp4_route_backward": (i, [vp, i, vp, ll, vp, vp, vp, ll, vp]),
+        "nvfp4_norm_create": (i, [ctypes.POINTER(NormConfig), ctypes.POINTER(vp)]),
+        "nvfp4_norm_forward": (i, [vp, i, vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, ll, vp, vp, vp]),
+        "nvfp4_norm_backward": (i, [vp, i, vp, ll, vp, ll, vp, vp, vp, ll, vp, ll, vp, vp]),
+        "nvfp4_swiglu_create": (i, [ctypes.POINTER(SwiGLUConfig), ctypes.POINTER(vp)]),
+        "nvfp4_swiglu_forward": (i, [vp, i, vp, ll, vp, ll, vp, ll, vp, vp, vp]),
+        "nvfp4_swiglu_backward": (i, [vp, i, vp, vp, vp, ll, vp, ll, vp, ll, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -132,6 +166,17 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _whole(t, shape, dtype, device, what):
+    """Address of a contiguous tensor of this shape and type on cuda:`device`."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{what}: expected a CUDA tensor on the handle's device, cuda:{device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
 
 
 def _rows(t, cols, dtype, device, what):
@@ -475,6 +520,227 @@ class Int4Linear(MoELayer):
     def nvfp4_moe_debug_packed_blob(self, stream=None):
         import torch
         n = (self.N + 31) // 32 * 32 * (self.K // 2 + 3 * (self.K // self.group))
+        out = torch.empty((n,), dtype=torch.uint8, device=f"cuda:{self.device}")
+        st = self.lib.nvfp4_moe_debug_packed_blob(self.h, _ptr(out), n, _stream(stream, self.device))
+        self._check(st, "nvfp4_moe_debug_packed_blob")
+        return out
+
+
+class _Operator(MoELayer):
+    """What the handles of the operators around the products share."""
+
+    def _open(self, name, cfg):
+        import torch
+        self.lib = load_library()
+        self.cfg, self.device = cfg, cfg.device
+        self._int8, self._int32, self._f32 = torch.int8, torch.int32, torch.float32
+        self._current_stream = torch._C._cuda_getCurrentRawStream
+        h = ctypes.c_void_p()
+        st = getattr(self.lib, name)(ctypes.byref(cfg), ctypes.byref(h))
+        if st != 0:
+            raise Nvfp4MoeError(st, f"{name}: " + self.lib.nvfp4_moe_status_string(st).decode())
+        self.h = h
+
+    def _st(self, stream):
+        return stream.cuda_stream if stream is not None else self._current_stream(self.device)
+
+    def _same_rows(self, what, rows, *others):
+        for n in others:
+            if n != rows:
+                raise ValueError(f"{what}: tensors of {rows} and of {n} rows")
+
+
+class Route(_Operator):
+    """Routing on its own (nvfp4_route_create ... nvfp4_moe_destroy)."""
+
+    def __init__(self, num_experts, top_k, score="softmax", renormalize=True, scale=1.0, groups=1, top_groups=None,
+                 group_top=1, logits_bf16=False, device=0):
+        import torch
+        code = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}[score]
+        self.E, self.k = num_experts, top_k
+        self._logits = torch.bfloat16 if logits_bf16 else torch.float32
+        self._open("nvfp4_route_create",
+                   RouteConfig(num_experts, top_k, groups, groups if top_groups is None else top_groups, group_top, code,
+                               1 if renormalize else 0, float(scale), 1 if logits_bf16 else 0, device))
+
+    def _matrix(self, t, what):
+        """(address, row stride, rows) of logits: rows of any stride, elements next to one another."""
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != self.E or t.dtype != self._logits:
+            raise ValueError(f"{what}: expected [tokens][{self.E}] {self._logits}, got {tuple(shape)} {t.dtype}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{what}: expected a CUDA tensor on the handle's device, cuda:{self.device}")
+        ld, one = t.stride()
+        if one != 1 and self.E > 1:
+            raise ValueError(f"{what}: expected contiguous rows")
+        return t.data_ptr(), ld if shape[0] > 1 else self.E, shape[0]
+
+    def nvfp4_route_forward(self, logits, ids, weights, offsets, perm, inv, bias=None, stream=None):
+        """ids, weights [T][k], offsets [E + 1], perm and inv [T * k], all of the caller's; returns (ids, weights)."""
+        what, dev, i32, f32 = "nvfp4_route_forward", self.device, self._int32, self._f32
+        lp, ld, T = self._matrix(logits, what)
+        n = (T * self.k,)
+        st = self.lib.nvfp4_route_forward(
+            self.h, T, lp, ld, None if bias is None else _whole(bias, (self.E,), f32, dev, what),
+            _whole(ids, (T, self.k), i32, dev, what), _whole(weights, (T, self.k), f32, dev, what),
+            _whole(offsets, (self.E + 1,), i32, dev, what), _whole(perm, n, i32, dev, what), _whole(inv, n, i32, dev, what),
+            self._st(stream))
+        if st:
+            self._check(st, what)
+        return ids, weights
+
+    def nvfp4_route_backward(self, logits, ids, dweights, dlogits, stream=None):
+        """The weights' gradient to the logits, for the choice ids."""
+        what, dev = "nvfp4_route_backward", self.device
+        lp, ld, T = self._matrix(logits, what)
+        dp, ld_dl, Td = self._matrix(dlogits, what)
+        self._same_rows(what, T, Td)
+        st = self.lib.nvfp4_route_backward(self.h, T, lp, ld, _whole(ids, (T, self.k), self._int32, dev, what),
+                                           _whole(dweights, (T, self.k), self._f32, dev, what), dp, ld_dl, self._st(stream))
+        if st:
+            self._check(st, what)
+        return dlogits
+
+
+class Norm(_Operator):
+    """RMS norm with the residual's addition (nvfp4_norm_create ... nvfp4_moe_destroy)."""
+
+    def __init__(self, hidden, eps=1e-6, act_f16=False, device=0):
+        import torch
+        self.H = hidden
+        self._act = torch.float16 if act_f16 else torch.bfloat16
+        self._open("nvfp4_norm_create", NormConfig(hidden, float(eps), 1 if act_f16 else 0, device))
+
+    def nvfp4_norm_forward(self, x, weight, residual=None, sum=None, y=None, q=None, q_scale=None, rstd=None, stream=None):
+        """sum (with a residual), y (16 bits), q with q_scale (int8 and a scale a row) and rstd are the caller's."""
+        what, dev, H, act = "nvfp4_norm_forward", self.device, self.H, self._act
+        xp, ldx, T = _rows(x, H, act, dev, what)
+
+        def rows(t, dt):
+            if t is None:
+                return None, 0
+            p, ld, n = _rows(t, H, dt, dev, what)
+            if n != T:
+                raise ValueError(f"{what}: tensors of {T} and of {n} rows")
+            return p, ld
+
+        (rp, ldr), (sp, lds), (yp, ldy), (qp, ldq) = rows(residual, act), rows(sum, act), rows(y, act), rows(q, self._int8)
+        f = lambda t: None if t is None else _whole(t, (T,), self._f32, dev, what)
+        st = self.lib.nvfp4_norm_forward(self.h, T, xp, ldx, rp, ldr, _whole(weight, (H,), act, dev, what), sp, lds, yp, ldy,
+                                         qp, ldq, f(q_scale), f(rstd), self._st(stream))
+        if st:
+            self._check(st, what)
+        return y if y is not None else q
+
+    def nvfp4_norm_backward(self, dy, sum, weight, rstd, dx, dweight=None, dsum=None, stream=None):
+        """dx, the gradient of sum, x and residual alike, and dweight (float32), both the caller's."""
+        what, dev, H, act = "nvfp4_norm_backward", self.device, self.H, self._act
+        dp, ldd, T = _rows(dy, H, act, dev, what)
+        sp, lds, Ts = _rows(sum, H, act, dev, what)
+        xp, ldx, Tx = _rows(dx, H, act, dev, what)
+        rp, ldr, Tr = (None, 0, T) if dsum is None else _rows(dsum, H, act, dev, what)
+        self._same_rows(what, T, Ts, Tx, Tr)
+        st = self.lib.nvfp4_norm_backward(self.h, T, dp, ldd, sp, lds, _whole(weight, (H,), act, dev, what),
+                                          _whole(rstd, (T,), self._f32, dev, what), rp, ldr, xp, ldx,
+                                          None if dweight is None else _whole(dweight, (H,), self._f32, dev, what),
+                                          self._st(stream))
+        if st:
+            self._check(st, what)
+        return dx
+
+
+class SwiGLU(_Operator):
+    """SwiGLU with 8-bit checkpoints (nvfp4_swiglu_create ... nvfp4_moe_destroy)."""
+
+    def __init__(self, inter, act_f16=False, device=0):
+        import torch
+        self.I = inter
+        self.blocks = -(-inter // 128)
+        self._act = torch.float16 if act_f16 else torch.bfloat16
+        self._open("nvfp4_swiglu_create", SwiGLUConfig(inter, 1 if act_f16 else 0, device))
+
+    def nvfp4_swiglu_forward(self, gate, up, out, codes=None, scales=None, stream=None):
+        """out = silu(gate) up; codes [R][2][I] int8 and scales [R][2][blocks] float32 keep gate and up."""
+        what, dev, I, act = "nvfp4_swiglu_forward", self.device, self.I, self._act
+        gp, ldg, R = _rows(gate, I, act, dev, what)
+        up_, ldu, Ru = _rows(up, I, act, dev, what)
+        op, ldo, Ro = _rows(out, I, act, dev, what)
+        self._same_rows(what, R, Ru, Ro)
+        st = self.lib.nvfp4_swiglu_forward(
+            self.h, R, gp, ldg, up_, ldu, op, ldo,
+            None if codes is None else _whole(codes, (R, 2, I), self._int8, dev, what),
+            None if scales is None else _whole(scales, (R, 2, self.blocks), self._f32, dev, what), self._st(stream))
+        if st:
+            self._check(st, what)
+        return out
+
+    def nvfp4_swiglu_backward(self, codes, scales, dh, dgate, dup, stream=None):
+        """dgate and dup from the forward's codes and scales."""
+        what, dev, I, act = "nvfp4_swiglu_backward", self.device, self.I, self._act
+        dp, ldd, R = _rows(dh, I, act, dev, what)
+        gp, ldg, Rg = _rows(dgate, I, act, dev, what)
+        up_, ldu, Ru = _rows(dup, I, act, dev, what)
+        self._same_rows(what, R, Rg, Ru)
+        st = self.lib.nvfp4_swiglu_backward(self.h, R, _whole(codes, (R, 2, I), self._int8, dev, what),
+                                            _whole(scales, (R, 2, self.blocks), self._f32, dev, what), dp, ldd, gp, ldg,
+                                            up_, ldu, self._st(stream))
+        if st:
+            self._check(st, what)
+        return dgate, dup
+
+
+class Int8Linear(_Operator):
+    """A dense linear with 8-bit integers on both sides (nvfp4_int8_create ... nvfp4_moe_destroy)."""
+
+    def __init__(self, out_features, in_features, max_tokens, out="bf16", device=0):
+        import torch
+        code = {"bf16": 0, "f32": 1, "f16": 2}[out]
+        self._out = (torch.bfloat16, torch.float32, torch.float16)[code]
+        self._x_types = {torch.bfloat16: 0, torch.float16: 1}
+        self.N, self.K = out_features, in_features
+        self._open("nvfp4_int8_create", Int8Config(out_features, in_features, max_tokens, code, device))
+
+    def nvfp4_int8_pack(self, w, w_scale, bias=None, stream=None):
+        """w [N][K] int8, w_scale [N] float32, bias [N] float32 or None."""
+        what, dev = "nvfp4_int8_pack", self.device
+        st = self.lib.nvfp4_int8_pack(self.h, _whole(w, (self.N, self.K), self._int8, dev, what),
+                                      _whole(w_scale, (self.N,), self._f32, dev, what),
+                                      None if bias is None else _whole(bias, (self.N,), self._f32, dev, what),
+                                      self._st(stream))
+        self._check(st, what)
+
+    def nvfp4_int8_quantize(self, x, q, q_scale, stream=None):
+        """q [T][K] int8 and q_scale [T] float32 of x [T][K], BF16 or FP16."""
+        what, dev = "nvfp4_int8_quantize", self.device
+        code = self._x_types.get(x.dtype)
+        if code is None:
+            raise ValueError(f"{what}: expected a bfloat16 or float16 x, got {x.dtype}")
+        xp, ldx, T = _rows(x, self.K, x.dtype, dev, what)
+        qp, ldq, Tq = _rows(q, self.K, self._int8, dev, what)
+        self._same_rows(what, T, Tq)
+        st = self.lib.nvfp4_int8_quantize(self.h, T, xp, code, ldx, qp, ldq, _whole(q_scale, (T,), self._f32, dev, what),
+                                          self._st(stream))
+        if st:
+            self._check(st, what)
+        return q, q_scale
+
+    def nvfp4_int8_forward(self, x, x_scale, out, stream=None):
+        """out [T][N] = x_scale w_scale (x [T][K] times the matrix) + bias, T <= max_tokens."""
+        what, dev = "nvfp4_int8_forward", self.device
+        xp, ldx, T = _rows(x, self.K, self._int8, dev, what)
+        if T <= 1:
+            ldx = -(-self.K // 16) * 16
+        op, ldo, To = _rows(out, self.N, self._out, dev, what)
+        self._same_rows(what, T, To)
+        st = self.lib.nvfp4_int8_forward(self.h, T, xp, ldx, _whole(x_scale, (T,), self._f32, dev, what), op, ldo,
+                                         self._st(stream))
+        if st:
+            self._check(st, what)
+        return out
+
+    def nvfp4_moe_debug_packed_blob(self, stream=None):
+        import torch
+        n = -(-self.N // 128) * 128 * -(-self.K // 128) * 128
         out = torch.empty((n,), dtype=torch.uint8, device=f"cuda:{self.device}")
         st = self.lib.nvfp4_moe_debug_packed_blob(self.h, _ptr(out), n, _stream(stream, self.device))
         self._check(st, "nvfp4_moe_debug_packed_blob")

@@ -9,98 +9,11 @@
 #include <string>
 #include <vector>
 
-#include "../../include/nvfp4_moe.h"
-#include "kernels.h"
+#include "handle.h"
 
 using namespace nvfp4moe;
 
-struct nvfp4_moe {
-  nvfp4_moe_config cfg;
-  bool linear = false;  // a dense linear (nvfp4_linear_create): cfg holds E = 1, hidden = N padded to 128, inter = K
-  int lin_n = 0;        // a dense linear's N (output features)
-  // a product handle (nvfp4_grouped_create, nvfp4_int4_create): `linear` is set too, so that no MoE call takes it,
-  // and ws holds the status word alone
-  enum Kind { kLayerOrLinear, kGrouped, kInt4 } kind = kLayerOrLinear;
-  nvfp4_int4_config i4{};
-  size_t product_bytes = 0;  // a product handle's packed matrix (matrices)
-  size_t l2_bytes = 0;       // a product handle's device's L2
-  bool i4_zeros = false;     // INT4: the last pack had zero points
-  RouteParams rp{};     // scoring rule (nvfp4_moe_set_scoring); rp.bias points at `bias` when set
-  float* bias = nullptr;  // [num_experts] device copy of the choice bias
-  void* w_router = nullptr;  // [num_experts][hidden] BF16 router weight (nvfp4_moe_set_router)
-  CUtensorMap w_router_map{};  // over w_router, box {64, 128}, 128B swizzle
-  bool have_router = false;
-  // W4A4 comparison variant (nvfp4_moe_set_act_quant)
-  bool w4a4 = false;
-  float* in_scale = nullptr;     // [E][2] device input scales (w13, w2); shared expert's unused
-  float* gs_eff = nullptr;       // [E][3] device tensor scales with the input scales folded in
-  float* hbound = nullptr;       // [E] max_f ||Wg_f|| ||Wu_f|| (written at pack): sizes h's FP16 prescale
-  std::vector<std::pair<uint8_t*, size_t>> data_regions;  // workspace buffers every forward rewrites
-  int checks = 0;  // NVFP4_MOE_CHECKS=1 at create: kernels check table-derived indices
-  std::vector<float> gs_host;    // [E][3] the packed tensor scales
-  std::vector<float> is_host;    // [E][2]
-  int path = NVFP4_MOE_PATH_AUTO;
-  int num_sms = 0;
-  bool packed = false;
-  bool log = false;
-  bool logged_path[3] = {false, false, false};
-  uint8_t* blob = nullptr;
-  float* gscale = nullptr;
-  void* ws_mem = nullptr;
-  size_t ws_bytes = 0;
-  Workspace ws{};
-  PrefillMaps maps{};
-  int last_T = 0, last_k = 0;
-  int last_hsrc = 0;  // where the last forward's hidden activations are (launch_hidden_to_f32's src)
-  bool last_routed = false;
-  int fault = 0;
-  bool profiling = false;
-  std::vector<cudaEvent_t> ev_pool;  // 5 events per profiled forward
-  size_t ev_used = 0;
-  char last_error[256] = {0};
-};
-
 namespace {
-
-struct DeviceGuard {
-  int prev = -1;
-  bool changed = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) changed = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (changed) cudaSetDevice(prev);
-  }
-};
-
-nvfp4_moe_status fail(nvfp4_moe* h, nvfp4_moe_status s, const std::string& msg) {
-  if (h) snprintf(h->last_error, sizeof(h->last_error), "%s", msg.c_str());
-  if (h && h->log) fprintf(stderr, "[nvfp4_moe] %s\n", msg.c_str());
-  return s;
-}
-
-nvfp4_moe_status cuda_fail(nvfp4_moe* h, cudaError_t e, const char* where) {
-  cudaGetLastError();  // reported here: left behind, it would be the next kernel launch's
-  return fail(h, NVFP4_MOE_ERR_CUDA, std::string(where) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
 
 // 2D BF16 [rows][cols], rows ld elements apart (0: cols), box = 64 columns x box_rows rows, 128B swizzle.
 bool encode_rows_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 16,
@@ -200,20 +113,6 @@ nvfp4_moe_status upload_gs_eff(nvfp4_moe* h, cudaStream_t st) {
   cudaError_t err = cudaMemcpyAsync(h->gs_eff, g.data(), sizeof(float) * g.size(), cudaMemcpyHostToDevice, st);
   if (err == cudaSuccess) err = cudaStreamSynchronize(st);  // g lives on this frame
   if (err != cudaSuccess) return cuda_fail(h, err, "W4A4 tensor scales upload");
-  return NVFP4_MOE_OK;
-}
-
-// Forward events: 5 per profiled forward (ev[i] stays NULL when profiling is off).
-nvfp4_moe_status take_events(nvfp4_moe* h, cudaEvent_t (&ev)[5]) {
-  if (!h->profiling) return NVFP4_MOE_OK;
-  for (int i = 0; i < 5; ++i) {
-    if (h->ev_used == h->ev_pool.size()) {
-      cudaEvent_t e0;
-      if (cudaEventCreate(&e0) != cudaSuccess) return cuda_fail(h, cudaGetLastError(), "event create");
-      h->ev_pool.push_back(e0);
-    }
-    ev[i] = h->ev_pool[h->ev_used++];
-  }
   return NVFP4_MOE_OK;
 }
 
@@ -916,9 +815,8 @@ nvfp4_moe_status nvfp4_linear_forward(nvfp4_moe_t h, int T, const void* x, void*
 // ---------------------------------------------------------------------------
 // Products outside the layer: grouped NVFP4 experts, the INT4 linear.
 // ---------------------------------------------------------------------------
-namespace {
 // A handle with a blob of `bytes`, n_scales tensor scales and a status word, on `device`.
-nvfp4_moe_status create_product(nvfp4_moe::Kind kind, int device, size_t bytes, int n_scales, nvfp4_moe** out) {
+nvfp4_moe_status nvfp4moe::create_product(nvfp4_moe::Kind kind, int device, size_t bytes, int n_scales, nvfp4_moe** out) {
   nvfp4_moe* h = new (std::nothrow) nvfp4_moe();
   if (!h) return NVFP4_MOE_ERR_WORKSPACE;
   h->kind = kind;
@@ -952,17 +850,7 @@ nvfp4_moe_status create_product(nvfp4_moe::Kind kind, int device, size_t bytes, 
   return NVFP4_MOE_OK;
 }
 
-bool device_ok(int device) {
-  int ndev = 0;
-  return cudaGetDeviceCount(&ndev) == cudaSuccess && device >= 0 && device < ndev;
-}
-
-// Event record around a product: its time counts as the down GEMM stage.
-void record(cudaEvent_t (&ev)[5], int i0, int i1, cudaStream_t st) {
-  for (int i = i0; i <= i1; ++i)
-    if (ev[i]) cudaEventRecord(ev[i], st);
-}
-
+namespace {
 nvfp4_moe_status grouped_impl(nvfp4_moe* h, bool backward, int R, const int32_t* offsets, const void* in,
                               int64_t ldi, void* out, int64_t ldo, cudaStream_t st) {
   const char* what = backward ? "grouped_backward" : "grouped_forward";

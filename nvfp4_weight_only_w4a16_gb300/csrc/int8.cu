@@ -1,0 +1,745 @@
+// Linear with 8-bit integers on both sides (nvfp4_int8_*):
+//   y[t][n] = sx[t] sw[n] sum_k xq[t][k] wq[n][k] + bias[n]
+//
+// The tensor cores of sm_103a that are fast take no integers, so both operands go through as FP16, which holds an 8-bit
+// integer exactly; so is a product, and an FP32 sum of up to 1024 of them (below or at 2^24, which the alignment of what a
+// tensor core adds does not cut).  Every 1024 terms the sums go to 32-bit integers, so that the whole sum is exact, and
+// splitting it over warps and CTAs in any order changes nothing.
+//
+// The matrix is packed as bytes q + 128, [N / 128][K / 16][128 rows][16 elements], filled up with zeros to whole 128 x 128
+// squares: a square is one 16 KB copy, a thread that owns a row reads 16 elements of it at a time without bank conflicts
+// (GEMM), and a warp's reads for a fragment of 16 rows are runs of 256 bytes (few tokens).
+#include <algorithm>
+#include <mutex>
+
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace nvfp4moe {
+
+namespace i8 {
+constexpr int kSquare = 16384;  // bytes of a 128 x 128 square
+constexpr int kSmemMax = 232448;
+}  // namespace i8
+
+// Four bytes q + 128 -> two FP16 pairs q: 1024 + byte by its bits, less 1152.
+__device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+__device__ __forceinline__ void bytes_to_f16(const uint4& w, uint32_t (&o)[8]) {
+  bytes_to_f16(w.x, o[0], o[1]);
+  bytes_to_f16(w.y, o[2], o[3]);
+  bytes_to_f16(w.z, o[4], o[5]);
+  bytes_to_f16(w.w, o[6], o[7]);
+}
+__device__ __forceinline__ uint4 biased(uint4 w) {
+  w.x ^= 0x80808080u, w.y ^= 0x80808080u, w.z ^= 0x80808080u, w.w ^= 0x80808080u;
+  return w;
+}
+
+// --------------------------------------------------------------------------------------------------------------------
+// Packing
+// --------------------------------------------------------------------------------------------------------------------
+size_t int8_packed_bytes(int N, int K) {
+  return (size_t)((N + 127) / 128) * ((K + 127) / 128) * i8::kSquare;
+}
+// One thread a 16-byte piece.
+__global__ void pack_int8_kernel(const int8_t* w, int N, int K, uint8_t* packed) {
+  const long long pieces = (K + 127) / 128 * 8, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long blocks = (N + 127) / 128;
+  if (i >= blocks * pieces * 128) return;
+  const long long row = i / (128 * pieces) * 128 + i % 128, p = i / 128 % pieces;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (row < N && 16 * p < K) v = *reinterpret_cast<const uint4*>(w + row * K + 16 * p);
+  reinterpret_cast<uint4*>(packed)[i] = biased(v);
+}
+cudaError_t launch_pack_int8(const int8_t* w_q, int N, int K, uint8_t* packed, cudaStream_t st) {
+  const long long n = (long long)int8_packed_bytes(N, K) / 16;
+  pack_int8_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(w_q, N, K, packed);
+  return cudaGetLastError();
+}
+
+struct Int8Args {
+  const uint8_t* packed;
+  const float *w_scale, *bias;
+  int N, K, T;
+  const int8_t* x;
+  const float* x_scale;
+  long long ldx;  // bytes
+  void* out;
+  long long ldo;  // elements
+  int out_type;
+  bool once;
+  DeviceStatus* st;
+  int fault;
+  // few tokens
+  int wk;          // warps along K: 1, 2, 4, 8 or 16
+  int slice;       // elements of K a warp takes at a time, a multiple of 64
+  int passes;      // of all warps along K
+  int batch;       // 16-row groups whose sums shared memory holds
+  // GEMM
+  int NB, NU;      // 128-feature blocks; units across the features
+  int tiles, per;  // token tiles, and tokens of each
+  int halves;      // 64-long steps of the reduction
+  int split;       // CTAs that share a unit
+};
+
+__device__ __forceinline__ void store_out(const Int8Args& a, long long at, float y) {
+  if (a.out_type == 1) static_cast<float*>(a.out)[at] = y;
+  else if (a.out_type == 2) static_cast<__half*>(a.out)[at] = __float2half_rn(y);
+  else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+}
+
+// --------------------------------------------------------------------------------------------------------------------
+// Up to 16 tokens.  Bound by the matrix's bytes.
+//
+// A warp keeps one slice of K (up to 256 elements) of all tokens in registers as B fragments and streams the matrix past
+// it, 16 rows at a time, through a ring of its own in shared memory: each lane copies what it will read itself, so there
+// is no barrier.  m16n8k16 sums a slice exactly in FP32; its integers are added to the CTA's sums in shared memory by
+// atomics, whose order does not matter.  A CTA takes a run of 16-row groups, its warps share K and, where K is short, the
+// groups; one barrier a batch of groups, and longer K in passes over the batch.
+// --------------------------------------------------------------------------------------------------------------------
+namespace i8v {
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kSlice = 256, kBlocks = kSlice / 64;  // 64-element blocks of a slice
+constexpr int kStage = 16 * kSlice;                 // bytes: 16 rows of a slice
+constexpr int kDepth = 3;
+constexpr int kRing = kWarps * kDepth * kStage;
+constexpr int kSumBytes = 32768;
+}  // namespace i8v
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// kTiles: groups of 8 tokens.
+template <int kTiles>
+__global__ void __launch_bounds__(i8v::kThreads, 1) int8_gemv_kernel(Int8Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  int* sums = reinterpret_cast<int*>(smem + i8v::kRing);  // [token][pitch]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * i8v::kDepth * i8v::kStage + lane * 16;
+  const int pitch = 16 * a.batch + 4;  // a lane's sums, rows r and r + 8 of tokens 2 c and 2 c + 1, in different banks
+  const int groups = (a.N + 15) / 16, per = groups / gridDim.x, extra = groups - per * gridDim.x;
+  const int g0 = blockIdx.x * per + min((int)blockIdx.x, extra), g1 = g0 + per + ((int)blockIdx.x < extra ? 1 : 0);
+  const int streams = i8v::kWarps / a.wk, stream = warp / a.wk;
+  const long long block_bytes = (long long)((a.K + 127) / 128) * i8::kSquare;
+  uint64_t first, normal;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+  const uint64_t policy = a.once ? first : normal;
+
+  // The warp's stages in order: batches, passes, groups.  `at` walks them twice: once to copy, once to use.
+  struct At {
+    int b0, pass, g;  // the batch's first group; the group
+  };
+  const auto batch_end = [&](const At& s) { return min(s.b0 + a.batch, g1); };
+  const auto valid = [&](const At& s) { return s.b0 < g1; };
+  const auto settle = [&](At& s) {  // the stream may have no group in a short batch
+    while (valid(s) && s.g >= batch_end(s)) {
+      if (++s.pass == a.passes) s.pass = 0, s.b0 += a.batch;
+      s.g = s.b0 + stream;
+    }
+  };
+  const auto k_of = [&](int pass) { return (pass * a.wk + warp % a.wk) * a.slice; };  // the slice's first element
+  const auto copy = [&](const At& s, int slot) {
+    const int k0 = k_of(s.pass);
+    // lane (r, c): rows r and r + 8, elements 16 c .. 16 c + 15 of each 64
+    const uint8_t* p = a.packed + (s.g >> 3) * block_bytes + (long long)(k0 / 16 + c) * 2048 + ((s.g & 7) * 16 + r) * 16;
+    const uint32_t d = ring + slot * i8v::kStage;
+#pragma unroll
+    for (int b = 0; b < i8v::kBlocks; ++b)
+      if (64 * b < a.slice && k0 + 64 * b < a.K) {
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(d + b * 1024), "l"(p + b * 8192), "l"(policy) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(d + b * 1024 + 512), "l"(p + b * 8192 + 128), "l"(policy) : "memory");
+      }
+  };
+  At ahead{g0, 0, g0 + stream}, now = ahead;
+  settle(ahead);
+  settle(now);
+  int slot_in = 0, slot = 0;
+  const auto push = [&] {
+    if (valid(ahead)) {
+      copy(ahead, slot_in);
+      ahead.g += streams;
+      settle(ahead);
+    }
+    slot_in = slot_in == i8v::kDepth - 1 ? 0 : slot_in + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // the matrix is no kernel's output: its copies start before the wait for the kernel before
+#pragma unroll
+  for (int i = 0; i < i8v::kDepth - 1; ++i) push();
+  for (int i = threadIdx.x; i < 8 * kTiles * pitch; i += i8v::kThreads) sums[i] = 0;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __syncthreads();
+
+  uint32_t x[kTiles][i8v::kBlocks][8];  // B fragments: lane (n = r, c) holds elements 16 c .. 16 c + 15 of each 64 of token n
+  int loaded = -1;
+  for (int b0 = g0; b0 < g1; b0 += a.batch) {
+    while (valid(now) && now.b0 == b0) {
+      if (now.pass != loaded) {
+        loaded = now.pass;
+        const int k0 = k_of(loaded);
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int b = 0; b < i8v::kBlocks; ++b) {
+            const int t = 8 * n + r, k = k0 + 64 * b + 16 * c;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (t < a.T && 64 * b < a.slice && k < a.K) v = *reinterpret_cast<const uint4*>(a.x + t * a.ldx + k);
+            bytes_to_f16(biased(v), x[n][b]);
+          }
+      }
+      push();
+      asm volatile("cp.async.wait_group %0;" ::"n"(i8v::kDepth - 1) : "memory");
+      float acc[kTiles][4];
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+      const int k0 = k_of(now.pass);
+#pragma unroll
+      for (int b = 0; b < i8v::kBlocks; ++b)
+        if (64 * b < a.slice && k0 + 64 * b < a.K) {
+          uint32_t lo[8], hi[8];
+          bytes_to_f16(lds128(ring + slot * i8v::kStage + b * 1024), lo);
+          bytes_to_f16(lds128(ring + slot * i8v::kStage + b * 1024 + 512), hi);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n)
+              mma_f16(acc[n], lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1], x[n][b][2 * j], x[n][b][2 * j + 1]);
+        }
+      slot = slot == i8v::kDepth - 1 ? 0 : slot + 1;
+      int* s = sums + 2 * c * pitch + (now.g - b0) * 16 + r;
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (8 * n + 2 * c + (i & 1) < a.T) atomicAdd(s + (8 * n + (i & 1)) * pitch + 8 * (i >> 1), __float2int_rn(acc[n][i]));
+      now.g += streams;
+      settle(now);
+    }
+    __syncthreads();
+    const int rows = 16 * (min(b0 + a.batch, g1) - b0), f0 = 16 * b0;
+    for (int i = threadIdx.x; i < rows * a.T; i += i8v::kThreads) {
+      const int t = i / rows, n = f0 + i - t * rows;
+      int* at = sums + t * pitch + i - t * rows;
+      if (n < a.N) {
+        const float s = a.x_scale[t] * __ldg(a.w_scale + n);
+        store_out(a, t * a.ldo + n, fmaf((float)*at, s, a.bias ? __ldg(a.bias + n) : 0.f));
+      }
+      *at = 0;
+    }
+    __syncthreads();
+  }
+}
+
+// --------------------------------------------------------------------------------------------------------------------
+// More tokens: a persistent tcgen05 GEMM, the matrix as the M operand and the tokens as the N operand.
+//
+// Both operands are converted on the way, by four warps: a square's rows into tensor memory (a thread its own lane), the
+// tokens into 128B-swizzled shared memory.  kCtas = 2: a pair of CTAs on 256 features, each with half of the tile's tokens.
+//
+// What this comes down to is shared memory's bandwidth, 128 bytes a cycle.  For 64 elements of the reduction a pair's CTA
+// with 192 tokens moves 8 KB of the matrix in and out, 6 KB of tokens in and out, and 12 KB of converted ones in and out:
+// 416 cycles, next to 384 of MMAs.  192 tokens, and not 256, because tensor memory then holds two sets of sums (384
+// columns) beside four stages of the matrix (128): the sums go to registers every 1024 elements, to stay exact, and that
+// passes under the next 1024's MMAs.
+//
+// kSplit: where there are few units, a cluster of CTAs takes one, a share of the reduction each, and adds the integers
+// through distributed shared memory.
+// --------------------------------------------------------------------------------------------------------------------
+namespace i8g {
+constexpr int kThreads = 448;                      // 4 converters, 8 epilogue, producer, MMA issuer
+constexpr int kConvWarps = 4, kEpiWarps = 8, kProducer = 12, kIssuer = 13;
+constexpr int kCtlBytes = 2048, kEpiBytes = 2048;  // per epilogue warp
+constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
+constexpr int kRoom = i8::kSmemMax - 1024 - kRingOff;
+constexpr int kSegment = 16;                       // 64-long steps whose sums FP32 holds exactly
+constexpr int kMaxStages = 8, kMaxRaw = 8, kMaxSplit = 8;
+
+template <int kCtas, int kTile>
+struct Plan {
+  static constexpr int kShare = kTile / kCtas;               // tokens of a CTA
+  static constexpr int kBBytes = kShare * 128;               // a stage of them, 64 elements in FP16
+  static constexpr int kXBytes = kShare * 128;               // a raw slot, 128 elements in bytes
+  static constexpr int kStages = kTile == 64 ? 6 : kTile == 128 ? 5 : 4;
+  static constexpr int kRaw = kTile == 64 ? 6 : kTile == 128 ? 4 : 5;  // slots of both raw rings
+  static constexpr uint32_t kOperand = 2 * kTile;            // its first column in tensor memory
+  static constexpr int kRings = kStages * kBBytes + kRaw * (kXBytes + i8::kSquare);
+  static_assert(kRings <= kRoom && kRaw <= kMaxRaw && kStages <= kMaxStages && 2 * kTile + 32 * kStages <= 512, "rings");
+  static_assert(kBBytes % 1024 == 0, "128B-swizzled tiles");
+};
+}  // namespace i8g
+
+struct Int8Ctl {
+  uint64_t raw_full[i8g::kMaxRaw], raw_empty[i8g::kMaxRaw];      // a square and its tokens
+  uint64_t full[i8g::kMaxStages], empty[i8g::kMaxStages];        // converted stages
+  uint64_t acc_full[2], acc_empty[2], mma_done;
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(sizeof(Int8Ctl) <= i8g::kCtlBytes, "control block");
+
+template <int kCtas, int kTile, bool kSplit>
+__global__ void __launch_bounds__(i8g::kThreads, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap x_map, Int8Args a) {
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  Int8Ctl& ctl = *reinterpret_cast<Int8Ctl*>(smem);
+  using Plan = i8g::Plan<kCtas, kTile>;
+  uint8_t* ring_b = smem + i8g::kRingOff;
+  uint8_t* raw_x = ring_b + Plan::kStages * Plan::kBBytes;
+  uint8_t* raw_w = raw_x + Plan::kRaw * Plan::kXBytes;
+  const uint32_t b_addr = smem_u32(ring_b), x_addr = smem_u32(raw_x), w_addr = smem_u32(raw_w);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(!kSplit || kCtas == 1, "a cluster is a pair or shares a unit");
+  const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
+  const int part = kSplit ? (int)cluster_rank() : 0;
+  const int first = kSplit ? blockIdx.x / a.split : blockIdx.x / kCtas;
+  const int stride = kSplit ? gridDim.x / a.split : gridDim.x / kCtas;  // split: no CTA has a second unit
+  const int squares = (a.halves + 1) / 2;
+  const int sq0 = kSplit ? part * squares / a.split : 0, sq1 = kSplit ? (part + 1) * squares / a.split : squares;
+  const int steps = 2 * (sq1 - sq0);  // 64-long; the packed matrix is whole squares
+  constexpr int kRound = 16 * kCtas;  // the MMA's columns come in these
+  const int total = a.tiles * a.NU;
+  volatile int* abort_flag = &ctl.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Plan::kRaw; ++s) {
+      mbar_init(ctl.raw_full + s, 1);
+      mbar_init(ctl.raw_empty + s, i8g::kConvWarps);
+    }
+    for (int s = 0; s < Plan::kStages; ++s) {
+      mbar_init(ctl.full + s, kCtas * i8g::kConvWarps);  // waited for by the pair's first CTA
+      mbar_init(ctl.empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(ctl.acc_full + b, 1);
+      mbar_init(ctl.acc_empty + b, kCtas * i8g::kEpiWarps);
+    }
+    mbar_init(&ctl.mma_done, 1);
+    ctl.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == i8g::kIssuer) {
+    if (kCtas == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (kCtas == 2) cluster_sync_all();  // the other CTA's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  // Unit u: feature block(s) u % NU of token tile u / NU.
+  const auto tokens_of = [&](int u, int& row0) {
+    const int t = u / a.NU;
+    row0 = t * a.per;
+    return min(a.per, a.T - row0);
+  };
+  const auto columns = [&](int tokens) { return (tokens + kRound - 1) & ~(kRound - 1); };
+
+  int acc[kTile / 2];  // epilogue: a feature's sums over half of the columns (kSplit: after the roles have met again)
+
+  if (warp == i8g::kProducer) {
+    // ---------------- the matrix's squares and the tokens that meet them ----------------
+    uint32_t it = 0;
+    RingPos p;
+    bool ok = true, waited = false;
+    for (int u = first; u < total && ok && a.fault != 1; u += stride) {
+      int row0;
+      const int share = columns(tokens_of(u, row0)) / kCtas;
+      row0 += rank * share;
+      // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
+      const int nb = min(u % a.NU * kCtas + rank, a.NB - 1);
+      const uint8_t* src = a.packed + ((long long)nb * squares + sq0) * i8::kSquare;
+      for (int s = sq0; s < sq1; ++s, ++it, p.step(Plan::kRaw), src += i8::kSquare) {
+        if (!warp_wait(ctl.raw_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 931)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(ctl.raw_full + p.slot, i8::kSquare + Plan::kXBytes);
+          bulk_g2s(raw_w + p.slot * i8::kSquare, src, i8::kSquare, ctl.raw_full + p.slot);
+        }
+        __syncwarp();
+        // the tokens may be the kernel before's, the matrix is not
+        if (!waited) grid_dependency_wait();
+        waited = true;
+        if (elect_one()) tma_2d(raw_x + p.slot * Plan::kXBytes, &x_map, s * 128, row0, ctl.raw_full + p.slot);
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) drain_copies(ctl.raw_full, it, Plan::kRaw);
+  } else if (warp == i8g::kIssuer) {
+    // ---------------- MMA issuer: the whole warp walks the loop, one lane issues ----------------
+    if (rank == 0) {
+      uint32_t j = 0;  // segments so far
+      RingPos p;
+      bool ok = true;
+      for (int u = first; u < total && ok; u += stride) {
+        int row0;
+        const uint32_t idesc = idesc_f16(128 * kCtas, columns(tokens_of(u, row0)));
+        for (int s = 0; s < steps && ok; s += i8g::kSegment, ++j) {
+          const uint32_t buf = j & 1u;
+          if (!warp_wait(ctl.acc_empty + buf, ((j >> 1) & 1u) ^ 1u, abort_flag, a.st, 932)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + buf * kTile;
+          const int end = min(s + i8g::kSegment, steps);
+          uint32_t add = 0;
+          for (int i = s; i < end; ++i, p.step(Plan::kStages)) {
+            if (!warp_wait(ctl.full + p.slot, p.phase, abort_flag, a.st, 933)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t bd = sw128_desc(b_addr + (uint32_t)(p.slot * Plan::kBBytes));
+            const uint32_t at = tmem + Plan::kOperand + (uint32_t)p.slot * 32u;  // 8 columns per 16 elements
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                if (kCtas == 2) umma_ts_pair(d, at + 8u * kk, bd + 2u * kk, idesc, kk ? 1u : add);
+                else umma_ts(d, at + 8u * kk, bd + 2u * kk, idesc, kk ? 1u : add);
+              }
+              if (kCtas == 2) umma_commit_pair(ctl.empty + p.slot);
+              else umma_commit(ctl.empty + p.slot);
+            }
+            add = 1;
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (elect_one()) {
+            if (kCtas == 2) umma_commit_pair(ctl.acc_full + buf);
+            else umma_commit(ctl.acc_full + buf);
+          }
+          __syncwarp();
+        }
+      }
+      // no MMA may outlive the shared and tensor memory it uses, also where a role has given up
+      if (elect_one()) {
+        if (kCtas == 2) umma_commit_pair_own(&ctl.mma_done);
+        else umma_commit(&ctl.mma_done);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&ctl.mma_done, 0) && globaltimer_ns() - t0 <= kWaitTimeoutNs) {}
+      }
+      __syncwarp();
+    }
+  } else if (warp < i8g::kConvWarps) {
+    // ---------------- converters: a raw slot makes two stages ----------------
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const uint32_t full0 = kCtas == 2 ? map_rank(ctl.full, 0) : 0u;  // the pair's first CTA's
+    RingPos raw, p;
+    bool ok = true;
+    for (int u = first; u < total && ok; u += stride) {
+      for (int s = 0; s < steps && ok; s += 2, raw.step(Plan::kRaw)) {
+        if (!warp_wait(ctl.raw_full + raw.slot, raw.phase, abort_flag, a.st, 934)) {
+          ok = false;
+          break;
+        }
+        const uint32_t w_slot = w_addr + raw.slot * i8::kSquare + (uint32_t)(32 * warp + lane) * 16u;
+        const uint32_t x_slot = x_addr + raw.slot * Plan::kXBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h, p.step(Plan::kStages)) {
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = lds128(w_slot + (4 * h + i) * 2048);
+          if (!warp_wait(ctl.empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 935)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // tokens: 8 rows of 16 elements a quarter of a warp; all lie in banks of their own, going in and coming out
+          const uint32_t st = b_addr + (uint32_t)(p.slot * Plan::kBBytes);
+          const int q = lane >> 3, m = lane & 7;
+#pragma unroll
+          for (int o = warp; o < Plan::kShare / 8; o += i8g::kConvWarps) {
+            const uint32_t row = (uint32_t)(8 * o + m) * 128u;
+            uint32_t v[8];
+            bytes_to_f16(biased(lds128(x_slot + row + (uint32_t)((4 * h + q) ^ m) * 16u)), v);
+            sts128(st + row + (uint32_t)((2 * q) ^ m) * 16u, v[0], v[1], v[2], v[3]);
+            sts128(st + row + (uint32_t)((2 * q + 1) ^ m) * 16u, v[4], v[5], v[6], v[7]);
+          }
+          uint32_t v[4][8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bytes_to_f16(w[i], v[i]);
+          tmem_st32(tmem + lanes + Plan::kOperand + (uint32_t)p.slot * 32u, v);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + p.slot * 8);
+            else mbar_arrive(ctl.full + p.slot);
+          }
+        }
+        if (!ok) break;
+        // what was read of the slot has been stored since
+        if (lane == 0) mbar_arrive(ctl.raw_empty + raw.slot);
+      }
+    }
+  } else {
+    // ---------------- epilogue: warp w reads TMEM lanes 32 (w % 4) .., one feature a lane, and half of the columns; two
+    // warps a quarter.  32 tokens x 32 features go through shared memory into 16-byte stores ----------------
+    const int quarter = warp & 3, half = (warp - i8g::kConvWarps) >> 2;
+    const uint32_t t_acc = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(half * (kTile / 2));
+    uint8_t* buf_s = smem + i8g::kCtlBytes + (warp - i8g::kConvWarps) * i8g::kEpiBytes;
+    if (!kSplit) grid_dependency_wait();  // x's scales, and what the output's memory holds, may be the kernel before's
+    uint32_t j = 0;
+    bool ok = true;
+    for (int u = first; u < total && ok; u += stride) {
+      int row0;
+      const int tokens = tokens_of(u, row0);
+#pragma unroll
+      for (int i = 0; i < kTile / 2; ++i) acc[i] = 0;
+      for (int s = 0; s < steps; s += i8g::kSegment, ++j) {
+        const uint32_t buf = j & 1u;
+        if (!warp_wait(ctl.acc_full + buf, (j >> 1) & 1u, abort_flag, a.st, 936)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // (columns past the tile's last: unwritten, not stored)
+#pragma unroll
+        for (int i = 0; i < kTile / 2; i += 16) {
+          uint32_t v[16];
+          tmem_ld16_nw(t_acc + buf * kTile + i, v);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int k = 0; k < 16; ++k) acc[i + k] += __float2int_rn(__uint_as_float(v[k]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 2) mbar_arrive_cluster(map_rank(ctl.acc_empty + buf, 0));
+          else mbar_arrive(ctl.acc_empty + buf);
+        }
+      }
+      if (!ok || kSplit) break;
+      const int f0 = 128 * (u % a.NU * kCtas + rank) + 32 * quarter;  // beyond N for a block computed twice
+      if (f0 >= a.N) continue;
+      const float sw = f0 + lane < a.N ? __ldg(a.w_scale + f0 + lane) : 0.f;
+      const float add = a.bias && f0 + lane < a.N ? __ldg(a.bias + f0 + lane) : 0.f;
+#pragma unroll
+      for (int col = 0; col < kTile / 2; col += 16) {
+        const int t0 = half * (kTile / 2) + col;
+        if (t0 >= tokens) break;
+        __syncwarp();
+        const float sx_lane = lane < 16 && t0 + lane < tokens ? a.x_scale[row0 + t0 + lane] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float y = fmaf((float)acc[col + i], sw * __shfl_sync(0xffffffffu, sx_lane, i), add);
+          if (a.out_type == 1) *reinterpret_cast<float*>(buf_s + i * 128 + lane * 4) = y;
+          else if (a.out_type == 2) *reinterpret_cast<__half*>(buf_s + i * 64 + lane * 2) = __float2half_rn(y);
+          else *reinterpret_cast<__nv_bfloat16*>(buf_s + i * 64 + lane * 2) = __float2bfloat16_rn(y);
+        }
+        __syncwarp();
+        if (a.out_type == 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 4 * i + (lane >> 3), f = f0 + 4 * (lane & 7);
+            if (t0 + row < tokens && f < a.N)
+              *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (long long)(row0 + t0 + row) * a.ldo + f) =
+                  *reinterpret_cast<const uint4*>(buf_s + row * 128 + (lane & 7) * 16);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = 8 * i + (lane >> 2), f = f0 + 8 * (lane & 3);
+            if (t0 + row < tokens && f < a.N)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (long long)(row0 + t0 + row) * a.ldo + f) =
+                  *reinterpret_cast<const uint4*>(buf_s + row * 64 + (lane & 3) * 16);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  grid_launch_dependents();
+  if (kCtas == 2) cluster_sync_all();  // neither CTA leaves while the other may still signal it
+  if constexpr (kSplit) {
+    int row0 = 0;
+    const int tokens = first < total ? tokens_of(first, row0) : 0;
+    int* sums = reinterpret_cast<int*>(ring_b);  // [token][128 features]; the copies and MMAs are done with the rings
+    if (warp >= i8g::kConvWarps && warp < i8g::kProducer && tokens && !*abort_flag) {
+      const int half = (warp - i8g::kConvWarps) >> 2, t0 = half * (kTile / 2);
+#pragma unroll
+      for (int i = 0; i < kTile / 2; ++i)
+        if (t0 + i < tokens) sums[(t0 + i) * 128 + 32 * (warp & 3) + lane] = acc[i];
+    }
+    cluster_sync_all();
+    grid_dependency_wait();
+    const int f = 128 * (first % a.NU) + 4 * lane;
+    if (f < a.N) {
+      const float4 sw = *reinterpret_cast<const float4*>(a.w_scale + f);
+      const float4 add = a.bias ? *reinterpret_cast<const float4*>(a.bias + f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = warp * a.split + part; t < tokens; t += i8g::kThreads / 32 * a.split) {
+        int4 n = make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < i8g::kMaxSplit; ++c)
+          if (c < a.split) {
+            const float4 v = ld_cluster(reinterpret_cast<const float*>(sums + t * 128 + 4 * lane), c);
+            n.x += __float_as_int(v.x), n.y += __float_as_int(v.y), n.z += __float_as_int(v.z), n.w += __float_as_int(v.w);
+          }
+        const float sx = a.x_scale[row0 + t];
+        const float y[4] = {fmaf((float)n.x, sw.x * sx, add.x), fmaf((float)n.y, sw.y * sx, add.y),
+                            fmaf((float)n.z, sw.z * sx, add.z), fmaf((float)n.w, sw.w * sx, add.w)};
+        const long long o = (long long)(row0 + t) * a.ldo + f;
+        if (a.out_type == 1) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+          uint32_t w[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            w[i] = a.out_type == 2 ? *reinterpret_cast<const uint32_t*>(&h) : *reinterpret_cast<const uint32_t*>(&b);
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) = make_uint2(w[0], w[1]);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while its sums are read
+  }
+  if (warp == i8g::kIssuer) {
+    tc_fence_after();
+    if (kCtas == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// --------------------------------------------------------------------------------------------------------------------
+// Launches
+// --------------------------------------------------------------------------------------------------------------------
+typedef void (*Int8Gemm)(const CUtensorMap, Int8Args);
+struct Int8Variant {
+  Int8Gemm fn;
+  int ctas, tile;
+  int cost;  // cycles of 64 elements of the reduction, about
+};
+static const Int8Variant kInt8Variants[] = {{int8_gemm_kernel<1, 64, false>, 1, 64, 360},
+                                            {int8_gemm_kernel<1, 128, false>, 1, 128, 520},
+                                            {int8_gemm_kernel<2, 192, false>, 2, 192, 430},
+                                            {int8_gemm_kernel<1, 64, true>, 1, 64, 360},
+                                            {int8_gemm_kernel<1, 128, true>, 1, 128, 520}};
+
+static cudaError_t set_int8_attrs() {  // once per device
+  constexpr int kCached = 64;
+  static std::mutex mu;
+  static bool done[kCached] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < kCached && done[dev]) return cudaSuccess;
+  for (const Int8Variant& v : kInt8Variants) {
+    e = cudaFuncSetAttribute((const void*)v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, i8::kSmemMax);
+    if (e != cudaSuccess) return e;
+  }
+  e = cudaFuncSetAttribute((const void*)int8_gemv_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, i8::kSmemMax);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute((const void*)int8_gemv_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, i8::kSmemMax);
+  if (e == cudaSuccess && dev >= 0 && dev < kCached) done[dev] = true;
+  return e;
+}
+
+static Int8Args args_of(const Int8Product& p) {
+  Int8Args a{};
+  a.packed = p.packed, a.w_scale = p.w_scale, a.bias = p.bias;
+  a.N = p.N, a.K = p.K, a.T = p.T;
+  a.x = p.x, a.x_scale = p.x_scale, a.ldx = p.ldx;
+  a.out = p.out, a.ldo = p.ldo, a.out_type = p.out_type;
+  a.once = p.once, a.st = p.status, a.fault = p.fault;
+  return a;
+}
+
+cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t st) {
+  cudaError_t e = set_int8_attrs();
+  if (e != cudaSuccess) return e;
+  Int8Args a = args_of(p);
+  const int blocks = (a.K + 63) / 64;
+  a.wk = 1;
+  while (a.wk < i8v::kWarps && a.wk * i8v::kBlocks < blocks) a.wk *= 2;
+  a.passes = (blocks + a.wk * i8v::kBlocks - 1) / (a.wk * i8v::kBlocks);
+  a.slice = (blocks + a.wk * a.passes - 1) / (a.wk * a.passes) * 64;
+  const int groups = (a.N + 15) / 16, tokens = a.T <= 8 ? 8 : 16;
+  a.batch = (i8v::kSumBytes / 4 / tokens - 4) / 16;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::min(groups, p.num_sms));
+  cfg.blockDim = dim3(i8v::kThreads);
+  cfg.dynamicSmemBytes = i8v::kRing + i8v::kSumBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return a.T <= 8 ? cudaLaunchKernelEx(&cfg, int8_gemv_kernel<1>, a) : cudaLaunchKernelEx(&cfg, int8_gemv_kernel<2>, a);
+}
+
+Int8Tiling int8_tiling(int N, int K, int T, int num_sms) {
+  // The variant whose rounds of units take the least time by the costs of a step above and some 3000 cycles a unit.
+  const int blocks = (N + 127) / 128, squares = (K + 127) / 128;
+  Int8Tiling best{};
+  double least = 1e300;
+  for (int i = 0; i < 5; ++i) {
+    const Int8Variant& v = kInt8Variants[i];
+    const long long units = (long long)((blocks + v.ctas - 1) / v.ctas) * ((T + v.tile - 1) / v.tile);
+    for (int split = i >= 3 ? 2 : 1; split <= (i >= 3 ? i8g::kMaxSplit : 1); split *= 2) {
+      if (i >= 3 && (units * split > num_sms * 15 / 16 || 2 * split > squares)) break;
+      const long long slots = num_sms / (v.ctas * split), rounds = (units + slots - 1) / slots;
+      const double t = (double)rounds * ((squares + split - 1) / split * 2.0 * v.cost + 3000.0);
+      if (t < least) least = t, best = {i, v.tile / v.ctas, split};
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_int8_gemm(const Int8Product& p, const Int8Tiling& t, const CUtensorMap& x_map, cudaStream_t st) {
+  cudaError_t e = set_int8_attrs();
+  if (e != cudaSuccess) return e;
+  const Int8Variant& v = kInt8Variants[t.variant];
+  Int8Args a = args_of(p);
+  a.NB = (a.N + 127) / 128;
+  a.NU = (a.NB + v.ctas - 1) / v.ctas;
+  a.tiles = (a.T + v.tile - 1) / v.tile;
+  const int round = 16 * v.ctas;
+  a.per = ((a.T + a.tiles - 1) / a.tiles + round - 1) / round * round;  // tiles of one size, so that none is a small rest
+  a.tiles = (a.T + a.per - 1) / a.per;
+  a.halves = (a.K + 63) / 64;
+  a.split = t.split;
+  cudaLaunchConfig_t cfg{};
+  const int units = a.tiles * a.NU;
+  cfg.gridDim = dim3((unsigned)(t.split > 1 ? units * t.split : std::min(units, p.num_sms / v.ctas) * v.ctas));
+  cfg.blockDim = dim3(i8g::kThreads);
+  cfg.dynamicSmemBytes = i8::kSmemMax;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)(t.split > 1 ? t.split : v.ctas);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, v.fn, x_map, a);
+}
+
+}  // namespace nvfp4moe

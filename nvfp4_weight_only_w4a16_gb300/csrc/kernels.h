@@ -223,6 +223,87 @@ cudaError_t launch_pack_int4(const uint8_t* w_q, const void* scale, const uint8_
 cudaError_t launch_pack_grouped(const uint8_t* w_q, const uint8_t* w_s, uint8_t* blob, int E, int N, int Np, int K,
                                 cudaStream_t st);
 
+// The operators around the products.
+struct RouteOp {  // router.cu
+  const void* logits;
+  long long ld, ld_dl;     // elements
+  int bf16;
+  int T, E, k;
+  int score, renorm;
+  float scale;
+  const float* bias;       // [E] or NULL
+  int groups, top_groups, group_top;
+  int32_t* ids;            // [T][k] (the backward's input)
+  float* weights;          // [T][k]
+  int32_t *offsets, *perm, *inv;
+  const float* dweights;   // backward: [T][k]
+  void* dlogits;           // backward: the logits' type
+  DeviceStatus* status;
+  int num_sms;
+};
+cudaError_t launch_route_forward(const RouteOp& p, cudaStream_t st);
+cudaError_t launch_route_backward(const RouteOp& p, cudaStream_t st);
+
+struct NormOp {  // norm.cu; strides in elements; weight NULL: the codes of x alone
+  const void *x, *res, *weight;
+  void *sum, *y;
+  int8_t* q;
+  float *q_scale, *rstd;
+  long long ldx, ldr, lds, ldy, ldq;
+  int T, H, f16, num_sms;
+  float eps;
+};
+cudaError_t launch_norm_forward(const NormOp& p, cudaStream_t st);
+struct NormBackOp {
+  const void *dy, *x, *weight, *dsum;
+  const float* rstd;
+  void* dx;
+  float *dweight, *part;   // part: norm_backward_parts rows of H, where there is a dweight
+  long long ld_dy, ldx, ld_dsum, ld_dx;
+  int T, H, f16, num_sms;
+};
+cudaError_t launch_norm_backward(const NormBackOp& p, cudaStream_t st);
+int norm_backward_parts(int H, int num_sms);
+
+struct SwigluOp {  // swiglu.cu; strides in elements; codes and scales NULL: nothing is kept
+  const void *gate, *up, *dh;
+  void *h, *dgate, *dup;
+  long long ld_gate, ld_up, ld_dh, ld_h, ld_dgate, ld_dup;
+  int8_t* codes;
+  float* scales;
+  long long R;
+  int I, f16, num_sms;
+};
+cudaError_t launch_swiglu_forward(const SwigluOp& p, cudaStream_t st);
+cudaError_t launch_swiglu_backward(const SwigluOp& p, cudaStream_t st);
+
+// y [T][N] = x [T][K] times an INT8 matrix, a scale per token and per output (int8.cu).
+struct Int8Product {
+  const uint8_t* packed;
+  const float *w_scale, *bias;  // [N]; bias NULL: none
+  int N, K, T;
+  const int8_t* x;
+  const float* x_scale;
+  long long ldx;                // bytes
+  void* out;
+  long long ldo;                // elements
+  int out_type;                 // 0 BF16, 1 FP32, 2 FP16
+  bool once;                    // the matrix is more than L2 holds
+  int num_sms;
+  DeviceStatus* status;
+  int fault;
+};
+size_t int8_packed_bytes(int N, int K);
+cudaError_t launch_pack_int8(const int8_t* w_q, int N, int K, uint8_t* packed, cudaStream_t st);
+cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t st);  // up to 16 tokens
+// How launch_int8_gemm cuts a product: kernel variant, tokens per TMA box, CTAs that share a unit's reduction.
+struct Int8Tiling {
+  int variant, box, split;
+};
+Int8Tiling int8_tiling(int N, int K, int T, int num_sms);
+// x_map: x as [T][K] bytes, box {128, tiling.box}, 128B swizzle.
+cudaError_t launch_int8_gemm(const Int8Product& p, const Int8Tiling& t, const CUtensorMap& x_map, cudaStream_t st);
+
 cudaError_t launch_combine(const LayerDims& d, int T, int k, const Workspace& ws, void* out,
                            cudaStream_t st);
 

@@ -1,0 +1,91 @@
+// 16-bit elements, and their codes in 8 bits: round(127 v / peak), peak the largest magnitude of the elements that share
+// a scale of peak / 127.
+#pragma once
+#include <cuda_runtime.h>
+#include "common.cuh"
+
+namespace nvfp4moe {
+
+// Pairs of BF16 or FP16 elements as FP32.
+template <bool kF16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if (kF16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (kF16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool kF16>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack16<kF16>(u[i]);
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+  }
+}
+template <bool kF16>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack16<kF16>(v[0], v[1]), pack16<kF16>(v[2], v[3]), pack16<kF16>(v[4], v[5]), pack16<kF16>(v[6], v[7]));
+}
+
+// Peaks are compared as FP32 bits: infinities, and NaNs behind them, are larger than every number.
+__device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// Whether codes_of can take a peak.  Others (zero, next to underflow, infinite, NaN) are the caller's.
+__device__ __forceinline__ bool plain_peak(float peak) { return peak >= 0x1p-100f && peak <= 0x1p100f; }
+
+// To the nearest, ties to even, of a quotient evaluated in 64 bits: that of 127 v and peak as FP32 numbers, or as products
+// of two 16-bit ones, is a midpoint or more than 2^-40 of its value away from it.
+__device__ __forceinline__ int code_of_64(double v, double peak) { return (int)rint(127.0 * v / peak); }
+
+// The codes of N values, four to a word, exactly.  In FP32 the quotient is off by less than 2e-5; where that leaves two
+// codes possible, 127 v less the code times the peak decides.  kBits, the values' significant bits: up to 16 that
+// remainder is exact in FP32 (127 v and code times peak have at most 23 bits, and a value whose code is not zero lies at
+// most 8 binary places below the peak); beyond, the quotient is evaluated in 64 bits.
+template <int kBits, int N>
+__device__ __forceinline__ void codes_of(const float (&v)[N], float peak, uint32_t (&out)[N / 4]) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer, whose low byte is the sum's
+  const float inv = 127.0f / peak;
+  uint32_t m[N];
+  float near = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float t = v[i] * inv, s = t + kMagic;
+    m[i] = __float_as_uint(s);
+    near = fmaxf(near, fabsf(t - (s - kMagic)));
+  }
+  if (near > 0.49998f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float t = v[i] * inv, r = __uint_as_float(m[i]) - kMagic;
+      if (fabsf(t - r) > 0.49998f) {
+        if (kBits <= 16) {
+          const float rem = fmaf(-r, peak, 127.0f * v[i]), a = 2.0f * fabsf(rem);
+          if (a > peak || (a == peak && (m[i] & 1u))) m[i] = __float_as_uint(r + copysignf(1.0f, rem) + kMagic);
+        } else {
+          m[i] = (uint32_t)code_of_64(v[i], peak);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const uint32_t a = __byte_perm(m[4 * i], m[4 * i + 1], 0x0040), b = __byte_perm(m[4 * i + 2], m[4 * i + 3], 0x0040);
+    out[i] = __byte_perm(a, b, 0x5410);
+  }
+}
+
+// Four codes as FP32: each byte, its sign bit turned over, as the low byte of 2^23 + 128 + code.
+__device__ __forceinline__ void codes_to_f32(uint32_t w, float (&v)[4]) {
+  const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)) - 8388736.0f;
+}
+
+}  // namespace nvfp4moe
