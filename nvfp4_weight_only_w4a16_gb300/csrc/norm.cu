@@ -237,20 +237,34 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
   long long t = (long long)blockIdx.x * kRows + threadIdx.x / TP;
   const long long step = (long long)gridDim.x * kRows;
   const float inv_h = 1.0f / (float)a.H;
-  for (int turn = 0; t - threadIdx.x / TP % (TP < 32 ? 32 / TP : 1) < a.T; t += step, turn ^= 1) {
-    const bool row_ok = t < a.T;
-    uint4 x4[V], d4[V], s4[V];
+  const auto fetch = [&](long long row, uint4 (&x)[V], uint4 (&d)[V], uint4 (&s)[V], float& r) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * TP;
-      x4[v] = d4[v] = s4[v] = make_uint4(0u, 0u, 0u, 0u);
-      if (row_ok && p < pieces) {
-        x4[v] = load16(a.x + t * a.ldx + 16ll * p);
-        d4[v] = load16(a.dy + t * a.ld_dy + 16ll * p);
-        if (a.dsum) s4[v] = load16(a.dsum + t * a.ld_dsum + 16ll * p);
+      x[v] = d[v] = s[v] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < a.T && p < pieces) {
+        x[v] = load16(a.x + row * a.ldx + 16ll * p);
+        d[v] = load16(a.dy + row * a.ld_dy + 16ll * p);
+        if (a.dsum) s[v] = load16(a.dsum + row * a.ld_dsum + 16ll * p);
       }
     }
-    const float rstd = row_ok ? a.rstd[t] : 0.f;
+    r = row < a.T ? a.rstd[row] : 0.f;
+  };
+  constexpr bool kAhead = V == 1;  // the next row is on its way while this one is reduced, where there are registers for it
+  uint4 x_n[V], d_n[V], s_n[V];
+  float rstd_n = 0.f;
+  if (kAhead) fetch(t, x_n, d_n, s_n, rstd_n);
+  for (int turn = 0; t - threadIdx.x / TP % (TP < 32 ? 32 / TP : 1) < a.T; t += step, turn ^= 1) {
+    const bool row_ok = t < a.T;
+    uint4 x4[V], d4[V], s4[V];
+    float rstd = rstd_n;
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x4[v] = x_n[v], d4[v] = d_n[v], s4[v] = s_n[v];
+      fetch(t + step, x_n, d_n, s_n, rstd_n);
+    } else {
+      fetch(t, x4, d4, s4, rstd);
+    }
     float c = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -310,8 +324,10 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* part, i
   grid_launch_dependents();
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
   float sum = 0.f;
-  if (col < H)
+  if (col < H) {
+#pragma unroll 10
     for (int i = run; i < parts; i += 32) sum += part[(long long)i * H + col];
+  }
   s[run][threadIdx.x & 31] = sum;
   __syncthreads();
   if (run == 0 && col < H) {
@@ -399,7 +415,7 @@ static NormShape norm_back_shape(int pieces) {
   if (pieces <= 32) return {32, 1};
   if (pieces <= 64) return {32, 2};
   if (pieces <= 256) return {256, 1};
-  if (pieces <= 512) return {256, 2};
+  if (pieces <= 512) return {512, 1};
   if (pieces <= 1024) return {512, 2};
   return {512, 4};
 }
@@ -428,7 +444,7 @@ static cudaError_t backward_of(const NormBackArgs& a, int grid, cudaStream_t st)
     case 32 * 8 + 1: return run_backward<kF16, 32, 1>(a, grid, st);
     case 32 * 8 + 2: return run_backward<kF16, 32, 2>(a, grid, st);
     case 256 * 8 + 1: return run_backward<kF16, 256, 1>(a, grid, st);
-    case 256 * 8 + 2: return run_backward<kF16, 256, 2>(a, grid, st);
+    case 512 * 8 + 1: return run_backward<kF16, 512, 1>(a, grid, st);
     case 512 * 8 + 2: return run_backward<kF16, 512, 2>(a, grid, st);
     default: return run_backward<kF16, 512, 4>(a, grid, st);
   }

@@ -37,6 +37,12 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 
 // Peaks are compared as FP32 bits: infinities, and NaNs behind them, are larger than every number.
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The largest magnitude of 8 elements, as the bits of an element; NaNs and infinities are larger than every number.
+__device__ __forceinline__ unsigned peak_of(const uint4& w) {
+  const unsigned m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
 // Whether codes_of can take a peak.  Others (zero, next to underflow, infinite, NaN) are the caller's.
 __device__ __forceinline__ bool plain_peak(float peak) { return peak >= 0x1p-100f && peak <= 0x1p100f; }
 
@@ -44,7 +50,7 @@ __device__ __forceinline__ bool plain_peak(float peak) { return peak >= 0x1p-100
 // of two 16-bit ones, is a midpoint or more than 2^-40 of its value away from it.
 __device__ __forceinline__ int code_of_64(double v, double peak) { return (int)rint(127.0 * v / peak); }
 
-// The codes of N values, four to a word, exactly.  In FP32 the quotient is off by less than 2e-5; where that leaves two
+// The codes of N values, four to a word, exactly.  In FP32 the quotient is off by less than 1e-5; where that leaves two
 // codes possible, 127 v less the code times the peak decides.  kBits, the values' significant bits: up to 16 that
 // remainder is exact in FP32 (127 v and code times peak have at most 23 bits, and a value whose code is not zero lies at
 // most 8 binary places below the peak); beyond, the quotient is evaluated in 64 bits.
@@ -52,31 +58,30 @@ template <int kBits, int N>
 __device__ __forceinline__ void codes_of(const float (&v)[N], float peak, uint32_t (&out)[N / 4]) {
   constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer, whose low byte is the sum's
   const float inv = 127.0f / peak;
-  uint32_t m[N];
-  float near = 0.f;
+  float m[N], near = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float t = v[i] * inv, s = t + kMagic;
-    m[i] = __float_as_uint(s);
-    near = fmaxf(near, fabsf(t - (s - kMagic)));
+    m[i] = fmaf(v[i], inv, kMagic);
+    near = fmaxf(near, fabsf(fmaf(v[i], inv, kMagic - m[i])));
   }
   if (near > 0.49998f) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float t = v[i] * inv, r = __uint_as_float(m[i]) - kMagic;
-      if (fabsf(t - r) > 0.49998f) {
+      const float r = m[i] - kMagic;
+      if (fabsf(fmaf(v[i], inv, -r)) > 0.49998f) {
         if (kBits <= 16) {
           const float rem = fmaf(-r, peak, 127.0f * v[i]), a = 2.0f * fabsf(rem);
-          if (a > peak || (a == peak && (m[i] & 1u))) m[i] = __float_as_uint(r + copysignf(1.0f, rem) + kMagic);
+          if (a > peak || (a == peak && (__float_as_uint(m[i]) & 1u))) m[i] += copysignf(1.0f, rem);
         } else {
-          m[i] = (uint32_t)code_of_64(v[i], peak);
+          m[i] = kMagic + (float)code_of_64(v[i], peak);
         }
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    const uint32_t a = __byte_perm(m[4 * i], m[4 * i + 1], 0x0040), b = __byte_perm(m[4 * i + 2], m[4 * i + 3], 0x0040);
+    const uint32_t a = __byte_perm(__float_as_uint(m[4 * i]), __float_as_uint(m[4 * i + 1]), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(m[4 * i + 2]), __float_as_uint(m[4 * i + 3]), 0x0040);
     out[i] = __byte_perm(a, b, 0x5410);
   }
 }

@@ -11,12 +11,14 @@
 // all experts); a token where some are not, one in a few hundred on random logits, is chosen again from scores in 64
 // bits.  Logits that are compared as they are need no such test.
 //
-// One warp a token, lane l with experts l V .. l V + V - 1, so that a lane's logits are one or two vector loads and the
-// lowest index among equals is the lowest lane's.  A CTA takes a run of tokens; bit t of bits[e] says that its token t
-// chose e, so that a row's place among its expert's is a population count, whatever the order the warps came in.  Few
-// tokens: one CTA does it all.  Else a second kernel turns the runs' counts into places and a third scatters; the counts
-// lie in `inv`, each run's in its own rows' part, which its CTA alone overwrites in the end, so that there is no
-// workspace and calls may overlap.
+// One warp a token, lane l with experts l, l + 32, ..  No rounds of warp maxima (at 9 of them, 8 experts chosen of 256, a
+// token took some 1800 cycles of latency): the (k + 1)-th largest of the lanes' own maxima is a bound that the k + 1
+// largest reach, and few others; those are laid out one to a lane, and each counts how many are ahead of it.
+//
+// A CTA takes a run of tokens; bit t of bits[e] says that its token t chose e, so that a row's place among its expert's
+// is a population count, whatever the order the warps came in.  Few tokens: one CTA does it all.  Else a second kernel
+// turns the runs' counts into places and a third scatters; the counts lie in `inv`, each run's in its own rows' part,
+// which its CTA alone overwrites in the end, so that there is no workspace and calls may overlap.
 #include <algorithm>
 
 #include "kernels.h"
@@ -27,15 +29,16 @@ namespace nvfp4moe {
 
 namespace rt {
 constexpr int kMaxExperts = 512;
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kOneCta = 128;  // tokens up to which one CTA does it all
 constexpr int kRun = 256;     // of a run, unless its counts need more
+constexpr int kMostShared = 208 * 1024;  // 512 experts: 128 KB of 32 warps' rows and 64 KB of a run's bits
 }  // namespace rt
 
 struct RouteArgs {
   const void* logits;
   long long ld;       // elements
-  int bf16, vec;      // vec: rows start on 16 bytes
+  int bf16;
   int T, E, k;
   int score, renorm;
   float scale;
@@ -61,51 +64,13 @@ __device__ __forceinline__ void run_of(const RouteArgs& a, int b, int& t0, int& 
   t1 = t0 + base + (b < extra ? 1 : 0);
 }
 
-// Lane's V logits of token t; beyond E: NaN, which no choice takes before a number.
+// Lane's logits l, l + 32, .. of token t; beyond E: NaN, which no choice takes before a number.
 template <int V>
 __device__ __forceinline__ void load_lane(const RouteArgs& a, int t, float (&v)[V]) {
-  const int e0 = (threadIdx.x & 31) * V;
-  const size_t at = (size_t)t * a.ld + e0;
-  if (a.vec && e0 + V <= a.E) {
-    if (a.bf16) {
-      constexpr int kW = V >= 2 ? V / 2 : 1;
-      uint32_t w[kW];
-      const uint16_t* p = static_cast<const uint16_t*>(a.logits) + at;
-      if constexpr (V >= 8) {
+  const int lane = threadIdx.x & 31;
+  const size_t at = (size_t)t * a.ld + lane;
 #pragma unroll
-        for (int i = 0; i < V / 8; ++i) {
-          const uint4 q = reinterpret_cast<const uint4*>(p)[i];
-          w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-        }
-      } else if constexpr (V == 4) {
-        const uint2 q = *reinterpret_cast<const uint2*>(p);
-        w[0] = q.x, w[1] = q.y;
-      } else if constexpr (V == 2) {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-      } else {
-        w[0] = *p;
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-    } else {
-      const float* p = static_cast<const float*>(a.logits) + at;
-      if constexpr (V >= 4) {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-          const float4 q = reinterpret_cast<const float4*>(p)[i];
-          v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-        }
-      } else if constexpr (V == 2) {
-        const float2 q = *reinterpret_cast<const float2*>(p);
-        v[0] = q.x, v[1] = q.y;
-      } else {
-        v[0] = *p;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = e0 + i < a.E ? load_logit(a.logits, a.bf16, at + i) : __uint_as_float(0x7FC00000u);
-  }
+  for (int i = 0; i < V; ++i) v[i] = lane + 32 * i < a.E ? load_logit(a.logits, a.bf16, at + 32 * i) : __uint_as_float(0x7FC00000u);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -164,26 +129,43 @@ __device__ __forceinline__ void merge_two(F& a, F& b, F c, F d) {
   b = b < lo ? lo : b;
 }
 
+// A warp's part of shared memory.
+struct RouteScratch {
+  uint32_t key[32];  // candidates: order key, expert, logit
+  int id[32];
+  float logit[32];
+};
+
 // Lane g < groups: the value of group g over the c of its members (NaN counts as -inf), and the magnitudes that went in.
+// Through shared memory (row [E]): every group gets as many lanes as there are for it, which start at different members
+// so as not to meet in a bank.
 template <class F, int V>
-__device__ __forceinline__ F group_value(const RouteArgs& a, const F (&c)[V], F* size) {
-  const int lane = threadIdx.x & 31, e0 = lane * V;
+__device__ __forceinline__ F group_value(const RouteArgs& a, const F (&c)[V], F* row, F* size) {
+  const int lane = threadIdx.x & 31;
   const F none = F(-INFINITY);
-  F mine = none;
-  for (int g = 0; g < a.groups; ++g) {
-    const int lo = g * a.group_size, hi = lo + a.group_size;
-    F x = none, y = none;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i >= lo && e0 + i < hi) merge_two(x, y, c[i] == c[i] ? c[i] : none, none);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const F x2 = __shfl_xor_sync(0xffffffffu, x, o), y2 = __shfl_xor_sync(0xffffffffu, y, o);
-      merge_two(x, y, x2, y2);
+  for (int i = 0; i < V; ++i)
+    if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i] == c[i] ? c[i] : none;
+  __syncwarp();
+  const int bits = 32 - __clz(a.groups - 1), per = 32 >> bits;  // lanes a group (groups >= 2)
+  const int g = lane / per, sub = lane % per, turns = (a.group_size + per - 1) / per;
+  F x = none, y = none;
+  if (g < a.groups)
+    for (int j = 0, at = g % turns; j < turns; ++j, at = at + 1 == turns ? 0 : at + 1) {
+      const int m = sub + at * per;
+      if (m < a.group_size) merge_two(x, y, row[g * a.group_size + m], none);
     }
-    if (lane == g) mine = a.group_top == 2 ? x + y : x, *size = a.group_top == 2 ? fabs(x) + fabs(y) : fabs(x);
+  for (int o = 1; o < per; o <<= 1) {
+    const F x2 = __shfl_xor_sync(0xffffffffu, x, o), y2 = __shfl_xor_sync(0xffffffffu, y, o);
+    merge_two(x, y, x2, y2);
   }
-  return mine == mine ? mine : none;  // (infinities of both signs)
+  __syncwarp();
+  F value = a.group_top == 2 ? x + y : x;
+  if (value != value) value = none;  // infinities of both signs
+  const F sizes = a.group_top == 2 ? fabs(x) + fabs(y) : fabs(x);
+  const int from = (lane * per) & 31;
+  *size = __shfl_sync(0xffffffffu, sizes, from);
+  return __shfl_sync(0xffffffffu, value, from);
 }
 
 // The groups kept, one bit each.  `apart`: whether the last one in and the first one out are further apart than they can
@@ -208,67 +190,61 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs& a, F mine, F si
 // Experts of the lane that may be chosen: bit i.
 template <int V>
 __device__ __forceinline__ unsigned eligible(const RouteArgs& a, unsigned groups) {
-  const int e0 = (threadIdx.x & 31) * V;
+  const int lane = threadIdx.x & 31;
   unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (e0 + i < a.E && (a.top_groups == a.groups || ((groups >> ((e0 + i) / a.group_size)) & 1u))) m |= 1u << i;
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
+    if (e < a.E && (a.top_groups == a.groups || ((groups >> (e / a.group_size)) & 1u))) m |= 1u << i;
+  }
   return m;
 }
 
-// The value of an order key (NaN for a NaN's).
+// The value of an order key; NaN for a NaN's (0, or 1 where 0 means none).
 __device__ __forceinline__ float key_float(uint32_t key) {
-  return key == 0u ? __uint_as_float(0x7FC00000u) : __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+  return key <= 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+// Order keys of doubles: larger value, larger key; NaN lowest.
+__device__ __forceinline__ unsigned long long double_key(double v) {
+  if (v != v) return 0ull;
+  if (v == 0.0) return 1ull << 63;
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v);
+  return b >> 63 ? ~b : b | (1ull << 63);
 }
 
-// The k largest keys among those marked in `avail`, by rounds; lane j gets choice j's expert and logit.  `apart`: whether
-// every one and the next differ by more than they can be wrong, tol and their own roundings; not looked at for tol < 0.
+// Choice by rounds, keys as above (0: not eligible): for tokens with more candidates than lanes.  Lane j gets the j-th.
 template <int V>
-__device__ __forceinline__ void choose(const RouteArgs& a, const uint32_t (&key)[V], const float (&l)[V], unsigned avail,
-                                       float tol, int* id, float* logit, bool* apart) {
+__device__ __noinline__ void choose_by_rounds(const RouteArgs& a, const unsigned long long (&key)[V], int* id) {
   const int lane = threadIdx.x & 31;
-  float before = INFINITY;
-  bool ok = true;
-  for (int j = 0; j <= a.k; ++j) {
-    if (j == a.k && tol < 0.f) break;
-    uint32_t best = 0;
-    int at = -1;
+  unsigned gone = 0;
+  for (int j = 0; j < a.k; ++j) {
+    unsigned long long best = 0;
+    int e = 0x7FFFFFFF;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (((avail >> i) & 1u) && (at < 0 || key[i] > best)) best = key[i], at = i;
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const unsigned who = __ballot_sync(0xffffffffu, at >= 0 && best == top);
-    if (who == 0) break;  // fewer than k + 1 are eligible
-    if (tol >= 0.f) {
-      const float v = key_float(top);
-      if (j > 0 && !(before - v > tol + (fabsf(before) + fabsf(v)) * 0x1p-22f)) ok = false;
-      before = v;
-      if (j == a.k) break;
+      if (!((gone >> i) & 1u) && key[i] > best) best = key[i], e = lane + 32 * i;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long b2 = __shfl_xor_sync(0xffffffffu, best, o);
+      const int e2 = __shfl_xor_sync(0xffffffffu, e, o);
+      if (b2 > best || (b2 == best && e2 < e)) best = b2, e = e2;
     }
-    const int owner = __ffs(who) - 1;
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (at == i) v = l[i];
-    const int e = __shfl_sync(0xffffffffu, lane * V + at, owner);
-    v = __shfl_sync(0xffffffffu, v, owner);
-    if (lane == owner) avail &= ~(1u << at);
-    if (lane == j) *id = e, *logit = v;
+    if ((e & 31) == lane) gone |= 1u << (e >> 5);
+    if (lane == j) *id = e;
   }
-  *apart = ok;
 }
 
-// The choice from scores in 64 bits.
+// The choice from scores in 64 bits: groups, if any, and experts.
 template <int V>
-__device__ __noinline__ void choose_64(const RouteArgs& a, const float (&l)[V], int* id, float* logit) {
-  const int lane = threadIdx.x & 31, e0 = lane * V;
+__device__ __noinline__ void choose_64(const RouteArgs& a, const float (&l)[V], double* row, int* id) {
+  const int lane = threadIdx.x & 31;
   Softmax<double> sm{0.f, 0.0, 0};
   if (!a.score) sm = softmax_of<double>(l);
   double c[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     c[i] = score_of<double>(l[i], a.score, sm, a.E);
-    if (a.bias && e0 + i < a.E) c[i] += (double)a.bias[e0 + i];
+    if (a.bias && lane + 32 * i < a.E) c[i] += (double)a.bias[lane + 32 * i];
     if (l[i] != l[i]) c[i] = __longlong_as_double(0x7FF8000000000000ll);
   }
   unsigned groups = ~0u;
@@ -277,97 +253,142 @@ __device__ __noinline__ void choose_64(const RouteArgs& a, const float (&l)[V], 
     double rated[V], size = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) rated[i] = a.bias || a.group_top == 2 ? c[i] : (double)l[i];
-    const double mine = group_value<double>(a, rated, &size);
+    const double mine = group_value<double>(a, rated, row, &size);
     groups = best_groups<double>(a, mine, size, 0.0, &apart);
   }
-  if (!a.bias) {
+  const unsigned open = eligible<V>(a, groups);
+  unsigned long long key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = (double)l[i];
-  }
-  unsigned avail = eligible<V>(a, groups);
-  for (int j = 0; j < a.k; ++j) {
-    // a number before a NaN, then the larger, then the lower index
-    double best = 0.0;
-    int at = -1;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (((avail >> i) & 1u) && (at < 0 || c[i] > best || (best != best && c[i] == c[i]))) best = c[i], at = i;
-    int e = at < 0 ? 0x7FFFFFFF : e0 + at;
-    double v = best;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
-      const int e2 = __shfl_xor_sync(0xffffffffu, e, o);
-      const bool none = e == 0x7FFFFFFF, none2 = e2 == 0x7FFFFFFF, nan = v != v, nan2 = v2 != v2;
-      const bool same = nan == nan2 && (nan || v == v2);
-      const bool take = !none2 && (none || (nan && !nan2) || (nan == nan2 && !nan && v2 > v) || (same && e2 < e));
-      if (take) v = v2, e = e2;
-    }
-    const int owner = e / V, i0 = e - owner * V;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i == i0) x = l[i];
-    x = __shfl_sync(0xffffffffu, x, owner);
-    if (lane == owner) avail &= ~(1u << i0);
-    if (lane == j) *id = e, *logit = x;
-  }
+  for (int i = 0; i < V; ++i) key[i] = (open >> i) & 1u ? double_key(a.bias ? c[i] : (double)l[i]) + 1ull : 0ull;
+  choose_by_rounds<V>(a, key, id);
 }
 
-// Token t's choice: lane j < k gets its j-th expert and weight.
+// Token t's choice: lane j < k gets its j-th expert and weight.  row: the warp's [E] doubles, where there are groups.
 template <int V>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int t, int* id, float* weight) {
-  const int lane = threadIdx.x & 31, e0 = lane * V;
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, RouteScratch& s, double* row, int* id, float* weight) {
+  const int lane = threadIdx.x & 31;
   float l[V];
   load_lane<V>(a, t, l);
   int nan = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) nan += e0 + i < a.E && l[i] != l[i];
-  nan = (int)__reduce_add_sync(0xffffffffu, (unsigned)nan);
-  if (nan && lane == 0) atomicAdd(&a.st->nan_logits, (unsigned)nan);
+  for (int i = 0; i < V; ++i) nan += lane + 32 * i < a.E && l[i] != l[i];
+  if (__any_sync(0xffffffffu, nan)) {
+    nan = (int)__reduce_add_sync(0xffffffffu, (unsigned)nan);
+    if (lane == 0) atomicAdd(&a.st->nan_logits, (unsigned)nan);
+  }
   const bool limited = a.top_groups < a.groups, sums = limited && a.group_top == 2;
   Softmax<float> sm{0.f, 0.f, 0};
   if (!a.score && (a.bias || sums || !a.renorm)) sm = softmax_of<float>(l);
-  float logit = 0.f;
-  bool apart = true;
-  {
-    uint32_t key[V];
-    float tol = -1.f, c[V];
-    if (a.bias || sums) {
-      float most = 0.f;
+  float tol = -1.f, c[V];
+  if (a.bias || sums) {
+    float most = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float s = score_of<float>(l[i], a.score, sm, a.E);
-        c[i] = a.bias && e0 + i < a.E ? s + a.bias[e0 + i] : s;
-        if (l[i] != l[i]) c[i] = l[i];
-        most = fmaxf(most, s);
-      }
-      tol = warp_max(most) * (a.score ? 0x1p-20f : 0x1p-17f);  // NaNs, a NaN bias's too, are never apart
+    for (int i = 0; i < V; ++i) {
+      const float x = score_of<float>(l[i], a.score, sm, a.E);
+      c[i] = a.bias && lane + 32 * i < a.E ? x + a.bias[lane + 32 * i] : x;
+      if (l[i] != l[i]) c[i] = l[i];
+      most = fmaxf(most, x);
     }
-    unsigned groups = ~0u;
-    if (limited) {
-      float rated[V], size = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) rated[i] = a.bias || sums ? c[i] : l[i];
-      bool far;
-      const float mine = group_value<float>(a, rated, &size);
-      groups = best_groups<float>(a, mine, size, tol < 0.f ? 0.f : 2.0f * tol, &far);
-      apart = far || tol < 0.f;  // logits are exact
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = float_key(a.bias ? c[i] : l[i]);
-    bool far = true;
-    choose<V>(a, key, l, eligible<V>(a, groups), a.bias ? tol : -1.f, id, &logit, &far);
-    apart = apart && far;
+    tol = warp_max(most) * (a.score ? 0x1p-20f : 0x1p-17f);  // NaNs, a NaN bias's too, are never apart
   }
-  if (!apart) {  // (copies, so that the arrays above stay in registers)
-    float l2[V], x = 0.f;
+  unsigned groups = ~0u;
+  bool exact = true;  // the groups are certain
+  if (limited) {
+    float rated[V], size = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) rated[i] = a.bias || sums ? c[i] : l[i];
+    const float mine = group_value<float>(a, rated, reinterpret_cast<float*>(row), &size);
+    bool far;
+    groups = best_groups<float>(a, mine, size, tol < 0.f ? 0.f : 2.0f * tol, &far);
+    exact = far || tol < 0.f;  // logits are exact
+  }
+  const unsigned open = eligible<V>(a, groups);
+  const bool close = a.bias != nullptr;  // the keys are of FP32 scores: look at the gaps
+  uint32_t key[V], m = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = (open >> i) & 1u ? max(float_key(a.bias ? c[i] : l[i]), 1u) : 0u;
+    m = max(m, key[i]);
+  }
+  // the bound: the (k + 1)-th largest of the lanes' maxima, less what two scores can be wrong
+  int ahead = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t v = __shfl_sync(0xffffffffu, m, j);
+    ahead += v > m || (v == m && j < lane);
+  }
+  uint32_t bound = __shfl_sync(0xffffffffu, m, __ffs(__ballot_sync(0xffffffffu, ahead == a.k)) - 1);
+  if (close && bound > 1u) {
+    const float v = key_float(bound);
+    bound = float_key(v - 2.0f * (tol + fabsf(v) * 0x1p-22f));
+  }
+  bound = max(bound, 1u);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool in = key[i] >= bound;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    const int at = n + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) s.key[at] = key[i], s.id[at] = lane + 32 * i, s.logit[at] = l[i];
+    n += __popc(who);
+  }
+  __syncwarp();
+  bool done = exact && n <= 32;
+  float logit = 0.f;
+  if (done) {
+    const uint32_t mine = lane < n ? s.key[lane] : 0u;
+    const int e = lane < n ? s.id[lane] : 0x7FFFFFFF;
+    const float x = lane < n ? s.logit[lane] : 0.f;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t v = __shfl_sync(0xffffffffu, mine, j);
+      const int f = __shfl_sync(0xffffffffu, e, j);
+      rank += v > mine || (v == mine && f < e);
+    }
+    bool apart = true;
+    if (close) {
+      // whether every one of the k + 1 first and the next differ by more than they can be wrong
+      __syncwarp();
+      if (lane < n) s.key[rank] = mine;
+      __syncwarp();
+      const float u = key_float(s.key[lane]), v = key_float(s.key[lane < 31 ? lane + 1 : 31]);
+      apart = __all_sync(0xffffffffu, lane >= a.k || lane + 1 >= n || u - v > tol + (fabsf(u) + fabsf(v)) * 0x1p-22f);
+    }
+    if (!apart) {  // again in 64 bits, of the candidates
+      Softmax<double> sm64{0.f, 0.0, 0};
+      if (!a.score) sm64 = softmax_of<double>(l);
+      unsigned long long k64 = 0;
+      if (lane < n) {
+        const double v = x != x ? (double)x : score_of<double>(x, a.score, sm64, a.E) + (double)a.bias[e];
+        k64 = double_key(v);
+      }
+      rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const unsigned long long v = __shfl_sync(0xffffffffu, k64, j);
+        const int f = __shfl_sync(0xffffffffu, e, j);
+        rank += v > k64 || (v == k64 && f < e);
+      }
+    }
+    __syncwarp();
+    if (lane < n) s.id[rank] = e, s.logit[rank] = x;
+    __syncwarp();
+    if (lane < a.k) *id = s.id[lane], logit = s.logit[lane];
+  } else {  // (copies, so that the arrays above stay in registers)
+    float l2[V];
     int e = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) l2[i] = l[i];
-    choose_64<V>(a, l2, &e, &x);
-    *id = e, logit = x;
+    if (exact && !close) {
+      unsigned long long key2[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) key2[i] = key[i];
+      choose_by_rounds<V>(a, key2, &e);
+    } else {
+      choose_64<V>(a, l2, row, &e);
+    }
+    if (lane < a.k) *id = e, logit = load_logit(a.logits, a.bf16, (size_t)t * a.ld + e);
   }
+  __syncwarp();  // the scratch is free again
   float w;
   if (!a.score && a.renorm) {
     w = warp_softmax_k(logit, a.k);
@@ -393,11 +414,14 @@ __device__ __forceinline__ int rows_before(const uint32_t* bits, int words, int 
 // kAll: the only run, tables included.
 template <int V, bool kAll>
 __global__ void __launch_bounds__(rt::kThreads) route_choose_kernel(RouteArgs a) {
-  extern __shared__ uint32_t bits[];  // [E][words]
+  extern __shared__ double rows_mem[];  // where there are groups: [warps][E]; then bits [E][words]
   __shared__ int scan[32], base[rt::kMaxExperts];
+  __shared__ RouteScratch scratch[rt::kThreads / 32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  double* row = rows_mem + warp * a.E;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(rows_mem + (a.top_groups < a.groups ? (blockDim.x >> 5) * a.E : 0));
   int t0, t1;
   run_of(a, blockIdx.x, t0, t1);
   for (int i = threadIdx.x; i < a.E * a.words; i += blockDim.x) bits[i] = 0u;
@@ -405,7 +429,7 @@ __global__ void __launch_bounds__(rt::kThreads) route_choose_kernel(RouteArgs a)
   for (int t = t0 + warp; t < t1; t += blockDim.x >> 5) {
     int id = 0;
     float w;
-    route_token<V>(a, t, &id, &w);
+    route_token<V>(a, t, scratch[warp], row, &id, &w);
     if (lane < a.k) {
       a.ids[(size_t)t * a.k + lane] = id;
       a.weights[(size_t)t * a.k + lane] = w;
@@ -433,57 +457,66 @@ __global__ void __launch_bounds__(rt::kThreads) route_choose_kernel(RouteArgs a)
   }
 }
 
-// The runs' counts into places: one cluster, each CTA some of the experts, which tell one another their sums.
+// The runs' counts into places: one cluster, each CTA some of the experts, which tell one another their sums.  A thread
+// has one expert's counts of a stretch of runs.
 namespace rt {
-constexpr int kScanCtas = 8, kScanThreads = 1024;
+constexpr int kScanCtas = 8, kScanThreads = 1024, kScanHeld = 8;
 }
 __global__ void __launch_bounds__(rt::kScanThreads) route_scan_kernel(RouteArgs a) {
-  constexpr int kCols = rt::kMaxExperts / rt::kScanCtas, kRows = rt::kScanThreads / kCols;  // 64 columns by 16 stretches
-  __shared__ int part[kRows][kCols];
-  __shared__ int mine[kCols];
+  __shared__ int part[rt::kScanThreads];
   __shared__ float sums[rt::kScanCtas];  // every CTA's, as bits
   __shared__ int scan[32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int cols = (a.E + rt::kScanCtas - 1) / rt::kScanCtas, rank = (int)cluster_rank();
-  const int c = threadIdx.x % kCols, r = threadIdx.x / kCols, e = rank * cols + c;
-  const bool ok = c < cols && e < a.E;
-  const int b0 = (int)((long long)a.runs * r / kRows), b1 = (int)((long long)a.runs * (r + 1) / kRows);
-  int n = 0;
-  if (ok)
-    for (int b = b0; b < b1; ++b) {
-      int t0, t1;
-      run_of(a, b, t0, t1);
-      n += a.inv[(size_t)t0 * a.k + e];
-    }
-  part[r][c] = n;
+  const int stretches = rt::kScanThreads / cols;
+  const int r = threadIdx.x / cols, c = threadIdx.x - r * cols, e = rank * cols + c;
+  const bool ok = r < stretches && e < a.E;
+  const int b0 = ok ? a.runs * r / stretches : 0, b1 = ok ? a.runs * (r + 1) / stretches : 0;
+  const int base = a.T / a.runs, extra = a.T - base * a.runs;
+  const auto at = [&](int b) { return a.inv + (size_t)(b * base + min(b, extra)) * a.k + e; };
+  int held[rt::kScanHeld], n = 0;  // the first ones, so that they are not read twice
+#pragma unroll
+  for (int i = 0; i < rt::kScanHeld; ++i) held[i] = b0 + i < b1 ? *at(b0 + i) : 0;
+#pragma unroll
+  for (int i = 0; i < rt::kScanHeld; ++i) n += held[i];
+  for (int b = b0 + rt::kScanHeld; b < b1; ++b) n += *at(b);
+  part[threadIdx.x] = n;
   __syncthreads();
-  int sum = 0;
-  if (r == 0)
-    for (int i = 0; i < kRows; ++i) sum += part[i][c];
+  int sum = 0, before = 0;  // of the expert; of its stretches before this one
+  if (ok)
+    for (int i = 0; i < stretches; ++i) {
+      const int v = part[i * cols + c];
+      before += i < r ? v : 0;
+      sum += v;
+    }
   int total;
-  const int before = block_exclusive_scan(sum, scan, &total);
+  const int lower = block_exclusive_scan(r == 0 ? sum : 0, scan, &total);  // experts of this CTA below; r = 0 comes first
   if (threadIdx.x < rt::kScanCtas) st_cluster(sums + rank, threadIdx.x, __int_as_float(total));
-  if (r == 0) mine[c] = before;
+  if (r == 0) part[c] = lower;
   cluster_sync_all();
-  int base = mine[c];
-  for (int i = 0; i < rank; ++i) base += __float_as_int(sums[i]);
-  if (ok && r == 0) a.offsets[e] = base;
-  if (rank == rt::kScanCtas - 1 && threadIdx.x == 0) a.offsets[a.E] = a.T * a.k;
   if (!ok) return;
-  for (int i = 0; i < r; ++i) base += part[i][c];
-  for (int b = b0; b < b1; ++b) {
-    int t0, t1;
-    run_of(a, b, t0, t1);
-    int32_t* at = a.inv + (size_t)t0 * a.k + e;
-    const int v = *at;
-    *at = base;
-    base += v;
+  int place = part[c];
+  for (int i = 0; i < rank; ++i) place += __float_as_int(sums[i]);
+  if (r == 0) a.offsets[e] = place;
+  if (r == 0 && e == a.E - 1) a.offsets[a.E] = a.T * a.k;
+  place += before;
+#pragma unroll
+  for (int i = 0; i < rt::kScanHeld; ++i)
+    if (b0 + i < b1) {
+      *at(b0 + i) = place;
+      place += held[i];
+    }
+  for (int b = b0 + rt::kScanHeld; b < b1; ++b) {
+    const int v = *at(b);
+    *at(b) = place;
+    place += v;
   }
 }
 
 __global__ void __launch_bounds__(rt::kThreads) route_scatter_rows_kernel(RouteArgs a) {
-  extern __shared__ uint32_t bits[];
+  extern __shared__ double rows_mem[];
+  uint32_t* bits = reinterpret_cast<uint32_t*>(rows_mem);
   __shared__ int base[rt::kMaxExperts];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -506,11 +539,14 @@ __global__ void __launch_bounds__(rt::kThreads) route_scatter_rows_kernel(RouteA
 }
 
 // dl of a token from the gradient of its weights.  An id outside 0 .. E - 1 counts as no choice.
+namespace rt {
+constexpr int kBackThreads = 256;
+}
 template <int V>
-__global__ void __launch_bounds__(rt::kThreads) route_backward_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(rt::kBackThreads) route_backward_kernel(RouteArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * V, warps = rt::kThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = rt::kBackThreads / 32;
   for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) {
     float l[V], d[V];
     load_lane<V>(a, t, l);
@@ -520,11 +556,11 @@ __global__ void __launch_bounds__(rt::kThreads) route_backward_kernel(RouteArgs 
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.f;
     for (int j = 0; j < a.k; ++j) {
-      const int at = __shfl_sync(0xffffffffu, id, j) - e0;
+      const int at = __shfl_sync(0xffffffffu, id, j) - lane;
       const float v = __shfl_sync(0xffffffffu, w, j);
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (at == i && e0 + i < a.E) d[i] = v, chosen |= 1u << i;
+        if (at == 32 * i && lane + 32 * i < a.E) d[i] = v, chosen |= 1u << i;
     }
     float s[V];  // the scores that the weights are made of
     if (a.score) {
@@ -560,12 +596,12 @@ __global__ void __launch_bounds__(rt::kThreads) route_backward_kernel(RouteArgs 
 #pragma unroll
       for (int i = 0; i < V; ++i) d[i] = s[i] * (d[i] - dot);
     }
-    const size_t at = (size_t)t * a.ld_dl + e0;
+    const size_t at = (size_t)t * a.ld_dl + lane;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (e0 + i < a.E) {
-        if (a.bf16) static_cast<__nv_bfloat16*>(a.dl)[at + i] = __float2bfloat16_rn(d[i]);
-        else static_cast<float*>(a.dl)[at + i] = d[i];
+      if (lane + 32 * i < a.E) {
+        if (a.bf16) static_cast<__nv_bfloat16*>(a.dl)[at + 32 * i] = __float2bfloat16_rn(d[i]);
+        else static_cast<float*>(a.dl)[at + 32 * i] = d[i];
       }
   }
 }
@@ -573,7 +609,6 @@ __global__ void __launch_bounds__(rt::kThreads) route_backward_kernel(RouteArgs 
 static RouteArgs args_of(const RouteOp& p) {
   RouteArgs a{};
   a.logits = p.logits, a.ld = p.ld, a.bf16 = p.bf16;
-  a.vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.ld * (p.bf16 ? 2 : 4) % 16 == 0;
   a.T = p.T, a.E = p.E, a.k = p.k;
   a.score = p.score, a.renorm = p.renorm, a.scale = p.scale, a.bias = p.bias;
   a.groups = p.groups, a.top_groups = p.top_groups, a.group_top = p.group_top, a.group_size = p.E / p.groups;
@@ -601,8 +636,8 @@ static RouteKernels kernels_of(int E) {
 
 static cudaError_t launch(RouteKernel f, int grid, int threads, size_t smem, const RouteArgs& a, cudaStream_t st,
                           int cluster = 1) {
-  if (smem > 32768) {  // 512 experts and one choice: up to 1024 tokens a run
-    const cudaError_t e = cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * rt::kMaxExperts * 32);
+  if (smem > 24576) {
+    const cudaError_t e = cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMostShared);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
@@ -624,18 +659,21 @@ cudaError_t launch_route_forward(const RouteOp& p, cudaStream_t st) {
   const int per = std::max(least, std::min(rt::kRun, (a.T + p.num_sms - 1) / p.num_sms));
   a.runs = a.T <= rt::kOneCta ? 1 : std::max(1, a.T / per);
   a.words = ((a.T + a.runs - 1) / a.runs + 31) / 32;
-  const size_t smem = sizeof(uint32_t) * a.E * a.words;
-  if (a.runs == 1) return launch(f.all, 1, rt::kThreads, smem, a, st);
-  cudaError_t e = launch(f.choose, a.runs, rt::kThreads, smem, a, st);
+  // warps: one a token up to all of them, and threads enough for an expert each
+  const int threads = std::min(rt::kThreads, std::max((a.E + 31) / 32, (a.T + a.runs - 1) / a.runs) * 32);
+  const size_t bits = sizeof(uint32_t) * a.E * a.words;
+  const size_t smem = bits + (a.top_groups < a.groups ? sizeof(double) * a.E * (threads / 32) : 0);
+  if (a.runs == 1) return launch(f.all, 1, threads, smem, a, st);
+  cudaError_t e = launch(f.choose, a.runs, threads, smem, a, st);
   if (e == cudaSuccess) e = launch(route_scan_kernel, rt::kScanCtas, rt::kScanThreads, 0, a, st, rt::kScanCtas);
-  if (e == cudaSuccess) e = launch(route_scatter_rows_kernel, a.runs, rt::kThreads, smem, a, st);
+  if (e == cudaSuccess) e = launch(route_scatter_rows_kernel, a.runs, rt::kThreads, bits, a, st);
   return e;
 }
 
 cudaError_t launch_route_backward(const RouteOp& p, cudaStream_t st) {
   RouteArgs a = args_of(p);
-  const int warps = rt::kThreads / 32;
-  return launch(kernels_of(a.E).backward, std::min((a.T + warps - 1) / warps, 4 * p.num_sms), rt::kThreads, 0, a, st);
+  const int warps = rt::kBackThreads / 32;
+  return launch(kernels_of(a.E).backward, std::min((a.T + warps - 1) / warps, 8 * p.num_sms), rt::kBackThreads, 0, a, st);
 }
 
 }  // namespace nvfp4moe

@@ -48,7 +48,13 @@ struct SwigluBlocks {
   }
 };
 
-__device__ __forceinline__ float sigmoid_fast(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + e^-g) by the hardware's 2^x and 1/x.
+__device__ __forceinline__ float sigmoid_fast(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
 
 template <bool kF16>
 __device__ __forceinline__ void load_elems(const uint8_t* p, bool ok, uint4 (&w)[2]) {
@@ -59,14 +65,13 @@ __device__ __forceinline__ void load_elems(const uint8_t* p, bool ok, uint4 (&w)
   }
 }
 
-// The codes of a block of which this thread holds 16 elements, and its scale.
+// The codes of a block of which this thread holds 16 elements (raw: as they came), and its scale.
 template <bool kF16>
-__device__ __forceinline__ uint4 checkpoint(const float (&v)[sg::kPer], float& scale) {
-  unsigned m = 0;
-#pragma unroll
-  for (int i = 0; i < sg::kPer; ++i) m = max(m, magnitude(v[i]));
+__device__ __forceinline__ uint4 checkpoint(const uint4 (&raw)[2], const float (&v)[sg::kPer], float& scale) {
+  unsigned m = max(peak_of(raw[0]), peak_of(raw[1]));
 #pragma unroll
   for (int o = 1; o < sg::kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = __float_as_uint(unpack16<kF16>(m).x);
   const float peak = __uint_as_float(m);
   uint32_t c[4] = {0u, 0u, 0u, 0u};
   scale = peak / 127.0f;
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(sg::kThreads, sg::kPerSm) swiglu_forward_kerne
     }
     if (kKeep) {
       float sg_, su;
-      const uint4 cg = checkpoint<kF16>(g, sg_), cu = checkpoint<kF16>(u, su);
+      const uint4 cg = checkpoint<kF16>(g4, g, sg_), cu = checkpoint<kF16>(u4, u, su);
       if (ok) {
         int8_t* c = a.codes + w.row * 2 * a.I + e;
         *reinterpret_cast<uint4*>(c) = cg;
