@@ -7,9 +7,9 @@
 //   tables: the T k routed rows t k + j by expert, ascending within one: offsets, perm, and its inverse
 //
 // The choice is that of c in 64 bits.  Comparing FP32 scores gives it wherever neighbours in the order are further apart
-// than those scores can be wrong (2^-20 of the token's largest score for sigmoids, 2^-17 for softmax, whose sum is over
-// all experts); a token where some are not, one in a few hundred on random logits, is chosen again from scores in 64
-// bits.  Logits that are compared as they are need no such test.
+// than those scores can be wrong (2^-17 of the token's largest score); a token where some are not, a few in a hundred on
+// random logits, is chosen again, its candidates scored in 64 bits.  Logits that are compared as they are need no such
+// test.
 //
 // One warp a token, lane l with experts l, l + 32, ..  No rounds of warp maxima (at 9 of them, 8 experts chosen of 256, a
 // token took some 1800 cycles of latency): the (k + 1)-th largest of the lanes' own maxima is a bound that the k + 1
@@ -120,20 +120,34 @@ __device__ __forceinline__ F score_of(float l, int sigmoid, const Softmax<F>& s,
   return sizeof(F) == 8 ? F(exp((double)l - (double)s.top) / s.sum) : F(expf(l - s.top) / (float)s.sum);
 }
 
-// The larger two of a pair of sorted pairs.
+// The larger two of two sorted pairs, and of a pair and one more.
+template <class F>
+__device__ __forceinline__ F larger(F a, F b) {
+  return a < b ? b : a;
+}
+template <class F>
+__device__ __forceinline__ F smaller(F a, F b) {
+  return a < b ? a : b;
+}
+template <>
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+template <>
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
 template <class F>
 __device__ __forceinline__ void merge_two(F& a, F& b, F c, F d) {
-  const F lo = a < c ? a : c;
-  a = a < c ? c : a;
-  b = b < d ? d : b;
-  b = b < lo ? lo : b;
+  b = larger(smaller(a, c), larger(b, d));
+  a = larger(a, c);
+}
+template <class F>
+__device__ __forceinline__ void merge_one(F& a, F& b, F c) {
+  b = larger(b, smaller(a, c));
+  a = larger(a, c);
 }
 
 // A warp's part of shared memory.
 struct RouteScratch {
-  uint32_t key[32];  // candidates: order key, expert, logit
+  uint32_t key[32];  // candidates: order key, expert
   int id[32];
-  float logit[32];
 };
 
 // Lane g < groups: the value of group g over the c of its members (NaN counts as -inf), and the magnitudes that went in.
@@ -153,7 +167,7 @@ __device__ __forceinline__ F group_value(const RouteArgs& a, const F (&c)[V], F*
   if (g < a.groups)
     for (int j = 0, at = g % turns; j < turns; ++j, at = at + 1 == turns ? 0 : at + 1) {
       const int m = sub + at * per;
-      if (m < a.group_size) merge_two(x, y, row[g * a.group_size + m], none);
+      if (m < a.group_size) merge_one(x, y, row[g * a.group_size + m]);
     }
   for (int o = 1; o < per; o <<= 1) {
     const F x2 = __shfl_xor_sync(0xffffffffu, x, o), y2 = __shfl_xor_sync(0xffffffffu, y, o);
@@ -187,18 +201,26 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs& a, F mine, F si
   return __ballot_sync(0xffffffffu, in);
 }
 
-// Experts of the lane that may be chosen: bit i.
+// The groups of the lane's experts, a byte each; none (32 and more) beyond E.
 template <int V>
-__device__ __forceinline__ unsigned eligible(const RouteArgs& a, unsigned groups) {
-  const int lane = threadIdx.x & 31;
-  unsigned m = 0;
+struct LaneGroups {
+  uint32_t w[(V + 3) / 4];
+  __device__ __forceinline__ explicit LaneGroups(const RouteArgs& a) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    if (e < a.E && (a.top_groups == a.groups || ((groups >> (e / a.group_size)) & 1u))) m |= 1u << i;
+    for (int i = 0; i < (V + 3) / 4; ++i) w[i] = 0x20202020u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane + 32 * i;
+      if (e < a.E) w[i / 4] ^= (uint32_t)(e / a.group_size | 0x20) << (8 * (i % 4));
+    }
   }
-  return m;
-}
+  // whether expert i's group has its bit set
+  __device__ __forceinline__ bool in(int i, unsigned groups) const {
+    const unsigned g = (w[i / 4] >> (8 * (i % 4))) & 0xFFu;
+    return g < 32 && ((groups >> (g & 31)) & 1u);
+  }
+};
 
 // The value of an order key; NaN for a NaN's (0, or 1 where 0 means none).
 __device__ __forceinline__ float key_float(uint32_t key) {
@@ -237,6 +259,7 @@ __device__ __noinline__ void choose_by_rounds(const RouteArgs& a, const unsigned
 // The choice from scores in 64 bits: groups, if any, and experts.
 template <int V>
 __device__ __noinline__ void choose_64(const RouteArgs& a, const float (&l)[V], double* row, int* id) {
+  const LaneGroups<V> of(a);
   const int lane = threadIdx.x & 31;
   Softmax<double> sm{0.f, 0.0, 0};
   if (!a.score) sm = softmax_of<double>(l);
@@ -256,23 +279,27 @@ __device__ __noinline__ void choose_64(const RouteArgs& a, const float (&l)[V], 
     const double mine = group_value<double>(a, rated, row, &size);
     groups = best_groups<double>(a, mine, size, 0.0, &apart);
   }
-  const unsigned open = eligible<V>(a, groups);
   unsigned long long key[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = (open >> i) & 1u ? double_key(a.bias ? c[i] : (double)l[i]) + 1ull : 0ull;
+  for (int i = 0; i < V; ++i) key[i] = of.in(i, groups) ? double_key(a.bias ? c[i] : (double)l[i]) + 1ull : 0ull;
   choose_by_rounds<V>(a, key, id);
 }
 
 // Token t's choice: lane j < k gets its j-th expert and weight.  row: the warp's [E] doubles, where there are groups.
 template <int V>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int t, RouteScratch& s, double* row, int* id, float* weight) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, const LaneGroups<V>& of, RouteScratch& s, double* row,
+                                            int* id, float* weight) {
   const int lane = threadIdx.x & 31;
   float l[V];
   load_lane<V>(a, t, l);
-  int nan = 0;
+  bool odd = false;
 #pragma unroll
-  for (int i = 0; i < V; ++i) nan += lane + 32 * i < a.E && l[i] != l[i];
-  if (__any_sync(0xffffffffu, nan)) {
+  for (int i = 0; i < V; ++i) odd |= lane + 32 * i < a.E && l[i] != l[i];
+  odd = __any_sync(0xffffffffu, odd);
+  if (odd) {
+    int nan = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) nan += lane + 32 * i < a.E && l[i] != l[i];
     nan = (int)__reduce_add_sync(0xffffffffu, (unsigned)nan);
     if (lane == 0) atomicAdd(&a.st->nan_logits, (unsigned)nan);
   }
@@ -281,15 +308,22 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, RouteScra
   if (!a.score && (a.bias || sums || !a.renorm)) sm = softmax_of<float>(l);
   float tol = -1.f, c[V];
   if (a.bias || sums) {
+    // by the hardware's 2^x and 1/x: a sigmoid is off by up to 2^-23 (3 + 1.2 |l|) of itself, a softmax by 2^-19 of the
+    // largest, l = log of it at most; tol covers two of them
     float most = 0.f;
+    const bool plain = a.score || (sm.top != INFINITY && sm.top != -INFINITY);
+    const float inv = a.score ? 1.0f : __fdividef(1.0f, sm.sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float x = score_of<float>(l[i], a.score, sm, a.E);
-      c[i] = a.bias && lane + 32 * i < a.E ? x + a.bias[lane + 32 * i] : x;
+      float x;
+      if (plain) x = a.score ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - sm.top) * inv;
+      else x = score_of<float>(l[i], 0, sm, a.E);
+      most = fmaxf(most, x);  // drops NaNs
+      c[i] = a.bias && lane + 32 * i < a.E ? x + __ldg(a.bias + lane + 32 * i) : x;
       if (l[i] != l[i]) c[i] = l[i];
-      most = fmaxf(most, x);
     }
-    tol = warp_max(most) * (a.score ? 0x1p-20f : 0x1p-17f);  // NaNs, a NaN bias's too, are never apart
+    most = warp_max(most);
+    tol = most * 0x1p-17f * fmaxf(1.0f, __logf(most) * -0x1p-4f);
   }
   unsigned groups = ~0u;
   bool exact = true;  // the groups are certain
@@ -302,53 +336,47 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, RouteScra
     groups = best_groups<float>(a, mine, size, tol < 0.f ? 0.f : 2.0f * tol, &far);
     exact = far || tol < 0.f;  // logits are exact
   }
-  const unsigned open = eligible<V>(a, groups);
   const bool close = a.bias != nullptr;  // the keys are of FP32 scores: look at the gaps
   uint32_t key[V], m = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    key[i] = (open >> i) & 1u ? max(float_key(a.bias ? c[i] : l[i]), 1u) : 0u;
+    key[i] = of.in(i, groups) ? max(float_key(a.bias ? c[i] : l[i]), 1u) : 0u;
     m = max(m, key[i]);
   }
   // the bound: the (k + 1)-th largest of the lanes' maxima, less what two scores can be wrong
-  int ahead = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t v = __shfl_sync(0xffffffffu, m, j);
-    ahead += v > m || (v == m && j < lane);
+  uint32_t bound = 0;
+  for (int j = 0; j <= a.k; ++j) {
+    bound = __reduce_max_sync(0xffffffffu, m);
+    const unsigned who = __ballot_sync(0xffffffffu, m == bound);
+    if (lane == __ffs(who) - 1) m = 0;
   }
-  uint32_t bound = __shfl_sync(0xffffffffu, m, __ffs(__ballot_sync(0xffffffffu, ahead == a.k)) - 1);
   if (close && bound > 1u) {
     const float v = key_float(bound);
     bound = float_key(v - 2.0f * (tol + fabsf(v) * 0x1p-22f));
   }
   bound = max(bound, 1u);
-  int n = 0;
+  int n = 0;  // candidates, in the experts' order
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const bool in = key[i] >= bound;
     const unsigned who = __ballot_sync(0xffffffffu, in);
     const int at = n + __popc(who & ((1u << lane) - 1u));
-    if (in && at < 32) s.key[at] = key[i], s.id[at] = lane + 32 * i, s.logit[at] = l[i];
+    if (in && at < 32) s.key[at] = key[i], s.id[at] = lane + 32 * i;
     n += __popc(who);
   }
   __syncwarp();
-  bool done = exact && n <= 32;
-  float logit = 0.f;
-  if (done) {
+  if (exact && n <= 32) {
     const uint32_t mine = lane < n ? s.key[lane] : 0u;
-    const int e = lane < n ? s.id[lane] : 0x7FFFFFFF;
-    const float x = lane < n ? s.logit[lane] : 0.f;
+    const int e = lane < n ? s.id[lane] : 0;
     int rank = 0;
     for (int j = 0; j < n; ++j) {
-      const uint32_t v = __shfl_sync(0xffffffffu, mine, j);
-      const int f = __shfl_sync(0xffffffffu, e, j);
-      rank += v > mine || (v == mine && f < e);
+      const uint32_t v = s.key[j];
+      rank += v > mine || (v == mine && j < lane);
     }
+    __syncwarp();
     bool apart = true;
     if (close) {
       // whether every one of the k + 1 first and the next differ by more than they can be wrong
-      __syncwarp();
       if (lane < n) s.key[rank] = mine;
       __syncwarp();
       const float u = key_float(s.key[lane]), v = key_float(s.key[lane < 31 ? lane + 1 : 31]);
@@ -359,36 +387,35 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, RouteScra
       if (!a.score) sm64 = softmax_of<double>(l);
       unsigned long long k64 = 0;
       if (lane < n) {
-        const double v = x != x ? (double)x : score_of<double>(x, a.score, sm64, a.E) + (double)a.bias[e];
-        k64 = double_key(v);
+        const float x = load_logit(a.logits, a.bf16, (size_t)t * a.ld + e);
+        k64 = double_key(x != x ? (double)x : score_of<double>(x, a.score, sm64, a.E) + (double)a.bias[e]);
       }
       rank = 0;
       for (int j = 0; j < n; ++j) {
         const unsigned long long v = __shfl_sync(0xffffffffu, k64, j);
-        const int f = __shfl_sync(0xffffffffu, e, j);
-        rank += v > k64 || (v == k64 && f < e);
+        rank += v > k64 || (v == k64 && j < lane);
       }
     }
+    if (lane < n) s.id[rank] = e;
     __syncwarp();
-    if (lane < n) s.id[rank] = e, s.logit[rank] = x;
-    __syncwarp();
-    if (lane < a.k) *id = s.id[lane], logit = s.logit[lane];
+    if (lane < a.k) *id = s.id[lane];
   } else {  // (copies, so that the arrays above stay in registers)
-    float l2[V];
     int e = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) l2[i] = l[i];
     if (exact && !close) {
       unsigned long long key2[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) key2[i] = key[i];
       choose_by_rounds<V>(a, key2, &e);
     } else {
+      float l2[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) l2[i] = l[i];
       choose_64<V>(a, l2, row, &e);
     }
-    if (lane < a.k) *id = e, logit = load_logit(a.logits, a.bf16, (size_t)t * a.ld + e);
+    if (lane < a.k) *id = e;
   }
   __syncwarp();  // the scratch is free again
+  const float logit = lane < a.k ? load_logit(a.logits, a.bf16, (size_t)t * a.ld + *id) : 0.f;
   float w;
   if (!a.score && a.renorm) {
     w = warp_softmax_k(logit, a.k);
@@ -426,10 +453,11 @@ __global__ void __launch_bounds__(rt::kThreads) route_choose_kernel(RouteArgs a)
   run_of(a, blockIdx.x, t0, t1);
   for (int i = threadIdx.x; i < a.E * a.words; i += blockDim.x) bits[i] = 0u;
   __syncthreads();
+  const LaneGroups<V> of(a);
   for (int t = t0 + warp; t < t1; t += blockDim.x >> 5) {
     int id = 0;
     float w;
-    route_token<V>(a, t, scratch[warp], row, &id, &w);
+    route_token<V>(a, t, of, scratch[warp], row, &id, &w);
     if (lane < a.k) {
       a.ids[(size_t)t * a.k + lane] = id;
       a.weights[(size_t)t * a.k + lane] = w;
