@@ -7,8 +7,8 @@
 //   tables: the T k routed rows t k + j by expert, ascending within one: offsets, perm, and its inverse
 //
 // The choice is that of c in 64 bits.  Comparing FP32 scores gives it wherever neighbours in the order are further apart
-// than those scores can be wrong (2^-17 of the token's largest score); a token where some are not, a few in a hundred on
-// random logits, is chosen again, its candidates scored in 64 bits.  Logits that are compared as they are need no such
+// than those scores can be wrong (2^-20 of the token's largest score, 2^-17 for softmax); a token where some are not, one
+// in some hundreds on random logits, is chosen again, its candidates scored in 64 bits.  Logits that are compared as they are need no such
 // test.
 //
 // One warp a token, lane l with experts l, l + 32, ..  No rounds of warp maxima (at 9 of them, 8 experts chosen of 256, a
@@ -20,6 +20,7 @@
 // turns the runs' counts into places and a third scatters; the counts lie in `inv`, each run's in its own rows' part,
 // which its CTA alone overwrites in the end, so that there is no workspace and calls may overlap.
 #include <algorithm>
+#include <mutex>
 
 #include "kernels.h"
 #include "route_common.cuh"
@@ -64,13 +65,20 @@ __device__ __forceinline__ void run_of(const RouteArgs& a, int b, int& t0, int& 
   t1 = t0 + base + (b < extra ? 1 : 0);
 }
 
-// Lane's logits l, l + 32, .. of token t; beyond E: NaN, which no choice takes before a number.
+// Lane's logits l, l + 32, .. of token t; beyond E: -inf, which no sum or maximum sees.
 template <int V>
 __device__ __forceinline__ void load_lane(const RouteArgs& a, int t, float (&v)[V]) {
   const int lane = threadIdx.x & 31;
   const size_t at = (size_t)t * a.ld + lane;
+  if (a.bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + at;
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = lane + 32 * i < a.E ? load_logit(a.logits, a.bf16, at + 32 * i) : __uint_as_float(0x7FC00000u);
+    for (int i = 0; i < V; ++i) v[i] = lane + 32 * i < a.E ? __uint_as_float((uint32_t)p[32 * i] << 16) : -INFINITY;
+  } else {
+    const float* p = static_cast<const float*>(a.logits) + at;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = lane + 32 * i < a.E ? p[32 * i] : -INFINITY;
+  }
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -120,6 +128,14 @@ __device__ __forceinline__ F score_of(float l, int sigmoid, const Softmax<F>& s,
   return sizeof(F) == 8 ? F(exp((double)l - (double)s.top) / s.sum) : F(expf(l - s.top) / (float)s.sum);
 }
 
+// 1 / (1 + e^-l) by the hardware's 2^x and 1/x.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
 // The larger two of two sorted pairs, and of a pair and one more.
 template <class F>
 __device__ __forceinline__ F larger(F a, F b) {
@@ -150,42 +166,42 @@ struct RouteScratch {
   int id[32];
 };
 
-// Lane g < groups: the value of group g over the c of its members (NaN counts as -inf), and the magnitudes that went in.
-// Through shared memory (row [E]): every group gets as many lanes as there are for it, which start at different members
-// so as not to meet in a bank.
-template <class F, int V>
-__device__ __forceinline__ F group_value(const RouteArgs& a, const F (&c)[V], F* row, F* size) {
+// Lane g < groups: the value of group g over its members' c in shared memory (row [E]; NaN counts as -inf), the
+// magnitudes that went in, and the smaller of them.  Every group gets as many lanes as there are for it, which start at different members so as not
+// to meet in a bank.
+template <class F>
+__device__ __forceinline__ F group_value(const RouteArgs& a, const F* row, F* size, F* least) {
   const int lane = threadIdx.x & 31;
   const F none = F(-INFINITY);
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i] == c[i] ? c[i] : none;
-  __syncwarp();
   const int bits = 32 - __clz(a.groups - 1), per = 32 >> bits;  // lanes a group (groups >= 2)
   const int g = lane / per, sub = lane % per, turns = (a.group_size + per - 1) / per;
   F x = none, y = none;
   if (g < a.groups)
     for (int j = 0, at = g % turns; j < turns; ++j, at = at + 1 == turns ? 0 : at + 1) {
       const int m = sub + at * per;
-      if (m < a.group_size) merge_one(x, y, row[g * a.group_size + m]);
+      if (m < a.group_size) {
+        const F c = row[g * a.group_size + m];
+        merge_one(x, y, c == c ? c : none);
+      }
     }
   for (int o = 1; o < per; o <<= 1) {
     const F x2 = __shfl_xor_sync(0xffffffffu, x, o), y2 = __shfl_xor_sync(0xffffffffu, y, o);
     merge_two(x, y, x2, y2);
   }
-  __syncwarp();
   F value = a.group_top == 2 ? x + y : x;
   if (value != value) value = none;  // infinities of both signs
   const F sizes = a.group_top == 2 ? fabs(x) + fabs(y) : fabs(x);
   const int from = (lane * per) & 31;
   *size = __shfl_sync(0xffffffffu, sizes, from);
+  *least = __shfl_sync(0xffffffffu, a.group_top == 2 ? y : x, from);
   return __shfl_sync(0xffffffffu, value, from);
 }
 
-// The groups kept, one bit each.  `apart`: whether the last one in and the first one out are further apart than they can
-// be wrong: `tol`, and 2^-21 of the magnitudes that they are made of.
+// The groups kept, one bit each.  `near`: the groups, if any, that may be on either side of the border: the last one in
+// and the first one out are no further apart than they can be wrong (`tol`, and 2^-21 of the magnitudes that they are made
+// of), and these are within twice that.
 template <class F>
-__device__ __forceinline__ unsigned best_groups(const RouteArgs& a, F mine, F size, F tol, bool* apart) {
+__device__ __forceinline__ unsigned best_groups(const RouteArgs& a, F mine, F size, F tol, unsigned* near) {
   const int lane = threadIdx.x & 31;
   int rank = 0;
   for (int g = 0; g < a.groups; ++g) {
@@ -195,30 +211,33 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs& a, F mine, F si
   const bool in = lane < a.groups && rank < a.top_groups;
   const int l = __ffs(__ballot_sync(0xffffffffu, lane < a.groups && rank == a.top_groups - 1)) - 1;
   const int n = __ffs(__ballot_sync(0xffffffffu, lane < a.groups && rank == a.top_groups)) - 1;
-  const F gap = __shfl_sync(0xffffffffu, mine, l) - __shfl_sync(0xffffffffu, mine, n);
+  const F last = __shfl_sync(0xffffffffu, mine, l), gap = last - __shfl_sync(0xffffffffu, mine, n);
   const F sizes = __shfl_sync(0xffffffffu, size, l) + __shfl_sync(0xffffffffu, size, n);
-  *apart = gap > tol + sizes * F(0x1p-21);
+  const F can = tol + sizes * F(0x1p-21);
+  *near = gap > can ? 0u : __ballot_sync(0xffffffffu, lane < a.groups && !(fabs(mine - last) > 2 * can));
   return __ballot_sync(0xffffffffu, in);
 }
 
-// The groups of the lane's experts, a byte each; none (32 and more) beyond E.
+// The groups of the lane's experts, a byte each, and which of them there are, a bit each.
 template <int V>
 struct LaneGroups {
-  uint32_t w[(V + 3) / 4];
-  __device__ __forceinline__ explicit LaneGroups(const RouteArgs& a) {
+  uint32_t w[(V + 3) / 4], all;
+  __device__ __forceinline__ explicit LaneGroups(const RouteArgs& a) : all(0) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < (V + 3) / 4; ++i) w[i] = 0x20202020u;
+    for (int i = 0; i < (V + 3) / 4; ++i) w[i] = 0u;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = lane + 32 * i;
-      if (e < a.E) w[i / 4] ^= (uint32_t)(e / a.group_size | 0x20) << (8 * (i % 4));
+      if (e < a.E) w[i / 4] |= (uint32_t)(e / a.group_size) << (8 * (i % 4)), all |= 1u << i;
     }
   }
-  // whether expert i's group has its bit set
-  __device__ __forceinline__ bool in(int i, unsigned groups) const {
-    const unsigned g = (w[i / 4] >> (8 * (i % 4))) & 0xFFu;
-    return g < 32 && ((groups >> (g & 31)) & 1u);
+  // those whose group has its bit set
+  __device__ __forceinline__ unsigned among(unsigned groups) const {
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m |= ((groups >> ((w[i / 4] >> (8 * (i % 4))) & 31u)) & 1u) << i;
+    return m & all;
   }
 };
 
@@ -234,113 +253,194 @@ __device__ __forceinline__ unsigned long long double_key(double v) {
   return b >> 63 ? ~b : b | (1ull << 63);
 }
 
-// Choice by rounds, keys as above (0: not eligible): for tokens with more candidates than lanes.  Lane j gets the j-th.
-template <int V>
-__device__ __noinline__ void choose_by_rounds(const RouteArgs& a, const unsigned long long (&key)[V], int* id) {
+// The softmax's sum in 64 bits.
+__device__ __noinline__ Softmax<double> softmax_64(const RouteArgs& a, int t, const Softmax<float>& sm) {
+  Softmax<double> r{sm.top, 0.0, sm.infinities};
+  if (!a.score && fabsf(sm.top) != INFINITY) {
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+      const float l = load_logit(a.logits, a.bf16, (size_t)t * a.ld + e);
+      if (l == l) r.sum += exp((double)l - (double)sm.top);
+    }
+    r.sum = warp_sum(r.sum);
+  }
+  return r;
+}
+
+// The choice in 64 bits, for the tokens that the fast way leaves open.  Small loops over shared memory (row [E]) on
+// purpose: its code is cold, and unrolled over the lane's experts its first use took 20 us, which such a token's CTA
+// then took longer than the others.
+__device__ __noinline__ void choose_64(const RouteArgs& a, int t, double* row, int* id) {
   const int lane = threadIdx.x & 31;
-  unsigned gone = 0;
+  const double nan = __longlong_as_double(0x7FF8000000000000ll);
+  const size_t at = (size_t)t * a.ld;
+  const bool limited = a.top_groups < a.groups, sums = limited && a.group_top == 2;
+  Softmax<float> top{-INFINITY, 0.f, 0};
+  if (!a.score) {
+    int n = 0;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32) {
+      const float l = load_logit(a.logits, a.bf16, at + e);
+      top.top = fmaxf(top.top, l);
+      n += l == INFINITY;
+    }
+    top.top = warp_max(top.top);
+    top.infinities = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  }
+  const Softmax<double> sm = softmax_64(a, t, top);
+  __syncwarp();
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 32) {
+    const float l = load_logit(a.logits, a.bf16, at + e);
+    double c = l;
+    if (a.bias || sums) c = score_of<double>(l, a.score, sm, a.E) + (a.bias ? (double)a.bias[e] : 0.0);
+    row[e] = l == l ? c : nan;
+  }
+  __syncwarp();
+  unsigned groups = ~0u;
+  if (limited) {
+    double size, least;
+    unsigned near;
+    const double mine = group_value<double>(a, row, &size, &least);
+    groups = best_groups<double>(a, mine, size, 0.0, &near);
+  }
+  unsigned open = 0;
+#pragma unroll 1
+  for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
+    if (!limited || ((groups >> (e / a.group_size)) & 1u)) open |= 1u << i;
+    if (!a.bias && sums) row[e] = load_logit(a.logits, a.bf16, at + e);
+  }
   for (int j = 0; j < a.k; ++j) {
     unsigned long long best = 0;
     int e = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!((gone >> i) & 1u) && key[i] > best) best = key[i], e = lane + 32 * i;
+#pragma unroll 1
+    for (int i = 0; open >> i; ++i)
+      if ((open >> i) & 1u) {
+        const unsigned long long key = double_key(row[lane + 32 * i]) + 1ull;
+        if (key > best) best = key, e = lane + 32 * i;
+      }
+    __syncwarp();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long b2 = __shfl_xor_sync(0xffffffffu, best, o);
       const int e2 = __shfl_xor_sync(0xffffffffu, e, o);
       if (b2 > best || (b2 == best && e2 < e)) best = b2, e = e2;
     }
-    if ((e & 31) == lane) gone |= 1u << (e >> 5);
+    if ((e & 31) == lane) open &= ~(1u << (e >> 5));
     if (lane == j) *id = e;
   }
 }
 
-// The choice from scores in 64 bits: groups, if any, and experts.
-template <int V>
-__device__ __noinline__ void choose_64(const RouteArgs& a, const float (&l)[V], double* row, int* id) {
-  const LaneGroups<V> of(a);
+// The groups kept, where those in `near` are too close for FP32: row [E] holds the experts' FP32 c as doubles, and those
+// of these groups that may count in their group's value, at least `bound`, are evaluated in 64 bits, one a lane.  False
+// where they are more than lanes.
+__device__ __noinline__ bool groups_64(const RouteArgs& a, int t, const Softmax<float>& sm, unsigned near, float bound,
+                                       RouteScratch& s, double* row, unsigned* groups) {
   const int lane = threadIdx.x & 31;
-  Softmax<double> sm{0.f, 0.0, 0};
-  if (!a.score) sm = softmax_of<double>(l);
-  double c[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    c[i] = score_of<double>(l[i], a.score, sm, a.E);
-    if (a.bias && lane + 32 * i < a.E) c[i] += (double)a.bias[lane + 32 * i];
-    if (l[i] != l[i]) c[i] = __longlong_as_double(0x7FF8000000000000ll);
+  int n = 0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    const bool in = e < a.E && ((near >> (e / a.group_size)) & 1u) && row[e] >= (double)bound;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    const int at = n + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) s.id[at] = e;
+    n += __popc(who);
   }
-  unsigned groups = ~0u;
-  if (a.top_groups < a.groups) {
-    bool apart;
-    double rated[V], size = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) rated[i] = a.bias || a.group_top == 2 ? c[i] : (double)l[i];
-    const double mine = group_value<double>(a, rated, row, &size);
-    groups = best_groups<double>(a, mine, size, 0.0, &apart);
+  __syncwarp();
+  if (n > 32) return false;
+  const Softmax<double> sm64 = softmax_64(a, t, sm);
+  if (lane < n) {
+    const int e = s.id[lane];
+    row[e] = score_of<double>(load_logit(a.logits, a.bf16, (size_t)t * a.ld + e), a.score, sm64, a.E) + (a.bias ? (double)a.bias[e] : 0.0);
   }
-  unsigned long long key[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = of.in(i, groups) ? double_key(a.bias ? c[i] : (double)l[i]) + 1ull : 0ull;
-  choose_by_rounds<V>(a, key, id);
+  __syncwarp();
+  double size, least;
+  unsigned still;
+  const double mine = group_value<double>(a, row, &size, &least);
+  *groups = best_groups<double>(a, mine, size, 0.0, &still);
+  return true;
 }
 
-// Token t's choice: lane j < k gets its j-th expert and weight.  row: the warp's [E] doubles, where there are groups.
+// Token t's choice: lane j < k gets its j-th expert and weight.  row: the warp's [E] doubles; bias [32 V], in shared memory.
 template <int V>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int t, const LaneGroups<V>& of, RouteScratch& s, double* row,
-                                            int* id, float* weight) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, const float (&l)[V], const LaneGroups<V>& of, const float* bias, RouteScratch& s,
+                                            double* row, int* id, float* weight) {
   const int lane = threadIdx.x & 31;
-  float l[V];
-  load_lane<V>(a, t, l);
-  bool odd = false;
+  float all = 0.f;  // NaN where one is (or infinities of both signs)
 #pragma unroll
-  for (int i = 0; i < V; ++i) odd |= lane + 32 * i < a.E && l[i] != l[i];
-  odd = __any_sync(0xffffffffu, odd);
+  for (int i = 0; i < V; ++i) all += l[i];
+  const bool odd = __any_sync(0xffffffffu, all != all);
   if (odd) {
     int nan = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) nan += lane + 32 * i < a.E && l[i] != l[i];
     nan = (int)__reduce_add_sync(0xffffffffu, (unsigned)nan);
-    if (lane == 0) atomicAdd(&a.st->nan_logits, (unsigned)nan);
+    if (nan && lane == 0) atomicAdd(&a.st->nan_logits, (unsigned)nan);
   }
   const bool limited = a.top_groups < a.groups, sums = limited && a.group_top == 2;
   Softmax<float> sm{0.f, 0.f, 0};
   if (!a.score && (a.bias || sums || !a.renorm)) sm = softmax_of<float>(l);
-  float tol = -1.f, c[V];
-  if (a.bias || sums) {
-    // by the hardware's 2^x and 1/x: a sigmoid is off by up to 2^-23 (3 + 1.2 |l|) of itself, a softmax by 2^-19 of the
-    // largest, l = log of it at most; tol covers two of them
-    float most = 0.f;
-    const bool plain = a.score || (sm.top != INFINITY && sm.top != -INFINITY);
-    const float inv = a.score ? 1.0f : __fdividef(1.0f, sm.sum);
+  float tol = -1.f, c[V];  // NaN where the logit is
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float x;
-      if (plain) x = a.score ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - sm.top) * inv;
-      else x = score_of<float>(l[i], 0, sm, a.E);
-      most = fmaxf(most, x);  // drops NaNs
-      c[i] = a.bias && lane + 32 * i < a.E ? x + __ldg(a.bias + lane + 32 * i) : x;
-      if (l[i] != l[i]) c[i] = l[i];
+  for (int i = 0; i < V; ++i) c[i] = l[i] + 0.0f;  // no negative zero
+  if (a.bias || sums) {
+    // By the hardware's 2^x (2^-22, and half a step of x) and 1/x (a step).  A sigmoid s is off by 2^-24 (7 + 1.5 |l|) s at
+    // most for l < 0, and by less than 2^-24 6 for l > 0, so by 2^-24 (7 - 1.5 log s) s for the largest s; a softmax, whose
+    // sum of E terms counts too, by 2^-24 43 of the largest.  tol covers two.
+    if (a.score) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = sigmoid_fast(c[i]);
+    } else if (sm.top != INFINITY && sm.top != -INFINITY) {
+      const float inv = __fdividef(1.0f, sm.sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = __expf(c[i] - sm.top) * inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = l[i] == l[i] ? score_of<float>(l[i], 0, sm, a.E) : l[i];
     }
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) most = fmaxf(most, c[i]);  // drops NaNs
     most = warp_max(most);
-    tol = most * 0x1p-17f * fmaxf(1.0f, __logf(most) * -0x1p-4f);
+    tol = most * (a.score ? 0x1p-23f * (8.0f - 1.5f * __logf(most)) : 0x1p-17f);
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] += bias[lane + 32 * i];
+    }
   }
-  unsigned groups = ~0u;
+  unsigned open = of.all;
   bool exact = true;  // the groups are certain
   if (limited) {
-    float rated[V], size = 0.f;
+    float size, least, *r = reinterpret_cast<float*>(row);
 #pragma unroll
-    for (int i = 0; i < V; ++i) rated[i] = a.bias || sums ? c[i] : l[i];
-    const float mine = group_value<float>(a, rated, reinterpret_cast<float*>(row), &size);
-    bool far;
-    groups = best_groups<float>(a, mine, size, tol < 0.f ? 0.f : 2.0f * tol, &far);
-    exact = far || tol < 0.f;  // logits are exact
+    for (int i = 0; i < V; ++i)
+      if (lane + 32 * i < a.E) r[lane + 32 * i] = c[i];
+    __syncwarp();
+    const float mine = group_value<float>(a, r, &size, &least);
+    unsigned near, groups = best_groups<float>(a, mine, size, tol < 0.f ? 0.f : 2.0f * tol, &near);
+    __syncwarp();
+    if (near && tol >= 0.f) {  // (logits are exact)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i];
+      __syncwarp();
+      const float low = -warp_max((near >> lane) & 1u ? -least : -INFINITY);
+      exact = groups_64(a, t, sm, near, low - 2.0f * (tol + fabsf(low) * 0x1p-22f), s, row, &groups);
+      __syncwarp();
+    }
+    open = of.among(groups);
   }
   const bool close = a.bias != nullptr;  // the keys are of FP32 scores: look at the gaps
-  uint32_t key[V], m = 0;
+  if (!close && sums) {  // the groups were of scores, the experts are of logits
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = l[i] + 0.0f;
+  }
+  uint32_t key[V], m = 0;  // order keys: 0 not eligible, 1 NaN
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    key[i] = of.in(i, groups) ? max(float_key(a.bias ? c[i] : l[i]), 1u) : 0u;
+    const uint32_t b = __float_as_uint(c[i]), k = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+    key[i] = (open >> i) & 1u ? (c[i] == c[i] ? k : 1u) : 0u;
     m = max(m, key[i]);
   }
   // the bound: the (k + 1)-th largest of the lanes' maxima, less what two scores can be wrong
@@ -383,8 +483,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, const Lan
       apart = __all_sync(0xffffffffu, lane >= a.k || lane + 1 >= n || u - v > tol + (fabsf(u) + fabsf(v)) * 0x1p-22f);
     }
     if (!apart) {  // again in 64 bits, of the candidates
-      Softmax<double> sm64{0.f, 0.0, 0};
-      if (!a.score) sm64 = softmax_of<double>(l);
+      const Softmax<double> sm64 = softmax_64(a, t, sm);
       unsigned long long k64 = 0;
       if (lane < n) {
         const float x = load_logit(a.logits, a.bf16, (size_t)t * a.ld + e);
@@ -399,19 +498,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, const Lan
     if (lane < n) s.id[rank] = e;
     __syncwarp();
     if (lane < a.k) *id = s.id[lane];
-  } else {  // (copies, so that the arrays above stay in registers)
+  } else {
     int e = 0;
-    if (exact && !close) {
-      unsigned long long key2[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) key2[i] = key[i];
-      choose_by_rounds<V>(a, key2, &e);
-    } else {
-      float l2[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) l2[i] = l[i];
-      choose_64<V>(a, l2, row, &e);
-    }
+    choose_64(a, t, row, &e);
     if (lane < a.k) *id = e;
   }
   __syncwarp();  // the scratch is free again
@@ -441,23 +530,31 @@ __device__ __forceinline__ int rows_before(const uint32_t* bits, int words, int 
 // kAll: the only run, tables included.
 template <int V, bool kAll>
 __global__ void __launch_bounds__(rt::kThreads) route_choose_kernel(RouteArgs a) {
-  extern __shared__ double rows_mem[];  // where there are groups: [warps][E]; then bits [E][words]
+  extern __shared__ double rows_mem[];  // [warps][E], then bits [E][words]
   __shared__ int scan[32], base[rt::kMaxExperts];
+  __shared__ float bias[32 * V];
   __shared__ RouteScratch scratch[rt::kThreads / 32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double* row = rows_mem + warp * a.E;
-  uint32_t* bits = reinterpret_cast<uint32_t*>(rows_mem + (a.top_groups < a.groups ? (blockDim.x >> 5) * a.E : 0));
+  uint32_t* bits = reinterpret_cast<uint32_t*>(rows_mem + (blockDim.x >> 5) * a.E);
   int t0, t1;
   run_of(a, blockIdx.x, t0, t1);
-  for (int i = threadIdx.x; i < a.E * a.words; i += blockDim.x) bits[i] = 0u;
-  __syncthreads();
   const LaneGroups<V> of(a);
-  for (int t = t0 + warp; t < t1; t += blockDim.x >> 5) {
+  for (int i = threadIdx.x; i < a.E * a.words; i += blockDim.x) bits[i] = 0u;
+  for (int i = threadIdx.x; i < 32 * V; i += blockDim.x) bias[i] = a.bias && i < a.E ? a.bias[i] : 0.f;
+  __syncthreads();
+  const int step = blockDim.x >> 5;
+  float next[V];
+  if (t0 + warp < t1) load_lane<V>(a, t0 + warp, next);
+  for (int t = t0 + warp; t < t1; t += step) {
     int id = 0;
-    float w;
-    route_token<V>(a, t, of, scratch[warp], row, &id, &w);
+    float w, l[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = next[i];
+    if (t + step < t1) load_lane<V>(a, t + step, next);
+    route_token<V>(a, t, l, of, bias, scratch[warp], row, &id, &w);
     if (lane < a.k) {
       a.ids[(size_t)t * a.k + lane] = id;
       a.weights[(size_t)t * a.k + lane] = w;
@@ -662,12 +759,28 @@ static RouteKernels kernels_of(int E) {
                     : kernels_for<16>();
 }
 
+static cudaError_t set_route_attrs() {  // once per device
+  constexpr int kCached = 64;
+  static std::mutex mu;
+  static bool done[kCached] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < kCached && done[dev]) return cudaSuccess;
+  for (int E = 32; E <= rt::kMaxExperts && e == cudaSuccess; E *= 2) {
+    const RouteKernels f = kernels_of(E);
+    for (const RouteKernel k : {f.all, f.choose})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMostShared);
+  }
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute((const void*)route_scatter_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMostShared);
+  if (e == cudaSuccess && dev >= 0 && dev < kCached) done[dev] = true;
+  return e;
+}
+
 static cudaError_t launch(RouteKernel f, int grid, int threads, size_t smem, const RouteArgs& a, cudaStream_t st,
                           int cluster = 1) {
-  if (smem > 24576) {
-    const cudaError_t e = cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, rt::kMostShared);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
   cudaLaunchAttribute at[2]{};
@@ -680,6 +793,8 @@ static cudaError_t launch(RouteKernel f, int grid, int threads, size_t smem, con
 }
 
 cudaError_t launch_route_forward(const RouteOp& p, cudaStream_t st) {
+  cudaError_t e = set_route_attrs();
+  if (e != cudaSuccess) return e;
   RouteArgs a = args_of(p);
   const RouteKernels f = kernels_of(a.E);
   // Runs: a CTA each, none with fewer tokens than hold its counts in `inv`
@@ -690,9 +805,9 @@ cudaError_t launch_route_forward(const RouteOp& p, cudaStream_t st) {
   // warps: one a token up to all of them, and threads enough for an expert each
   const int threads = std::min(rt::kThreads, std::max((a.E + 31) / 32, (a.T + a.runs - 1) / a.runs) * 32);
   const size_t bits = sizeof(uint32_t) * a.E * a.words;
-  const size_t smem = bits + (a.top_groups < a.groups ? sizeof(double) * a.E * (threads / 32) : 0);
+  const size_t smem = bits + sizeof(double) * a.E * (threads / 32);
   if (a.runs == 1) return launch(f.all, 1, threads, smem, a, st);
-  cudaError_t e = launch(f.choose, a.runs, threads, smem, a, st);
+  e = launch(f.choose, a.runs, threads, smem, a, st);
   if (e == cudaSuccess) e = launch(route_scan_kernel, rt::kScanCtas, rt::kScanThreads, 0, a, st, rt::kScanCtas);
   if (e == cudaSuccess) e = launch(route_scatter_rows_kernel, a.runs, rt::kThreads, bits, a, st);
   return e;
