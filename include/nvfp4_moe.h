@@ -734,7 +734,9 @@ typedef struct nvfp4_int8_config {
 } nvfp4_int8_config;
 
 /* Allocate an INT8 handle: the packed matrix (N*K bytes, both rounded up to
- * multiples of 128) on config->device.  Synchronous.  *out is NULL on failure. */
+ * multiples of 128) and, for max_tokens above 64, a workspace that holds as many
+ * tokens in FP16 (256 MB at most) on config->device.  Synchronous.  *out is NULL on
+ * failure. */
 nvfp4_moe_status nvfp4_int8_create(const nvfp4_int8_config* config, nvfp4_moe_t* out);
 
 /* Copy the matrix into the handle's device layout.  DEVICE inputs:
@@ -758,10 +760,12 @@ nvfp4_moe_status nvfp4_int8_quantize(nvfp4_moe_t h, int T, const void* x, int x_
 /* out [T][N] as above, 0 <= T <= max_tokens; x [T][K] int8 and out DEVICE, 16-byte
  * aligned, rows ldx / ldo elements apart (at least the row length, ldx a multiple
  * of 16 and ldo of 8, at most 2^24), not overlapping; x_scale [T] float, whose NaNs
- * and infinities reach their row.  Enqueued on `stream`; no host synchronisation,
- * no allocation and no workspace: calls on one handle may overlap and be captured
- * (above 16 tokens the tensor descriptor over x is encoded on the host, so a
- * captured graph replays with the pointers it was captured with). */
+ * and infinities reach their row.  Enqueued on `stream`; no host synchronisation
+ * and no allocation; calls may be captured (above 16 tokens the tensor descriptor
+ * over x is encoded on the host, so a captured graph replays with the pointers it
+ * was captured with).  Up to 64 tokens calls on one handle may overlap.  Above,
+ * they use its workspace: serialise those on one stream, captured ones too (graphs
+ * that may run at the same time need a handle each). */
 nvfp4_moe_status nvfp4_int8_forward(nvfp4_moe_t h, int T, const int8_t* x, int64_t ldx, const float* x_scale, void* out,
                                     int64_t ldo, cudaStream_t stream);
 

@@ -15,20 +15,6 @@ using namespace nvfp4moe;
 
 namespace {
 
-// 2D BF16 [rows][cols], rows ld elements apart (0: cols), box = 64 columns x box_rows rows, 128B swizzle.
-bool encode_rows_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 16,
-                     uint64_t ld = 0) {
-  EncodeTiledFn fn = get_encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {(ld ? ld : cols) * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct Carver {
   size_t off = 0;
   std::vector<std::pair<void**, size_t>> items;
@@ -309,6 +295,7 @@ void nvfp4_moe_destroy(nvfp4_moe_t h) {
     if (h->gs_eff) cudaFree(h->gs_eff);
     if (h->hbound) cudaFree(h->hbound);
     if (h->ws_mem) cudaFree(h->ws_mem);
+    if (h->ws_mem2) cudaFree(h->ws_mem2);
     cudaGetLastError();
   }
   delete h;

@@ -277,6 +277,15 @@ nvfp4_moe_status nvfp4_int8_create(const nvfp4_int8_config* c, nvfp4_moe_t* out)
                                             2 * c->out_features, &h);
   if (s != NVFP4_MOE_OK) return s;
   h->i8 = *c;
+  const size_t bytes = int8_workspace_bytes(c->in_features, c->max_tokens);
+  if (bytes) {
+    DeviceGuard g(c->device);
+    if (cudaMalloc(&h->ws_mem2, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      nvfp4_moe_destroy(h);
+      return NVFP4_MOE_ERR_WORKSPACE;
+    }
+  }
   *out = h;
   return NVFP4_MOE_OK;
 }
@@ -352,19 +361,28 @@ nvfp4_moe_status nvfp4_int8_forward(nvfp4_moe_t h, int T, const int8_t* x, int64
   p.out_type = h->i8.out_dtype;
   p.once = h->product_bytes > h->l2_bytes;
   p.num_sms = h->num_sms, p.status = h->ws.status, p.fault = h->fault;
-  const bool few = T <= kDecodeMaxTokens;
-  Int8Tiling t{};
-  CUtensorMap map{};
-  if (!few) {
-    t = int8_tiling(N, K, T, h->num_sms);
-    if (!encode_bytes_map(&map, x, (uint64_t)T, (uint64_t)K, (uint32_t)t.box, (uint64_t)ldx))
-      return bad(h, NVFP4_MOE_ERR_CUDA, what, "cuTensorMapEncodeTiled failed");
-  }
   cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
   const nvfp4_moe_status s = take_events(h, ev);
   if (s != NVFP4_MOE_OK) return s;
   record(ev, 0, 2, st);
-  const cudaError_t e = few ? launch_int8_gemv(p, st) : launch_int8_gemm(p, t, map, st);
+  cudaError_t e = cudaSuccess;
+  if (T <= kDecodeMaxTokens) {
+    e = launch_int8_gemv(p, st);
+  } else {
+    const int chunk = int8_chunk_tokens(K), Kp = (K + 127) / 128 * 128, size = p.out_type == NVFP4_MOE_OUT_F32 ? 4 : 2;
+    for (int t0 = 0; t0 < T && e == cudaSuccess; t0 += chunk) {
+      p.T = T - t0 < chunk ? T - t0 : chunk;
+      p.x = x + t0 * ldx, p.x_scale = x_scale + t0, p.out = static_cast<uint8_t*>(out) + t0 * ldo * size;
+      const Int8Tiling t = int8_tiling(N, K, p.T, h->num_sms);
+      CUtensorMap map{};
+      if (t.fp16) e = launch_int8_tokens(p, h->ws_mem2, st);
+      if (e != cudaSuccess) break;
+      if (!(t.fp16 ? encode_rows_map(&map, h->ws_mem2, (uint64_t)p.T, (uint64_t)Kp, (uint32_t)t.box)
+                   : encode_bytes_map(&map, p.x, (uint64_t)p.T, (uint64_t)K, (uint32_t)t.box, (uint64_t)ldx)))
+        return bad(h, NVFP4_MOE_ERR_CUDA, what, "cuTensorMapEncodeTiled failed");
+      e = launch_int8_gemm(p, t, map, st);
+    }
+  }
   if (e != cudaSuccess) return cuda_fail(h, e, what);
   record(ev, 3, 4, st);
   return NVFP4_MOE_OK;

@@ -49,6 +49,7 @@ struct nvfp4_moe {
   uint8_t* blob = nullptr;
   float* gscale = nullptr;
   void* ws_mem = nullptr;
+  void* ws_mem2 = nullptr;     // INT8: tokens in FP16
   size_t ws_bytes = 0;
   nvfp4moe::Workspace ws{};
   nvfp4moe::PrefillMaps maps{};
@@ -102,6 +103,20 @@ inline EncodeTiledFn get_encode_fn() {
       fn = reinterpret_cast<EncodeTiledFn>(p);
   }
   return fn;
+}
+
+// 2D 16-bit [rows][cols], rows ld elements apart (0: cols), box = 64 columns x box_rows rows, 128B swizzle.
+inline bool encode_rows_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 16,
+                     uint64_t ld = 0) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {(ld ? ld : cols) * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // 2D bytes [rows][cols], rows ld apart, box = 128 columns x box_rows rows, 128B swizzle.

@@ -257,44 +257,56 @@ __global__ void __launch_bounds__(i8v::kThreads, 1) int8_gemv_kernel(Int8Args a)
 // --------------------------------------------------------------------------------------------------------------------
 // More tokens: a persistent tcgen05 GEMM, the matrix as the M operand and the tokens as the N operand.
 //
-// Both operands are converted on the way, by four warps: a square's rows into tensor memory (a thread its own lane), the
-// tokens into 128B-swizzled shared memory.  kCtas = 2: a pair of CTAs on 256 features, each with half of the tile's tokens.
+// The matrix is converted on the way, a square's rows into tensor memory, a thread its own lane.  Up to 64 tokens so are
+// the tokens, into 128B-swizzled shared memory; more are written as FP16 to the handle's workspace by a kernel of its own
+// first and come by TMA: converted again for every 256 features, by whichever warps, they were what the MMAs waited for
+// (16384 tokens of 12576 x 4096 1286 us).
 //
-// What this comes down to is shared memory's bandwidth, 128 bytes a cycle.  For 64 elements of the reduction a pair's CTA
-// with 192 tokens moves 8 KB of the matrix in and out, 6 KB of tokens in and out, and 12 KB of converted ones in and out:
-// 416 cycles, next to 384 of MMAs.  192 tokens, and not 256, because tensor memory then holds two sets of sums (384
-// columns) beside four stages of the matrix (128): the sums go to registers every 1024 elements, to stay exact, and that
-// passes under the next 1024's MMAs.
+// kCtas = 2: a pair of CTAs on 256 features, each with half of the tile's tokens.  192 tokens, and not 256, because tensor
+// memory then holds two sets of sums (384 columns) beside four stages of the matrix (128): the sums go to registers every
+// 1024 elements, to stay exact, and that passes under the next 1024's MMAs.
+//
+// A warp takes some 370 cycles for its 32 rows of 64 elements, most of it waiting, and the MMAs of 192 tokens 384.  With
+// fewer tokens, where the matrix's bytes are what there is to wait for, two teams of four warps take turns.
 //
 // kSplit: where there are few units, a cluster of CTAs takes one, a share of the reduction each, and adds the integers
 // through distributed shared memory.
 // --------------------------------------------------------------------------------------------------------------------
 namespace i8g {
-constexpr int kThreads = 448;                      // 4 converters, 8 epilogue, producer, MMA issuer
-constexpr int kConvWarps = 4, kEpiWarps = 8, kProducer = 12, kIssuer = 13;
+constexpr int kEpiWarps = 8;
 constexpr int kCtlBytes = 2048, kEpiBytes = 2048;  // per epilogue warp
 constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
 constexpr int kRoom = i8::kSmemMax - 1024 - kRingOff;
 constexpr int kSegment = 16;                       // 64-long steps whose sums FP32 holds exactly
+constexpr int kStagesA = 4;                        // of the matrix, 64 elements each: 32 columns of tensor memory
 constexpr int kMaxStages = 8, kMaxRaw = 8, kMaxSplit = 8;
 
 template <int kCtas, int kTile>
 struct Plan {
+  static constexpr bool kPre = kTile > 64;                   // tokens come in FP16
+  static constexpr int kTeams = kTile == 192 ? 1 : 2;        // of four warps that convert the matrix
+  static constexpr int kTokenWarps = kPre ? 0 : 4;           // that convert tokens, half of them a team
+  // warps: converters of the matrix, epilogue, converters of tokens, matrix producer, token producer, MMA issuer
+  static constexpr int kRowWarps = 4 * kTeams, kToken0 = kRowWarps + kEpiWarps, kProducer = kToken0 + kTokenWarps;
+  static constexpr int kTokens = kProducer + 1, kIssuer = kTokens + 1, kThreads = 32 * (kIssuer + 1);
   static constexpr int kShare = kTile / kCtas;               // tokens of a CTA
   static constexpr int kBBytes = kShare * 128;               // a stage of them, 64 elements in FP16
-  static constexpr int kXBytes = kShare * 128;               // a raw slot, 128 elements in bytes
-  static constexpr int kStages = kTile == 64 ? 6 : kTile == 128 ? 5 : 4;
-  static constexpr int kRaw = kTile == 64 ? 6 : kTile == 128 ? 4 : 5;  // slots of both raw rings
-  static constexpr uint32_t kOperand = 2 * kTile;            // its first column in tensor memory
-  static constexpr int kRings = kStages * kBBytes + kRaw * (kXBytes + i8::kSquare);
-  static_assert(kRings <= kRoom && kRaw <= kMaxRaw && kStages <= kMaxStages && 2 * kTile + 32 * kStages <= 512, "rings");
+  static constexpr int kXBytes = kPre ? 0 : kShare * 128;    // a raw slot of them, 128 elements in bytes
+  static constexpr int kStagesB = kTile == 192 ? 8 : kTile == 128 ? 6 : kStagesA;
+  static constexpr int kRaw = 6;                             // raw slots, squares
+  static constexpr uint32_t kOperand = 2 * kTile;            // the matrix's first column in tensor memory
+  static constexpr int kRings = kStagesB * kBBytes + kRaw * (kXBytes + i8::kSquare);
+  static_assert(kRings <= kRoom && kRaw <= kMaxRaw && kStagesB <= kMaxStages && 2 * kTile + 32 * kStagesA <= 512, "rings");
   static_assert(kBBytes % 1024 == 0, "128B-swizzled tiles");
+  // a team meets every slot of a ring again itself: a parity wait must not run two phases ahead of its barrier
+  static_assert(kRaw % kTeams == 0 && kStagesA % (2 * kTeams) == 0, "teams");
 };
 }  // namespace i8g
 
 struct Int8Ctl {
-  uint64_t raw_full[i8g::kMaxRaw], raw_empty[i8g::kMaxRaw];      // a square and its tokens
-  uint64_t full[i8g::kMaxStages], empty[i8g::kMaxStages];        // converted stages
+  uint64_t raw_full[i8g::kMaxRaw], raw_empty[i8g::kMaxRaw];      // a square (and its tokens' bytes)
+  uint64_t a_full[i8g::kStagesA], a_empty[i8g::kStagesA];        // converted stages (and their tokens)
+  uint64_t b_full[i8g::kMaxStages], b_empty[i8g::kMaxStages];    // tokens in FP16
   uint64_t acc_full[2], acc_empty[2], mma_done;
   uint32_t tmem;
   int abort_flag;
@@ -302,14 +314,14 @@ struct Int8Ctl {
 static_assert(sizeof(Int8Ctl) <= i8g::kCtlBytes, "control block");
 
 template <int kCtas, int kTile, bool kSplit>
-__global__ void __launch_bounds__(i8g::kThreads, 1)
+__global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap x_map, Int8Args a) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   Int8Ctl& ctl = *reinterpret_cast<Int8Ctl*>(smem);
   using Plan = i8g::Plan<kCtas, kTile>;
   uint8_t* ring_b = smem + i8g::kRingOff;
-  uint8_t* raw_x = ring_b + Plan::kStages * Plan::kBBytes;
+  uint8_t* raw_x = ring_b + Plan::kStagesB * Plan::kBBytes;
   uint8_t* raw_w = raw_x + Plan::kRaw * Plan::kXBytes;
   const uint32_t b_addr = smem_u32(ring_b), x_addr = smem_u32(raw_x), w_addr = smem_u32(raw_w);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -326,13 +338,18 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
   volatile int* abort_flag = &ctl.abort_flag;
 
   if (threadIdx.x == 0) {
+    constexpr int kConverters = 4 + Plan::kTokenWarps / Plan::kTeams;  // warps that convert a square
     for (int s = 0; s < Plan::kRaw; ++s) {
       mbar_init(ctl.raw_full + s, 1);
-      mbar_init(ctl.raw_empty + s, i8g::kConvWarps);
+      mbar_init(ctl.raw_empty + s, kConverters);
     }
-    for (int s = 0; s < Plan::kStages; ++s) {
-      mbar_init(ctl.full + s, kCtas * i8g::kConvWarps);  // waited for by the pair's first CTA
-      mbar_init(ctl.empty + s, 1);
+    for (int s = 0; s < i8g::kStagesA; ++s) {
+      mbar_init(ctl.a_full + s, kCtas * kConverters);  // waited for by the pair's first CTA
+      mbar_init(ctl.a_empty + s, 1);
+    }
+    for (int s = 0; s < Plan::kStagesB; ++s) {
+      mbar_init(ctl.b_full + s, 1);  // the same
+      mbar_init(ctl.b_empty + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(ctl.acc_full + b, 1);
@@ -342,7 +359,7 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
     ctl.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == i8g::kIssuer) {
+  if (warp == Plan::kIssuer) {
     if (kCtas == 2) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
                    "r"(512)
@@ -368,17 +385,16 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
   };
   const auto columns = [&](int tokens) { return (tokens + kRound - 1) & ~(kRound - 1); };
 
-  int acc[kTile / 2];  // epilogue: a feature's sums over half of the columns (kSplit: after the roles have met again)
+  int acc[kTile / 2];  // epilogue: a feature's sums over half of the columns (kSplit: until after the roles have met again)
 
-  if (warp == i8g::kProducer) {
-    // ---------------- the matrix's squares and the tokens that meet them ----------------
+  if (warp == Plan::kProducer) {
+    // ---------------- the matrix's squares, and the bytes of the tokens that meet them ----------------
     uint32_t it = 0;
     RingPos p;
     bool ok = true, waited = false;
     for (int u = first; u < total && ok && a.fault != 1; u += stride) {
       int row0;
-      const int share = columns(tokens_of(u, row0)) / kCtas;
-      row0 += rank * share;
+      tokens_of(u, row0);
       // the last pair of an odd number of blocks: the second CTA computes the first one's block again, unstored
       const int nb = min(u % a.NU * kCtas + rank, a.NB - 1);
       const uint8_t* src = a.packed + ((long long)nb * squares + sq0) * i8::kSquare;
@@ -392,19 +408,52 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
           bulk_g2s(raw_w + p.slot * i8::kSquare, src, i8::kSquare, ctl.raw_full + p.slot);
         }
         __syncwarp();
-        // the tokens may be the kernel before's, the matrix is not
-        if (!waited) grid_dependency_wait();
-        waited = true;
-        if (elect_one()) tma_2d(raw_x + p.slot * Plan::kXBytes, &x_map, s * 128, row0, ctl.raw_full + p.slot);
-        __syncwarp();
+        if constexpr (!Plan::kPre) {
+          // the tokens may be the kernel before's, the matrix is not
+          if (!waited) grid_dependency_wait();
+          waited = true;
+          if (elect_one()) tma_2d(raw_x + p.slot * Plan::kXBytes, &x_map, s * 128, row0, ctl.raw_full + p.slot);
+          __syncwarp();
+        }
       }
     }
     if (!ok && lane == 0) drain_copies(ctl.raw_full, it, Plan::kRaw);
-  } else if (warp == i8g::kIssuer) {
+  } else if (warp == Plan::kTokens) {
+    // ---------------- tokens in FP16: this CTA's half of the tile, 64 elements a stage ----------------
+    if constexpr (Plan::kPre) {
+      grid_dependency_wait();
+      uint32_t it = 0;
+      RingPos p;
+      bool ok = true;
+      for (int u = first; u < total && ok && a.fault != 1; u += stride) {
+        int row0;
+        const int share = columns(tokens_of(u, row0)) / kCtas;
+        row0 += rank * share;
+        for (int s = 2 * sq0; s < 2 * sq1; ++s, ++it, p.step(Plan::kStagesB)) {
+          if (!warp_wait(ctl.b_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 937)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            uint8_t* dst = ring_b + p.slot * Plan::kBBytes;
+            if (rank == 0) mbar_arrive_expect_tx(ctl.b_full + p.slot, (uint32_t)(kCtas * Plan::kBBytes));
+            if (kCtas == 2) tma_2d_pair(dst, &x_map, s * 64, row0, map_rank(ctl.b_full + p.slot, 0));
+            else tma_2d(dst, &x_map, s * 64, row0, ctl.b_full + p.slot);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) {
+        if (rank == 0) drain_copies(ctl.b_full, it, Plan::kStagesB);
+        else
+          for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // its copies complete on the first CTA's barriers
+      }
+    }
+  } else if (warp == Plan::kIssuer) {
     // ---------------- MMA issuer: the whole warp walks the loop, one lane issues ----------------
     if (rank == 0) {
       uint32_t j = 0;  // segments so far
-      RingPos p;
+      RingPos pa, pb;
       bool ok = true;
       for (int u = first; u < total && ok; u += stride) {
         int row0;
@@ -419,22 +468,27 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
           const uint32_t d = tmem + buf * kTile;
           const int end = min(s + i8g::kSegment, steps);
           uint32_t add = 0;
-          for (int i = s; i < end; ++i, p.step(Plan::kStages)) {
-            if (!warp_wait(ctl.full + p.slot, p.phase, abort_flag, a.st, 933)) {
+          for (int i = s; i < end; ++i, pa.step(i8g::kStagesA), pb.step(Plan::kStagesB)) {
+            if ((Plan::kPre && !warp_wait(ctl.b_full + pb.slot, pb.phase, abort_flag, a.st, 938)) ||
+                !warp_wait(ctl.a_full + pa.slot, pa.phase, abort_flag, a.st, 933)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t bd = sw128_desc(b_addr + (uint32_t)(p.slot * Plan::kBBytes));
-            const uint32_t at = tmem + Plan::kOperand + (uint32_t)p.slot * 32u;  // 8 columns per 16 elements
+            const uint64_t bd = sw128_desc(b_addr + (uint32_t)(pb.slot * Plan::kBBytes));
+            const uint32_t at = tmem + Plan::kOperand + (uint32_t)pa.slot * 32u;  // 8 columns per 16 elements
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
                 if (kCtas == 2) umma_ts_pair(d, at + 8u * kk, bd + 2u * kk, idesc, kk ? 1u : add);
                 else umma_ts(d, at + 8u * kk, bd + 2u * kk, idesc, kk ? 1u : add);
               }
-              if (kCtas == 2) umma_commit_pair(ctl.empty + p.slot);
-              else umma_commit(ctl.empty + p.slot);
+              if (kCtas == 2) umma_commit_pair(ctl.a_empty + pa.slot);
+              else umma_commit(ctl.a_empty + pa.slot);
+              if (Plan::kPre) {
+                if (kCtas == 2) umma_commit_pair(ctl.b_empty + pb.slot);
+                else umma_commit(ctl.b_empty + pb.slot);
+              }
             }
             add = 1;
             __syncwarp();
@@ -456,65 +510,77 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp < i8g::kConvWarps) {
-    // ---------------- converters: a raw slot makes two stages ----------------
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const uint32_t full0 = kCtas == 2 ? map_rank(ctl.full, 0) : 0u;  // the pair's first CTA's
+  } else if (warp < Plan::kRowWarps || warp >= Plan::kToken0) {
+    // ---------------- converters: a raw slot makes two stages; the teams take turns at the slots ----------------
+    const bool rows = warp < Plan::kRowWarps;
+    constexpr int kTeamTokens = Plan::kPre ? 1 : Plan::kTokenWarps / Plan::kTeams;  // a team's warps for tokens
+    constexpr int kOctets = Plan::kPre ? 1 : Plan::kShare / 8 / kTeamTokens;        // of 8 tokens, of one of them
+    const int team = rows ? warp / 4 : (warp - Plan::kToken0) / kTeamTokens;
+    const int w0 = rows ? warp % 4 : (warp - Plan::kToken0) % kTeamTokens;
+    const uint32_t lanes = (uint32_t)(32 * w0) << 16;
+    const uint32_t full0 = kCtas == 2 ? map_rank(ctl.a_full, 0) : 0u;  // the pair's first CTA's
+    const int all = first < total ? ((total - first - 1) / stride + 1) * (sq1 - sq0) : 0;  // squares of this CTA
     RingPos raw, p;
+    raw.slot = team;
+    p.slot = 2 * team;
     bool ok = true;
-    for (int u = first; u < total && ok; u += stride) {
-      for (int s = 0; s < steps && ok; s += 2, raw.step(Plan::kRaw)) {
-        if (!warp_wait(ctl.raw_full + raw.slot, raw.phase, abort_flag, a.st, 934)) {
-          ok = false;
-          break;
-        }
-        const uint32_t w_slot = w_addr + raw.slot * i8::kSquare + (uint32_t)(32 * warp + lane) * 16u;
-        const uint32_t x_slot = x_addr + raw.slot * Plan::kXBytes;
+    for (int n = team; n < all && ok; n += Plan::kTeams, raw.step(Plan::kRaw, Plan::kTeams)) {
+      if (!warp_wait(ctl.raw_full + raw.slot, raw.phase, abort_flag, a.st, 934)) break;
+      const uint32_t w_slot = w_addr + raw.slot * i8::kSquare + (uint32_t)(32 * w0 + lane) * 16u;
+      const uint32_t x_slot = x_addr + raw.slot * Plan::kXBytes;
 #pragma unroll
-        for (int h = 0; h < 2; ++h, p.step(Plan::kStages)) {
-          uint4 w[4];
+      for (int h = 0; h < 2; ++h, p.step(i8g::kStagesA)) {
+        if (rows) {
+          uint32_t v[4][8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = lds128(w_slot + (4 * h + i) * 2048);
-          if (!warp_wait(ctl.empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 935)) {
+          for (int i = 0; i < 4; ++i) bytes_to_f16(lds128(w_slot + (4 * h + i) * 2048), v[i]);
+          if (!warp_wait(ctl.a_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 935)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          // tokens: 8 rows of 16 elements a quarter of a warp; all lie in banks of their own, going in and coming out
-          const uint32_t st = b_addr + (uint32_t)(p.slot * Plan::kBBytes);
-          const int q = lane >> 3, m = lane & 7;
-#pragma unroll
-          for (int o = warp; o < Plan::kShare / 8; o += i8g::kConvWarps) {
-            const uint32_t row = (uint32_t)(8 * o + m) * 128u;
-            uint32_t v[8];
-            bytes_to_f16(biased(lds128(x_slot + row + (uint32_t)((4 * h + q) ^ m) * 16u)), v);
-            sts128(st + row + (uint32_t)((2 * q) ^ m) * 16u, v[0], v[1], v[2], v[3]);
-            sts128(st + row + (uint32_t)((2 * q + 1) ^ m) * 16u, v[4], v[5], v[6], v[7]);
-          }
-          uint32_t v[4][8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) bytes_to_f16(w[i], v[i]);
           tmem_st32(tmem + lanes + Plan::kOperand + (uint32_t)p.slot * 32u, v);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) {
-            if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + p.slot * 8);
-            else mbar_arrive(ctl.full + p.slot);
+        } else if constexpr (!Plan::kPre) {
+          // 8 tokens of 16 elements a quarter of a warp; all lie in banks of their own, going in and coming out.  All
+          // reads first: there is no other warp to hide what one takes
+          uint4 x[kOctets];
+          const int q = lane >> 3, m = lane & 7;
+#pragma unroll
+          for (int o = 0; o < kOctets; ++o)
+            x[o] = lds128(x_slot + (uint32_t)(8 * (w0 + kTeamTokens * o) + m) * 128u + (uint32_t)((4 * h + q) ^ m) * 16u);
+          if (!warp_wait(ctl.a_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 939)) {
+            ok = false;
+            break;
           }
+          const uint32_t st = b_addr + (uint32_t)(p.slot * Plan::kBBytes);
+#pragma unroll
+          for (int o = 0; o < kOctets; ++o) {
+            const uint32_t row = st + (uint32_t)(8 * (w0 + kTeamTokens * o) + m) * 128u;
+            uint32_t u[8];
+            bytes_to_f16(biased(x[o]), u);
+            sts128(row + (uint32_t)((2 * q) ^ m) * 16u, u[0], u[1], u[2], u[3]);
+            sts128(row + (uint32_t)((2 * q + 1) ^ m) * 16u, u[4], u[5], u[6], u[7]);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        if (!ok) break;
-        // what was read of the slot has been stored since
-        if (lane == 0) mbar_arrive(ctl.raw_empty + raw.slot);
+        __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + p.slot * 8);
+          else mbar_arrive(ctl.a_full + p.slot);
+        }
       }
+      if (Plan::kTeams == 2) p.step(i8g::kStagesA, 2);  // the other team's
+      // what was read of the slot has been stored since
+      if (ok && lane == 0) mbar_arrive(ctl.raw_empty + raw.slot);
     }
   } else {
     // ---------------- epilogue: warp w reads TMEM lanes 32 (w % 4) .., one feature a lane, and half of the columns; two
     // warps a quarter.  32 tokens x 32 features go through shared memory into 16-byte stores ----------------
-    const int quarter = warp & 3, half = (warp - i8g::kConvWarps) >> 2;
+    const int quarter = warp & 3, half = (warp - Plan::kRowWarps) >> 2;
     const uint32_t t_acc = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(half * (kTile / 2));
-    uint8_t* buf_s = smem + i8g::kCtlBytes + (warp - i8g::kConvWarps) * i8g::kEpiBytes;
+    uint8_t* buf_s = smem + i8g::kCtlBytes + (warp - Plan::kRowWarps) * i8g::kEpiBytes;
     if (!kSplit) grid_dependency_wait();  // x's scales, and what the output's memory holds, may be the kernel before's
     uint32_t j = 0;
     bool ok = true;
@@ -551,37 +617,31 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
       if (f0 >= a.N) continue;
       const float sw = f0 + lane < a.N ? __ldg(a.w_scale + f0 + lane) : 0.f;
       const float add = a.bias && f0 + lane < a.N ? __ldg(a.bias + f0 + lane) : 0.f;
+      // 16 bytes a lane: FP32 4 tokens of 8 lanes at a time, else 8 of 4
+      const bool f32 = a.out_type == 1;
+      const int row = f32 ? lane >> 3 : lane >> 2, f = f32 ? 4 * (lane & 7) : 8 * (lane & 3), size = f32 ? 4 : 2;
+      const long long step = a.ldo * 16;  // bytes from 4, or 8, tokens to the next
+      int left = f0 + f < a.N ? tokens - half * (kTile / 2) - row : 0;
+      const float* sx = a.x_scale + row0 + half * (kTile / 2);
+      uint8_t* out = static_cast<uint8_t*>(a.out) + ((long long)(row0 + half * (kTile / 2) + row) * a.ldo + f0 + f) * size;
+      const uint8_t* from = buf_s + row * (32 * size) + f * size;
 #pragma unroll
       for (int col = 0; col < kTile / 2; col += 16) {
-        const int t0 = half * (kTile / 2) + col;
-        if (t0 >= tokens) break;
+        if (half * (kTile / 2) + col >= tokens) break;
         __syncwarp();
-        const float sx_lane = lane < 16 && t0 + lane < tokens ? a.x_scale[row0 + t0 + lane] : 0.f;
+        const float sx_lane = half * (kTile / 2) + col + (lane & 15) < tokens ? sx[col + (lane & 15)] : 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float y = fmaf((float)acc[col + i], sw * __shfl_sync(0xffffffffu, sx_lane, i), add);
-          if (a.out_type == 1) *reinterpret_cast<float*>(buf_s + i * 128 + lane * 4) = y;
+          if (f32) *reinterpret_cast<float*>(buf_s + i * 128 + lane * 4) = y;
           else if (a.out_type == 2) *reinterpret_cast<__half*>(buf_s + i * 64 + lane * 2) = __float2half_rn(y);
           else *reinterpret_cast<__nv_bfloat16*>(buf_s + i * 64 + lane * 2) = __float2bfloat16_rn(y);
         }
         __syncwarp();
-        if (a.out_type == 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 4 * i + (lane >> 3), f = f0 + 4 * (lane & 7);
-            if (t0 + row < tokens && f < a.N)
-              *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (long long)(row0 + t0 + row) * a.ldo + f) =
-                  *reinterpret_cast<const uint4*>(buf_s + row * 128 + (lane & 7) * 16);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = 8 * i + (lane >> 2), f = f0 + 8 * (lane & 3);
-            if (t0 + row < tokens && f < a.N)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (long long)(row0 + t0 + row) * a.ldo + f) =
-                  *reinterpret_cast<const uint4*>(buf_s + row * 64 + (lane & 3) * 16);
-          }
-        }
+        // (a loop: as 96 tokens' addresses it would not fit the registers)
+#pragma unroll 1
+        for (int i = 0; i < 16; i += f32 ? 4 : 8, out += step, left -= f32 ? 4 : 8)
+          if (left > 0) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(from + i * (32 * size));
       }
     }
   }
@@ -594,8 +654,8 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
     int row0 = 0;
     const int tokens = first < total ? tokens_of(first, row0) : 0;
     int* sums = reinterpret_cast<int*>(ring_b);  // [token][128 features]; the copies and MMAs are done with the rings
-    if (warp >= i8g::kConvWarps && warp < i8g::kProducer && tokens && !*abort_flag) {
-      const int half = (warp - i8g::kConvWarps) >> 2, t0 = half * (kTile / 2);
+    if (warp >= Plan::kRowWarps && warp < Plan::kToken0 && tokens && !*abort_flag) {
+      const int half = (warp - Plan::kRowWarps) >> 2, t0 = half * (kTile / 2);
 #pragma unroll
       for (int i = 0; i < kTile / 2; ++i)
         if (t0 + i < tokens) sums[(t0 + i) * 128 + 32 * (warp & 3) + lane] = acc[i];
@@ -606,7 +666,7 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
     if (f < a.N) {
       const float4 sw = *reinterpret_cast<const float4*>(a.w_scale + f);
       const float4 add = a.bias ? *reinterpret_cast<const float4*>(a.bias + f) : make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int t = warp * a.split + part; t < tokens; t += i8g::kThreads / 32 * a.split) {
+      for (int t = warp * a.split + part; t < tokens; t += Plan::kThreads / 32 * a.split) {
         int4 n = make_int4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < i8g::kMaxSplit; ++c)
@@ -635,7 +695,7 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
     __syncwarp();
     cluster_sync_all();  // no CTA leaves while its sums are read
   }
-  if (warp == i8g::kIssuer) {
+  if (warp == Plan::kIssuer) {
     tc_fence_after();
     if (kCtas == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -648,14 +708,33 @@ __global__ void __launch_bounds__(i8g::kThreads, 1)
 typedef void (*Int8Gemm)(const CUtensorMap, Int8Args);
 struct Int8Variant {
   Int8Gemm fn;
-  int ctas, tile;
+  int ctas, tile, threads;
+  bool split;
   int cost;  // cycles of 64 elements of the reduction, about
 };
-static const Int8Variant kInt8Variants[] = {{int8_gemm_kernel<1, 64, false>, 1, 64, 360},
-                                            {int8_gemm_kernel<1, 128, false>, 1, 128, 520},
-                                            {int8_gemm_kernel<2, 192, false>, 2, 192, 430},
-                                            {int8_gemm_kernel<1, 64, true>, 1, 64, 360},
-                                            {int8_gemm_kernel<1, 128, true>, 1, 128, 520}};
+template <int kCtas, int kTile, bool kSplit>
+static constexpr Int8Variant int8_variant(int cost) {
+  return {int8_gemm_kernel<kCtas, kTile, kSplit>, kCtas, kTile, i8g::Plan<kCtas, kTile>::kThreads, kSplit, cost};
+}
+static const Int8Variant kInt8Variants[] = {int8_variant<1, 64, false>(320), int8_variant<1, 128, false>(320),
+                                            int8_variant<2, 192, false>(400), int8_variant<1, 64, true>(320),
+                                            int8_variant<1, 128, true>(320)};
+
+// Tokens as FP16: a thread 16 elements, zeros from K on.
+__global__ void __launch_bounds__(256) int8_tokens_kernel(const int8_t* x, long long ldx, int T, int K, int Kp, uint16_t* out) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int pieces = Kp / 16;
+  const long long n = (long long)T * pieces;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const int t = (int)(i / pieces), k = 16 * (int)(i - (long long)t * pieces);
+    uint32_t v[8];
+    bytes_to_f16(biased(k < K ? *reinterpret_cast<const uint4*>(x + t * ldx + k) : make_uint4(0u, 0u, 0u, 0u)), v);
+    uint4* o = reinterpret_cast<uint4*>(out + (long long)t * Kp + k);
+    o[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    o[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 
 static cudaError_t set_int8_attrs() {  // once per device
   constexpr int kCached = 64;
@@ -711,19 +790,27 @@ cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t st) {
   return a.T <= 8 ? cudaLaunchKernelEx(&cfg, int8_gemv_kernel<1>, a) : cudaLaunchKernelEx(&cfg, int8_gemv_kernel<2>, a);
 }
 
+int int8_chunk_tokens(int K) {
+  const int Kp = (K + 127) / 128 * 128;
+  return std::max(192, (1 << 27) / Kp / 192 * 192);
+}
+size_t int8_workspace_bytes(int K, int max_tokens) {
+  return max_tokens > 64 ? sizeof(uint16_t) * ((K + 127) / 128 * 128) * std::min(max_tokens, int8_chunk_tokens(K)) : 0;
+}
+
 Int8Tiling int8_tiling(int N, int K, int T, int num_sms) {
   // The variant whose rounds of units take the least time by the costs of a step above and some 3000 cycles a unit.
   const int blocks = (N + 127) / 128, squares = (K + 127) / 128;
   Int8Tiling best{};
   double least = 1e300;
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < (int)(sizeof(kInt8Variants) / sizeof(kInt8Variants[0])); ++i) {
     const Int8Variant& v = kInt8Variants[i];
     const long long units = (long long)((blocks + v.ctas - 1) / v.ctas) * ((T + v.tile - 1) / v.tile);
-    for (int split = i >= 3 ? 2 : 1; split <= (i >= 3 ? i8g::kMaxSplit : 1); split *= 2) {
-      if (i >= 3 && (units * split > num_sms * 15 / 16 || 2 * split > squares)) break;
+    for (int split = v.split ? 2 : 1; split <= (v.split ? i8g::kMaxSplit : 1); split *= 2) {
+      if (v.split && (units * split > num_sms * 15 / 16 || 2 * split > squares)) break;
       const long long slots = num_sms / (v.ctas * split), rounds = (units + slots - 1) / slots;
       const double t = (double)rounds * ((squares + split - 1) / split * 2.0 * v.cost + 3000.0);
-      if (t < least) least = t, best = {i, v.tile / v.ctas, split};
+      if (t < least) least = t, best = {i, v.tile / v.ctas, split, v.tile > 64};
     }
   }
   return best;
@@ -745,7 +832,7 @@ cudaError_t launch_int8_gemm(const Int8Product& p, const Int8Tiling& t, const CU
   cudaLaunchConfig_t cfg{};
   const int units = a.tiles * a.NU;
   cfg.gridDim = dim3((unsigned)(t.split > 1 ? units * t.split : std::min(units, p.num_sms / v.ctas) * v.ctas));
-  cfg.blockDim = dim3(i8g::kThreads);
+  cfg.blockDim = dim3((unsigned)v.threads);
   cfg.dynamicSmemBytes = i8::kSmemMax;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
@@ -756,6 +843,20 @@ cudaError_t launch_int8_gemm(const Int8Product& p, const Int8Tiling& t, const CU
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at, cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, v.fn, x_map, a);
+}
+
+cudaError_t launch_int8_tokens(const Int8Product& p, void* out, cudaStream_t st) {
+  const int Kp = (p.K + 127) / 128 * 128;
+  const long long threads = (long long)p.T * (Kp / 16);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::min((threads + 255) / 256, (long long)p.num_sms * 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, int8_tokens_kernel, p.x, p.ldx, p.T, p.K, Kp, static_cast<uint16_t*>(out));
 }
 
 }  // namespace nvfp4moe

@@ -296,12 +296,17 @@ struct Int8Product {
 size_t int8_packed_bytes(int N, int K);
 cudaError_t launch_pack_int8(const int8_t* w_q, int N, int K, uint8_t* packed, cudaStream_t st);
 cudaError_t launch_int8_gemv(const Int8Product& p, cudaStream_t st);  // up to 16 tokens
-// How launch_int8_gemm cuts a product: kernel variant, tokens per TMA box, CTAs that share a unit's reduction.
+// How launch_int8_gemm cuts a product: kernel variant, tokens per TMA box, CTAs that share a unit's reduction, and whether
+// it reads the tokens in FP16 (launch_int8_tokens), rows of K rounded up to 128, or as they are.
 struct Int8Tiling {
   int variant, box, split;
+  bool fp16;
 };
 Int8Tiling int8_tiling(int N, int K, int T, int num_sms);
-// x_map: x as [T][K] bytes, box {128, tiling.box}, 128B swizzle.
+int int8_chunk_tokens(int K);                                // tokens that one call's workspace holds at most
+size_t int8_workspace_bytes(int K, int max_tokens);          // 0: no call needs one
+cudaError_t launch_int8_tokens(const Int8Product& p, void* out, cudaStream_t st);
+// x_map: the tokens in FP16, box {64, tiling.box}, or x as [T][K] bytes, box {128, tiling.box}; 128B swizzle.
 cudaError_t launch_int8_gemm(const Int8Product& p, const Int8Tiling& t, const CUtensorMap& x_map, cudaStream_t st);
 
 cudaError_t launch_combine(const LayerDims& d, int T, int k, const Workspace& ws, void* out,

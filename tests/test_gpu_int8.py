@@ -146,7 +146,7 @@ def test_quantize(T, K, dt):
     h.close()
 
 
-@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("T", [5, 60, 300])
 def test_graph_overlapping_calls_and_both_paths_alike(T):
     N, K = 1040, 1536
     x, w, sx, sw, b = _case(3, N, K, T)
@@ -169,7 +169,7 @@ def test_graph_overlapping_calls_and_both_paths_alike(T):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, _want(x, w, sx, sw, b, "bf16"))
-    streams = [torch.cuda.Stream() for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(4 if T <= 64 else 1)]   # above 64 tokens calls share a workspace
     outs = [[out() for _ in range(8)] for _ in streams]
     torch.cuda.synchronize()
     for i in range(8):
