@@ -192,7 +192,7 @@ nvfp4_moe_status nvfp4_norm_backward(nvfp4_moe_t h, int T, const void* dy, int64
   NormBackOp p{};
   p.dy = dy, p.ld_dy = ld_dy, p.x = sum, p.ldx = ld_sum, p.weight = weight, p.rstd = rstd;
   p.dsum = dsum, p.ld_dsum = ld_dsum, p.dx = dx, p.ld_dx = ld_dx;
-  p.dweight = dweight, p.part = reinterpret_cast<float*>(h->blob);
+  p.dweight = dweight, p.part = reinterpret_cast<float*>(h->blob), p.status = h->ws.status;
   p.T = T, p.H = H, p.f16 = h->norm.act_dtype == NVFP4_MOE_ACT_F16, p.num_sms = h->num_sms;
   return launched(h, launch_norm_backward(p, st), what);
 }

@@ -259,6 +259,7 @@ struct NormBackOp {
   const float* rstd;
   void* dx;
   float *dweight, *part;   // part: norm_backward_parts rows of H, where there is a dweight
+  DeviceStatus* status;
   long long ld_dy, ldx, ld_dsum, ld_dx;
   int T, H, f16, num_sms;
 };

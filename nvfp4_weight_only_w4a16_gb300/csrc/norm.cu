@@ -13,6 +13,7 @@
 // Sums are FP32; where squares or products leave its range (the mean below 2^-80 or the sum above 2^120, the peak beyond
 // 2^+-100) the row's statistics are formed again in 64 bits.  A row whose products are all below 2^-149 counts as zeros.
 #include <algorithm>
+#include <mutex>
 
 #include "kernels.h"
 #include "quant8.cuh"
@@ -192,8 +193,9 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
           for (int i = 0; i < 8; ++i) pr[i] = a.weight ? h[i] * w[i] : h[i];
           if (!odd) {
             if (peak_bits) {
-              if (kF16) codes_of<22>(pr, peak, c);
-              else codes_of<16>(pr, peak, c);
+              if (!a.weight) codes_of_elements(pr, peak, c);
+              else if (kF16) codes_of_products<22>(pr, peak, c);
+              else codes_of_products<16>(pr, peak, c);
             }
           } else if (finite && peak64 > 0.0) {
 #pragma unroll
@@ -218,10 +220,8 @@ struct NormBackArgs {
 };
 
 template <bool kF16, int TP, int V>
-__global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
-    norm_backward_kernel(NormBackArgs a) {
-  constexpr int kRows = TP <= 32 ? nm::kSmallThreads / TP : 1;
-  __shared__ float red[2][32];
+__global__ void __launch_bounds__(nm::kSmallThreads) norm_backward_kernel(NormBackArgs a) {
+  constexpr int kRows = nm::kSmallThreads / TP;
   const int lane = threadIdx.x % TP, pieces = a.H / 8;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
   uint4 x_n[V], d_n[V], s_n[V];
   float rstd_n = 0.f;
   if (kAhead) fetch(t, x_n, d_n, s_n, rstd_n);
-  for (int turn = 0; t - threadIdx.x / TP % (TP < 32 ? 32 / TP : 1) < a.T; t += step, turn ^= 1) {
+  for (; t - threadIdx.x / TP % (TP < 32 ? 32 / TP : 1) < a.T; t += step) {
     const bool row_ok = t < a.T;
     uint4 x4[V], d4[V], s4[V];
     float rstd = rstd_n;
@@ -280,14 +280,7 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
       }
     }
 #pragma unroll
-    for (int o = 1; o < (TP < 32 ? TP : 32); o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    if constexpr (TP > 32) {
-      if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = c;
-      __syncthreads();
-      c = (threadIdx.x & 31) < TP / 32 ? red[turn][threadIdx.x & 31] : 0.f;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    }
+    for (int o = 1; o < TP; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
     c *= inv_h;
     if (row_ok) {
 #pragma unroll
@@ -310,6 +303,141 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * TP;
+      if (p >= pieces) continue;
+      *reinterpret_cast<float4*>(out + 8 * p) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+      *reinterpret_cast<float4*>(out + 8 * p + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+    }
+  }
+}
+
+// The same for rows longer than a warp holds: one CTA takes kRows rows at a time, which bulk copies have brought to a ring
+// in shared memory, as far ahead as that holds (with the rows in registers 25 KB a multiprocessor were on their way, and
+// 8191 rows of 4096 took 58 us).  One barrier a turn; once it is passed, the turn's rows are in registers and the slot is
+// free.
+namespace nm {
+constexpr int kRingBytes = 216 * 1024, kMaxSlots = 8;
+}
+template <bool kF16, int TP, int V, int kRows>
+__global__ void __launch_bounds__(TP) norm_backward_ring_kernel(NormBackArgs a, int slots, int slot_bytes, DeviceStatus* st) {
+  extern __shared__ __align__(16) uint8_t ring[];  // [slot][x, dy, dsum][kRows][H]
+  __shared__ uint64_t full[nm::kMaxSlots];
+  __shared__ float red[2][kRows][TP / 32];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pieces = a.H / 8;
+  const uint32_t bytes = 2u * a.H;
+  if (tid == 0) {
+    for (int s = 0; s < slots; ++s) mbar_init(full + s, 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int turns = (a.T + kRows - 1) / kRows;  // of the grid; this CTA's are blockIdx.x, + gridDim.x, ..
+  const auto copy = [&](int turn, int slot) {   // thread 0
+    const long long t = (long long)turn * kRows;
+    const int n = min(kRows, a.T - (int)t);
+    uint8_t* to = ring + (size_t)slot * slot_bytes;
+    mbar_arrive_expect_tx(full + slot, bytes * n * (a.dsum ? 3 : 2));
+    for (int r = 0; r < n; ++r) {
+      bulk_g2s(to + r * bytes, a.x + (t + r) * a.ldx, bytes, full + slot);
+      bulk_g2s(to + (kRows + r) * bytes, a.dy + (t + r) * a.ld_dy, bytes, full + slot);
+      if (a.dsum) bulk_g2s(to + (2 * kRows + r) * bytes, a.dsum + (t + r) * a.ld_dsum, bytes, full + slot);
+    }
+  };
+  uint32_t issued = 0;
+  int next = blockIdx.x;  // the turn to copy
+  if (tid == 0)
+    for (; issued < (uint32_t)slots && next < turns; ++issued, next += gridDim.x) copy(next, issued);
+  uint4 w4[V];
+  float dw[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = tid + v * TP;
+    w4[v] = p < pieces ? load16(a.weight + 16ll * p) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+  }
+  const float inv_h = 1.0f / (float)a.H;
+  RingPos pos;
+  bool gave_up = false;
+  for (int turn = blockIdx.x, k = 0; turn < turns; turn += gridDim.x, k ^= 1, pos.step(slots)) {
+    const long long t = (long long)turn * kRows;
+    const int n = min(kRows, a.T - (int)t);
+    float rstd[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) rstd[r] = r < n ? a.rstd[t + r] : 0.f;
+    const bool landed = mbar_wait(full + pos.slot, pos.phase, &abort_flag, st, 941);
+    const uint8_t* slot = ring + (size_t)pos.slot * slot_bytes;
+    uint4 x4[kRows][V], d4[kRows][V], s4[kRows][V];
+    float c[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      c[r] = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int p = tid + v * TP;
+        x4[r][v] = d4[r][v] = s4[r][v] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < n && p < pieces) {
+          x4[r][v] = load16(slot + r * bytes + 16 * p);
+          d4[r][v] = load16(slot + (kRows + r) * bytes + 16 * p);
+          if (a.dsum) s4[r][v] = load16(slot + (2 * kRows + r) * bytes + 16 * p);
+        }
+        float x[8], d[8], w[8];
+        unpack8<kF16>(x4[r][v], x);
+        unpack8<kF16>(d4[r][v], d);
+        unpack8<kF16>(w4[v], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float nx = x[i] * rstd[r];
+          c[r] = fmaf(d[i] * w[i], nx, c[r]);
+          dw[v][i] = fmaf(d[i], nx, dw[v][i]);
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) c[r] += __shfl_xor_sync(0xffffffffu, c[r], o);
+      if (lane == 0) red[k][r][warp] = c[r];
+    }
+    if (__syncthreads_or(!landed)) {  // one answer for the CTA
+      gave_up = true;
+      break;
+    }
+    if (tid == 0 && next < turns) {
+      copy(next, pos.slot);
+      ++issued, next += gridDim.x;
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      c[r] = lane < TP / 32 ? red[k][r][lane] : 0.f;
+#pragma unroll
+      for (int o = 1; o < TP / 32; o <<= 1) c[r] += __shfl_xor_sync(0xffffffffu, c[r], o);
+      c[r] = __shfl_sync(0xffffffffu, c[r], 0) * inv_h;
+      if (r < n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int p = tid + v * TP;
+          if (p >= pieces) continue;
+          float x[8], d[8], w[8], s[8], o[8];
+          unpack8<kF16>(x4[r][v], x);
+          unpack8<kF16>(d4[r][v], d);
+          unpack8<kF16>(w4[v], w);
+          unpack8<kF16>(s4[r][v], s);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = fmaf(rstd[r], fmaf(-c[r], x[i] * rstd[r], d[i] * w[i]), s[i]);
+          *reinterpret_cast<uint4*>(a.dx + (t + r) * a.ld_dx + 16ll * p) = pack8<kF16>(o);
+        }
+      }
+    }
+  }
+  if (gave_up) {
+    if (tid == 0) drain_copies(full, issued, slots);
+    return;
+  }
+  if (a.part) {
+    float* out = a.part + (long long)blockIdx.x * a.H;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = tid + v * TP;
       if (p >= pieces) continue;
       *reinterpret_cast<float4*>(out + 8 * p) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
       *reinterpret_cast<float4*>(out + 8 * p + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
@@ -408,45 +536,68 @@ cudaError_t launch_norm_forward(const NormOp& p, cudaStream_t st) {
   return p.f16 ? forward_of<true>(a, p.num_sms, st) : forward_of<false>(a, p.num_sms, st);
 }
 
-// The backward's shapes: dw of 8 V elements stays in registers beside three rows.
-static NormShape norm_back_shape(int pieces) {
-  if (pieces <= 8) return {8, 1};
-  if (pieces <= 16) return {16, 1};
-  if (pieces <= 32) return {32, 1};
-  if (pieces <= 64) return {32, 2};
-  if (pieces <= 256) return {256, 1};
-  if (pieces <= 512) return {512, 1};
-  if (pieces <= 1024) return {512, 2};
-  return {512, 4};
+// The backward: rows within a warp as in the forward, longer ones through the ring.
+struct NormBackShape {
+  int tp, v, rows;  // threads a row, pieces a thread, rows of a CTA at a time
+  int per_sm;       // CTAs a multiprocessor
+};
+static NormBackShape norm_back_shape(int pieces) {
+  if (pieces <= 8) return {8, 1, 16, 4};
+  if (pieces <= 16) return {16, 1, 8, 4};
+  if (pieces <= 32) return {32, 1, 4, 4};
+  if (pieces <= 64) return {32, 2, 4, 4};
+  if (pieces <= 256) return {256, 1, 4, 2};
+  if (pieces <= 512) return {512, 1, 2, 1};
+  if (pieces <= 1024) return {512, 2, 1, 1};
+  return {512, 4, 1, 1};
 }
-static int norm_back_rows(int pieces) {  // of a CTA at a time
-  const int tp = norm_back_shape(pieces).tp;
-  return tp <= 32 ? nm::kSmallThreads / tp : 1;
+static int norm_back_parts(const NormBackShape& s, int grid) { return grid * (s.tp <= 32 ? s.rows : 1); }
+int norm_backward_parts(int H, int num_sms) {
+  const NormBackShape s = norm_back_shape(H / 8);
+  return norm_back_parts(s, num_sms * s.per_sm);
 }
-static int norm_back_ctas(int pieces) {  // per multiprocessor
-  const int tp = norm_back_shape(pieces).tp;
-  return tp <= 32 ? 4 : 1024 / tp;
-}
-int norm_backward_parts(int H, int num_sms) { return num_sms * norm_back_ctas(H / 8) * norm_back_rows(H / 8); }
 
 template <bool kF16, int TP, int V>
 static cudaError_t run_backward(const NormBackArgs& a, int grid, cudaStream_t st) {
   cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = dependent(dim3(grid), dim3(TP <= 32 ? nm::kSmallThreads : TP), st, &at);
+  const cudaLaunchConfig_t cfg = dependent(dim3(grid), dim3(nm::kSmallThreads), st, &at);
   return cudaLaunchKernelEx(&cfg, norm_backward_kernel<kF16, TP, V>, a);
 }
+template <bool kF16, int TP, int V, int kRows>
+static cudaError_t run_ring(const NormBackArgs& a, const NormBackShape& s, int grid, DeviceStatus* status, cudaStream_t st) {
+  constexpr int kCached = 64;
+  static std::mutex mu;
+  static bool done[kCached] = {};  // the opt-in shared-memory size, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!(dev >= 0 && dev < kCached && done[dev])) {
+      e = cudaFuncSetAttribute((const void*)norm_backward_ring_kernel<kF16, TP, V, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               nm::kRingBytes);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < kCached) done[dev] = true;
+    }
+  }
+  const int slot = 3 * kRows * 2 * a.H, room = nm::kRingBytes / s.per_sm - (s.per_sm > 1 ? 4096 : 0);
+  const int slots = std::min(nm::kMaxSlots, room / slot);
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = dependent(dim3(grid), dim3(TP), st, &at);
+  cfg.dynamicSmemBytes = (size_t)slots * slot;
+  return cudaLaunchKernelEx(&cfg, norm_backward_ring_kernel<kF16, TP, V, kRows>, a, slots, slot, status);
+}
 template <bool kF16>
-static cudaError_t backward_of(const NormBackArgs& a, int grid, cudaStream_t st) {
-  const NormShape s = norm_back_shape(a.H / 8);
+static cudaError_t backward_of(const NormBackArgs& a, const NormBackShape& s, int grid, DeviceStatus* status, cudaStream_t st) {
   switch (s.tp * 8 + s.v) {
     case 8 * 8 + 1: return run_backward<kF16, 8, 1>(a, grid, st);
     case 16 * 8 + 1: return run_backward<kF16, 16, 1>(a, grid, st);
     case 32 * 8 + 1: return run_backward<kF16, 32, 1>(a, grid, st);
     case 32 * 8 + 2: return run_backward<kF16, 32, 2>(a, grid, st);
-    case 256 * 8 + 1: return run_backward<kF16, 256, 1>(a, grid, st);
-    case 512 * 8 + 1: return run_backward<kF16, 512, 1>(a, grid, st);
-    case 512 * 8 + 2: return run_backward<kF16, 512, 2>(a, grid, st);
-    default: return run_backward<kF16, 512, 4>(a, grid, st);
+    case 256 * 8 + 1: return run_ring<kF16, 256, 1, 4>(a, s, grid, status, st);
+    case 512 * 8 + 1: return run_ring<kF16, 512, 1, 2>(a, s, grid, status, st);
+    case 512 * 8 + 2: return run_ring<kF16, 512, 2, 1>(a, s, grid, status, st);
+    default: return run_ring<kF16, 512, 4, 1>(a, s, grid, status, st);
   }
 }
 
@@ -460,13 +611,13 @@ cudaError_t launch_norm_backward(const NormBackOp& p, cudaStream_t st) {
   a.dx = static_cast<uint8_t*>(p.dx), a.ld_dx = 2 * p.ld_dx;
   a.part = p.dweight ? p.part : nullptr;
   a.T = p.T, a.H = p.H;
-  const int rows = norm_back_rows(p.H / 8);
-  const int grid = std::min((p.T + rows - 1) / rows, p.num_sms * norm_back_ctas(p.H / 8));
-  cudaError_t e = p.f16 ? backward_of<true>(a, grid, st) : backward_of<false>(a, grid, st);
+  const NormBackShape s = norm_back_shape(p.H / 8);
+  const int grid = std::min((p.T + s.rows - 1) / s.rows, p.num_sms * s.per_sm);
+  cudaError_t e = p.f16 ? backward_of<true>(a, s, grid, p.status, st) : backward_of<false>(a, s, grid, p.status, st);
   if (e != cudaSuccess || !p.dweight) return e;
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = dependent(dim3((p.H + 31) / 32), dim3(1024), st, &at);
-  return cudaLaunchKernelEx(&cfg, norm_dweight_kernel, (const float*)p.part, grid * rows, p.H, p.dweight);
+  return cudaLaunchKernelEx(&cfg, norm_dweight_kernel, (const float*)p.part, norm_back_parts(s, grid), p.H, p.dweight);
 }
 
 }  // namespace nvfp4moe

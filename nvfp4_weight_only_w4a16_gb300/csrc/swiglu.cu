@@ -4,10 +4,10 @@
 //
 // Bound by memory: 8 bytes an element either way (two 16-bit rows in or out, one the other way, two bytes of codes).
 // A thread takes 16 elements of gate and of up, eight threads a block of 128, so that all loads and stores are 16
-// bytes wide and a block's peak takes three shuffles.  The arithmetic is about 35 instructions an element and has to
-// stay below what memory allows (some 55 at full issue), so exp and the reciprocal are the hardware's approximations
-// (relative error 2^-21 for |g| up to 16, next to the result's rounding of 2^-9 or 2^-12), no code is converted to or
-// from an integer (both go by the low bits of a float), and the exact rounding of codes looks at 16 elements at once.
+// bytes wide and a block's peak takes three shuffles.  Few instructions an element count (at 41 the forward took 316 us
+// for 131072 x 1536), so exp and the reciprocal are the hardware's approximations (relative error 2^-21 for |g| up to 16,
+// next to the result's rounding of 2^-9 or 2^-12), no code is converted to or from an integer (both go by the low bits of
+// a float), and the exact rounding of a code takes no test.
 #include <algorithm>
 
 #include "kernels.h"
@@ -74,12 +74,14 @@ __device__ __forceinline__ uint4 checkpoint(const uint4 (&raw)[2], const float (
   m = __float_as_uint(unpack16<kF16>(m).x);
   const float peak = __uint_as_float(m);
   uint32_t c[4] = {0u, 0u, 0u, 0u};
-  scale = peak / 127.0f;
+  scale = 0.f;
   if (plain_peak(peak)) {
-    codes_of<11>(v, peak, c);
+    codes_of_elements(v, peak, c);
+    scale = scale_of_peak(peak);
   } else if (m >= 0x7F800000u) {
     scale = __uint_as_float(0x7FC00000u);
   } else if (m) {  // too small, or too large, for FP32 quotients
+    scale = peak / 127.0f;
 #pragma unroll
     for (int i = 0; i < sg::kPer; ++i) c[i >> 2] |= ((uint32_t)code_of_64(v[i], peak) & 255u) << (8 * (i & 3));
   }
