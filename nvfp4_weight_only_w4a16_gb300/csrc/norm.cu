@@ -310,45 +310,52 @@ __global__ void __launch_bounds__(nm::kSmallThreads) norm_backward_kernel(NormBa
   }
 }
 
-// The same for rows longer than a warp holds: one CTA takes kRows rows at a time, which bulk copies have brought to a ring
-// in shared memory, as far ahead as that holds (with the rows in registers 25 KB a multiprocessor were on their way, and
-// 8191 rows of 4096 took 58 us).  One barrier a turn; once it is passed, the turn's rows are in registers and the slot is
-// free.
+// The same for rows longer than a warp holds.  A warp of its own brings the rows by bulk copies to a ring in shared memory,
+// as far ahead as that holds; the others read a row there twice, before and after its sum is known, so that few registers
+// are taken and two or three CTAs a multiprocessor hide one another's barriers.  (8191 rows of 4096: 58 us with the rows in
+// registers, 25 KB a multiprocessor on their way; 55 with one CTA a multiprocessor and the rows copied from the ring to
+// registers.)
 namespace nm {
-constexpr int kRingBytes = 216 * 1024, kMaxSlots = 8;
+constexpr int kRingBytes = 216 * 1024, kMaxSlots = 8;  // of a multiprocessor
 }
-template <bool kF16, int TP, int V, int kRows>
-__global__ void __launch_bounds__(TP) norm_backward_ring_kernel(NormBackArgs a, int slots, int slot_bytes, DeviceStatus* st) {
-  extern __shared__ __align__(16) uint8_t ring[];  // [slot][x, dy, dsum][kRows][H]
-  __shared__ uint64_t full[nm::kMaxSlots];
-  __shared__ float red[2][kRows][TP / 32];
+template <bool kF16, int TP, int V, int kPerSm>
+__global__ void __launch_bounds__(TP + 32, kPerSm) norm_backward_ring_kernel(NormBackArgs a, int slots, DeviceStatus* st) {
+  extern __shared__ __align__(16) uint8_t ring[];  // [slot][x, dy, dsum][H]
+  __shared__ uint64_t full[nm::kMaxSlots], empty[nm::kMaxSlots];
+  __shared__ float red[2][TP / 32];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pieces = a.H / 8;
   const uint32_t bytes = 2u * a.H;
   if (tid == 0) {
-    for (int s = 0; s < slots; ++s) mbar_init(full + s, 1);
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, TP / 32);
+    }
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
-  const int turns = (a.T + kRows - 1) / kRows;  // of the grid; this CTA's are blockIdx.x, + gridDim.x, ..
-  const auto copy = [&](int turn, int slot) {   // thread 0
-    const long long t = (long long)turn * kRows;
-    const int n = min(kRows, a.T - (int)t);
-    uint8_t* to = ring + (size_t)slot * slot_bytes;
-    mbar_arrive_expect_tx(full + slot, bytes * n * (a.dsum ? 3 : 2));
-    for (int r = 0; r < n; ++r) {
-      bulk_g2s(to + r * bytes, a.x + (t + r) * a.ldx, bytes, full + slot);
-      bulk_g2s(to + (kRows + r) * bytes, a.dy + (t + r) * a.ld_dy, bytes, full + slot);
-      if (a.dsum) bulk_g2s(to + (2 * kRows + r) * bytes, a.dsum + (t + r) * a.ld_dsum, bytes, full + slot);
+  RingPos pos;
+  if (warp == TP / 32) {
+    if (lane == 0) {
+      uint32_t issued = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; t < a.T && ok; t += gridDim.x, pos.step(slots)) {
+        ok = mbar_wait(empty + pos.slot, pos.phase ^ 1u, &abort_flag, st, 942);
+        if (!ok) break;
+        uint8_t* to = ring + (size_t)pos.slot * 3 * bytes;
+        mbar_arrive_expect_tx(full + pos.slot, bytes * (a.dsum ? 3 : 2));
+        bulk_g2s(to, a.x + t * a.ldx, bytes, full + pos.slot);
+        bulk_g2s(to + bytes, a.dy + t * a.ld_dy, bytes, full + pos.slot);
+        if (a.dsum) bulk_g2s(to + 2 * bytes, a.dsum + t * a.ld_dsum, bytes, full + pos.slot);
+        ++issued;
+      }
+      if (!ok) drain_copies(full, issued, slots);
     }
-  };
-  uint32_t issued = 0;
-  int next = blockIdx.x;  // the turn to copy
-  if (tid == 0)
-    for (; issued < (uint32_t)slots && next < turns; ++issued, next += gridDim.x) copy(next, issued);
+    return;
+  }
   uint4 w4[V];
   float dw[V][8];
 #pragma unroll
@@ -359,88 +366,71 @@ __global__ void __launch_bounds__(TP) norm_backward_ring_kernel(NormBackArgs a, 
     for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
   }
   const float inv_h = 1.0f / (float)a.H;
-  RingPos pos;
-  bool gave_up = false;
-  for (int turn = blockIdx.x, k = 0; turn < turns; turn += gridDim.x, k ^= 1, pos.step(slots)) {
-    const long long t = (long long)turn * kRows;
-    const int n = min(kRows, a.T - (int)t);
-    float rstd[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) rstd[r] = r < n ? a.rstd[t + r] : 0.f;
+  int k = 0;
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x, k ^= 1, pos.step(slots)) {
+    const float rstd = a.rstd[t];
     const bool landed = mbar_wait(full + pos.slot, pos.phase, &abort_flag, st, 941);
-    const uint8_t* slot = ring + (size_t)pos.slot * slot_bytes;
-    uint4 x4[kRows][V], d4[kRows][V], s4[kRows][V];
-    float c[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      c[r] = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int p = tid + v * TP;
-        x4[r][v] = d4[r][v] = s4[r][v] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n && p < pieces) {
-          x4[r][v] = load16(slot + r * bytes + 16 * p);
-          d4[r][v] = load16(slot + (kRows + r) * bytes + 16 * p);
-          if (a.dsum) s4[r][v] = load16(slot + (2 * kRows + r) * bytes + 16 * p);
-        }
-        float x[8], d[8], w[8];
-        unpack8<kF16>(x4[r][v], x);
-        unpack8<kF16>(d4[r][v], d);
-        unpack8<kF16>(w4[v], w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float nx = x[i] * rstd[r];
-          c[r] = fmaf(d[i] * w[i], nx, c[r]);
-          dw[v][i] = fmaf(d[i], nx, dw[v][i]);
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) c[r] += __shfl_xor_sync(0xffffffffu, c[r], o);
-      if (lane == 0) red[k][r][warp] = c[r];
-    }
-    if (__syncthreads_or(!landed)) {  // one answer for the CTA
-      gave_up = true;
-      break;
-    }
-    if (tid == 0 && next < turns) {
-      copy(next, pos.slot);
-      ++issued, next += gridDim.x;
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      c[r] = lane < TP / 32 ? red[k][r][lane] : 0.f;
-#pragma unroll
-      for (int o = 1; o < TP / 32; o <<= 1) c[r] += __shfl_xor_sync(0xffffffffu, c[r], o);
-      c[r] = __shfl_sync(0xffffffffu, c[r], 0) * inv_h;
-      if (r < n) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int p = tid + v * TP;
-          if (p >= pieces) continue;
-          float x[8], d[8], w[8], s[8], o[8];
-          unpack8<kF16>(x4[r][v], x);
-          unpack8<kF16>(d4[r][v], d);
-          unpack8<kF16>(w4[v], w);
-          unpack8<kF16>(s4[r][v], s);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fmaf(rstd[r], fmaf(-c[r], x[i] * rstd[r], d[i] * w[i]), s[i]);
-          *reinterpret_cast<uint4*>(a.dx + (t + r) * a.ld_dx + 16ll * p) = pack8<kF16>(o);
-        }
-      }
-    }
-  }
-  if (gave_up) {
-    if (tid == 0) drain_copies(full, issued, slots);
-    return;
-  }
-  if (a.part) {
-    float* out = a.part + (long long)blockIdx.x * a.H;
+    const uint8_t* slot = ring + (size_t)pos.slot * 3 * bytes;
+    float c = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = tid + v * TP;
       if (p >= pieces) continue;
-      *reinterpret_cast<float4*>(out + 8 * p) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-      *reinterpret_cast<float4*>(out + 8 * p + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+      float x[8], d[8], w[8];
+      unpack8<kF16>(load16(slot + 16 * p), x);
+      unpack8<kF16>(load16(slot + bytes + 16 * p), d);
+      unpack8<kF16>(w4[v], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float dr = d[i] * rstd;
+        c = fmaf(dr * w[i], x[i], c);
+        dw[v][i] = fmaf(dr, x[i], dw[v][i]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if (lane == 0) red[k][warp] = c;
+    uint32_t lost;  // one answer for all of them
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(lost)
+                 : "r"(landed ? 0u : 1u), "n"(TP)
+                 : "memory");
+    if (lost) return;
+    c = lane < TP / 32 ? red[k][lane] : 0.f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    c *= -inv_h * rstd * rstd;
+    uint4 out[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = tid + v * TP;
+      if (p >= pieces) continue;
+      float x[8], d[8], w[8], s[8], o[8];
+      unpack8<kF16>(load16(slot + 16 * p), x);
+      unpack8<kF16>(load16(slot + bytes + 16 * p), d);
+      unpack8<kF16>(a.dsum ? load16(slot + 2 * bytes + 16 * p) : make_uint4(0u, 0u, 0u, 0u), s);
+      unpack8<kF16>(w4[v], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(d[i], w[i] * rstd, fmaf(x[i], c, s[i]));
+      out[v] = pack8<kF16>(o);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + pos.slot);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = tid + v * TP;
+      if (p < pieces) *reinterpret_cast<uint4*>(a.dx + t * a.ld_dx + 16ll * p) = out[v];
+    }
+  }
+  if (a.part) {
+    float* to = a.part + (long long)blockIdx.x * a.H;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = tid + v * TP;
+      if (p >= pieces) continue;
+      *reinterpret_cast<float4*>(to + 8 * p) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+      *reinterpret_cast<float4*>(to + 8 * p + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
     }
   }
 }
@@ -546,8 +536,9 @@ static NormBackShape norm_back_shape(int pieces) {
   if (pieces <= 16) return {16, 1, 8, 4};
   if (pieces <= 32) return {32, 1, 4, 4};
   if (pieces <= 64) return {32, 2, 4, 4};
-  if (pieces <= 256) return {256, 1, 4, 2};
-  if (pieces <= 512) return {512, 1, 2, 1};
+  if (pieces <= 128) return {128, 1, 1, 6};
+  if (pieces <= 256) return {256, 1, 1, 3};
+  if (pieces <= 512) return {256, 2, 1, 3};
   if (pieces <= 1024) return {512, 2, 1, 1};
   return {512, 4, 1, 1};
 }
@@ -563,9 +554,9 @@ static cudaError_t run_backward(const NormBackArgs& a, int grid, cudaStream_t st
   const cudaLaunchConfig_t cfg = dependent(dim3(grid), dim3(nm::kSmallThreads), st, &at);
   return cudaLaunchKernelEx(&cfg, norm_backward_kernel<kF16, TP, V>, a);
 }
-template <bool kF16, int TP, int V, int kRows>
-static cudaError_t run_ring(const NormBackArgs& a, const NormBackShape& s, int grid, DeviceStatus* status, cudaStream_t st) {
-  constexpr int kCached = 64;
+template <bool kF16, int TP, int V, int kPerSm>
+static cudaError_t run_ring(const NormBackArgs& a, int grid, DeviceStatus* status, cudaStream_t st) {
+  constexpr int kCached = 64, kRoom = (nm::kRingBytes / kPerSm - 1024 * (kPerSm - 1)) & ~1023;
   static std::mutex mu;
   static bool done[kCached] = {};  // the opt-in shared-memory size, once per device
   int dev = 0;
@@ -574,18 +565,17 @@ static cudaError_t run_ring(const NormBackArgs& a, const NormBackShape& s, int g
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!(dev >= 0 && dev < kCached && done[dev])) {
-      e = cudaFuncSetAttribute((const void*)norm_backward_ring_kernel<kF16, TP, V, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               nm::kRingBytes);
+      e = cudaFuncSetAttribute((const void*)norm_backward_ring_kernel<kF16, TP, V, kPerSm>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kRoom);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < kCached) done[dev] = true;
     }
   }
-  const int slot = 3 * kRows * 2 * a.H, room = nm::kRingBytes / s.per_sm - (s.per_sm > 1 ? 4096 : 0);
-  const int slots = std::min(nm::kMaxSlots, room / slot);
+  const int slots = std::min(nm::kMaxSlots, kRoom / (6 * a.H));
   cudaLaunchAttribute at;
-  cudaLaunchConfig_t cfg = dependent(dim3(grid), dim3(TP), st, &at);
-  cfg.dynamicSmemBytes = (size_t)slots * slot;
-  return cudaLaunchKernelEx(&cfg, norm_backward_ring_kernel<kF16, TP, V, kRows>, a, slots, slot, status);
+  cudaLaunchConfig_t cfg = dependent(dim3(grid), dim3(TP + 32), st, &at);
+  cfg.dynamicSmemBytes = (size_t)slots * 6 * a.H;
+  return cudaLaunchKernelEx(&cfg, norm_backward_ring_kernel<kF16, TP, V, kPerSm>, a, slots, status);
 }
 template <bool kF16>
 static cudaError_t backward_of(const NormBackArgs& a, const NormBackShape& s, int grid, DeviceStatus* status, cudaStream_t st) {
@@ -594,10 +584,11 @@ static cudaError_t backward_of(const NormBackArgs& a, const NormBackShape& s, in
     case 16 * 8 + 1: return run_backward<kF16, 16, 1>(a, grid, st);
     case 32 * 8 + 1: return run_backward<kF16, 32, 1>(a, grid, st);
     case 32 * 8 + 2: return run_backward<kF16, 32, 2>(a, grid, st);
-    case 256 * 8 + 1: return run_ring<kF16, 256, 1, 4>(a, s, grid, status, st);
-    case 512 * 8 + 1: return run_ring<kF16, 512, 1, 2>(a, s, grid, status, st);
-    case 512 * 8 + 2: return run_ring<kF16, 512, 2, 1>(a, s, grid, status, st);
-    default: return run_ring<kF16, 512, 4, 1>(a, s, grid, status, st);
+    case 128 * 8 + 1: return run_ring<kF16, 128, 1, 6>(a, grid, status, st);
+    case 256 * 8 + 1: return run_ring<kF16, 256, 1, 3>(a, grid, status, st);
+    case 256 * 8 + 2: return run_ring<kF16, 256, 2, 3>(a, grid, status, st);
+    case 512 * 8 + 2: return run_ring<kF16, 512, 2, 1>(a, grid, status, st);
+    default: return run_ring<kF16, 512, 4, 1>(a, grid, status, st);
   }
 }
 
