@@ -630,8 +630,8 @@ nvfp4_moe_status nvfp4_route_forward(nvfp4_moe_t h, int T, const void* logits, i
                                      cudaStream_t stream);
 
 /* dlogits [T][E] (the logits' type, rows ld_dl apart) from dweights [T][top_k]
- * for the choice ids, top_k different experts a token; the choice itself is
- * constant.  An id outside 0..E-1 counts as none.  Softmax whose largest logit is
+ * for the choice ids; the choice itself is constant.  An id outside 0..E-1 counts
+ * as none, an expert named twice twice.  Softmax whose largest logit is
  * infinite, NaN logits, and renormalised sigmoids that are all 0 have no gradient
  * (zeros).  dlogits may be logits. */
 nvfp4_moe_status nvfp4_route_backward(nvfp4_moe_t h, int T, const void* logits, int64_t ld, const int32_t* ids,

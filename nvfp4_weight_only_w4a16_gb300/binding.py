@@ -170,13 +170,32 @@ def _ptr(t):
 
 def _whole(t, shape, dtype, device, what):
     """Address of a contiguous tensor of this shape and type on cuda:`device`."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{what}: expected {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{what}: expected a CUDA tensor on the handle's device, cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
     return t.data_ptr()
+
+
+def _whole_or_none(t, shape, dtype, device, what):
+    return None if t is None else _whole(t, shape, dtype, device, what)
+
+
+def _rows_like(t, shape, dtype, device, what):
+    """(address, row stride) of a matrix of this shape on cuda:`device` whose rows are contiguous; (None, 0) of None."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{what}: expected a CUDA tensor on the handle's device, cuda:{device}")
+    ld, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{what}: expected contiguous rows")
+    # a single row has no stride to speak of
+    return t.data_ptr(), ld if shape[0] > 1 else -(-shape[1] // 8) * 8
 
 
 def _rows(t, cols, dtype, device, what):
@@ -544,11 +563,6 @@ class _Operator(MoELayer):
     def _st(self, stream):
         return stream.cuda_stream if stream is not None else self._current_stream(self.device)
 
-    def _same_rows(self, what, rows, *others):
-        for n in others:
-            if n != rows:
-                raise ValueError(f"{what}: tensors of {rows} and of {n} rows")
-
 
 class Route(_Operator):
     """Routing on its own (nvfp4_route_create ... nvfp4_moe_destroy)."""
@@ -581,7 +595,7 @@ class Route(_Operator):
         lp, ld, T = self._matrix(logits, what)
         n = (T * self.k,)
         st = self.lib.nvfp4_route_forward(
-            self.h, T, lp, ld, None if bias is None else _whole(bias, (self.E,), f32, dev, what),
+            self.h, T, lp, ld, _whole_or_none(bias, (self.E,), f32, dev, what),
             _whole(ids, (T, self.k), i32, dev, what), _whole(weights, (T, self.k), f32, dev, what),
             _whole(offsets, (self.E + 1,), i32, dev, what), _whole(perm, n, i32, dev, what), _whole(inv, n, i32, dev, what),
             self._st(stream))
@@ -594,7 +608,8 @@ class Route(_Operator):
         what, dev = "nvfp4_route_backward", self.device
         lp, ld, T = self._matrix(logits, what)
         dp, ld_dl, Td = self._matrix(dlogits, what)
-        self._same_rows(what, T, Td)
+        if T != Td:
+            raise ValueError(f"{what}: logits of {T} tokens, their gradient of {Td}")
         st = self.lib.nvfp4_route_backward(self.h, T, lp, ld, _whole(ids, (T, self.k), self._int32, dev, what),
                                            _whole(dweights, (T, self.k), self._f32, dev, what), dp, ld_dl, self._st(stream))
         if st:
@@ -615,19 +630,14 @@ class Norm(_Operator):
         """sum (with a residual), y (16 bits), q with q_scale (int8 and a scale a row) and rstd are the caller's."""
         what, dev, H, act = "nvfp4_norm_forward", self.device, self.H, self._act
         xp, ldx, T = _rows(x, H, act, dev, what)
-
-        def rows(t, dt):
-            if t is None:
-                return None, 0
-            p, ld, n = _rows(t, H, dt, dev, what)
-            if n != T:
-                raise ValueError(f"{what}: tensors of {T} and of {n} rows")
-            return p, ld
-
-        (rp, ldr), (sp, lds), (yp, ldy), (qp, ldq) = rows(residual, act), rows(sum, act), rows(y, act), rows(q, self._int8)
-        f = lambda t: None if t is None else _whole(t, (T,), self._f32, dev, what)
+        shape, vec, f32 = (T, H), (T,), self._f32
+        rp, ldr = _rows_like(residual, shape, act, dev, what)
+        sp, lds = _rows_like(sum, shape, act, dev, what)
+        yp, ldy = _rows_like(y, shape, act, dev, what)
+        qp, ldq = _rows_like(q, shape, self._int8, dev, what)
         st = self.lib.nvfp4_norm_forward(self.h, T, xp, ldx, rp, ldr, _whole(weight, (H,), act, dev, what), sp, lds, yp, ldy,
-                                         qp, ldq, f(q_scale), f(rstd), self._st(stream))
+                                         qp, ldq, _whole_or_none(q_scale, vec, f32, dev, what),
+                                         _whole_or_none(rstd, vec, f32, dev, what), self._st(stream))
         if st:
             self._check(st, what)
         return y if y is not None else q
@@ -636,14 +646,13 @@ class Norm(_Operator):
         """dx, the gradient of sum, x and residual alike, and dweight (float32), both the caller's."""
         what, dev, H, act = "nvfp4_norm_backward", self.device, self.H, self._act
         dp, ldd, T = _rows(dy, H, act, dev, what)
-        sp, lds, Ts = _rows(sum, H, act, dev, what)
-        xp, ldx, Tx = _rows(dx, H, act, dev, what)
-        rp, ldr, Tr = (None, 0, T) if dsum is None else _rows(dsum, H, act, dev, what)
-        self._same_rows(what, T, Ts, Tx, Tr)
+        shape = (T, H)
+        sp, lds = _rows_like(sum, shape, act, dev, what)
+        xp, ldx = _rows_like(dx, shape, act, dev, what)
+        rp, ldr = _rows_like(dsum, shape, act, dev, what)
         st = self.lib.nvfp4_norm_backward(self.h, T, dp, ldd, sp, lds, _whole(weight, (H,), act, dev, what),
                                           _whole(rstd, (T,), self._f32, dev, what), rp, ldr, xp, ldx,
-                                          None if dweight is None else _whole(dweight, (H,), self._f32, dev, what),
-                                          self._st(stream))
+                                          _whole_or_none(dweight, (H,), self._f32, dev, what), self._st(stream))
         if st:
             self._check(st, what)
         return dx
@@ -663,13 +672,13 @@ class SwiGLU(_Operator):
         """out = silu(gate) up; codes [R][2][I] int8 and scales [R][2][blocks] float32 keep gate and up."""
         what, dev, I, act = "nvfp4_swiglu_forward", self.device, self.I, self._act
         gp, ldg, R = _rows(gate, I, act, dev, what)
-        up_, ldu, Ru = _rows(up, I, act, dev, what)
-        op, ldo, Ro = _rows(out, I, act, dev, what)
-        self._same_rows(what, R, Ru, Ro)
-        st = self.lib.nvfp4_swiglu_forward(
-            self.h, R, gp, ldg, up_, ldu, op, ldo,
-            None if codes is None else _whole(codes, (R, 2, I), self._int8, dev, what),
-            None if scales is None else _whole(scales, (R, 2, self.blocks), self._f32, dev, what), self._st(stream))
+        shape = (R, I)
+        up_, ldu = _rows_like(up, shape, act, dev, what)
+        op, ldo = _rows_like(out, shape, act, dev, what)
+        st = self.lib.nvfp4_swiglu_forward(self.h, R, gp, ldg, up_, ldu, op, ldo,
+                                           _whole_or_none(codes, (R, 2, I), self._int8, dev, what),
+                                           _whole_or_none(scales, (R, 2, self.blocks), self._f32, dev, what),
+                                           self._st(stream))
         if st:
             self._check(st, what)
         return out
@@ -678,9 +687,9 @@ class SwiGLU(_Operator):
         """dgate and dup from the forward's codes and scales."""
         what, dev, I, act = "nvfp4_swiglu_backward", self.device, self.I, self._act
         dp, ldd, R = _rows(dh, I, act, dev, what)
-        gp, ldg, Rg = _rows(dgate, I, act, dev, what)
-        up_, ldu, Ru = _rows(dup, I, act, dev, what)
-        self._same_rows(what, R, Rg, Ru)
+        shape = (R, I)
+        gp, ldg = _rows_like(dgate, shape, act, dev, what)
+        up_, ldu = _rows_like(dup, shape, act, dev, what)
         st = self.lib.nvfp4_swiglu_backward(self.h, R, _whole(codes, (R, 2, I), self._int8, dev, what),
                                             _whole(scales, (R, 2, self.blocks), self._f32, dev, what), dp, ldd, gp, ldg,
                                             up_, ldu, self._st(stream))
@@ -705,8 +714,7 @@ class Int8Linear(_Operator):
         what, dev = "nvfp4_int8_pack", self.device
         st = self.lib.nvfp4_int8_pack(self.h, _whole(w, (self.N, self.K), self._int8, dev, what),
                                       _whole(w_scale, (self.N,), self._f32, dev, what),
-                                      None if bias is None else _whole(bias, (self.N,), self._f32, dev, what),
-                                      self._st(stream))
+                                      _whole_or_none(bias, (self.N,), self._f32, dev, what), self._st(stream))
         self._check(st, what)
 
     def nvfp4_int8_quantize(self, x, q, q_scale, stream=None):
@@ -716,8 +724,7 @@ class Int8Linear(_Operator):
         if code is None:
             raise ValueError(f"{what}: expected a bfloat16 or float16 x, got {x.dtype}")
         xp, ldx, T = _rows(x, self.K, x.dtype, dev, what)
-        qp, ldq, Tq = _rows(q, self.K, self._int8, dev, what)
-        self._same_rows(what, T, Tq)
+        qp, ldq = _rows_like(q, (T, self.K), self._int8, dev, what)
         st = self.lib.nvfp4_int8_quantize(self.h, T, xp, code, ldx, qp, ldq, _whole(q_scale, (T,), self._f32, dev, what),
                                           self._st(stream))
         if st:
@@ -730,8 +737,7 @@ class Int8Linear(_Operator):
         xp, ldx, T = _rows(x, self.K, self._int8, dev, what)
         if T <= 1:
             ldx = -(-self.K // 16) * 16
-        op, ldo, To = _rows(out, self.N, self._out, dev, what)
-        self._same_rows(what, T, To)
+        op, ldo = _rows_like(out, (T, self.N), self._out, dev, what)
         st = self.lib.nvfp4_int8_forward(self.h, T, xp, ldx, _whole(x_scale, (T,), self._f32, dev, what), op, ldo,
                                          self._st(stream))
         if st:

@@ -663,71 +663,88 @@ __global__ void __launch_bounds__(rt::kThreads) route_scatter_rows_kernel(RouteA
   }
 }
 
-// dl of a token from the gradient of its weights.  An id outside 0 .. E - 1 counts as no choice.
+// dl of a token from the gradient of its weights.  Renormalised weights and sigmoids move with the chosen logits alone:
+// lanes j < k form those and lay them into a row of zeros in shared memory.  Plain softmax: s (d - sum d s) of all E, d the
+// weights' gradient laid out so.  One slot after the other, so that an expert named twice gets both, in one order.
+// An id outside 0 .. E - 1 counts as no choice.
 namespace rt {
 constexpr int kBackThreads = 256;
 }
 template <int V>
 __global__ void __launch_bounds__(rt::kBackThreads) route_backward_kernel(RouteArgs a) {
+  __shared__ float rows[rt::kBackThreads / 32][32 * V];
   grid_dependency_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = rt::kBackThreads / 32;
+  const bool sparse = a.score || a.renorm;
+  float* row = rows[warp];
   for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) {
-    float l[V], d[V];
-    load_lane<V>(a, t, l);
-    unsigned chosen = 0;
+    float l[V];
+    if (!sparse) load_lane<V>(a, t, l);
     const int id = lane < a.k ? a.cids[(size_t)t * a.k + lane] : -1;
-    const float w = lane < a.k ? a.dw[(size_t)t * a.k + lane] * a.scale : 0.f;
+    float v = lane < a.k ? a.dw[(size_t)t * a.k + lane] * a.scale : 0.f;
+    const bool ok = (unsigned)id < (unsigned)a.E;
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = 0.f;
+    for (int i = 0; i < V; ++i) row[lane + 32 * i] = 0.f;
+    Softmax<float> sm{0.f, 0.f, 0};
+    if (sparse) {
+      const float x = ok ? load_logit(a.logits, a.bf16, (size_t)t * a.ld + id) : __uint_as_float(0x7FC00000u);
+      const bool counts = x == x;
+      if (a.score) {
+        const float s = counts ? score_of<float>(x, 1, sm, a.E) : 0.f, rest = counts ? score_of<float>(-x, 1, sm, a.E) : 0.f;
+        if (a.renorm) {
+          const float sum = warp_sum(s), dot = warp_sum(counts ? v * s : 0.f);
+          v = sum > 0.f ? (v - dot / sum) / sum : 0.f;
+        }
+        v = counts && v != 0.f ? v * s * rest : 0.f;
+      } else {
+        const float top = warp_max(counts ? x : -INFINITY);
+        const bool flat = fabsf(top) == INFINITY;  // weights that do not move with the logits
+        const float e = counts && !flat ? expf(x - top) : 0.f, sum = warp_sum(e), s = flat ? 0.f : e / sum;
+        const float dot = warp_sum(counts ? v * s : 0.f);
+        v = counts ? s * (v - dot) : 0.f;
+      }
+    } else {
+      sm.top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sm.top = fmaxf(sm.top, l[i]);
+      sm.top = warp_max(sm.top);
+    }
+    __syncwarp();
     for (int j = 0; j < a.k; ++j) {
-      const int at = __shfl_sync(0xffffffffu, id, j) - lane;
-      const float v = __shfl_sync(0xffffffffu, w, j);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (at == 32 * i && lane + 32 * i < a.E) d[i] = v, chosen |= 1u << i;
+      if (lane == j && ok) row[id] += v;
+      __syncwarp();
     }
-    float s[V];  // the scores that the weights are made of
-    if (a.score) {
+    float o[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = score_of<float>(l[i], 1, Softmax<float>{}, a.E);
-    } else {
-      // renormalised: the softmax of the chosen logits alone
-      float m[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) m[i] = !a.renorm || ((chosen >> i) & 1u) ? l[i] : __uint_as_float(0x7FC00000u);
-      const Softmax<float> sm = softmax_of<float>(m);
-      const bool flat = sm.top == INFINITY || sm.top == -INFINITY;  // weights that do not move with the logits
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = flat ? 0.f : score_of<float>(m[i], 0, sm, a.E);
-    }
-    if (a.score && a.renorm) {
-      float sum = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if ((chosen >> i) & 1u) sum += s[i], dot = fmaf(d[i], s[i], dot);
-      sum = warp_sum(sum), dot = warp_sum(dot);
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = ((chosen >> i) & 1u) && sum > 0.f ? (d[i] - dot / sum) / sum : 0.f;
-    }
-    if (a.score) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = d[i] == 0.f || l[i] != l[i] ? 0.f : d[i] * s[i] * score_of<float>(-l[i], 1, Softmax<float>{}, a.E);
-    } else {
+    for (int i = 0; i < V; ++i) o[i] = row[lane + 32 * i];
+    if (!sparse) {
+      const bool flat = fabsf(sm.top) == INFINITY;
       float dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) dot = fmaf(d[i], s[i], dot);
-      dot = warp_sum(dot);
+      for (int i = 0; i < V; ++i) {
+        l[i] = l[i] == l[i] && !flat ? __expf(l[i] - sm.top) : 0.f;
+        sm.sum += l[i];
+        dot = fmaf(o[i], l[i], dot);
+      }
+      const float inv = flat ? 0.f : 1.0f / warp_sum(sm.sum);
+      dot = warp_sum(dot) * inv;
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = s[i] * (d[i] - dot);
+      for (int i = 0; i < V; ++i) o[i] = l[i] * inv * (o[i] - dot);
     }
     const size_t at = (size_t)t * a.ld_dl + lane;
+    if (a.bf16) {
+      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.dl) + at;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < a.E) {
-        if (a.bf16) static_cast<__nv_bfloat16*>(a.dl)[at + 32 * i] = __float2bfloat16_rn(d[i]);
-        else static_cast<float*>(a.dl)[at + 32 * i] = d[i];
-      }
+      for (int i = 0; i < V; ++i)
+        if (lane + 32 * i < a.E) p[32 * i] = __float2bfloat16_rn(o[i]);
+    } else {
+      float* p = static_cast<float*>(a.dl) + at;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (lane + 32 * i < a.E) p[32 * i] = o[i];
+    }
+    __syncwarp();
   }
 }
 

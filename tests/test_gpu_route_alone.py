@@ -191,6 +191,24 @@ def test_ids_that_name_no_expert():
     h.close()
 
 
+@pytest.mark.parametrize("score,renorm", list(itertools.product(["softmax", "sigmoid"], [False, True])))
+def test_an_expert_named_twice_counts_twice(score, renorm):
+    E, k = 40, 6
+    rng = np.random.default_rng(2)
+    h = P.Route(E, k, score=score, renormalize=renorm)
+    l, dw = dev(rng.standard_normal((50, E)).astype(np.float32)), dev(rng.standard_normal((50, k)).astype(np.float32))
+    ids = dev(rng.integers(0, 4, (50, k)).astype(np.int32))
+    dl = [torch.empty_like(l) for _ in range(2)]
+    for d in dl:
+        h.nvfp4_route_backward(l, ids, dw, d)
+    assert torch.equal(*dl)
+    x = l.double().cpu().requires_grad_()
+    (route_weights_of(x, ids.cpu().long(), score, renorm, 1.0) * dw.double().cpu()).sum().backward()
+    # k slots whose terms are at most |dw| s, each off by the scores' bound (test_backward), added k times
+    within(f64(dl[0]), x.grad.numpy(), 8 * (E / 32 + 40) * U * k * np.abs(f64(dw)).max(axis=1, keepdims=True), "dlogits")
+    h.close()
+
+
 def test_strides_and_no_tokens():
     rng = np.random.default_rng(3)
     for E, bf16, pad in ((64, False, 3), (64, False, 4), (64, True, 8), (60, True, 1), (256, False, 0)):
