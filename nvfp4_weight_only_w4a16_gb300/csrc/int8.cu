@@ -81,7 +81,7 @@ struct Int8Args {
   // GEMM
   int NB, NU;      // 128-feature blocks; units across the features
   int tiles, per;  // token tiles, and tokens of each
-  int halves;      // 64-long steps of the reduction
+  int squares;     // 128-long steps of the reduction
   int split;       // CTAs that share a unit
 };
 
@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(i8v::kThreads, 1) int8_gemv_kernel(Int8Args a)
 // 1024 elements, to stay exact, and that passes under the next 1024's MMAs.
 //
 // A warp takes some 370 cycles for its 32 rows of 64 elements, most of it waiting, and the MMAs of 192 tokens 384.  With
-// fewer tokens, where the matrix's bytes are what there is to wait for, two teams of four warps take turns.
+// fewer tokens, where the matrix's bytes are what there is to wait for, two teams of four warps take turns.  So does the
+// issuer take 80 cycles a wait and 50 a commit, next to 30 an MMA: with both for every four MMAs it was what all variants
+// waited for (460 cycles for 64 elements), and where tensor memory has the room a stage is a whole square.
 //
 // kSplit: where there are few units, a cluster of CTAs takes one, a share of the reduction each, and adds the integers
 // through distributed shared memory.
@@ -277,9 +279,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kCtlBytes = 2048, kEpiBytes = 2048;  // per epilogue warp
 constexpr int kRingOff = kCtlBytes + kEpiWarps * kEpiBytes;
 constexpr int kRoom = i8::kSmemMax - 1024 - kRingOff;
-constexpr int kSegment = 16;                       // 64-long steps whose sums FP32 holds exactly
-constexpr int kStagesA = 4;                        // of the matrix, 64 elements each: 32 columns of tensor memory
-constexpr int kMaxStages = 8, kMaxRaw = 8, kMaxSplit = 8;
+constexpr int kSegment = 8;                        // squares whose sums FP32 holds exactly
+constexpr int kStagesA = 4;                        // of the matrix, in tensor memory: 32 columns for 64 elements
+constexpr int kMaxStages = 4, kMaxRaw = 8, kMaxSplit = 8;
 
 template <int kCtas, int kTile>
 struct Plan {
@@ -290,16 +292,17 @@ struct Plan {
   static constexpr int kRowWarps = 4 * kTeams, kToken0 = kRowWarps + kEpiWarps, kProducer = kToken0 + kTokenWarps;
   static constexpr int kTokens = kProducer + 1, kIssuer = kTokens + 1, kThreads = 32 * (kIssuer + 1);
   static constexpr int kShare = kTile / kCtas;               // tokens of a CTA
-  static constexpr int kBBytes = kShare * 128;               // a stage of them, 64 elements in FP16
+  static constexpr int kBBytes = kShare * 256;               // a stage of them, 128 elements in FP16: two halves of 64
   static constexpr int kXBytes = kPre ? 0 : kShare * 128;    // a raw slot of them, 128 elements in bytes
-  static constexpr int kStagesB = kTile == 192 ? 8 : kTile == 128 ? 6 : kStagesA;
+  static constexpr int kStagesB = kTile == 128 ? 3 : 4;
   static constexpr int kRaw = 6;                             // raw slots, squares
+  static constexpr int kHalves = kTile == 192 ? 1 : 2;       // of a square in a stage of the matrix, 64 elements each
   static constexpr uint32_t kOperand = 2 * kTile;            // the matrix's first column in tensor memory
   static constexpr int kRings = kStagesB * kBBytes + kRaw * (kXBytes + i8::kSquare);
-  static_assert(kRings <= kRoom && kRaw <= kMaxRaw && kStagesB <= kMaxStages && 2 * kTile + 32 * kStagesA <= 512, "rings");
-  static_assert(kBBytes % 1024 == 0, "128B-swizzled tiles");
+  static_assert(kRings <= kRoom && kRaw <= kMaxRaw && kStagesB <= kMaxStages && 2 * kTile + 32 * kHalves * kStagesA <= 512, "rings");
+  static_assert(kBBytes % 2048 == 0 && (kPre || (kStagesB == kStagesA && kHalves == 2)), "128B-swizzled tiles");
   // a team meets every slot of a ring again itself: a parity wait must not run two phases ahead of its barrier
-  static_assert(kRaw % kTeams == 0 && kStagesA % (2 * kTeams) == 0, "teams");
+  static_assert(kRaw % kTeams == 0 && kStagesA % kTeams == 0 && (kTeams == 1 || kHalves == 2), "teams");
 };
 }  // namespace i8g
 
@@ -330,9 +333,9 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
   const int part = kSplit ? (int)cluster_rank() : 0;
   const int first = kSplit ? blockIdx.x / a.split : blockIdx.x / kCtas;
   const int stride = kSplit ? gridDim.x / a.split : gridDim.x / kCtas;  // split: no CTA has a second unit
-  const int squares = (a.halves + 1) / 2;
+  const int squares = a.squares;
   const int sq0 = kSplit ? part * squares / a.split : 0, sq1 = kSplit ? (part + 1) * squares / a.split : squares;
-  const int steps = 2 * (sq1 - sq0);  // 64-long; the packed matrix is whole squares
+  const int steps = sq1 - sq0;        // squares
   constexpr int kRound = 16 * kCtas;  // the MMA's columns come in these
   const int total = a.tiles * a.NU;
   volatile int* abort_flag = &ctl.abort_flag;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
     }
     if (!ok && lane == 0) drain_copies(ctl.raw_full, it, Plan::kRaw);
   } else if (warp == Plan::kTokens) {
-    // ---------------- tokens in FP16: this CTA's half of the tile, 64 elements a stage ----------------
+    // ---------------- tokens in FP16: this CTA's half of the tile, 128 elements a stage ----------------
     if constexpr (Plan::kPre) {
       grid_dependency_wait();
       uint32_t it = 0;
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
         int row0;
         const int share = columns(tokens_of(u, row0)) / kCtas;
         row0 += rank * share;
-        for (int s = 2 * sq0; s < 2 * sq1; ++s, ++it, p.step(Plan::kStagesB)) {
+        for (int s = sq0; s < sq1; ++s, ++it, p.step(Plan::kStagesB)) {
           if (!warp_wait(ctl.b_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 937)) {
             ok = false;
             break;
@@ -437,8 +440,12 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
           if (elect_one()) {
             uint8_t* dst = ring_b + p.slot * Plan::kBBytes;
             if (rank == 0) mbar_arrive_expect_tx(ctl.b_full + p.slot, (uint32_t)(kCtas * Plan::kBBytes));
-            if (kCtas == 2) tma_2d_pair(dst, &x_map, s * 64, row0, map_rank(ctl.b_full + p.slot, 0));
-            else tma_2d(dst, &x_map, s * 64, row0, ctl.b_full + p.slot);
+            const uint32_t bar0 = kCtas == 2 ? map_rank(ctl.b_full + p.slot, 0) : 0u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (kCtas == 2) tma_2d_pair(dst + h * (Plan::kBBytes / 2), &x_map, s * 128 + h * 64, row0, bar0);
+              else tma_2d(dst + h * (Plan::kBBytes / 2), &x_map, s * 128 + h * 64, row0, ctl.b_full + p.slot);
+            }
           }
           __syncwarp();
         }
@@ -468,30 +475,38 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
           const uint32_t d = tmem + buf * kTile;
           const int end = min(s + i8g::kSegment, steps);
           uint32_t add = 0;
-          for (int i = s; i < end; ++i, pa.step(i8g::kStagesA), pb.step(Plan::kStagesB)) {
-            if ((Plan::kPre && !warp_wait(ctl.b_full + pb.slot, pb.phase, abort_flag, a.st, 938)) ||
-                !warp_wait(ctl.a_full + pa.slot, pa.phase, abort_flag, a.st, 933)) {
+          for (int i = s; i < end && ok; ++i, pb.step(Plan::kStagesB)) {
+            if (Plan::kPre && !warp_wait(ctl.b_full + pb.slot, pb.phase, abort_flag, a.st, 938)) {
               ok = false;
               break;
             }
-            tc_fence_after();
             const uint64_t bd = sw128_desc(b_addr + (uint32_t)(pb.slot * Plan::kBBytes));
-            const uint32_t at = tmem + Plan::kOperand + (uint32_t)pa.slot * 32u;  // 8 columns per 16 elements
-            if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                if (kCtas == 2) umma_ts_pair(d, at + 8u * kk, bd + 2u * kk, idesc, kk ? 1u : add);
-                else umma_ts(d, at + 8u * kk, bd + 2u * kk, idesc, kk ? 1u : add);
+            for (int g = 0; g < 2 / Plan::kHalves; ++g, pa.step(i8g::kStagesA)) {
+              if (!warp_wait(ctl.a_full + pa.slot, pa.phase, abort_flag, a.st, 933)) {
+                ok = false;
+                break;
               }
-              if (kCtas == 2) umma_commit_pair(ctl.a_empty + pa.slot);
-              else umma_commit(ctl.a_empty + pa.slot);
-              if (Plan::kPre) {
-                if (kCtas == 2) umma_commit_pair(ctl.b_empty + pb.slot);
-                else umma_commit(ctl.b_empty + pb.slot);
+              tc_fence_after();
+              const uint32_t at = tmem + Plan::kOperand + (uint32_t)(pa.slot * 32 * Plan::kHalves);  // 8 columns per 16 elements
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4 * Plan::kHalves; ++kk) {
+                  const int k = 4 * g + kk;  // of the square's 8
+                  const uint64_t bk = bd + (uint32_t)((k >> 2) * (Plan::kBBytes / 2) >> 4) + 2u * (k & 3);
+                  if (kCtas == 2) umma_ts_pair(d, at + 8u * kk, bk, idesc, k ? 1u : add);
+                  else umma_ts(d, at + 8u * kk, bk, idesc, k ? 1u : add);
+                }
+                if (kCtas == 2) umma_commit_pair(ctl.a_empty + pa.slot);
+                else umma_commit(ctl.a_empty + pa.slot);
+                if (Plan::kPre && g == 2 / Plan::kHalves - 1) {
+                  if (kCtas == 2) umma_commit_pair(ctl.b_empty + pb.slot);
+                  else umma_commit(ctl.b_empty + pb.slot);
+                }
               }
+              __syncwarp();
             }
             add = 1;
-            __syncwarp();
           }
           if (!ok) break;
           if (elect_one()) {
@@ -511,7 +526,7 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
       __syncwarp();
     }
   } else if (warp < Plan::kRowWarps || warp >= Plan::kToken0) {
-    // ---------------- converters: a raw slot makes two stages; the teams take turns at the slots ----------------
+    // ---------------- converters: a raw slot makes a stage or two; the teams take turns at the slots ----------------
     const bool rows = warp < Plan::kRowWarps;
     constexpr int kTeamTokens = Plan::kPre ? 1 : Plan::kTokenWarps / Plan::kTeams;  // a team's warps for tokens
     constexpr int kOctets = Plan::kPre ? 1 : Plan::kShare / 8 / kTeamTokens;        // of 8 tokens, of one of them
@@ -521,57 +536,66 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
     const uint32_t full0 = kCtas == 2 ? map_rank(ctl.a_full, 0) : 0u;  // the pair's first CTA's
     const int all = first < total ? ((total - first - 1) / stride + 1) * (sq1 - sq0) : 0;  // squares of this CTA
     RingPos raw, p;
-    raw.slot = team;
-    p.slot = 2 * team;
+    raw.slot = p.slot = team;
+    const auto tell = [&] {  // the stage is written
+      __syncwarp();
+      if (lane == 0) {
+        if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + p.slot * 8);
+        else mbar_arrive(ctl.a_full + p.slot);
+      }
+    };
     bool ok = true;
     for (int n = team; n < all && ok; n += Plan::kTeams, raw.step(Plan::kRaw, Plan::kTeams)) {
       if (!warp_wait(ctl.raw_full + raw.slot, raw.phase, abort_flag, a.st, 934)) break;
-      const uint32_t w_slot = w_addr + raw.slot * i8::kSquare + (uint32_t)(32 * w0 + lane) * 16u;
-      const uint32_t x_slot = x_addr + raw.slot * Plan::kXBytes;
+      if (rows) {
+        const uint32_t slot = w_addr + raw.slot * i8::kSquare + (uint32_t)(32 * w0 + lane) * 16u;
 #pragma unroll
-      for (int h = 0; h < 2; ++h, p.step(i8g::kStagesA)) {
-        if (rows) {
+        for (int h = 0; h < 2; ++h) {
           uint32_t v[4][8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) bytes_to_f16(lds128(w_slot + (4 * h + i) * 2048), v[i]);
-          if (!warp_wait(ctl.a_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 935)) {
-            ok = false;
-            break;
+          for (int i = 0; i < 4; ++i) bytes_to_f16(lds128(slot + (4 * h + i) * 2048), v[i]);
+          if (Plan::kHalves == 1 || h == 0) {
+            if (!warp_wait(ctl.a_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 935)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
           }
-          tc_fence_after();
-          tmem_st32(tmem + lanes + Plan::kOperand + (uint32_t)p.slot * 32u, v);
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          tc_fence_before();
-        } else if constexpr (!Plan::kPre) {
-          // 8 tokens of 16 elements a quarter of a warp; all lie in banks of their own, going in and coming out.  All
-          // reads first: there is no other warp to hide what one takes
-          uint4 x[kOctets];
-          const int q = lane >> 3, m = lane & 7;
+          tmem_st32(tmem + lanes + Plan::kOperand + (uint32_t)(p.slot * 32 * Plan::kHalves) + (Plan::kHalves == 2 ? 32u * h : 0u), v);
+          if (Plan::kHalves == 1 || h == 1) {
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            tell();
+            p.step(i8g::kStagesA, Plan::kTeams);
+          }
+        }
+      } else if constexpr (!Plan::kPre) {
+        // 8 tokens of 16 elements a quarter of a warp; all lie in banks of their own, going in and coming out.  All
+        // reads first: there is no other warp to hide what one takes
+        const uint32_t slot = x_addr + raw.slot * Plan::kXBytes;
+        uint4 x[2][kOctets];
+        const int q = lane >> 3, m = lane & 7;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int o = 0; o < kOctets; ++o)
-            x[o] = lds128(x_slot + (uint32_t)(8 * (w0 + kTeamTokens * o) + m) * 128u + (uint32_t)((4 * h + q) ^ m) * 16u);
-          if (!warp_wait(ctl.a_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 939)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = b_addr + (uint32_t)(p.slot * Plan::kBBytes);
+            x[h][o] = lds128(slot + (uint32_t)(8 * (w0 + kTeamTokens * o) + m) * 128u + (uint32_t)((4 * h + q) ^ m) * 16u);
+        if (!warp_wait(ctl.a_empty + p.slot, p.phase ^ 1u, abort_flag, a.st, 939)) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int o = 0; o < kOctets; ++o) {
-            const uint32_t row = st + (uint32_t)(8 * (w0 + kTeamTokens * o) + m) * 128u;
+            const uint32_t row = b_addr + (uint32_t)(p.slot * Plan::kBBytes + h * (Plan::kBBytes / 2)) +
+                                 (uint32_t)(8 * (w0 + kTeamTokens * o) + m) * 128u;
             uint32_t u[8];
-            bytes_to_f16(biased(x[o]), u);
+            bytes_to_f16(biased(x[h][o]), u);
             sts128(row + (uint32_t)((2 * q) ^ m) * 16u, u[0], u[1], u[2], u[3]);
             sts128(row + (uint32_t)((2 * q + 1) ^ m) * 16u, u[4], u[5], u[6], u[7]);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncwarp();
-        if (lane == 0) {
-          if (kCtas == 2 && rank) mbar_arrive_cluster(full0 + p.slot * 8);
-          else mbar_arrive(ctl.a_full + p.slot);
-        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tell();
+        p.step(i8g::kStagesA, Plan::kTeams);
       }
-      if (Plan::kTeams == 2) p.step(i8g::kStagesA, 2);  // the other team's
       // what was read of the slot has been stored since
       if (ok && lane == 0) mbar_arrive(ctl.raw_empty + raw.slot);
     }
@@ -710,15 +734,15 @@ struct Int8Variant {
   Int8Gemm fn;
   int ctas, tile, threads;
   bool split;
-  int cost;  // cycles of 64 elements of the reduction, about
+  double square, base;  // us that a square takes a unit, and that a call takes beside its squares, measured
 };
 template <int kCtas, int kTile, bool kSplit>
-static constexpr Int8Variant int8_variant(int cost) {
-  return {int8_gemm_kernel<kCtas, kTile, kSplit>, kCtas, kTile, i8g::Plan<kCtas, kTile>::kThreads, kSplit, cost};
+static constexpr Int8Variant int8_variant(double square, double base) {
+  return {int8_gemm_kernel<kCtas, kTile, kSplit>, kCtas, kTile, i8g::Plan<kCtas, kTile>::kThreads, kSplit, square, base};
 }
-static const Int8Variant kInt8Variants[] = {int8_variant<1, 64, false>(320), int8_variant<1, 128, false>(320),
-                                            int8_variant<2, 192, false>(400), int8_variant<1, 64, true>(320),
-                                            int8_variant<1, 128, true>(320)};
+static const Int8Variant kInt8Variants[] = {int8_variant<1, 64, false>(0.35, 3.2), int8_variant<1, 128, false>(0.48, 3.2),
+                                            int8_variant<2, 192, false>(0.53, 4.5), int8_variant<1, 64, true>(0.35, 4.3),
+                                            int8_variant<1, 128, true>(0.48, 5.0)};
 
 // Tokens as FP16: a thread 16 elements, zeros from K on.
 __global__ void __launch_bounds__(256) int8_tokens_kernel(const int8_t* x, long long ldx, int T, int K, int Kp, uint16_t* out) {
@@ -799,18 +823,26 @@ size_t int8_workspace_bytes(int K, int max_tokens) {
 }
 
 Int8Tiling int8_tiling(int N, int K, int T, int num_sms) {
-  // The variant whose rounds of units take the least time by the costs of a step above and some 3000 cycles a unit.
+  // The variant whose rounds of units take the least time by what was measured of each: its squares, 0.6 us a unit, and its
+  // base, with 2 us and the bytes at 6 TB/s where the tokens are converted first.  Of the variants in that order, us, for
+  // 12576 x 4096 and 64 tokens 15 / - / -, 128 26 / 21 / 24, 256 37 / 36 / 40, 512 70 / 51 / 42, 2048 - / 172 / 140; for
+  // 4096 x 4096 and 64 tokens 15 whole, 10 and 9 with 2 and 4 CTAs a unit; 128 tokens 11 with tiles of 64 and 2 CTAs, 13
+  // of 128 and 4.  Clusters of 4 fit the machine 36 at a time, of 8 some 13 (512 x 4096, 192 tokens, 12 units of 8 CTAs
+  // 7.5 us, 256 tokens, 16 units, 13.5).
   const int blocks = (N + 127) / 128, squares = (K + 127) / 128;
   Int8Tiling best{};
   double least = 1e300;
   for (int i = 0; i < (int)(sizeof(kInt8Variants) / sizeof(kInt8Variants[0])); ++i) {
     const Int8Variant& v = kInt8Variants[i];
     const long long units = (long long)((blocks + v.ctas - 1) / v.ctas) * ((T + v.tile - 1) / v.tile);
+    const bool fp16 = v.tile > 64;
     for (int split = v.split ? 2 : 1; split <= (v.split ? i8g::kMaxSplit : 1); split *= 2) {
-      if (v.split && (units * split > num_sms * 15 / 16 || 2 * split > squares)) break;
-      const long long slots = num_sms / (v.ctas * split), rounds = (units + slots - 1) / slots;
-      const double t = (double)rounds * ((squares + split - 1) / split * 2.0 * v.cost + 3000.0);
-      if (t < least) least = t, best = {i, v.tile / v.ctas, split, v.tile > 64};
+      const long long slots = num_sms * (split == 8 ? 11 : split > 1 ? 15 : 16) / 16 / (v.ctas * split);
+      if (v.split && (units > slots || 2 * split > squares)) break;
+      const long long rounds = (units + slots - 1) / slots;
+      const double t = (double)rounds * ((squares + split - 1) / split * v.square + 0.6) + v.base +
+                       (fp16 ? 2.0 + (double)T * squares * 128 * 3 / 6e6 : 0.0);
+      if (t < least) least = t, best = {i, v.tile / v.ctas, split, fp16};
     }
   }
   return best;
@@ -827,7 +859,7 @@ cudaError_t launch_int8_gemm(const Int8Product& p, const Int8Tiling& t, const CU
   const int round = 16 * v.ctas;
   a.per = ((a.T + a.tiles - 1) / a.tiles + round - 1) / round * round;  // tiles of one size, so that none is a small rest
   a.tiles = (a.T + a.per - 1) / a.per;
-  a.halves = (a.K + 63) / 64;
+  a.squares = (a.K + 127) / 128;
   a.split = t.split;
   cudaLaunchConfig_t cfg{};
   const int units = a.tiles * a.NU;
