@@ -181,34 +181,52 @@ __global__ void __launch_bounds__(i8v::kThreads, 1) int8_gemv_kernel(Int8Args a)
     slot_in = slot_in == i8v::kDepth - 1 ? 0 : slot_in + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // the matrix is no kernel's output: its copies start before the wait for the kernel before
-#pragma unroll
-  for (int i = 0; i < i8v::kDepth - 1; ++i) push();
+  // The matrix is no kernel's output: its copies start before the wait for the kernel before.  One stage of them: what is
+  // asked for after two, 20 MB over the machine, comes 3 us later, and the tokens are wanted first (4096 x 4096, 1 token,
+  // from memory 8.2 us).
+  push();
   for (int i = threadIdx.x; i < 8 * kTiles * pitch; i += i8v::kThreads) sums[i] = 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (threadIdx.x < a.T) sx[threadIdx.x] = a.x_scale[threadIdx.x];
+  uint32_t x[kTiles][i8v::kBlocks][8];  // B fragments: lane (n = r, c) holds elements 16 c .. 16 c + 15 of each 64 of token n
+  const auto load_x = [&](int pass, uint4 (&v)[kTiles][i8v::kBlocks]) {
+    const int k0 = k_of(pass);
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int b = 0; b < i8v::kBlocks; ++b) {
+        const int t = 8 * n + r, k = k0 + 64 * b + 16 * c;
+        v[n][b] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < a.T && 64 * b < a.slice && k < a.K) v[n][b] = *reinterpret_cast<const uint4*>(a.x + t * a.ldx + k);
+      }
+  };
+  const auto convert_x = [&](const uint4 (&v)[kTiles][i8v::kBlocks]) {
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int b = 0; b < i8v::kBlocks; ++b) bytes_to_f16(biased(v[n][b]), x[n][b]);
+  };
+  int loaded = 0;
+  {
+    uint4 v[kTiles][i8v::kBlocks];
+    load_x(0, v);
+    const float s = threadIdx.x < a.T ? a.x_scale[threadIdx.x] : 0.f;
+#pragma unroll
+    for (int i = 1; i < i8v::kDepth - 1; ++i) push();
+    if (threadIdx.x < a.T) sx[threadIdx.x] = s;
+    convert_x(v);
+  }
   __syncthreads();
 
-  uint32_t x[kTiles][i8v::kBlocks][8];  // B fragments: lane (n = r, c) holds elements 16 c .. 16 c + 15 of each 64 of token n
-  int loaded = -1;
   for (int b0 = g0; b0 < g1; b0 += a.batch) {
     const int rows = 16 * (min(b0 + a.batch, g1) - b0), f0 = 16 * b0;
     for (int i = threadIdx.x; i < rows; i += i8v::kThreads)
       if (f0 + i < a.N) sw[i] = a.w_scale[f0 + i], add[i] = a.bias ? a.bias[f0 + i] : 0.f;
     while (valid(now) && now.b0 == b0) {
       if (now.pass != loaded) {
-        loaded = now.pass;
-        const int k0 = k_of(loaded);
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int b = 0; b < i8v::kBlocks; ++b) {
-            const int t = 8 * n + r, k = k0 + 64 * b + 16 * c;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (t < a.T && 64 * b < a.slice && k < a.K) v = *reinterpret_cast<const uint4*>(a.x + t * a.ldx + k);
-            bytes_to_f16(biased(v), x[n][b]);
-          }
+        uint4 v[kTiles][i8v::kBlocks];
+        load_x(loaded = now.pass, v);
+        convert_x(v);
       }
       push();
       asm volatile("cp.async.wait_group %0;" ::"n"(i8v::kDepth - 1) : "memory");
