@@ -30,8 +30,9 @@ namespace nvfp4moe {
 
 namespace rt {
 constexpr int kMaxExperts = 512;
-constexpr int kThreads = 1024;
-constexpr int kOneCta = 128;  // tokens up to which one CTA does it all
+constexpr int kThreads = 768;   // of 80 registers; 1024 of 64 spill (16384 x 256 in groups 40.2 us, 39.0)
+constexpr int kOneCta = 72;     // tokens up to which one CTA does it all (256 experts in groups, 64 tokens: 15.1 us, 16.2 as
+                                // three kernels; 96: 19.8, 16.1)
 constexpr int kRun = 256;     // of a run, unless its counts need more
 constexpr int kMostShared = 208 * 1024;  // 512 experts: 128 KB of 32 warps' rows and 64 KB of a run's bits
 }  // namespace rt
@@ -194,6 +195,45 @@ __device__ __forceinline__ F group_value(const RouteArgs& a, const F* row, F* si
   const int from = (lane * per) & 31;
   *size = __shfl_sync(0xffffffffu, sizes, from);
   *least = __shfl_sync(0xffffffffu, a.group_top == 2 ? y : x, from);
+  return __shfl_sync(0xffffffffu, value, from);
+}
+
+// The same where groups are of 32 experts, so that group i is register i of all lanes (groups = V): the lanes halve the
+// registers they keep, exchanging the others, with each of the first steps.  c holds no NaN.
+template <int V>
+__device__ __forceinline__ float group_value_32(const RouteArgs& a, const float (&c)[V], float* size, float* least) {
+  const int lane = threadIdx.x & 31;
+  float x[V], y[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = c[i];
+  int o = 16;
+#pragma unroll
+  for (int n = V / 2; n >= 1; n /= 2, o /= 2) {  // registers kept
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = upper ? x[i + n] : x[i], x2 = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i + n], o);
+      if (n == V / 2) {
+        y[i] = fminf(keep, x2);
+        x[i] = fmaxf(keep, x2);
+      } else {
+        const float keep_y = upper ? y[i + n] : y[i], y2 = __shfl_xor_sync(0xffffffffu, upper ? y[i] : y[i + n], o);
+        x[i] = keep, y[i] = keep_y;
+        merge_two(x[i], y[i], x2, y2);
+      }
+    }
+  }
+#pragma unroll
+  for (; o >= 1; o /= 2) {
+    const float x2 = __shfl_xor_sync(0xffffffffu, x[0], o), y2 = __shfl_xor_sync(0xffffffffu, y[0], o);
+    merge_two(x[0], y[0], x2, y2);
+  }
+  float value = a.group_top == 2 ? x[0] + y[0] : x[0];
+  if (value != value) value = -INFINITY;  // infinities of both signs
+  // group g is with the lanes whose first bits, from 16 down, are g's
+  const int from = (lane * (32 / V)) & 31;
+  *size = __shfl_sync(0xffffffffu, a.group_top == 2 ? fabsf(x[0]) + fabsf(y[0]) : fabsf(x[0]), from);
+  *least = __shfl_sync(0xffffffffu, a.group_top == 2 ? y[0] : x[0], from);
   return __shfl_sync(0xffffffffu, value, from);
 }
 
@@ -412,12 +452,20 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, const flo
   unsigned open = of.all;
   bool exact = true;  // the groups are certain
   if (limited) {
-    float size, least, *r = reinterpret_cast<float*>(row);
+    float size, least, mine;
+    if (V > 1 && a.group_size == 32 && a.groups == V) {
+      float clean[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < a.E) r[lane + 32 * i] = c[i];
-    __syncwarp();
-    const float mine = group_value<float>(a, r, &size, &least);
+      for (int i = 0; i < V; ++i) clean[i] = c[i] == c[i] ? c[i] : -INFINITY;
+      mine = group_value_32<V>(a, clean, &size, &least);
+    } else {
+      float* r = reinterpret_cast<float*>(row);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (lane + 32 * i < a.E) r[lane + 32 * i] = c[i];
+      __syncwarp();
+      mine = group_value<float>(a, r, &size, &least);
+    }
     unsigned near, groups = best_groups<float>(a, mine, size, tol < 0.f ? 0.f : 2.0f * tol, &near);
     __syncwarp();
     if (near && tol >= 0.f) {  // (logits are exact)
@@ -429,7 +477,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, const flo
       exact = groups_64(a, t, sm, near, low - 2.0f * (tol + fabsf(low) * 0x1p-22f), s, row, &groups);
       __syncwarp();
     }
-    open = of.among(groups);
+    open = V > 1 && a.group_size == 32 && a.groups == V ? groups : of.among(groups);
   }
   const bool close = a.bias != nullptr;  // the keys are of FP32 scores: look at the gaps
   if (!close && sums) {  // the groups were of scores, the experts are of logits
