@@ -854,6 +854,7 @@ Int8Tiling int8_tiling(int N, int K, int T, int num_sms) {
     const Int8Variant& v = kInt8Variants[i];
     const long long units = (long long)((blocks + v.ctas - 1) / v.ctas) * ((T + v.tile - 1) / v.tile);
     const bool fp16 = v.tile > 64;
+    if (fp16 && T <= 64) continue;  // calls of up to 64 tokens use no workspace
     for (int split = v.split ? 2 : 1; split <= (v.split ? i8g::kMaxSplit : 1); split *= 2) {
       const long long slots = num_sms * (split == 8 ? 11 : split > 1 ? 15 : 16) / 16 / (v.ctas * split);
       if (v.split && (units > slots || 2 * split > squares)) break;

@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(rt::kScanThreads) route_scan_kernel(RouteArgs 
   grid_dependency_wait();
   grid_launch_dependents();
   const int cols = (a.E + rt::kScanCtas - 1) / rt::kScanCtas, rank = (int)cluster_rank();
-  const int stretches = rt::kScanThreads / cols;
+  const int stretches = min(rt::kScanThreads / cols, 64);  // few experts: each thread adds up all of its own's
   const int r = threadIdx.x / cols, c = threadIdx.x - r * cols, e = rank * cols + c;
   const bool ok = r < stretches && e < a.E;
   const int b0 = ok ? a.runs * r / stretches : 0, b1 = ok ? a.runs * (r + 1) / stretches : 0;

@@ -44,7 +44,8 @@ def _check(h, logits, bias, outs, E, k, kw):
 
 SHAPES = [(1, 1, 1, 1, 1), (1, 8, 2, 1, 1), (2, 128, 8, 1, 1), (16, 256, 8, 8, 4), (33, 60, 6, 6, 3), (128, 64, 4, 4, 2),
           (129, 256, 8, 8, 4), (130, 72, 3, 1, 1), (257, 32, 16, 4, 2), (1500, 160, 8, 8, 3), (700, 512, 1, 1, 1),
-          (1030, 512, 1, 16, 5), (1100, 384, 12, 32, 7), (40000, 16, 3, 2, 1), (4097, 256, 8, 8, 4)]
+          (1030, 512, 1, 16, 5), (1100, 384, 12, 32, 7), (40000, 16, 3, 2, 1), (4097, 256, 8, 8, 4),
+          (20, 16, 16, 1, 1), (73, 128, 16, 4, 1), (72, 512, 16, 16, 1), (90, 64, 5, 2, 1), (3000, 1, 1, 1, 1), (5000, 8, 8, 2, 2)]
 
 
 @pytest.mark.parametrize("T,E,k,groups,top", SHAPES)
