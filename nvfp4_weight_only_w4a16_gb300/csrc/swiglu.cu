@@ -2,7 +2,8 @@
 //   forward : h = silu(g) u, and g and u as round(127 v / peak), peak / 127 per 128 elements of a row
 //   backward: dg = dh u s (1 + g (1 - s)), du = dh g s, with s = 1 / (1 + e^-g) and g and u from the codes
 //
-// Bound by memory: 8 bytes an element either way (two 16-bit rows in or out, one the other way, two bytes of codes).
+// Bound by memory: 8 bytes an element either way (two 16-bit rows in or out, one the other way, two bytes of codes;
+// 131072 x 1536, 1.6 GB: 248 us forward, 243 backward, 0.98 and 1.0 of the copy rate).
 // A thread takes 16 elements of gate and of up, eight threads a block of 128, so that all loads and stores are 16
 // bytes wide and a block's peak takes three shuffles.  Few instructions an element count (at 41 the forward took 316 us
 // for 131072 x 1536), so exp and the reciprocal are the hardware's approximations (relative error 2^-21 for |g| up to 16,
