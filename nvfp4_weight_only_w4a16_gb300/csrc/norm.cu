@@ -7,9 +7,9 @@
 // of 16-bit numbers, so that the rounding of sums cannot turn a code over.
 //
 // Bound by memory (16384 x 4096 with the residual, in 16 and 8 bits: 604 MB, 97 us, 0.92 of the copy rate; its gradient,
-// 8191 rows, 268 MB, 45 us, 0.89; two rows alone 2.3 us, the way of one row through one CTA).  A row stays in the registers of the threads that share it (`TP` threads of `V` pieces of 8
-// elements): one read, one reduction, one write.  Rows up to 1024 elements take 8 to 32 lanes of a warp and no barrier,
-// longer ones a CTA, whose next row is on its way while this one is reduced.
+// 8191 rows, 268 MB, 45 us, 0.89; two rows alone 2.5 us).  A row stays in the registers of the threads that share it (`TP`
+// threads of `V` pieces of 8 elements): one read, one reduction, one write.  Rows up to 1024 elements take
+// 8 to 32 lanes of a warp and no barrier, longer ones a CTA, whose next row is on its way while this one is reduced.
 //
 // Sums are FP32; where squares or products leave its range (the mean below 2^-80 or the sum above 2^120, the peak beyond
 // 2^+-100) the row's statistics are formed again in 64 bits.  A row whose products are all below 2^-149 counts as zeros.
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(nm::kSmallThreads) norm_backward_kernel(NormBa
 // as far ahead as that holds; the others read a row there twice, before and after its sum is known, so that few registers
 // are taken and two or three CTAs a multiprocessor hide one another's barriers.  (8191 rows of 4096: 58 us with the rows in
 // registers, 25 KB a multiprocessor on their way; 55 with one CTA a multiprocessor and the rows copied from the ring to
-// registers.)
+// registers; 45 as it is.  2048 rows of 16384, as many bytes, take 67: two such rows fill the ring.)
 namespace nm {
 constexpr int kRingBytes = 216 * 1024, kMaxSlots = 8;  // of a multiprocessor
 }
