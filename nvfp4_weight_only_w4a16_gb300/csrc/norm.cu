@@ -6,7 +6,7 @@
 // The codes do not depend on rstd: they are the rounded quotients of w h and its largest magnitude, both exact products
 // of 16-bit numbers, so that the rounding of sums cannot turn a code over.
 //
-// Bound by memory (16384 x 4096 with the residual, in 16 and 8 bits: 604 MB, 97 us, 0.92 of the copy rate; its gradient,
+// Bound by memory (16384 x 4096 with the residual, in 16 and 8 bits: 604 MB, 93 us, 0.97 of the copy rate; its gradient,
 // 8191 rows, 268 MB, 45 us, 0.89; two rows alone 2.5 us).  A row stays in the registers of the threads that share it (`TP`
 // threads of `V` pieces of 8 elements): one read, one reduction, one write.  Rows up to 1024 elements take
 // 8 to 32 lanes of a warp and no barrier, longer ones a CTA, whose next row is on its way while this one is reduced.
@@ -14,6 +14,7 @@
 // Sums are FP32; where squares or products leave its range (the mean below 2^-80 or the sum above 2^120, the peak beyond
 // 2^+-100) the row's statistics are formed again in 64 bits.  A row whose products are all below 2^-149 counts as zeros.
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "kernels.h"
@@ -491,9 +492,21 @@ static NormShape norm_shape(int pieces, int T, int num_sms) {
 template <bool kF16, int TP, int V>
 static cudaError_t run_forward(const NormArgs& a, int num_sms, cudaStream_t st) {
   constexpr int threads = TP <= 32 ? nm::kSmallThreads : TP, rows = threads / (TP <= 32 ? TP : threads);
-  constexpr int per_sm = TP <= 32 ? 8 : 1024 / TP;
+  // As many CTAs as run at a time: the last ones of 8 a multiprocessor, of which registers let 3 run, found the machine half
+  // empty (16384 x 4096 97 us, 93 so; 1000 rows 9.8, 8.2).  Long calls whose threads hold four pieces do better with
+  // twice as many (65536 x 1024 101 us once, 95 twice; 4096 x 16384 102, 97; the
+  // 16384 rows of 4096 alike; but 8000 rows of 4096 48.2, 49.5, and 262144 of 128, one piece a thread, 55.4, 56.5).
+  static std::atomic<int> resident{0};  // of a multiprocessor; all devices that run this code are alike
+  int per_sm = resident.load(std::memory_order_relaxed);
+  if (!per_sm) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_forward_kernel<kF16, TP, V>, threads, 0);
+    if (e != cudaSuccess) return e;
+    per_sm = std::max(per_sm, 1);
+    resident.store(per_sm, std::memory_order_relaxed);
+  }
   cudaLaunchAttribute at;
-  const int grid = std::min((a.T + rows - 1) / rows, num_sms * per_sm);
+  const int turns = (a.T + rows - 1) / rows, wave = num_sms * per_sm;
+  const int grid = std::min(turns, V >= 4 && turns >= 24 * wave ? 2 * wave : wave);
   const cudaLaunchConfig_t cfg = dependent(dim3(grid), dim3(threads), st, &at);
   return cudaLaunchKernelEx(&cfg, norm_forward_kernel<kF16, TP, V>, a);
 }

@@ -20,8 +20,8 @@
 // turns the runs' counts into places and a third scatters; the counts lie in `inv`, each run's in its own rows' part,
 // which its CTA alone overwrites in the end, so that there is no workspace and calls may overlap.
 //
-// Bound by instructions: 16384 tokens of 256 experts take 800 warp instructions a token as a softmax, 1150 with a bias and
-// groups, and 25 and 36 us with the scan and the scatter, where their bytes would take 3.  Few tokens wait for one token's
+// 16384 tokens of 256 experts take 800 warp instructions a token as a softmax, 1150 with a bias and groups, issued in two
+// thirds of the slots by six warps a scheduler, and 25 and 36 us with the scan and the scatter; their bytes would take 3.  Few tokens wait for one token's
 // way through a warp and for the launches (2 tokens of 128 experts 4.1 us; 128 of 256 in groups 16).
 #include <algorithm>
 #include <mutex>
@@ -34,7 +34,8 @@ namespace nvfp4moe {
 
 namespace rt {
 constexpr int kMaxExperts = 512;
-constexpr int kThreads = 768;   // of 80 registers; 1024 of 64 spill (16384 x 256 in groups 40.2 us, 39.0)
+constexpr int kThreads = 768;   // of 80 registers; 1024 of 64 spill (16384 x 256 in groups 40.2 us, 39.0); 896 of 72 gain
+                                // there (35.8, 36.4) and lose below (8192 tokens 27.3, 25.7)
 constexpr int kOneCta = 72;     // tokens up to which one CTA does it all (256 experts in groups, 64 tokens: 15.1 us, 16.2 as
                                 // three kernels; 96: 19.8, 16.1)
 constexpr int kRun = 256;     // of a run, unless its counts need more
