@@ -658,7 +658,7 @@ typedef struct nvfp4_norm_config {
   int device;    /* CUDA device ordinal */
 } nvfp4_norm_config;
 
-/* Synchronous.  The handle holds the workspace of dweight (some H * 2.5 KB). */
+/* Synchronous.  The handle holds the workspace of dweight (at most H * 4 KB). */
 nvfp4_moe_status nvfp4_norm_create(const nvfp4_norm_config* config, nvfp4_moe_t* out);
 
 /* T 0..2^20 rows of H, DEVICE, 16-byte aligned (q: 8), rows ld elements apart: at

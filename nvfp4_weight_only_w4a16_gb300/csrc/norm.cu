@@ -224,6 +224,7 @@ struct NormBackArgs {
 template <bool kF16, int TP, int V>
 __global__ void __launch_bounds__(nm::kSmallThreads) norm_backward_kernel(NormBackArgs a) {
   constexpr int kRows = nm::kSmallThreads / TP;
+  __shared__ float fold[kRows][8 * TP * V];
   const int lane = threadIdx.x % TP, pieces = a.H / 8;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -300,14 +301,20 @@ __global__ void __launch_bounds__(nm::kSmallThreads) norm_backward_kernel(NormBa
       }
     }
   }
+  // The CTA's rows together, so that the few CTAs that add up the parts have few to read (64000 x 64: 23 us with a part a row,
+  // 8 so).
   if (a.part) {
-    float* out = a.part + ((long long)blockIdx.x * kRows + threadIdx.x / TP) * a.H;
+    float* to = fold[threadIdx.x / TP];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int p = lane + v * TP;
-      if (p >= pieces) continue;
-      *reinterpret_cast<float4*>(out + 8 * p) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-      *reinterpret_cast<float4*>(out + 8 * p + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[8 * (lane + v * TP) + i] = dw[v][i];
+    __syncthreads();
+    for (int h = threadIdx.x; h < a.H; h += nm::kSmallThreads) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) sum += fold[i][h];
+      a.part[(long long)blockIdx.x * a.H + h] = sum;
     }
   }
 }
@@ -545,22 +552,22 @@ struct NormBackShape {
   int tp, v, rows;  // threads a row, pieces a thread, rows of a CTA at a time
   int per_sm;       // CTAs a multiprocessor
 };
+// As many CTAs as run at a time, by registers or by the ring (131072 x 256: 56 us with 4, 49 with 6).  Rows of 4104 to 6144
+// by 256 threads, two CTAs (6552 x 5120 46 us; one CTA of 512 threads 58; 666 rows of 6144 12.2, 10.9); longer ones that way
+// would hold four pieces a thread (4095 x 8192 66 us, 50 as it is).
 static NormBackShape norm_back_shape(int pieces) {
-  if (pieces <= 8) return {8, 1, 16, 4};
-  if (pieces <= 16) return {16, 1, 8, 4};
-  if (pieces <= 32) return {32, 1, 4, 4};
-  if (pieces <= 64) return {32, 2, 4, 4};
+  if (pieces <= 8) return {8, 1, 16, 5};
+  if (pieces <= 16) return {16, 1, 8, 5};
+  if (pieces <= 32) return {32, 1, 4, 6};
+  if (pieces <= 64) return {32, 2, 4, 5};
   if (pieces <= 128) return {128, 1, 1, 6};
   if (pieces <= 256) return {256, 1, 1, 3};
   if (pieces <= 512) return {256, 2, 1, 3};
+  if (pieces <= 768) return {256, 3, 1, 2};
   if (pieces <= 1024) return {512, 2, 1, 1};
   return {512, 4, 1, 1};
 }
-static int norm_back_parts(const NormBackShape& s, int grid) { return grid * (s.tp <= 32 ? s.rows : 1); }
-int norm_backward_parts(int H, int num_sms) {
-  const NormBackShape s = norm_back_shape(H / 8);
-  return norm_back_parts(s, num_sms * s.per_sm);
-}
+int norm_backward_parts(int H, int num_sms) { return num_sms * norm_back_shape(H / 8).per_sm; }  // one a CTA
 
 template <bool kF16, int TP, int V>
 static cudaError_t run_backward(const NormBackArgs& a, int grid, cudaStream_t st) {
@@ -601,6 +608,7 @@ static cudaError_t backward_of(const NormBackArgs& a, const NormBackShape& s, in
     case 128 * 8 + 1: return run_ring<kF16, 128, 1, 6>(a, grid, status, st);
     case 256 * 8 + 1: return run_ring<kF16, 256, 1, 3>(a, grid, status, st);
     case 256 * 8 + 2: return run_ring<kF16, 256, 2, 3>(a, grid, status, st);
+    case 256 * 8 + 3: return run_ring<kF16, 256, 3, 2>(a, grid, status, st);
     case 512 * 8 + 2: return run_ring<kF16, 512, 2, 1>(a, grid, status, st);
     default: return run_ring<kF16, 512, 4, 1>(a, grid, status, st);
   }
@@ -622,7 +630,7 @@ cudaError_t launch_norm_backward(const NormBackOp& p, cudaStream_t st) {
   if (e != cudaSuccess || !p.dweight) return e;
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = dependent(dim3((p.H + 31) / 32), dim3(1024), st, &at);
-  return cudaLaunchKernelEx(&cfg, norm_dweight_kernel, (const float*)p.part, norm_back_parts(s, grid), p.H, p.dweight);
+  return cudaLaunchKernelEx(&cfg, norm_dweight_kernel, (const float*)p.part, grid, p.H, p.dweight);
 }
 
 }  // namespace nvfp4moe

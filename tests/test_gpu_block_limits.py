@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import nvfp4_weight_only_w4a16_gb300 as P
-from tests.block_ops import DEV
+from tests.block_ops import DEV, U, f64, half_step, norm_backward, within
 from tests.test_gpu_int8 import _run
 
 pytestmark = pytest.mark.gpu
@@ -49,6 +49,25 @@ def test_norm_of_rows_far_apart(H):
         torch.cuda.empty_cache()
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert n.nvfp4_moe_get_status()[0] == 0
+    n.close()
+
+
+# every thread layout with more rows than its CTAs hold at a time, and a last turn that few of them have
+@pytest.mark.parametrize("T,H", [(40003, 8), (30001, 64), (15001, 128), (12345, 256), (9001, 512), (5001, 1024), (2501, 2048),
+                                 (1501, 5120), (1001, 8192)])
+def test_norm_gradient_of_many_rows(T, H):
+    n = P.Norm(H)
+    h, dy, w = _rand(T, H) * 2, _rand(T, H) * 2.0 ** -4, _rand(H)
+    y, rstd = torch.empty_like(h), torch.empty((T,), device=DEV)
+    n.nvfp4_norm_forward(h, w, y=y, rstd=rstd)
+    dx, dw = torch.empty_like(h), torch.empty((H,), device=DEV)
+    n.nvfp4_norm_backward(dy, h, w, rstd, dx, dweight=dw)
+    want, b, want_w, b_w = norm_backward(f64(dy), f64(h), f64(w), f64(rstd), 0.0)
+    within(f64(dx), want, b + half_step(abs(want) + b, torch.bfloat16), "dx")
+    within(f64(dw), want_w, b_w + U * abs(want_w), "dweight")
+    dw2 = torch.empty_like(dw)
+    n.nvfp4_norm_backward(dy, h, w, rstd, dx, dweight=dw2)
+    assert torch.equal(dw2, dw)
     n.close()
 
 
