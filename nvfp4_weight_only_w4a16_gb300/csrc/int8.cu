@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(i8v::kThreads, 1) int8_gemv_kernel(Int8Args a)
 // kSplit: where there are few units, a cluster of CTAs takes one, a share of the reduction each, and adds the integers
 // through distributed shared memory.
 //
-// 16384 tokens of 12576 x 4096 take 952 us by themselves, 1.77 PFLOP/s with the tokens' conversion, and 1046 among calls
-// that keep the card at its power limit, 1.61; a library's BF16 product runs at 1.74 when sustained.
+// 16384 tokens of 12576 x 4096 take 952 us by themselves, 1.77 PFLOP/s with the tokens' conversion, and 1046 to 1058 among
+// calls that keep the card at its power limit, 1.60 to 1.61; a library's BF16 product runs at 1.74 when sustained.
 // --------------------------------------------------------------------------------------------------------------------
 namespace i8g {
 constexpr int kEpiWarps = 8;

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(nm::kSmallThreads) norm_backward_kernel(NormBa
 // as far ahead as that holds; the others read a row there twice, before and after its sum is known, so that few registers
 // are taken and two or three CTAs a multiprocessor hide one another's barriers.  (8191 rows of 4096: 58 us with the rows in
 // registers, 25 KB a multiprocessor on their way; 55 with one CTA a multiprocessor and the rows copied from the ring to
-// registers; 45 as it is.  2048 rows of 16384, as many bytes, take 67: two such rows fill the ring.)
+// registers; 45 as it is.  2047 rows of 16384, as many bytes, take 65: two such rows fill the ring.)
 namespace nm {
 constexpr int kRingBytes = 216 * 1024, kMaxSlots = 8;  // of a multiprocessor
 }
