@@ -432,7 +432,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, const flo
   if (a.bias || sums) {
     // By the hardware's 2^x (2^-22, and half a step of x) and 1/x (a step).  A sigmoid s is off by 2^-24 (7 + 1.5 |l|) s at
     // most for l < 0, and by less than 2^-24 6 for l > 0, so by 2^-24 (7 - 1.5 log s) s for the largest s; a softmax, whose
-    // sum of E terms counts too, by 2^-24 43 of the largest.  tol covers two.
+    // sum of E terms counts too, by 2^-24 43 of the largest.  Both are flushed to 0 below 2^-126.  tol covers two.
     if (a.score) {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = sigmoid_fast(c[i]);
@@ -447,8 +447,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, const flo
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) most = fmaxf(most, c[i]);  // drops NaNs
-    most = warp_max(most);
-    tol = most * (a.score ? 0x1p-23f * (8.0f - 1.5f * __logf(most)) : 0x1p-17f);
+    most = fmaxf(warp_max(most), 0x1p-126f);
+    tol = most * (a.score ? 0x1p-23f * (8.0f - 1.5f * __logf(most)) : 0x1p-17f) + 0x1p-124f;
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] += bias[lane + 32 * i];
