@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(rt::kScanThreads) route_scan_kernel(RouteArgs 
   __shared__ int part[rt::kScanThreads];
   __shared__ float sums[rt::kScanCtas];  // every CTA's, as bits
   __shared__ int scan[32];
+  cluster_arrive();  // the sums wait for it: every CTA has begun
   grid_dependency_wait();
   grid_launch_dependents();
   const int cols = (a.E + rt::kScanCtas - 1) / rt::kScanCtas, rank = (int)cluster_rank();
@@ -670,6 +671,7 @@ __global__ void __launch_bounds__(rt::kScanThreads) route_scan_kernel(RouteArgs 
     }
   int total;
   const int lower = block_exclusive_scan(r == 0 ? sum : 0, scan, &total);  // experts of this CTA below; r = 0 comes first
+  cluster_wait();
   if (threadIdx.x < rt::kScanCtas) st_cluster(sums + rank, threadIdx.x, __int_as_float(total));
   if (r == 0) part[c] = lower;
   cluster_sync_all();
