@@ -591,7 +591,10 @@ nvfp4_moe_status nvfp4_int4_forward(nvfp4_moe_t h, int T, const void* x, int64_t
  * -inf), and so does an expert whose bias is NaN; a bias of -inf or of the
  * type's lowest value keeps an expert behind all others.  Softmax where no
  * logit is above -inf: s = 1 / E for each -inf; where some are +inf: those share 1.
- * Renormalised weights whose sum is 0 are scale / top_k each.
+ * Weights are FP32: a sigmoid below 2^-127 is 0 in them.  Renormalised ones whose
+ * sigmoids sum to less than 2^-25 are the softmax of the chosen logits, which they
+ * are then to a rounding, however small; those whose scores are all 0 (-inf, NaN)
+ * are scale / top_k each.
  *
  * A route handle is an nvfp4_moe_t: nvfp4_moe_destroy, nvfp4_moe_last_error and
  * nvfp4_moe_get_status (which counts NaN logits) apply to it; the other
@@ -632,8 +635,8 @@ nvfp4_moe_status nvfp4_route_forward(nvfp4_moe_t h, int T, const void* logits, i
 /* dlogits [T][E] (the logits' type, rows ld_dl apart) from dweights [T][top_k]
  * for the choice ids; the choice itself is constant.  An id outside 0..E-1 counts
  * as none, an expert named twice twice.  Softmax whose largest logit is
- * infinite, NaN logits, and renormalised sigmoids that are all 0 have no gradient
- * (zeros).  dlogits may be logits. */
+ * infinite, NaN logits, and renormalised sigmoids whose logits are all -inf have no
+ * gradient (zeros).  dlogits may be logits. */
 nvfp4_moe_status nvfp4_route_backward(nvfp4_moe_t h, int T, const void* logits, int64_t ld, const int32_t* ids,
                                       const float* dweights, void* dlogits, int64_t ld_dl, cudaStream_t stream);
 

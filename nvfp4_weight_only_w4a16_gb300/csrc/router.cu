@@ -40,6 +40,9 @@ constexpr int kOneCta = 72;     // tokens up to which one CTA does it all (256 e
                                 // three kernels; 96: 19.8, 16.1)
 constexpr int kRun = 256;     // of a run, unless its counts need more
 constexpr int kMostShared = 208 * 1024;  // 512 experts: 128 KB of 32 warps' rows and 64 KB of a run's bits
+// Sigmoids below this are e^l to a rounding, and what they are renormalised to is the softmax of their logits: it holds
+// where they themselves are lost to FP32 (from l = -88.7 down).  Of chosen ones only -inf and NaN are 0 then.
+constexpr float kLowSigmoids = 0x1p-25f;
 }  // namespace rt
 
 struct RouteArgs {
@@ -566,7 +569,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, const flo
     if (a.renorm) {
       float sum = 0.f;
       for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, w, j);
-      w = sum > 0.f ? w / sum : 1.0f / (float)a.k;
+      w = sum >= rt::kLowSigmoids ? w / sum : warp_softmax_k(logit, a.k);
     }
   }
   *weight = w * a.scale;
@@ -746,10 +749,17 @@ __global__ void __launch_bounds__(rt::kBackThreads) route_backward_kernel(RouteA
       const float x = ok ? load_logit(a.logits, a.bf16, (size_t)t * a.ld + id) : __uint_as_float(0x7FC00000u);
       const bool counts = x == x;
       if (a.score) {
-        const float s = counts ? score_of<float>(x, 1, sm, a.E) : 0.f, rest = counts ? score_of<float>(-x, 1, sm, a.E) : 0.f;
-        if (a.renorm) {
-          const float sum = warp_sum(s), dot = warp_sum(counts ? v * s : 0.f);
-          v = sum > 0.f ? (v - dot / sum) / sum : 0.f;
+        float s = counts ? score_of<float>(x, 1, sm, a.E) : 0.f;
+        const float rest = counts ? score_of<float>(-x, 1, sm, a.E) : 0.f;
+        if (a.renorm) {  // of the weights, w rest (d - sum w d): no quotient by a sum that may be as small as a score
+          float sum = warp_sum(s);
+          if (sum < rt::kLowSigmoids) {
+            const float top = warp_max(counts ? x : -INFINITY);
+            s = counts && top != -INFINITY ? expf(x - top) : 0.f;
+            sum = warp_sum(s);
+          }
+          s = sum > 0.f ? s / sum : 0.f;
+          v -= warp_sum(counts ? v * s : 0.f);
         }
         v = counts && v != 0.f ? v * s * rest : 0.f;
       } else {
