@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(TP + 32, kPerSm) norm_backward_ring_kernel(Nor
       unpack8<kF16>(w4[v], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float dr = d[i] * rstd;
-        c = fmaf(dr * w[i], x[i], c);
-        dw[v][i] = fmaf(dr, x[i], dw[v][i]);
+        const float n = x[i] * rstd;
+        c = fmaf(d[i] * w[i], n, c);
+        dw[v][i] = fmaf(d[i], n, dw[v][i]);
       }
     }
     __syncwarp();
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(TP + 32, kPerSm) norm_backward_ring_kernel(Nor
     c = lane < TP / 32 ? red[k][lane] : 0.f;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    c *= -inv_h * rstd * rstd;
+    c *= inv_h;
     uint4 out[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(TP + 32, kPerSm) norm_backward_ring_kernel(Nor
       unpack8<kF16>(a.dsum ? load16(slot + 2 * bytes + 16 * p) : make_uint4(0u, 0u, 0u, 0u), s);
       unpack8<kF16>(w4[v], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(d[i], w[i] * rstd, fmaf(x[i], c, s[i]));
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(rstd, fmaf(-c, x[i] * rstd, d[i] * w[i]), s[i]);
       out[v] = pack8<kF16>(o);
     }
     __syncwarp();
