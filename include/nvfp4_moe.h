@@ -646,9 +646,11 @@ nvfp4_moe_status nvfp4_route_backward(nvfp4_moe_t h, int T, const void* logits, 
  *   y   = weight * sum * rstd, rstd = 1 / sqrt(mean(sum^2) + eps)
  *   q   = round(127 v / max |v|), v = weight * sum; q_scale = max |y| / 127
  * so that y is about q * q_scale: the input of nvfp4_int8_forward.  q is the
- * exactly rounded quotient, ties to even, in -127..127.  A row of zeros has codes
- * and a scale of 0 (one whose products are all below 2^-149 too); one that is not
- * finite has codes 0 and a scale of NaN.
+ * exactly rounded quotient, ties to even, in -127..127.  A row of zeros has y, codes
+ * and a scale of 0 also where eps is 0 (codes and scale too where its products are
+ * all below 2^-149); one that is not finite has codes 0 and a scale of NaN.  Without
+ * eps rstd may be beyond FP32 (a row below 2^-128): it is infinite then, y, q and
+ * q_scale are right all the same, and the row has no gradient (NaN or infinite).
  * Backward, of sum (which is x's and the residual's):
  *   dx = rstd * (weight * dy) - sum * rstd^3 / H * sum_h(weight * dy * sum) + dsum
  *   dweight = sum over the rows of dy * sum * rstd

@@ -66,7 +66,8 @@ __device__ __forceinline__ void row_reduce(F& sum, F& top, F* red) {
 __device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
 template <bool kF16, int TP, int V>
-__global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
+// (rows of 4104 to 8192: 6 registers over two CTAs a multiprocessor without the bound)
+__global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP, TP == 256 ? 2 : 0)
     norm_forward_kernel(NormArgs a) {
   constexpr int kRows = TP <= 32 ? nm::kSmallThreads / TP : 1;  // rows of a CTA at a time
   __shared__ float red[2][64];
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
     const float peak = __uint_as_float(peak_bits), mean = ss / (float)a.H + a.eps;
     float rstd = 1.0f / sqrtf(mean), scale = a.weight ? peak * rstd / 127.0f : peak / 127.0f;
     double peak64 = 0.0;
+    float up = 1.0f;  // rstd's second factor, where it is beyond FP32: without eps, of rows below the normal numbers
     bool finite = true;
     // out of FP32's range; a peak of zero is that of a row of zeros
     bool odd = (a.weight && !(mean >= 0x1p-80f && ss <= 0x1p120f)) || (a.q && peak_bits && !plain_peak(peak));
@@ -164,16 +166,19 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
       if (bad) p64 = INFINITY;
       if (TP > 32) __syncthreads();  // red64 of the row before
       row_reduce<TP>(s64, p64, red64);
-      if (a.weight) rstd = (float)(1.0 / sqrt(s64 / a.H + (double)a.eps));
+      const double mean64 = s64 / a.H + (double)a.eps, r64 = mean64 == 0.0 ? 0.0 : 1.0 / sqrt(mean64);
+      if (a.weight) rstd = mean64 == 0.0 ? INFINITY : (float)r64;
       peak64 = p64;
-      scale = (float)(a.weight ? p64 * (double)rstd / 127.0 : p64 / 127.0);
-      finite = p64 <= 1.7e308 && (!a.weight || rstd <= 3.4e38f);
+      scale = (float)(a.weight ? p64 * r64 / 127.0 : p64 / 127.0);
+      finite = p64 <= 1.7e308;
+      if (rstd == INFINITY) up = (float)(r64 * 0x1p-64);  // 0 for a row of zeros, which stays so
     }
     if (row_ok) {
       if (lane == 0) {
         if (a.rstd) a.rstd[t] = rstd;
         if (a.q) a.q_scale[t] = finite ? scale : __uint_as_float(0x7FC00000u);
       }
+      if (rstd == INFINITY) rstd = 0x1p64f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int p = lane + v * TP;
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP)
         if (a.y) {
           float y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
+          for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * up * w[i];
           *reinterpret_cast<uint4*>(a.y + t * a.ldy + 16ll * p) = pack8<kF16>(y);
         }
         if (a.q) {
