@@ -144,10 +144,10 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP, TP == 256 ?
     double peak64 = 0.0;
     float up = 1.0f;  // rstd's second factor, where it is beyond FP32: without eps, of rows below the normal numbers
     bool finite = true;
-    // out of FP32's range; a peak of zero is that of a row of zeros
-    bool odd = (a.weight && !(mean >= 0x1p-80f && ss <= 0x1p120f)) || (a.q && peak_bits && !plain_peak(peak));
-    if (TP < 32) odd = __any_sync(0xffffffffu, odd);  // a warp's rows go together
-    if (odd) {
+    // out of FP32's range: its mean, or what its codes are made of (a peak of zero is that of a row of zeros).  Each alone
+    // decides what is taken from the 64-bit sums, so that a row is the same whatever its neighbours and outputs are
+    const bool far = a.weight && !(mean >= 0x1p-80f && ss <= 0x1p120f), odd = far || (a.q && peak_bits && !plain_peak(peak));
+    if (TP < 32 ? __any_sync(0xffffffffu, odd) : odd) {  // a warp's rows go together
       double s64 = 0.0, p64 = 0.0;
       bool bad = false;
 #pragma unroll
@@ -167,11 +167,15 @@ __global__ void __launch_bounds__(TP <= 32 ? nm::kSmallThreads : TP, TP == 256 ?
       if (TP > 32) __syncthreads();  // red64 of the row before
       row_reduce<TP>(s64, p64, red64);
       const double mean64 = s64 / a.H + (double)a.eps, r64 = mean64 == 0.0 ? 0.0 : 1.0 / sqrt(mean64);
-      if (a.weight) rstd = mean64 == 0.0 ? INFINITY : (float)r64;
-      peak64 = p64;
-      scale = (float)(a.weight ? p64 * r64 / 127.0 : p64 / 127.0);
-      finite = p64 <= 1.7e308;
-      if (rstd == INFINITY) up = (float)(r64 * 0x1p-64);  // 0 for a row of zeros, which stays so
+      if (far) {
+        rstd = mean64 == 0.0 ? INFINITY : (float)r64;
+        if (rstd == INFINITY) up = (float)(r64 * 0x1p-64);  // 0 for a row of zeros, which stays so
+      }
+      if (odd) {
+        peak64 = p64;
+        scale = (float)(a.weight ? p64 * r64 / 127.0 : p64 / 127.0);
+        finite = p64 <= 1.7e308;
+      }
     }
     if (row_ok) {
       if (lane == 0) {

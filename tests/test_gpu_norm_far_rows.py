@@ -66,3 +66,52 @@ def test_zeros_and_the_smallest_rows_without_eps(T, H):
     n.nvfp4_norm_forward(x, w, q=q2, q_scale=s2)
     assert torch.equal(y2, y) and torch.equal(q2, q) and torch.equal(s2, s)
     n.close()
+
+
+@pytest.mark.parametrize("dt", [BF16, torch.float16])
+@pytest.mark.parametrize("H", [8, 64, 72, 128, 256])
+def test_rows_do_not_depend_on_their_neighbours(H, dt):
+    """Rows that share a warp with zeros, infinities, NaNs or rows out of range are as they are among ordinary ones."""
+    rng = np.random.default_rng(H)
+    T = 130
+    x, w = _rand(rng, (T, H), dt), _rand(rng, (H,), dt)
+    among = x.clone()
+    odd = rng.choice(T, T // 3, replace=False)
+    for i, v in zip(odd, rng.choice([0.0, float("inf"), float("nan"), 2.0 ** -110, 2.0 ** 110], len(odd))):
+        among[i] = among[i].float().mul(v).to(dt) if np.isfinite(v) else torch.full((H,), v, dtype=dt, device=DEV)
+    rest = torch.from_numpy(np.setdiff1d(np.arange(T), odd)).to(DEV)
+    got = []
+    for rows in (x, among):
+        y, q = torch.empty_like(x), torch.empty((T, H), dtype=torch.int8, device=DEV)
+        s, rstd, s2 = (torch.empty((T,), device=DEV) for _ in range(3))
+        n, lin = P.Norm(H, 0.0, act_f16=dt == torch.float16), None
+        n.nvfp4_norm_forward(rows, w, y=y, q=q, q_scale=s, rstd=rstd)
+        out = [y, q, s, rstd]
+        if H % 16 == 0:
+            lin, q2 = P.Int8Linear(16, H, 16), torch.empty_like(q)
+            lin.nvfp4_int8_quantize(rows, q2, s2)
+            out += [q2, s2]
+            lin.close()
+        got.append([t[rest].clone() for t in out])
+        n.close()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("H", [64, 128, 256, 4096])
+def test_rows_do_not_depend_on_what_is_asked_of_them(H):
+    """Products beyond what codes are formed of in FP32: y and rstd are the same without the codes."""
+    rng = np.random.default_rng(H)
+    T = 300
+    x, w = _rand(rng, (T, H), BF16), _rand(rng, (H,), BF16, 2.0 ** 105)
+    n, got = P.Norm(H, 0.0), []
+    for codes_too in (False, True):
+        y, rstd = torch.empty_like(x), torch.empty((T,), device=DEV)
+        q, s = torch.empty((T, H), dtype=torch.int8, device=DEV), torch.empty((T,), device=DEV)
+        n.nvfp4_norm_forward(x, w, y=y, rstd=rstd, **(dict(q=q, q_scale=s) if codes_too else {}))
+        got.append((y, rstd))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    want, rr = norm(f64(x), f64(w), 0.0)
+    qq, peak = codes(f64(x) * f64(w))
+    assert np.array_equal(f64(q), qq)
+    within(f64(s), peak * rr / 127.0, (R_ERR + 3 * U) * peak * rr / 127.0, "q_scale")
+    n.close()
