@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) drain_copies(ctl.raw_full, it, kRaw);
+    if (lane == 0) drain_copies(ctl.raw_full, it, kRaw);
   } else if (warp == 1 || (kIssuers == 2 && warp == 3)) {
     // ---------------- MMA issuers: the whole warp walks the loop, one lane issues.  Issuer h takes every kIssuers-th
     // square of the CTA's sequence, into its own accumulator ----------------
@@ -426,9 +426,9 @@ __global__ void __launch_bounds__(gg::kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
+    if (lane == 0) {
       if (rank == 0) drain_copies(ctl.b_full, it, kStagesB);
-      else
+      else if (!ok)
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // its copies complete on the first CTA's barriers
     }
   } else if (warp >= 8) {

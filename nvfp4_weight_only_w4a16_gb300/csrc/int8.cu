@@ -443,7 +443,7 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
         }
       }
     }
-    if (!ok && lane == 0) drain_copies(ctl.raw_full, it, Plan::kRaw);
+    if (lane == 0) drain_copies(ctl.raw_full, it, Plan::kRaw);
   } else if (warp == Plan::kTokens) {
     // ---------------- tokens in FP16: this CTA's half of the tile, 128 elements a stage ----------------
     if constexpr (Plan::kPre) {
@@ -473,9 +473,9 @@ __global__ void __launch_bounds__((i8g::Plan<kCtas, kTile>::kThreads), 1)
           __syncwarp();
         }
       }
-      if (!ok && lane == 0) {
+      if (lane == 0) {
         if (rank == 0) drain_copies(ctl.b_full, it, Plan::kStagesB);
-        else
+        else if (!ok)
           for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // its copies complete on the first CTA's barriers
       }
     }

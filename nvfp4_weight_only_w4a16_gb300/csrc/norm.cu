@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(TP + 32, kPerSm) norm_backward_ring_kernel(Nor
         if (a.dsum) bulk_g2s(to + 2 * bytes, a.dsum + t * a.ld_dsum, bytes, full + pos.slot);
         ++issued;
       }
-      if (!ok) drain_copies(full, issued, slots);
+      drain_copies(full, issued, slots);
     }
     return;
   }

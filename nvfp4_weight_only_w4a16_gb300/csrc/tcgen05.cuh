@@ -192,9 +192,10 @@ struct RingPos {
   }
 };
 
-// After a role has given up: wait (bounded) for its own copies still in flight into
+// At a producer's end: wait (bounded) for its own copies still in flight into
 // a ring of n slots, of which copy i (< issued) went to slot i % n and completes
-// phase i / n of full[i % n], so that none lands after the CTA has left.
+// phase i / n of full[i % n], so that none lands after the CTA has left.  Also where
+// the producer itself has got to its end: those that use the copies may have given up.
 __device__ __forceinline__ void drain_copies(uint64_t* full, uint32_t issued, int n) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = issued > (uint32_t)n ? issued - n : 0u; i < issued; ++i)

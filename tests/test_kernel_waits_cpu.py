@@ -35,3 +35,14 @@ def test_every_cta_of_a_cluster_has_begun_before_another_reaches_into_it(text):
     before, in the order of the text."""
     barrier = re.search(r"\bcluster_(?:wait|sync_all)\(\)", text)
     assert barrier and barrier.start() < re.search(REACHES, text).start()
+
+
+@pytest.mark.parametrize("file,rings", [("norm.cu", 1), ("int8.cu", 2), ("grouped.cu", 2)])
+def test_a_producer_waits_for_its_copies_however_it_ends(file, rings):
+    """A consumer whose wait has run out leaves copies in flight that a producer at its end no longer knows of: no copy
+    may land in the shared memory of a CTA that has left, so the wait for them hangs on no verdict of the producer's."""
+    code = _code(os.path.join(CSRC, file))
+    ends = [m.start() for m in re.finditer(r"\bdrain_copies\(", code)]
+    assert len(ends) == rings
+    for at in ends:
+        assert "ok" not in re.search(r"[;}][^;}]*$", code[:at]).group(0)
