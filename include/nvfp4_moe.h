@@ -697,7 +697,8 @@ nvfp4_moe_status nvfp4_norm_backward(nvfp4_moe_t h, int T, const void* dy, int64
  * Backward, with g and u = codes * scales, s = 1 / (1 + exp(-g)):
  *   dgate = dh * u * s * (1 + g * (1 - s)),  dup = dh * g * s
  * A block of 128 that is not finite comes back as NaN.  exp is evaluated to about
- * 2^-21; all arithmetic is FP32, with one rounding at the end.
+ * 2^-21 (|g| 2^-24 where |g| is larger than 16), and s below 2^-126, from g = -87.3
+ * down, counts as 0; all arithmetic is FP32, with one rounding at the end.
  * A SwiGLU handle is an nvfp4_moe_t like a route handle.
  * ------------------------------------------------------------------------- */
 typedef struct nvfp4_swiglu_config {
